@@ -261,6 +261,216 @@ wl_status wl_step_launch(wl_step step, void *hip_stream);
  * of the step is still running (for example by synchronizing its stream). */
 wl_status wl_step_destroy(wl_step step);
 
+/* ---------------------------------------------------------------------------
+ * The rest of a decoder layer, between the projections: norms with a block's
+ * residual, rotary positions, a paged cache of keys and values, attention over
+ * it. Conventions as above (device pointers, caller's buffers, checks on the
+ * host before anything is enqueued, one rounding of every result, no atomics),
+ * with these additions:
+ *   - `dtype` (WL_DTYPE_BF16 or WL_DTYPE_F32) is the type of every tensor whose
+ *     type is not stated.
+ *   - Rows may be strided: `ld...` is the distance of two tokens' rows in
+ *     elements, so that Q, K and V can lie side by side as wl_qkv_fused leaves
+ *     them. It is a multiple of 8 and at least the row's width.
+ *   - An output may be exactly one of its call's inputs where that is stated
+ *     (same pointer, same ld); any other overlap is WL_ERR_INVALID_ARG.
+ *   - Index arrays (positions, sequences, slots, lengths, page table) are device
+ *     int32, read when the work runs, so a recorded step follows them. The host
+ *     cannot check them; the kernels do, as stated at each operation, and never
+ *     read or write outside the tensors whatever they hold.
+ * Serving only: these operations have no gradients (a rotation by the negated
+ * positions is the rotation's transpose).
+ */
+
+/* Norms around a block, fused with its gate and its residual:
+ *   p  = post ? rms(y) (post + offset) : y       the norm behind the block
+ *   x' = res_scale x + branch_scale gate p       the residual stream
+ *   n  = rms(x') (pre + offset)                  the norm before the next block
+ *   rms(z) = z / sqrt(mean_i z_i^2 + eps)
+ * n is formed from the unrounded x'. y == NULL: no block (x' = res_scale x).
+ *   x, y          [T][d]; y may be NULL
+ *   post, pre     [d]; NULL means no post norm / every weight pre + offset is 1
+ *   gate          [d] with gate_ld 0, or [T] rows gate_ld apart; NULL means 1
+ *   x_out, n_out  [T][d]; either may be NULL, not both; each may be x or y
+ * d: a multiple of 8, at most 32768. offset is 1 where weights are stored as
+ * w - 1, else 0. Sums are fp32. */
+typedef struct {
+    const void *x, *y, *post, *pre, *gate;
+    void *x_out, *n_out;
+    int32_t T, d, gate_ld, dtype;
+    float eps, offset, res_scale, branch_scale;
+} wl_norm_args;
+wl_status wl_norm_residual(const wl_norm_args *a, void *hip_stream);
+
+/* Rotary positions. The first `rot` elements of a head are rot/2 pairs: (e,
+ * e + rot/2) in the half style, (2e, 2e+1) in the interleaved one. Pair e of a
+ * token at position p becomes
+ *   (a, b) -> scale (a cos t - b sin t, a sin t + b cos t),  t = p freq[e]
+ * the rest of the head is kept. t is formed and reduced to one turn in fp64, so
+ * far positions cost no accuracy; the turn itself is fp32.
+ *   freq   device fp64 [rot/2], radians per position, 8-byte aligned
+ *   pos    device int32 [T] (negative ones allowed)
+ *   rot    a multiple of 8, 8 <= rot <= d */
+enum { WL_ROPE_HALF = 0, WL_ROPE_INTERLEAVED = 1 };
+typedef struct {
+    const double *freq;
+    const int32_t *pos;
+    int32_t rot, style;
+    float scale;
+} wl_rotary;
+
+/* Frequencies of wl_rotary for `rot` rotated elements, on the host:
+ *   WL_ROPE_PLAIN   f_e = base^(-2e/rot)
+ *   WL_ROPE_LINEAR  f_e / factor (positions interpolated)
+ *   WL_ROPE_BASE    base replaced by base factor^(rot/(rot-2)): the slowest pair
+ *                   turns `factor` times slower, the fastest as before
+ *   WL_ROPE_PARTS   by parts: with n_e = original f_e / (2 pi) turns over the
+ *                   original context and g = clamp((n_e - slow)/(fast - slow), 0, 1),
+ *                   f_e (g + (1 - g)/factor); *scale = 0.1 ln(factor) + 1
+ *                   (*scale is 1 in the others)
+ * freq: host fp64 [rot/2], written. base > 1, factor >= 1, original > 0,
+ * fast > slow (the last three in WL_ROPE_PARTS only); rot as in wl_rotary, and
+ * above 2 pairs in WL_ROPE_BASE. */
+enum { WL_ROPE_PLAIN = 0, WL_ROPE_LINEAR = 1, WL_ROPE_BASE = 2, WL_ROPE_PARTS = 3 };
+wl_status wl_rope_frequencies(int32_t rot, double base, int32_t scaling, double factor, double original,
+                              double slow, double fast, double *freq, float *scale);
+
+/* Q and K rotated (and normalised per head first, where weights are given):
+ *   head -> rotary( q_weight ? rms(head) (q_weight + offset) : head )
+ *   q, q_out  [T] rows of n_q heads of d; q_out may be q
+ *   k, k_out  [T] rows of n_k heads of d; k_out may be k
+ *   q_weight, k_weight  [d] or NULL
+ *   rotary    NULL: no rotation (per-head norm only)
+ * n_q >= 0, n_k >= 0, not both 0 (pointers of an empty side are ignored);
+ * d: a multiple of 8, at most 256. */
+typedef struct {
+    const void *q, *k, *q_weight, *k_weight;
+    void *q_out, *k_out;
+    const wl_rotary *rotary;
+    int32_t T, n_q, n_k, d, ldq, ldk, ldq_out, ldk_out, dtype;
+    float eps, offset;
+} wl_rope_args;
+wl_status wl_rope(const wl_rope_args *a, void *hip_stream);
+
+/* A paged cache of keys and values.
+ *   k, v     [n_pages][n_kv][page][d] of the format's type, 16-byte aligned
+ *   k_scale, v_scale  fp32 [n_pages][n_kv][page], 16-byte aligned, in the
+ *            quantised formats (ignored in the others)
+ *   table    device int32 [n_seq][max_pages]: the page that holds slots
+ *            [i page, (i+1) page) of a sequence. A page number outside
+ *            [0, n_pages) is no page: nothing is written to or read from it.
+ * Formats: WL_CACHE_BF16, WL_CACHE_F32, and one byte per element with one scale
+ * per token and head, most = the row's largest magnitude:
+ *   WL_CACHE_INT8  scale = most / 127, code = round(127 x / most)
+ *   WL_CACHE_E4M3  scale = most / 448, code = e4m3(448 x / most)  (OCP, finite)
+ * to nearest even; a row of zeros has scale 0, and a row with an infinity or a
+ * NaN reads back as NaN. dtype bf16 goes with bf16, int8 and e4m3 caches, dtype
+ * f32 with f32, int8 and e4m3 ones (else WL_ERR_UNSUPPORTED).
+ * page: a power of two from 16 to 1024; d: a multiple of 16, at most 256. The
+ * pools may hold more than 2^31 elements. */
+enum { WL_CACHE_BF16 = 0, WL_CACHE_F32 = 1, WL_CACHE_INT8 = 2, WL_CACHE_E4M3 = 3 };
+typedef struct {
+    void *k, *v;
+    float *k_scale, *v_scale;
+    const int32_t *table;
+    int32_t n_pages, page, n_kv, d, n_seq, max_pages, format;
+} wl_cache;
+
+/* Writes tokens into the cache, with wl_rope's norm and rotation of K, and of Q
+ * beside it, in the same launch. K is stored as rounded once from the fp32
+ * rotated value, V as it is.
+ *   k, v   [T] rows of cache->n_kv heads of cache->d
+ *   seq    device int32 [T]: the sequence of each token. A token whose seq is
+ *          outside [0, n_seq) is skipped: nothing of it is written, q_out neither.
+ *   slot   device int32 [T]: its place in the sequence. A slot outside
+ *          [0, max_pages page) or without a page: K and V are not written.
+ *   q, q_out  [T] rows of n_q heads, q_out may be q; n_q == 0: no Q
+ *   rotary    NULL: no rotation. Its pos may be NULL: the slots are the positions
+ *   q_weight, k_weight, eps, offset  as in wl_rope
+ * Two tokens of one call with the same seq and slot: either may be stored, whole
+ * elements of both may be mixed. */
+typedef struct {
+    const wl_cache *cache;
+    const void *k, *v, *q, *q_weight, *k_weight;
+    void *q_out;
+    const int32_t *seq, *slot;
+    const wl_rotary *rotary;
+    int32_t T, n_q, ldk, ldv, ldq, ldq_out, dtype;
+    float eps, offset;
+} wl_cache_write_args;
+wl_status wl_cache_write(const wl_cache_write_args *a, void *hip_stream);
+
+/* Reads tokens back: k_out, v_out [T] rows of n_kv heads of d, as dtype. A token
+ * whose seq, slot or page is invalid (as in wl_cache_write) leaves its rows as
+ * they were. k_out or v_out may be NULL. */
+typedef struct {
+    const wl_cache *cache;
+    const int32_t *seq, *slot;
+    void *k_out, *v_out;
+    int32_t T, ldk, ldv, dtype;
+} wl_cache_read_args;
+wl_status wl_cache_read(const wl_cache_read_args *a, void *hip_stream);
+
+/* Attention of new tokens over the cache, which holds them already:
+ *   o = sum_j w_j v_j,  w = softmax_j( scale q . k_j )  over the visible keys j
+ * for every query head h, with key/value head h / (n_q / n_kv).
+ *   q, o      [T] rows of n_q heads of cache->d (o may be q)
+ *   q_start   device int32 [n_seq + 1]: rows [q_start[s], q_start[s+1]) of q are
+ *             sequence s's, rows outside every sequence are left as they were
+ *   kv_len    device int32 [n_seq]: keys of the sequence, the new tokens' last.
+ *             Query i of m has its own key in slot kv_len - m + i.
+ *   max_q, max_kv  the largest q_start[s+1] - q_start[s] and kv_len[s]: these fix
+ *             the launch. Queries beyond max_q get no result, keys beyond max_kv
+ *             (or beyond max_pages page) are not seen.
+ *   mask      WL_ATTN_CAUSAL  query i sees the slots up to its own
+ *             WL_ATTN_TREE    every slot before the new tokens, and new token j
+ *                             where bit j % 32 of tree[row][j / 32] is set
+ *             WL_ATTN_FULL    every slot below kv_len
+ *   tree      device [T][tree_words] (WL_ATTN_TREE only)
+ *   window    0, or how many positions back a query sees: of a query at position
+ *             p, slots above p - window (in WL_ATTN_TREE the mask alone decides
+ *             over new tokens; not in WL_ATTN_FULL)
+ *   q_pos     device int32 [T]: the queries' positions for the window in
+ *             WL_ATTN_TREE; NULL means their slots
+ * A query that sees no key, or whose every score is -inf, gives zeros. A key
+ * that a query does not see has no influence on it, whatever it holds; the same
+ * goes for slots from kv_len on. n_q is a multiple of n_kv.
+ * Products of bf16 tensors run on the matrix cores with fp32 sums; weights are
+ * rounded to bf16 for the second product and their sum is taken of the rounded
+ * ones (bf16 caches); dtype f32 is fp32 throughout.
+ *   ws   ws_bytes >= wl_attention_workspace_bytes(a), prepared as the other
+ *        operations' (its first WL_SYNC_BYTES are not touched, so that one
+ *        workspace serves a whole layer); NULL is accepted where that is 0 */
+enum { WL_ATTN_CAUSAL = 0, WL_ATTN_TREE = 1, WL_ATTN_FULL = 2 };
+typedef struct {
+    const wl_cache *cache;
+    const void *q;
+    void *o;
+    const int32_t *q_start, *kv_len;
+    const uint32_t *tree;
+    const int32_t *q_pos;
+    int32_t T, n_q, ldq, ldo, max_q, max_kv, mask, window, tree_words, dtype;
+    float scale;
+} wl_attention_args;
+/* 0 for invalid arguments too (the call then says which). */
+size_t wl_attention_workspace_bytes(const wl_attention_args *a);
+wl_status wl_attention(const wl_attention_args *a, void *ws, size_t ws_bytes, void *hip_stream);
+
+/* Steps of whole layers: wl_step_create for a list that mixes projection calls
+ * with the operations above, so that a decode step of a model is one graph.
+ *   op    WL_OP_LINEAR, WL_OP_QKV, WL_OP_MLP: args is a wl_call (whose op says
+ *         the same); the others: args is the operation's argument struct
+ * Launched and destroyed as any step; positions, slots, lengths, page tables are
+ * read at each launch, max_q and max_kv are fixed here (give the largest that
+ * the step will meet). Every operation is checked as by its own entry point. */
+enum { WL_OP_NORM = 3, WL_OP_ROPE = 4, WL_OP_CACHE_WRITE = 5, WL_OP_CACHE_READ = 6, WL_OP_ATTENTION = 7 };
+typedef struct {
+    int32_t op;
+    const void *args;
+} wl_step_op;
+size_t wl_step_ops_workspace_bytes(const wl_step_op *ops, int32_t n_ops);
+wl_status wl_step_create_ops(const wl_step_op *ops, int32_t n_ops, void *ws, size_t ws_bytes, wl_step *step);
+
 /* Size of a set of theta bundles against the dense weights they replace
  * ("What weightless inference costs", "Compression": the ratio of the theta
  * bundle, W0 + s + U + V across every layer and family, to the original

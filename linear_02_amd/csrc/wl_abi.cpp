@@ -15,23 +15,20 @@
 #include <string>
 #include <vector>
 
+#include "wl_abi.h"
 #include "wl_kernels.h"
 
 namespace {
-
 thread_local std::string g_error;
-std::atomic<int> g_spin_limit{wl::kSpinLimit};   // polls before a decode workgroup computes V^T x itself
-// 0 auto, 1 GEMV, 2 matrix-core GEMM, 3 GEMV always after a V^T x launch, 4 skinny,
-// 5 GEMV with the MLP as two launches (gate/up, then down)
-std::atomic<int> g_regime{0};
+}
+
+namespace wl {
 
 // WL_LOG is read once per process.
 bool log_on() {
     static const bool on = getenv("WL_LOG") != nullptr;
     return on;
 }
-
-constexpr size_t kAlign = 256;
 
 wl_status fail(wl_status st, const char *fmt, ...) {
     char buf[512];
@@ -49,20 +46,21 @@ wl_status ok() {
     return WL_OK;
 }
 
-size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
+const char *last_message() { return g_error.c_str(); }
 
-bool aligned(const void *p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+}  // namespace wl
 
-struct Range {
-    const void *p;
-    size_t bytes;
-};
+using namespace wl::abi;
+using wl::fail;
+using wl::log_on;
+using wl::ok;
 
-bool overlaps(Range a, Range b) {
-    if (!a.p || !b.p || a.bytes == 0 || b.bytes == 0) return false;
-    const uintptr_t a0 = (uintptr_t)a.p, b0 = (uintptr_t)b.p;
-    return a0 < b0 + b.bytes && b0 < a0 + a.bytes;
-}
+namespace {
+
+std::atomic<int> g_spin_limit{wl::kSpinLimit};   // polls before a decode workgroup computes V^T x itself
+// 0 auto, 1 GEMV, 2 matrix-core GEMM, 3 GEMV always after a V^T x launch, 4 skinny,
+// 5 GEMV with the MLP as two launches (gate/up, then down)
+std::atomic<int> g_regime{0};
 
 const int64_t kMaxElems = (int64_t)1 << 31;
 
@@ -964,6 +962,54 @@ wl_status check_calls(const wl_call *calls, int32_t n_calls) {
     return WL_OK;
 }
 
+wl_status run_op(const wl_step_op &o, void *ws, size_t ws_bytes, hipStream_t s) {
+    switch (o.op) {
+        case WL_OP_NORM: return wl_norm_residual(static_cast<const wl_norm_args *>(o.args), s);
+        case WL_OP_ROPE: return wl_rope(static_cast<const wl_rope_args *>(o.args), s);
+        case WL_OP_CACHE_WRITE: return wl_cache_write(static_cast<const wl_cache_write_args *>(o.args), s);
+        case WL_OP_CACHE_READ: return wl_cache_read(static_cast<const wl_cache_read_args *>(o.args), s);
+        case WL_OP_ATTENTION: return wl_attention(static_cast<const wl_attention_args *>(o.args), ws, ws_bytes, s);
+        default: return run_call(*static_cast<const wl_call *>(o.args), ws, ws_bytes, s);
+    }
+}
+
+// Captures run(0, stream), .., run(n - 1, stream) into a graph and instantiates
+// it; name(k) is the caller's number of the k-th call, for messages.
+template <class Run, class Name>
+wl_status record(int n, Run run, Name name, wl_step *step) {
+    hipStream_t cs = nullptr;
+    hipError_t e = hipStreamCreateWithFlags(&cs, hipStreamNonBlocking);
+    if (e != hipSuccess) return fail(WL_ERR_HIP, "capture stream: %s", hipGetErrorString(e));
+    e = hipStreamBeginCapture(cs, hipStreamCaptureModeThreadLocal);
+    if (e != hipSuccess) {
+        (void)hipStreamDestroy(cs);
+        return fail(WL_ERR_HIP, "begin capture: %s", hipGetErrorString(e));
+    }
+    for (int k = 0; k < n; ++k) {
+        const wl_status st = run(k, cs);
+        if (st != WL_OK) {
+            const std::string msg = "call " + std::to_string(name(k)) + ": " + g_error;
+            hipGraph_t g = nullptr;
+            (void)hipStreamEndCapture(cs, &g);
+            if (g) (void)hipGraphDestroy(g);
+            (void)hipStreamDestroy(cs);
+            return fail(st, "%s", msg.c_str());
+        }
+    }
+    hipGraph_t graph = nullptr;
+    e = hipStreamEndCapture(cs, &graph);
+    (void)hipStreamDestroy(cs);
+    if (e != hipSuccess || !graph) return fail(WL_ERR_HIP, "end capture: %s", hipGetErrorString(e));
+    hipGraphExec_t exec = nullptr;
+    e = hipGraphInstantiate(&exec, graph, nullptr, nullptr, 0);
+    if (e != hipSuccess) {
+        (void)hipGraphDestroy(graph);
+        return fail(WL_ERR_HIP, "graph instantiation: %s", hipGetErrorString(e));
+    }
+    *step = new wl_step_s{graph, exec};
+    return ok();
+}
+
 }  // namespace
 
 size_t wl_step_workspace_bytes(const wl_call *calls, int32_t n_calls) {
@@ -1022,37 +1068,52 @@ wl_status wl_step_create(const wl_call *calls, int32_t n_calls, int32_t flags, v
         order = grouped;
     }
 
-    hipStream_t cs = nullptr;
-    hipError_t e = hipStreamCreateWithFlags(&cs, hipStreamNonBlocking);
-    if (e != hipSuccess) return fail(WL_ERR_HIP, "capture stream: %s", hipGetErrorString(e));
-    e = hipStreamBeginCapture(cs, hipStreamCaptureModeThreadLocal);
-    if (e != hipSuccess) {
-        (void)hipStreamDestroy(cs);
-        return fail(WL_ERR_HIP, "begin capture: %s", hipGetErrorString(e));
+    return record(n_calls, [&](int k, hipStream_t cs) { return run_call(calls[order[k]], ws, ws_bytes, cs); },
+                  [&](int k) { return order[k]; }, step);
+}
+
+size_t wl_step_ops_workspace_bytes(const wl_step_op *ops, int32_t n_ops) {
+    if (!ops || n_ops <= 0 || n_ops > kMaxStepCalls) return 0;
+    // A step without projections or split attention still needs a workspace pointer.
+    size_t most = WL_SYNC_BYTES;
+    for (int i = 0; i < n_ops; ++i) {
+        if (!ops[i].args || ops[i].op < WL_OP_LINEAR || ops[i].op > WL_OP_ATTENTION) return 0;
+        size_t b = 0;
+        if (ops[i].op <= WL_OP_MLP) {
+            const wl_call *c = static_cast<const wl_call *>(ops[i].args);
+            if (c->op != ops[i].op || (b = wl_step_workspace_bytes(c, 1)) == 0) return 0;
+        } else if (ops[i].op == WL_OP_ATTENTION) {
+            b = wl_attention_workspace_bytes(static_cast<const wl_attention_args *>(ops[i].args));
+        }
+        most = b > most ? b : most;
     }
-    for (int k : order) {
-        st = run_call(calls[k], ws, ws_bytes, cs);
-        if (st != WL_OK) {
-            const std::string msg = "call " + std::to_string(k) + ": " + g_error;
-            hipGraph_t g = nullptr;
-            (void)hipStreamEndCapture(cs, &g);
-            if (g) (void)hipGraphDestroy(g);
-            (void)hipStreamDestroy(cs);
-            return fail(st, "%s", msg.c_str());
+    return most;
+}
+
+wl_status wl_step_create_ops(const wl_step_op *ops, int32_t n_ops, void *ws, size_t ws_bytes, wl_step *step) {
+    if (!step) return fail(WL_ERR_INVALID_ARG, "step is NULL");
+    *step = nullptr;
+    if (!ops) return fail(WL_ERR_INVALID_ARG, "ops is NULL");
+    if (n_ops <= 0 || n_ops > kMaxStepCalls)
+        return fail(WL_ERR_INVALID_ARG, "n_ops=%d is outside [1, %d]", n_ops, kMaxStepCalls);
+    for (int i = 0; i < n_ops; ++i) {
+        if (!ops[i].args) return fail(WL_ERR_INVALID_ARG, "op %d: args is NULL", i);
+        if (ops[i].op < WL_OP_LINEAR || ops[i].op > WL_OP_ATTENTION)
+            return fail(WL_ERR_INVALID_ARG, "op %d: op=%d is unknown", i, ops[i].op);
+        if (ops[i].op <= WL_OP_MLP) {
+            const wl_call *c = static_cast<const wl_call *>(ops[i].args);
+            if (c->op != ops[i].op) return fail(WL_ERR_INVALID_ARG, "op %d: op=%d, its call says %d", i, ops[i].op, c->op);
+            const wl_status st = check_calls(c, 1);
+            if (st != WL_OK) {
+                const std::string msg = "op " + std::to_string(i) + ": " + g_error;
+                return fail(st, "%s", msg.c_str());
+            }
         }
     }
-    hipGraph_t graph = nullptr;
-    e = hipStreamEndCapture(cs, &graph);
-    (void)hipStreamDestroy(cs);
-    if (e != hipSuccess || !graph) return fail(WL_ERR_HIP, "end capture: %s", hipGetErrorString(e));
-    hipGraphExec_t exec = nullptr;
-    e = hipGraphInstantiate(&exec, graph, nullptr, nullptr, 0);
-    if (e != hipSuccess) {
-        (void)hipGraphDestroy(graph);
-        return fail(WL_ERR_HIP, "graph instantiation: %s", hipGetErrorString(e));
-    }
-    *step = new wl_step_s{graph, exec};
-    return ok();
+    wl_status st = check_ws(wl_step_ops_workspace_bytes(ops, n_ops), ws, ws_bytes);
+    if (st != WL_OK) return st;
+    return record(n_ops, [&](int k, hipStream_t cs) { return run_op(ops[k], ws, ws_bytes, cs); },
+                  [](int k) { return k; }, step);
 }
 
 wl_status wl_step_launch(wl_step step, void *hip_stream) {

@@ -57,6 +57,36 @@ class Call(ctypes.Structure):
 
 STEP_GROUP_SHARED_W0 = 1
 
+# The operations between the projections: norms, rotary positions, cache, attention.
+OP_NORM, OP_ROPE, OP_CACHE_WRITE, OP_CACHE_READ, OP_ATTENTION = 3, 4, 5, 6, 7
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+ROPE_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "parts": 3}
+MASKS = {"causal": 0, "tree": 1, "full": 2}
+CACHE_FORMATS = {torch.bfloat16: 0, torch.float32: 1, torch.int8: 2, torch.float8_e4m3fn: 3}
+
+
+def _struct(name: str, pointers: str, ints: str, floats: str = "") -> type:
+    """A ctypes struct of pointers, then int32 fields, then fp32 ones."""
+    fields = [(f, t) for names, t in ((pointers, ctypes.c_void_p), (ints, ctypes.c_int32), (floats, ctypes.c_float))
+              for f in names.split()]
+    return type(name, (ctypes.Structure,), {"_fields_": fields})
+
+
+NormArgs = _struct("NormArgs", "x y post pre gate x_out n_out", "T d gate_ld dtype", "eps offset res_scale branch_scale")
+Rotary = _struct("Rotary", "freq pos", "rot style", "scale")
+RopeArgs = _struct("RopeArgs", "q k q_weight k_weight q_out k_out rotary",
+                   "T n_q n_k d ldq ldk ldq_out ldk_out dtype", "eps offset")
+CacheStruct = _struct("CacheStruct", "k v k_scale v_scale table", "n_pages page n_kv d n_seq max_pages format")
+CacheWriteArgs = _struct("CacheWriteArgs", "cache k v q q_weight k_weight q_out seq slot rotary",
+                         "T n_q ldk ldv ldq ldq_out dtype", "eps offset")
+CacheReadArgs = _struct("CacheReadArgs", "cache seq slot k_out v_out", "T ldk ldv dtype")
+AttentionArgs = _struct("AttentionArgs", "cache q o q_start kv_len tree q_pos",
+                        "T n_q ldq ldo max_q max_kv mask window tree_words dtype", "scale")
+
+
+class StepOp(ctypes.Structure):
+    _fields_ = [("op", ctypes.c_int32), ("args", ctypes.c_void_p)]
+
 
 def _load(path: str = LIBRARY) -> ctypes.CDLL:
     if not os.path.exists(path):
@@ -99,6 +129,21 @@ def _load(path: str = LIBRARY) -> ctypes.CDLL:
     lib.wl_step_launch.restype = ctypes.c_int
     lib.wl_step_destroy.argtypes = [vp]
     lib.wl_step_destroy.restype = ctypes.c_int
+    for name, args in (("wl_norm_residual", NormArgs), ("wl_rope", RopeArgs), ("wl_cache_write", CacheWriteArgs),
+                       ("wl_cache_read", CacheReadArgs)):
+        getattr(lib, name).argtypes = [ctypes.POINTER(args), vp]
+        getattr(lib, name).restype = ctypes.c_int
+    lib.wl_rope_frequencies.argtypes = [i32, ctypes.c_double, i32] + [ctypes.c_double] * 4 + \
+        [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_float)]
+    lib.wl_rope_frequencies.restype = ctypes.c_int
+    lib.wl_attention_workspace_bytes.argtypes = [ctypes.POINTER(AttentionArgs)]
+    lib.wl_attention_workspace_bytes.restype = sz
+    lib.wl_attention.argtypes = [ctypes.POINTER(AttentionArgs), vp, sz, vp]
+    lib.wl_attention.restype = ctypes.c_int
+    lib.wl_step_ops_workspace_bytes.argtypes = [ctypes.POINTER(StepOp), i32]
+    lib.wl_step_ops_workspace_bytes.restype = sz
+    lib.wl_step_create_ops.argtypes = [ctypes.POINTER(StepOp), i32, vp, sz, ctypes.POINTER(vp)]
+    lib.wl_step_create_ops.restype = ctypes.c_int
     lib.wl_workspace_init.argtypes = [vp, sz, vp]
     lib.wl_workspace_init.restype = ctypes.c_int
     lib.wl_sync_bytes.argtypes = []
@@ -392,3 +437,322 @@ class Step:
             self.close()
         except Exception:
             pass
+
+
+# ---- the operations between the projections ------------------------------------
+#
+# Each has a ``..._call`` that checks its tensors, allocates the outputs that are
+# not given and returns an OpCall, and a function that makes the call and
+# launches it on the current stream. An OpCall can be launched again (new values
+# in the same tensors) or recorded with others in a LayerStep.
+
+
+class OpCall:
+    """A checked call of one operation: ``out`` are its outputs, ``launch`` runs it
+    on the current stream of its device. Keeps its tensors alive."""
+
+    __slots__ = ("op", "args", "out", "device", "fn", "ws", "keep")
+
+    def __init__(self, op, fn, args, out, device, keep, ws=None):
+        self.op, self.fn, self.args, self.out, self.device, self.keep, self.ws = op, fn, args, out, device, keep, ws
+
+    def launch(self):
+        if self.device.index != torch.cuda.current_device():
+            with torch.cuda.device(self.device):
+                return self._launch()
+        return self._launch()
+
+    def _launch(self):
+        if self.op != OP_ATTENTION:
+            _check(self.fn(self.args, _stream(self.device)))
+            return self.out
+        need = int(lib.wl_attention_workspace_bytes(self.args))
+        ws = self.ws if self.ws is not None else WORKSPACE.get(self.device, need)
+        _check(self.fn(self.args, _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _stream(self.device)))
+        return self.out
+
+
+def _tensor(t, name: str, like: torch.Tensor, dtype=None) -> None:
+    if t.device != like.device or not t.is_cuda:
+        raise ValueError(f"{name} must be on the device of the call's first tensor ({like.device})")
+    if t.dtype != (dtype or like.dtype):
+        raise ValueError(f"{name} must be {dtype or like.dtype}")
+
+
+def _matrix(t, name: str, like: torch.Tensor, T: int, width: int) -> int:
+    """Row stride of a [T][width] tensor whose rows are contiguous."""
+    _tensor(t, name, like)
+    if t.dim() != 2 or t.shape[0] != T or t.shape[1] != width or (width > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be [{T}][{width}] with contiguous rows")
+    return t.stride(0) if T > 1 else width
+
+
+def _vector(t, name: str, like: torch.Tensor, n: int, dtype=None):
+    if t is None:
+        return None
+    _tensor(t, name, like, dtype)
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with {n} elements")
+    return t.data_ptr()
+
+
+def _first(t, name: str) -> torch.Tensor:
+    if t.dtype not in _CODES or not t.is_cuda or t.dim() != 2:
+        raise ValueError(f"{name} must be a bf16 or fp32 device matrix")
+    return t
+
+
+def norm_call(x, y=None, post=None, pre=None, gate=None, eps: float = 1e-6, offset: float = 0.0,
+              res_scale: float = 1.0, branch_scale: float = 1.0, x_out=None, n_out=None, want_x: bool = True,
+              want_n: bool = True) -> OpCall:
+    """wl_norm_residual as an OpCall; out = (x_out, n_out). want_x / want_n False
+    leave that output out (None)."""
+    T, d = _first(x, "x").shape
+    for name, t in (("x", x), ("y", y), ("x_out", x_out), ("n_out", n_out)):
+        if t is not None and (_matrix(t, name, x, T, d) != d or not t.is_contiguous()):
+            raise ValueError(f"{name} must be contiguous")
+    gate_ld = 0
+    if gate is not None:
+        if gate.dim() == 1:
+            _vector(gate, "gate", x, d)
+        else:
+            gate_ld = _matrix(gate, "gate", x, T, d)
+    if want_x and x_out is None:
+        x_out = torch.empty_like(x)
+    if want_n and n_out is None:
+        n_out = torch.empty_like(x)
+    args = NormArgs(x.data_ptr(), _ptr(y), _vector(post, "post", x, d), _vector(pre, "pre", x, d), _ptr(gate),
+                    _ptr(x_out), _ptr(n_out), T, d, gate_ld, _CODES[x.dtype], eps, offset, res_scale, branch_scale)
+    return OpCall(OP_NORM, lib.wl_norm_residual, args, (x_out, n_out), x.device, (x, y, post, pre, gate))
+
+
+def wl_norm_residual(x, **kw):
+    """(x', n): p = rms(y) (post + offset), x' = res_scale x + branch_scale gate p,
+    n = rms(x') (pre + offset); see norm_call for the arguments."""
+    return norm_call(x, **kw).launch()
+
+
+def rope_frequencies(rot: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0,
+                     original: float = 4096.0, slow: float = 1.0, fast: float = 32.0, device="cuda"):
+    """(freq, scale) of Rope for ``rot`` rotated elements (wl_rope_frequencies):
+    scaling "plain", "linear", "base" or "parts"."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling {scaling!r} is not one of {sorted(ROPE_SCALINGS)}")
+    buf, scale = (ctypes.c_double * max(int(rot) // 2, 1))(), ctypes.c_float()
+    _check(lib.wl_rope_frequencies(int(rot), base, ROPE_SCALINGS[scaling], factor, original, slow, fast, buf,
+                                   ctypes.byref(scale)))
+    return torch.tensor(list(buf), dtype=torch.float64, device=device), float(scale.value)
+
+
+class Rope:
+    """How heads are rotated: fp64 radians per position of every pair, the pairs'
+    style, a factor on cos and sin."""
+
+    __slots__ = ("freq", "interleaved", "scale")
+
+    def __init__(self, freq: torch.Tensor, interleaved: bool = False, scale: float = 1.0):
+        self.freq, self.interleaved, self.scale = freq, interleaved, scale
+
+    def struct(self, pos, T: int, like: torch.Tensor):
+        f = _vector(self.freq, "freq", like, self.freq.numel(), torch.float64)
+        return Rotary(f, _vector(pos, "pos", like, T, torch.int32), 2 * self.freq.numel(),
+                      ROPE_INTERLEAVED if self.interleaved else ROPE_HALF, self.scale)
+
+
+def _at(struct) -> int | None:
+    return None if struct is None else ctypes.addressof(struct)
+
+
+def _heads(t, name: str, d: int) -> int:
+    if d < 1 or t.dim() != 2 or t.shape[1] % d:
+        raise ValueError(f"{name} must be a matrix of whole heads of {d}")
+    return t.shape[1] // d
+
+
+def rope_call(q, k, pos, rope: Rope | None, d: int, q_norm=None, k_norm=None, eps: float = 1e-6,
+              offset: float = 0.0, q_out=None, k_out=None) -> OpCall:
+    """wl_rope as an OpCall; out = (q_out, k_out). q or k may be None; both may be
+    column ranges of one wider matrix (Q/K/V side by side), and their own outputs."""
+    first = _first(q if q is not None else k, "q" if q is not None else "k")
+    T = first.shape[0]
+    n, ld, ldo, outs = [0, 0], [0, 0], [0, 0], [q_out, k_out]
+    for i, (t, name) in enumerate(((q, "q"), (k, "k"))):
+        if t is None:
+            continue
+        n[i] = _heads(t, name, d)
+        ld[i] = _matrix(t, name, first, T, n[i] * d)
+        if outs[i] is None:
+            outs[i] = torch.empty(T, n[i] * d, dtype=t.dtype, device=t.device)
+        ldo[i] = _matrix(outs[i], name + "_out", first, T, n[i] * d)
+    rot = None if rope is None else rope.struct(pos, T, first)
+    args = RopeArgs(_ptr(q), _ptr(k), _vector(q_norm, "q_norm", first, d), _vector(k_norm, "k_norm", first, d),
+                    _ptr(outs[0]), _ptr(outs[1]), _at(rot), T, n[0], n[1], d, ld[0], ld[1], ldo[0], ldo[1],
+                    _CODES[first.dtype], eps, offset)
+    return OpCall(OP_ROPE, lib.wl_rope, args, tuple(outs), first.device, (q, k, pos, rope, rot, q_norm, k_norm))
+
+
+def wl_rope(q, k, pos, rope, d, **kw):
+    """(q, k) rotated by their positions, each head normalised first where q_norm /
+    k_norm are given; see rope_call."""
+    return rope_call(q, k, pos, rope, d, **kw).launch()
+
+
+class Cache:
+    """A paged cache of keys and values: k, v [n_pages][n_kv][page][d] (bf16, fp32,
+    int8 or float8_e4m3fn), table int32 [n_seq][max_pages] of page numbers, and
+    fp32 [n_pages][n_kv][page] scales for the one-byte types."""
+
+    __slots__ = ("k", "v", "table", "k_scale", "v_scale", "struct")
+
+    def __init__(self, k, v, table, k_scale=None, v_scale=None):
+        if k.dtype not in CACHE_FORMATS or k.dim() != 4 or not k.is_contiguous() or not k.is_cuda:
+            raise ValueError("k must be a contiguous [n_pages][n_kv][page][d] device tensor of a cache type")
+        _tensor(v, "v", k)
+        if v.shape != k.shape or not v.is_contiguous():
+            raise ValueError("v must be contiguous and shaped as k")
+        _tensor(table, "table", k, torch.int32)
+        if table.dim() != 2 or not table.is_contiguous():
+            raise ValueError("table must be a contiguous [n_seq][max_pages] tensor")
+        n_pages, n_kv, page, d = k.shape
+        scales = [None, None]
+        if k.dtype.itemsize == 1:
+            for i, (t, name) in enumerate(((k_scale, "k_scale"), (v_scale, "v_scale"))):
+                if t is None or t.shape != k.shape[:3]:
+                    raise ValueError(f"{name} must be [n_pages][n_kv][page]")
+                scales[i] = _vector(t, name, k, t.numel(), torch.float32)
+        self.k, self.v, self.table, self.k_scale, self.v_scale = k, v, table, k_scale, v_scale
+        self.struct = CacheStruct(k.data_ptr(), v.data_ptr(), scales[0], scales[1], table.data_ptr(), n_pages, page,
+                                  n_kv, d, table.shape[0], table.shape[1], CACHE_FORMATS[k.dtype])
+
+
+def new_cache(n_pages: int, n_kv: int, page: int, d: int, table: torch.Tensor, dtype=torch.bfloat16) -> Cache:
+    """A Cache of uninitialised pages on the table's device."""
+    shape = (n_pages, n_kv, page, d)
+    k, v = (torch.empty(shape, dtype=dtype, device=table.device) for _ in range(2))
+    scales = [torch.empty(shape[:3], dtype=torch.float32, device=table.device) if dtype.itemsize == 1 else None
+              for _ in range(2)]
+    return Cache(k, v, table, *scales)
+
+
+def cache_write_call(cache: Cache, k, v, seq, slot, q=None, rope: Rope | None = None, pos=None, q_norm=None,
+                     k_norm=None, eps: float = 1e-6, offset: float = 0.0, q_out=None) -> OpCall:
+    """wl_cache_write as an OpCall; out = q_out (None without q). pos None: the slots
+    are the positions."""
+    c = cache.struct
+    T = _first(k, "k").shape[0]
+    width = c.n_kv * c.d
+    _tensor(cache.k, "the cache", k, cache.k.dtype)
+    n_q = ldq = ldo = 0
+    if q is not None:
+        n_q = _heads(q, "q", c.d)
+        ldq = _matrix(q, "q", k, T, n_q * c.d)
+        if q_out is None:
+            q_out = torch.empty(T, n_q * c.d, dtype=q.dtype, device=q.device)
+        ldo = _matrix(q_out, "q_out", k, T, n_q * c.d)
+    rot = None if rope is None else rope.struct(pos, T, k)
+    args = CacheWriteArgs(_at(c), k.data_ptr(), v.data_ptr(), _ptr(q), _vector(q_norm, "q_norm", k, c.d),
+                          _vector(k_norm, "k_norm", k, c.d), _ptr(q_out), _vector(seq, "seq", k, T, torch.int32),
+                          _vector(slot, "slot", k, T, torch.int32), _at(rot), T, n_q, _matrix(k, "k", k, T, width),
+                          _matrix(v, "v", k, T, width), ldq, ldo, _CODES[k.dtype], eps, offset)
+    return OpCall(OP_CACHE_WRITE, lib.wl_cache_write, args, q_out, k.device,
+                  (cache, k, v, seq, slot, q, rope, rot, pos, q_norm, k_norm))
+
+
+def wl_cache_write(cache, k, v, seq, slot, **kw):
+    """Writes the tokens' K and V into the cache, K (and q beside it) normalised and
+    rotated on the way; returns the rotated q, or None. See cache_write_call."""
+    return cache_write_call(cache, k, v, seq, slot, **kw).launch()
+
+
+def cache_read_call(cache: Cache, seq, slot, dtype: torch.dtype | None = None, k_out=None, v_out=None) -> OpCall:
+    """wl_cache_read as an OpCall; out = (k, v), [T][n_kv * d] of dtype (None: fp32
+    for an fp32 cache, else bf16). Rows of tokens without a place in the cache keep
+    what the outputs held (new ones are uninitialised)."""
+    c, T = cache.struct, seq.numel()
+    if dtype is None:
+        dtype = torch.float32 if cache.k.dtype == torch.float32 else torch.bfloat16
+    outs = [t if t is not None else torch.empty(T, c.n_kv * c.d, dtype=dtype, device=cache.k.device)
+            for t in (k_out, v_out)]
+    first = _first(outs[0], "k_out")
+    _tensor(first, "k_out", cache.k, dtype)
+    args = CacheReadArgs(_at(c), _vector(seq, "seq", first, T, torch.int32), _vector(slot, "slot", first, T, torch.int32),
+                         outs[0].data_ptr(), outs[1].data_ptr(), T, _matrix(outs[0], "k_out", first, T, c.n_kv * c.d),
+                         _matrix(outs[1], "v_out", first, T, c.n_kv * c.d), _CODES[dtype])
+    return OpCall(OP_CACHE_READ, lib.wl_cache_read, args, tuple(outs), first.device, (cache, seq, slot))
+
+
+def wl_cache_read(cache, seq, slot, **kw):
+    """(k, v) of the tokens at (seq, slot), read back from the cache."""
+    return cache_read_call(cache, seq, slot, **kw).launch()
+
+
+def attention_call(q, cache: Cache, q_start, kv_len, max_q: int, max_kv: int, scale: float, mask: str | None = None,
+                   window: int = 0, tree=None, q_pos=None, o=None, ws: torch.Tensor | None = None) -> OpCall:
+    """wl_attention as an OpCall; out = o. mask: "causal" (the default), "full", or
+    "tree" (the default where ``tree``, int32 [T][words], is given)."""
+    c = cache.struct
+    T = _first(q, "q").shape[0]
+    n_q = _heads(q, "q", c.d)
+    _tensor(cache.k, "the cache", q, cache.k.dtype)
+    if o is None:
+        o = torch.empty(T, n_q * c.d, dtype=q.dtype, device=q.device)
+    mask = mask or ("causal" if tree is None else "tree")
+    if mask not in MASKS:
+        raise ValueError(f"mask {mask!r} is not one of {sorted(MASKS)}")
+    if (tree is None) == (mask == "tree"):
+        raise ValueError("tree goes with mask='tree'")
+    words = 0
+    if tree is not None:
+        if tree.dim() != 2 or tree.shape[0] != T:
+            raise ValueError(f"tree must be [{T}][words]")
+        words = tree.shape[1]
+    elif q_pos is not None:
+        raise ValueError("q_pos goes with mask='tree'")
+    n_seq = c.n_seq
+    args = AttentionArgs(_at(c), q.data_ptr(), o.data_ptr(), _vector(q_start, "q_start", q, n_seq + 1, torch.int32),
+                         _vector(kv_len, "kv_len", q, n_seq, torch.int32),
+                         _vector(tree, "tree", q, T * words, torch.int32), _vector(q_pos, "q_pos", q, T, torch.int32),
+                         T, n_q, _matrix(q, "q", q, T, n_q * c.d), _matrix(o, "o", q, T, n_q * c.d), max_q, max_kv,
+                         MASKS[mask], window, words, _CODES[q.dtype], scale)
+    return OpCall(OP_ATTENTION, lib.wl_attention, args, o, q.device, (q, cache, q_start, kv_len, tree, q_pos), ws)
+
+
+def wl_attention(q, cache, q_start, kv_len, max_q, max_kv, scale, **kw):
+    """softmax(scale q k) v of the tokens over the cache; see attention_call."""
+    return attention_call(q, cache, q_start, kv_len, max_q, max_kv, scale, **kw).launch()
+
+
+class LayerStep(Step):
+    """A step of whole layers: projection calls as in Step, (op, thetas, x, y), mixed
+    with OpCalls, recorded into one HIP graph (wl_step_create_ops) and launched
+    with one call. Values in the calls' tensors are read at each launch."""
+
+    def __init__(self, calls, ws: torch.Tensor | None = None):
+        n = len(calls)
+        ops = (StepOp * n)()
+        self._keep = [calls]
+        device = None
+        for i, call in enumerate(calls):
+            if isinstance(call, OpCall):
+                ops[i].op, ops[i].args = call.op, ctypes.addressof(call.args)
+                device = call.device
+                continue
+            op, thetas, x, y = call
+            if len(thetas) != (1 if op == OP_LINEAR else 3):
+                raise ValueError(f"call {i}: {len(thetas)} thetas for op {op}")
+            c = Call()
+            structs = [make_theta(t) for t in thetas]
+            c.op, c.x, c.y, c.T = op, _ptr(x), _ptr(y), _io(x, int(thetas[0]["d_in"]), thetas[0]["W0"].dtype)
+            for j, st in enumerate(structs):
+                c.th[j] = ctypes.pointer(st)
+            self._keep += [structs, c]
+            ops[i].op, ops[i].args = op, ctypes.addressof(c)
+            device = x.device
+        need = int(lib.wl_step_ops_workspace_bytes(ops, n))
+        if need == 0:
+            raise ValueError("invalid calls for a step")
+        self.ws = ws if ws is not None else new_workspace(need, device)
+        self.device = device
+        h = ctypes.c_void_p()
+        _check(lib.wl_step_create_ops(ops, n, _ptr(self.ws), self.ws.numel() * self.ws.element_size(), ctypes.byref(h)))
+        self.handle = h
