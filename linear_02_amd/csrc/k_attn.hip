@@ -1,6 +1,6 @@
-// Attention over the paged cache:
-//   o = sum_j w_j v_j,  w = softmax_j(scale q . k_j) over the keys j a query sees.
-#include "wl_attn.h"
+// Attention over the paged cache: which kernel runs, how a long sequence's keys
+// are divided, and the join of the parts.
+#include "wl_attn_mfma.h"
 
 namespace wl {
 
@@ -32,21 +32,105 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnJob a) {
 }
 
 template <class E, int F>
-void run(const AttnJob &a, hipStream_t s) {
+void run_rows(const AttnJob &a, hipStream_t s) {
     const int64_t units = (int64_t)a.T * a.n_q;
     hipLaunchKernelGGL((attn_rows_kernel<E, F>), dim3((unsigned)((units + 3) / 4)), dim3(256), 0, s, a);
 }
 
+// Joins the parts of every row: a wave per row, lane p weighs part p.
+template <class E>
+__global__ __launch_bounds__(256) void join_kernel(AttnJob a, Split sp) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int64_t w = (int64_t)blockIdx.x * 4 + wave;
+    const int64_t unit = w / sp.rows;
+    const int r = (int)(w - unit * sp.rows), s = (int)(unit / a.c.n_kv), kvh = (int)(unit % a.c.n_kv);
+    if (s >= a.c.n_seq) return;
+    const Seq q = seq_of(a, s);
+    if (r >= q.rows * a.group) return;
+    const int64_t first = unit * sp.n_split * sp.rows + r;
+    float2 v = make_float2(kNegInf, 0.0f);
+    if (lane < sp.n_split) v = sp.ml[first + (int64_t)lane * sp.rows];
+    float m = v.x;
+#pragma unroll
+    for (int x = 1; x < 64; x <<= 1) m = fmaxf(m, __shfl_xor(m, x));
+    const float up = v.x == kNegInf && v.y == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(v.x - m);
+    const float l = wave_sum(up == 0.0f ? 0.0f : up * v.y);
+    const int at = 4 * lane;
+    f32x4 sum{0, 0, 0, 0};
+    for (int p = 0; p < sp.n_split; ++p) {
+        const float u = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(up), p));
+        if (u == 0.0f) continue;
+        if (at < a.c.d) sum += *reinterpret_cast<const f32x4 *>(sp.part + (first + (int64_t)p * sp.rows) * a.c.d + at) * u;
+    }
+    if (at >= a.c.d) return;
+    const int i = r / a.group;
+    const float o[4] = {sum.x, sum.y, sum.z, sum.w};
+    float e[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) e[k] = l == 0.0f ? 0.0f : o[k] / l;
+    put4(static_cast<E *>(a.o) + (size_t)(q.q0 + i) * a.ldo + (size_t)(kvh * a.group + r - i * a.group) * a.c.d + at, e);
+}
+
+enum Kind { kRows, kFew };
+
+struct Plan {
+    Kind kind;
+    Split sp;
+};
+
+constexpr int kWorkgroups = 512;   // wanted: two per CU
+constexpr int kMinChunk = 256;     // keys
+
+Plan plan_of(const AttnJob &a, bool f32) {
+    Plan p{};
+    p.sp.n_split = 1;
+    p.kind = f32 || (int64_t)a.max_q * a.group > kFewRows ? kRows : kFew;
+    if (p.kind == kRows) return p;
+    p.sp.rows = a.max_q * a.group;
+    // Most keys that the queries of one sequence see between them; pieces start at a multiple of 32.
+    int64_t span = a.max_kv;
+    if (a.mask == kMaskCausal && a.window && (int64_t)a.window + a.max_q < span) span = (int64_t)a.window + a.max_q;
+    span += 31;
+    const int64_t units = (int64_t)a.c.n_seq * a.c.n_kv;
+    int64_t chunk = (span * units + kWorkgroups - 1) / kWorkgroups;
+    if (chunk < kMinChunk) chunk = kMinChunk;
+    if (chunk < (span + kMaxSplit - 1) / kMaxSplit) chunk = (span + kMaxSplit - 1) / kMaxSplit;
+    chunk = (chunk + 127) / 128 * 128;
+    p.sp.chunk = (int)(chunk < (1 << 30) ? chunk : (1 << 30));
+    p.sp.n_split = (int)((span + chunk - 1) / chunk);
+    return p;
+}
+
+size_t part_floats(const AttnJob &a, const Split &sp) {
+    return (size_t)a.c.n_seq * a.c.n_kv * sp.n_split * sp.rows;
+}
+
 }  // namespace
 
-size_t attention_scratch(const AttnJob &a, int fmt, bool f32) { return 0; }
+size_t attention_scratch(const AttnJob &a, int fmt, bool f32) {
+    const Plan p = plan_of(a, f32);
+    return p.sp.n_split > 1 ? part_floats(a, p.sp) * (a.c.d + 2) * 4 : 0;
+}
 
 hipError_t launch_attention(const AttnJob &a, int fmt, bool f32, void *ws, hipStream_t s) {
+    Plan p = plan_of(a, f32);
+    if (p.kind == kFew) {
+        if (p.sp.n_split > 1) {
+            p.sp.part = static_cast<float *>(ws);
+            p.sp.ml = reinterpret_cast<float2 *>(p.sp.part + part_floats(a, p.sp) * a.c.d);
+        }
+        launch_few(a, fmt, p.sp, s);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess || p.sp.n_split == 1) return e;
+        const int64_t waves = (int64_t)a.c.n_seq * a.c.n_kv * p.sp.rows;
+        hipLaunchKernelGGL((join_kernel<uint16_t>), dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, s, a, p.sp);
+        return hipGetLastError();
+    }
     switch (fmt) {
-        case kFmtBf16: run<uint16_t, kFmtBf16>(a, s); break;
-        case kFmtF32: run<float, kFmtF32>(a, s); break;
-        case kFmtInt8: f32 ? run<float, kFmtInt8>(a, s) : run<uint16_t, kFmtInt8>(a, s); break;
-        default: f32 ? run<float, kFmtE4m3>(a, s) : run<uint16_t, kFmtE4m3>(a, s);
+        case kFmtBf16: run_rows<uint16_t, kFmtBf16>(a, s); break;
+        case kFmtF32: run_rows<float, kFmtF32>(a, s); break;
+        case kFmtInt8: f32 ? run_rows<float, kFmtInt8>(a, s) : run_rows<uint16_t, kFmtInt8>(a, s); break;
+        default: f32 ? run_rows<float, kFmtE4m3>(a, s) : run_rows<uint16_t, kFmtE4m3>(a, s);
     }
     return hipGetLastError();
 }

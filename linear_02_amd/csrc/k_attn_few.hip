@@ -1,0 +1,345 @@
+// Attention with few query rows per key/value head (single tokens, small trees):
+// at most 32 rows, a row being a new token and one of the query heads that share
+// the key/value head.
+//
+// Bound by reading the keys and values once. Every wave works alone on a stretch
+// of keys, 32 at a time, with no barrier in its loop: K comes from global memory
+// straight into the registers of the score product (a key's row is the operand
+// row, 64 contiguous bytes per four lanes), V through a patch of LDS of the wave's
+// own that the transposing reads turn. The next 32 keys' loads are issued as soon
+// as the registers are free, so 32 keys of K and V per wave are under way while
+// the present ones are worked on. The matrix cores do 16 rows for the price of
+// one, so the weights are fed as a bf16 head plus a bf16 remainder and lose
+// nothing. The four waves of a workgroup join their outputs in LDS; workgroups
+// that divide a long sequence leave partial outputs that a second launch joins.
+#include "wl_attn_mfma.h"
+
+namespace wl {
+
+namespace {
+
+constexpr int kWaves = 4;
+
+// F: cache format; DT: padded head width; NT: tiles of 16 query rows.
+template <int F, int DT, int NT>
+struct Few {
+    static constexpr bool kCodes = F == kFmtInt8 || F == kFmtE4m3;
+    static constexpr int kSteps = DT / 32;              // 32-wide steps of the score product
+    static constexpr int kLoads = kCodes ? DT / 64 : DT / 32;   // 16-byte pieces per key row and lane
+    static constexpr int kBlocks = DT / 16;             // 16-wide blocks of the output
+    static constexpr int kRow = kCodes ? DT : 2 * DT;   // bytes of a V row in LDS
+    // Two workgroups per CU where 256 registers hold the 32 keys' K and V beside the outputs.
+    static constexpr int kPerCu = DT == 256 && (NT == 2 || !kCodes) ? 1 : 2;
+    static constexpr int kPatch = 16 * DT * 4;          // LDS bytes per wave (V: 32 rows, at most this; outputs: 16 rows fp32)
+    u32x4 q[NT][kSteps];
+    f32x4 o[NT][kBlocks];
+    float m[NT], l[NT];
+};
+
+// Global addresses of 32 keys' rows for one lane, in two halves of 16 keys.
+struct KeyRows {
+    int64_t row[2];     // this lane's key (lane & 15)
+    int64_t first[2];   // the half's first key
+    uint32_t valid;     // bits of the keys that have a page
+};
+
+__device__ __forceinline__ KeyRows key_rows(const AttnJob &a, int s, int kvh, int j0, int last) {
+    KeyRows k;
+    k.valid = 0;
+    const int mask = (1 << a.c.page_shift) - 1;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+        // Past the last key the last one is read again, so no load leaves the pages.
+        const int first = __builtin_amdgcn_readfirstlane(min(j0 + 16 * b, last));
+        const int mine = min(j0 + 16 * b + (int)(threadIdx.x & 15), last);
+        int page = a.c.table[(int64_t)s * a.c.max_pages + (first >> a.c.page_shift)];
+        const bool ok = (unsigned)page < (unsigned)a.c.n_pages;
+        if (ok) k.valid |= 0xFFFFu << (16 * b);
+        const int64_t at = ((int64_t)(ok ? page : 0) * a.c.n_kv + kvh) << a.c.page_shift;
+        k.row[b] = at + (mine & mask);
+        k.first[b] = at + (first & mask & ~15);
+    }
+    return k;
+}
+
+template <int F, int DT, int NT>
+__global__ __launch_bounds__(256, (Few<F, DT, NT>::kPerCu)) void few_kernel(AttnJob a, Split sp) {
+    typedef Few<F, DT, NT> P;
+    constexpr bool kCodes = P::kCodes;
+    __shared__ __align__(16) char lds[kWaves * P::kPatch];
+    __shared__ float2 ml[kWaves][16];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n = lane & 15, g = lane >> 4;
+    int u = blockIdx.x;
+    const int kvh = u % a.c.n_kv;
+    u /= a.c.n_kv;
+    const int split = u % sp.n_split, s = u / sp.n_split;
+    const Seq q = seq_of(a, s);
+    const int rows = q.rows * a.group, d = a.c.d;
+    if (rows == 0) return;
+
+    // Query rows of this lane's columns, and what they see.
+    P st;
+    Sees see[NT];
+    int lo = 0x7FFFFFFF, hi = 0;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const int r = 16 * t + n, i = r / a.group;
+        const bool on = r < rows;
+        const uint16_t *qp = static_cast<const uint16_t *>(a.q) + (size_t)(q.q0 + (on ? i : 0)) * a.ldq +
+                             (size_t)(kvh * a.group + (on ? r - i * a.group : 0)) * d;
+#pragma unroll
+        for (int k = 0; k < P::kSteps; ++k) {
+            const int at = kCodes ? 64 * (k >> 1) + 16 * g + 8 * (k & 1) : 32 * k + 8 * g;
+            st.q[t][k] = u32x4{0, 0, 0, 0};
+            if (on && at < d) st.q[t][k] = ldg(reinterpret_cast<const u32x4 *>(qp + at));
+        }
+        see[t] = sees(a, q, i);
+        if (on) {
+            lo = min(lo, see[t].tree ? min(see[t].lo, max(q.ctx, 0)) : see[t].lo);
+            hi = max(hi, see[t].tree ? q.kv : see[t].hi);
+        } else {
+            see[t] = Sees{0, 0x7FFFFFFF, nullptr};   // an unused column: never the reason to mask
+        }
+#pragma unroll
+        for (int b = 0; b < P::kBlocks; ++b) st.o[t][b] = f32x4{0, 0, 0, 0};
+        st.m[t] = kNegInf, st.l[t] = 0.0f;
+    }
+#pragma unroll
+    for (int x = 1; x < 16; x <<= 1) {
+        lo = min(lo, __shfl_xor(lo, x));
+        hi = max(hi, __shfl_xor(hi, x));
+    }
+    lo = __builtin_amdgcn_readfirstlane(lo) & ~31;
+    hi = __builtin_amdgcn_readfirstlane(hi);
+    // This workgroup's keys, and this wave's: a stretch of whole 32s.
+    const int64_t c0 = (int64_t)lo + (int64_t)split * sp.chunk;
+    const int w0 = c0 < hi ? (int)c0 : hi, w1 = (int)min((int64_t)hi, c0 + sp.chunk);
+    const int per = ((w1 - w0 + kWaves * 32 - 1) / (kWaves * 32)) * 32;
+    const int k0 = min(w0 + wave * per, w1), k1 = min(k0 + per, w1), last = k1 - 1;
+
+    char *patch = lds + wave * P::kPatch;
+    if (k0 < k1) {
+        u32x4 kr[2][P::kLoads], vr[2][P::kLoads];
+        f32x4 ks[2], vs[2];
+        uint32_t valid;
+        auto load = [&](const void *pool, const KeyRows &k, u32x4 (&to)[2][P::kLoads]) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const char *row = static_cast<const char *>(pool) + k.row[b] * d * (kCodes ? 1 : 2);
+#pragma unroll
+                for (int i = 0; i < P::kLoads; ++i) {
+                    const int at = 64 * i + 16 * g;   // bytes
+                    to[b][i] = ldg(reinterpret_cast<const u32x4 *>(row + (at < d * (kCodes ? 1 : 2) ? at : 0)));
+                }
+            }
+        };
+        auto load_scale = [&](const float *pool, const KeyRows &k, f32x4 (&to)[2]) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) to[b] = ldg(reinterpret_cast<const f32x4 *>(pool + k.first[b] + 4 * g));
+        };
+        // LDS places. V row of key r: 16-byte piece c at c ^ f(r), so that the rows
+        // one transposing read takes together lie on different banks.
+        constexpr int kMask = DT >= 128 ? 7 : 3;
+        int put[2], get[8];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const int f = kCodes ? ((n & 3) | b << 2) & kMask : (n & kMask) << 1;
+            put[b] = (16 * b + n) * P::kRow + ((g ^ f) << 4);
+        }
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+            if (kCodes) {
+                const int e = n >> 1, key = 16 * (e >> 2) + 4 * g + (e & 3);
+                get[x] = key * P::kRow + (((x ^ e) & kMask) << 4) + 8 * (n & 1);
+            } else {
+                const int key = 4 * g + (n >> 2);
+                get[x] = key * P::kRow + (((x ^ key) & kMask) << 5) + 8 * (n & 3);
+            }
+        }
+        KeyRows at = key_rows(a, s, kvh, k0, last);
+        load(a.c.k, at, kr);
+        if (kCodes) load_scale(a.c.k_scale, at, ks);
+        load(a.c.v, at, vr);
+        if (kCodes) load_scale(a.c.v_scale, at, vs);
+        valid = at.valid;
+        for (int j0 = k0; j0 < k1; j0 += 32) {
+            const int next = j0 + 32 < k1 ? j0 + 32 : j0;
+            at = key_rows(a, s, kvh, next, last);
+            // scores
+            f32x4 sc[NT][2];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) sc[t][0] = sc[t][1] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int k = 0; k < P::kSteps; ++k) {
+                    const u32x4 w = kr[b][kCodes ? k >> 1 : k];
+                    const u32x4 kf = kCodes ? (k & 1 ? widen8<F>(w.z, w.w) : widen8<F>(w.x, w.y)) : w;
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) sc[t][b] = mfma16(kf, st.q[t][k], sc[t][b]);
+                }
+            f32x4 mul[2] = {f32x4{a.scale2, a.scale2, a.scale2, a.scale2}, f32x4{a.scale2, a.scale2, a.scale2, a.scale2}};
+            if (kCodes) mul[0] *= ks[0], mul[1] *= ks[1];
+            load(a.c.k, at, kr);
+            if (kCodes) load_scale(a.c.k_scale, at, ks);
+            // V into the patch
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int i = 0; i < P::kLoads; ++i)
+                    *reinterpret_cast<u32x4 *>(patch + (put[b] ^ (i << 6))) = vr[b][i];
+            f32x4 vm[2];
+            if (kCodes) vm[0] = vs[0], vm[1] = vs[1];
+            load(a.c.v, at, vr);
+            if (kCodes) load_scale(a.c.v_scale, at, vs);
+            // weights
+            u32x4 ph[NT], pl[NT];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                const uint32_t vis = visible32(a, q, see[t], j0) & valid & bits(0, k1 - j0);
+                float x[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = sc[t][e >> 2][e & 3] * mul[e >> 2][e & 3];
+                if (__any(vis != 0xFFFFFFFFu)) {
+                    const uint32_t mine = vis >> (4 * g);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = mine & (1u << (16 * (e >> 2) + (e & 3))) ? x[e] : kNegInf;
+                }
+                float top = x[0];
+#pragma unroll
+                for (int e = 1; e < 8; ++e) top = fmaxf(top, x[e]);
+                top = groups_max(top);
+                if (__any(top > st.m[t] + 8.0f)) {
+                    // The reference moves only when a score passes it by 2^8: sums stay in range.
+                    const float now = fmaxf(st.m[t], top), up = now == st.m[t] ? 1.0f : __builtin_amdgcn_exp2f(st.m[t] - now);
+                    st.m[t] = now;
+                    st.l[t] *= up;
+#pragma unroll
+                    for (int b = 0; b < P::kBlocks; ++b) st.o[t][b] *= up;
+                }
+                const float ref = st.m[t] == kNegInf ? 0.0f : st.m[t];
+                float p[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    p[e] = __builtin_amdgcn_exp2f(x[e] - ref);
+                    st.l[t] += p[e];
+                    if (kCodes) p[e] = p[e] == 0.0f ? 0.0f : p[e] * vm[e >> 2][e & 3];
+                }
+                uint32_t h[4], r[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    h[e] = pack2(p[2 * e], p[2 * e + 1]);
+                    r[e] = pack2(p[2 * e] - bf16_f(h[e] & 0xFFFFu), p[2 * e + 1] - __uint_as_float(h[e] & 0xFFFF0000u));
+                }
+                ph[t] = u32x4{h[0], h[1], h[2], h[3]};
+                pl[t] = u32x4{r[0], r[1], r[2], r[3]};
+            }
+            // outputs
+#pragma unroll
+            for (int b = 0; b < P::kBlocks; ++b) {
+                u32x4 vf;
+                if (kCodes) {
+                    const u32x2 w = read_tr8(patch + get[b & 7] + (b >> 3) * 128);
+                    vf = widen8<F>(w.x, w.y);
+                } else {
+                    const char *p = patch + get[b & 7] + (b >> 3) * 256;
+                    const u32x2 x = read_tr16(p), y = read_tr16(p + 16 * P::kRow);
+                    vf = u32x4{x.x, x.y, y.x, y.y};
+                }
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    st.o[t][b] = mfma16(vf, ph[t], st.o[t][b]);
+                    st.o[t][b] = mfma16(vf, pl[t], st.o[t][b]);
+                }
+            }
+            valid = at.valid;
+        }
+    }
+
+    // Join the four waves, 16 rows at a time: row n of the patch holds the wave's output.
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        if (16 * t >= rows) break;
+        st.l[t] = groups_sum(st.l[t]);
+        float check = st.l[t] * 0.0f;
+        float *out = reinterpret_cast<float *>(patch);
+#pragma unroll
+        for (int b = 0; b < P::kBlocks; ++b) {
+            if (16 * b < d) check += st.o[t][b].x * 0.0f + st.o[t][b].y * 0.0f + st.o[t][b].z * 0.0f + st.o[t][b].w * 0.0f;
+            *reinterpret_cast<f32x4 *>(out + n * DT + 16 * b + 4 * g) = st.o[t][b];
+        }
+        if (g == 0) ml[wave][n] = make_float2(st.m[t], st.l[t]);
+        // A row with an infinity or a NaN is done again key by key: one that it does
+        // not see may have got in as 0 * NaN.
+        uint64_t odd = __ballot(16 * t + n < rows && check != 0.0f);
+        odd |= odd >> 32;
+        odd |= odd >> 16;
+        for (uint32_t left = (uint32_t)odd & 0xFFFFu; left; left &= left - 1) {
+            const int c = __ffs(left) - 1, r = 16 * t + c, i = r / a.group;
+            float acc[4], m, l;
+            one_row<uint16_t, F>(a, q, i, kvh * a.group + r - i * a.group, k0, k1, acc, m, l);
+            if (4 * lane < DT) *reinterpret_cast<f32x4 *>(out + c * DT + 4 * lane) = f32x4{acc[0], acc[1], acc[2], acc[3]};
+            if (lane == 0) ml[wave][c] = make_float2(m, l);
+        }
+        __syncthreads();
+        for (int x = threadIdx.x; x < 16 * DT / 4; x += 256) {
+            const int c = x / (DT / 4), at = 4 * (x % (DT / 4)), r = 16 * t + c;
+            if (r >= rows || at >= d) continue;
+            float m = kNegInf, l = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) m = fmaxf(m, ml[w][c].x);
+            f32x4 sum{0, 0, 0, 0};
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
+                const float2 v = ml[w][c];
+                if (v.x == kNegInf && v.y == 0.0f) continue;
+                const float up = __builtin_amdgcn_exp2f(v.x - m);
+                l += up * v.y;
+                sum += *reinterpret_cast<const f32x4 *>(lds + w * P::kPatch + (c * DT + at) * 4) * up;
+            }
+            if (sp.n_split > 1) {
+                const int64_t row = ((int64_t)(s * (int64_t)a.c.n_kv + kvh) * sp.n_split + split) * sp.rows + r;
+                *reinterpret_cast<f32x4 *>(sp.part + row * d + at) = sum;
+                if (at == 0) sp.ml[row] = make_float2(m, l);
+            } else {
+                const float v[4] = {sum.x, sum.y, sum.z, sum.w};
+                float w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[e] = l == 0.0f ? 0.0f : v[e] / l;
+                const int i = r / a.group;
+                put4(static_cast<uint16_t *>(a.o) + (size_t)(q.q0 + i) * a.ldo + (size_t)(kvh * a.group + r - i * a.group) * d + at, w);
+            }
+        }
+        if (NT > 1) __syncthreads();
+    }
+}
+
+template <int F, int DT, int NT>
+void run(const AttnJob &a, const Split &sp, hipStream_t s) {
+    const int64_t blocks = (int64_t)a.c.n_seq * sp.n_split * a.c.n_kv;
+    hipLaunchKernelGGL((few_kernel<F, DT, NT>), dim3((unsigned)blocks), dim3(256), 0, s, a, sp);
+}
+
+template <int F>
+void pick(const AttnJob &a, const Split &sp, hipStream_t s) {
+    const bool two = a.max_q * a.group > 16;
+    if (a.c.d <= 64)
+        two ? run<F, 64, 2>(a, sp, s) : run<F, 64, 1>(a, sp, s);
+    else if (a.c.d <= 128)
+        two ? run<F, 128, 2>(a, sp, s) : run<F, 128, 1>(a, sp, s);
+    else
+        two ? run<F, 256, 2>(a, sp, s) : run<F, 256, 1>(a, sp, s);
+}
+
+}  // namespace
+
+void launch_few(const AttnJob &a, int fmt, const Split &sp, hipStream_t s) {
+    switch (fmt) {
+        case kFmtBf16: pick<kFmtBf16>(a, sp, s); break;
+        case kFmtInt8: pick<kFmtInt8>(a, sp, s); break;
+        default: pick<kFmtE4m3>(a, sp, s);
+    }
+}
+
+}  // namespace wl
