@@ -71,7 +71,7 @@ __global__ __launch_bounds__(256) void join_kernel(AttnJob a, Split sp) {
     put4(static_cast<E *>(a.o) + (size_t)(q.q0 + i) * a.ldo + (size_t)(kvh * a.group + r - i * a.group) * a.c.d + at, e);
 }
 
-enum Kind { kRows, kFew };
+enum Kind { kRows, kFew, kTile };
 
 struct Plan {
     Kind kind;
@@ -84,14 +84,14 @@ constexpr int kMinChunk = 256;     // keys
 Plan plan_of(const AttnJob &a, bool f32) {
     Plan p{};
     p.sp.n_split = 1;
-    p.kind = f32 || (int64_t)a.max_q * a.group > kFewRows ? kRows : kFew;
+    p.kind = f32 ? kRows : (int64_t)a.max_q * a.group > kFewRows ? kTile : kFew;
     if (p.kind == kRows) return p;
     p.sp.rows = a.max_q * a.group;
     // Most keys that the queries of one sequence see between them; pieces start at a multiple of 32.
     int64_t span = a.max_kv;
     if (a.mask == kMaskCausal && a.window && (int64_t)a.window + a.max_q < span) span = (int64_t)a.window + a.max_q;
     span += 31;
-    const int64_t units = (int64_t)a.c.n_seq * a.c.n_kv;
+    const int64_t units = (int64_t)a.c.n_seq * a.c.n_kv * (p.kind == kTile ? (p.sp.rows + kTileRows - 1) / kTileRows : 1);
     int64_t chunk = (span * units + kWorkgroups - 1) / kWorkgroups;
     if (chunk < kMinChunk) chunk = kMinChunk;
     if (chunk < (span + kMaxSplit - 1) / kMaxSplit) chunk = (span + kMaxSplit - 1) / kMaxSplit;
@@ -114,12 +114,12 @@ size_t attention_scratch(const AttnJob &a, int fmt, bool f32) {
 
 hipError_t launch_attention(const AttnJob &a, int fmt, bool f32, void *ws, hipStream_t s) {
     Plan p = plan_of(a, f32);
-    if (p.kind == kFew) {
+    if (p.kind != kRows) {
         if (p.sp.n_split > 1) {
             p.sp.part = static_cast<float *>(ws);
             p.sp.ml = reinterpret_cast<float2 *>(p.sp.part + part_floats(a, p.sp) * a.c.d);
         }
-        launch_few(a, fmt, p.sp, s);
+        p.kind == kFew ? launch_few(a, fmt, p.sp, s) : launch_tile(a, fmt, p.sp, s);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess || p.sp.n_split == 1) return e;
         const int64_t waves = (int64_t)a.c.n_seq * a.c.n_kv * p.sp.rows;

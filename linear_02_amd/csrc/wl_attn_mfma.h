@@ -101,6 +101,9 @@ struct Split {
 constexpr int kFewRows = 32;      // most query rows per key/value head of the few-row kernel
 constexpr int kMaxSplit = 64;     // one lane each in the join
 
+constexpr int kTileRows = 128;    // query rows per workgroup of the many-row kernel
+
 void launch_few(const AttnJob &a, int fmt, const Split &sp, hipStream_t s);
+void launch_tile(const AttnJob &a, int fmt, const Split &sp, hipStream_t s);
 
 }  // namespace wl
