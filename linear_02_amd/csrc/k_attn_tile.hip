@@ -14,259 +14,51 @@ namespace {
 
 constexpr int kRowsPerWave = 32, kNT = kRowsPerWave / 16;
 
-template <int F, int DT>
-__global__ __launch_bounds__(256, 2) void tile_kernel(AttnJob a, Split sp, int tiles) {
-    constexpr bool kCodes = F == kFmtInt8 || F == kFmtE4m3;
-    constexpr int kSteps = DT / 32, kBlocks = DT / 16;
-    constexpr int kRow = 2 * DT, kSide = 32 * kRow;          // LDS bytes of a row, of 32 keys
-    constexpr int kPieces = DT / 8;                          // 16-byte pieces of a row
-    constexpr int kMaskV = DT >= 128 ? 7 : 3;
-    __shared__ __align__(16) char lds[2][2][kSide];          // [buffer][K, V]
-    __shared__ __align__(16) float lds_scale[2][2][32];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int n = lane & 15, g = lane >> 4;
+struct TileArgs {
+    AttnJob a;
+    Split sp;
+    int tiles;   // of 128 rows, per sequence and key/value head
+};
+
+// Which rows and keys a workgroup works on.
+struct Work {
+    int kvh, split, tile, s;
+};
+__device__ __forceinline__ Work work_of(const TileArgs &x) {
+    Work w;
     int u = blockIdx.x;
-    const int kvh = u % a.c.n_kv;
-    u /= a.c.n_kv;
-    const int split = u % sp.n_split;
-    u /= sp.n_split;
-    const int tile = tiles - 1 - u % tiles, s = u / tiles;   // the longest rows first
+    w.kvh = u % x.a.c.n_kv;
+    u /= x.a.c.n_kv;
+    w.split = u % x.sp.n_split;
+    u /= x.sp.n_split;
+    w.tile = x.tiles - 1 - u % x.tiles;   // the longest rows first
+    w.s = u / x.tiles;
+    return w;
+}
+
+// Which of keys j0 .. j0 + 31 this lane's row of tile `first` (0 or 16) sees. Only
+// at the edges of what the wave's rows see, so from the arguments in memory.
+__device__ __forceinline__ uint32_t seen(const TileArgs &x, int first, int j0) {
+    const Work work = work_of(x);
+    const Seq q = seq_of(x.a, work.s);
+    const int r = work.tile * 128 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * kRowsPerWave + first + (threadIdx.x & 15);
+    return visible32(x.a, q, sees(x.a, q, r / x.a.group), j0);
+}
+
+// Writes a wave's outputs: lane (n, g) holds elements 16 b + 4 g .. + 3 of row n.
+template <int F, int DT>
+__device__ __forceinline__ void finish(const TileArgs &x, f32x4 (&o)[kNT][DT / 16], float (&m)[kNT], float (&l)[kNT], int k0, int k1) {
+    constexpr int kBlocks = DT / 16;
+    const AttnJob &a = x.a;
+    const Split &sp = x.sp;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15, g = lane >> 4;
+    const Work work = work_of(x);
+    const int kvh = work.kvh, split = work.split, tile = work.tile, s = work.s;
     const Seq q = seq_of(a, s);
     const int rows = q.rows * a.group, d = a.c.d, r0 = tile * 128 + wave * kRowsPerWave;
-    if (tile * 128 >= rows) return;
-
-    u32x4 qf[kNT][kSteps];
-    f32x4 o[kNT][kBlocks];
-    float m[kNT], l[kNT];
-    Sees see[kNT];
-    int lo = 0x7FFFFFFF, hi = 0;
-    const uint32_t sign = a.scale2 < 0.0f ? 0x80008000u : 0u;   // a negative scale goes into the queries
-    const float scale2 = fmaxf(fabsf(a.scale2), 0x1p-126f);   // not 0: -inf marks an unseen key
 #pragma unroll
     for (int t = 0; t < kNT; ++t) {
-        const int r = r0 + 16 * t + n, i = r / a.group;
-        const bool on = r < rows;
-        const uint16_t *qp = static_cast<const uint16_t *>(a.q) + (size_t)(q.q0 + (on ? i : 0)) * a.ldq +
-                             (size_t)(kvh * a.group + (on ? r - i * a.group : 0)) * d;
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k) {
-            const int at = 32 * k + 8 * g;
-            qf[t][k] = u32x4{0, 0, 0, 0};
-            if (on && at < d) qf[t][k] = ldg(reinterpret_cast<const u32x4 *>(qp + at)) ^ sign;
-        }
-        see[t] = sees(a, q, i);
-        if (on) {
-            lo = min(lo, see[t].tree ? min(see[t].lo, max(q.ctx, 0)) : see[t].lo);
-            hi = max(hi, see[t].tree ? q.kv : see[t].hi);
-        } else {
-            see[t] = Sees{0, 0x7FFFFFFF, nullptr};   // an unused column: never the reason to mask
-        }
-#pragma unroll
-        for (int b = 0; b < kBlocks; ++b) o[t][b] = f32x4{0, 0, 0, 0};
-        m[t] = kNegInf, l[t] = 0.0f;
-    }
-#pragma unroll
-    for (int x = 1; x < 16; x <<= 1) {
-        lo = min(lo, __shfl_xor(lo, x));
-        hi = max(hi, __shfl_xor(hi, x));
-    }
-    // Keys of this wave's rows, of the workgroup's, and the piece of them that is this workgroup's.
-    __shared__ int range[2][4];
-    if (lane == 0) range[0][wave] = lo, range[1][wave] = hi;
-    __syncthreads();
-    const int wlo = __builtin_amdgcn_readfirstlane(lo), whi = __builtin_amdgcn_readfirstlane(hi);
-    lo = min(min(range[0][0], range[0][1]), min(range[0][2], range[0][3]));
-    hi = max(max(range[1][0], range[1][1]), max(range[1][2], range[1][3]));
-    lo = __builtin_amdgcn_readfirstlane(lo) & ~31;
-    hi = __builtin_amdgcn_readfirstlane(hi);
-    const int64_t c0 = (int64_t)lo + (int64_t)split * sp.chunk;
-    const int k0 = c0 < hi ? (int)c0 : hi, k1 = (int)min((int64_t)hi, c0 + sp.chunk), last = k1 - 1;
-
-    if (k0 < k1) {
-        const int pmask = (1 << a.c.page_shift) - 1;
-        const int32_t *table = a.c.table + (int64_t)s * a.c.max_pages;
-        const int bytes = d * (kCodes ? 1 : 2);              // of a cache row
-        int page[2];                                         // of the keys that are staged next
-        auto look = [&](int j0) {
-#pragma unroll
-            for (int b = 0; b < 2; ++b) page[b] = table[min(j0 + 16 * b, last) >> a.c.page_shift];
-        };
-        // The 16 keys of half b: element row of the first, and whether they have a page.
-        auto base = [&](int j0, int b, bool &ok) {
-            ok = (unsigned)page[b] < (unsigned)a.c.n_pages;
-            return (((int64_t)(ok ? page[b] : 0) * a.c.n_kv + kvh) << a.c.page_shift) + (min(j0 + 16 * b, last) & pmask & ~15);
-        };
-        // Within a half: rows behind the last key read that key again.
-        auto row_at = [&](int j0, int b, int r) { return min(r, last - min(j0 + 16 * b, last & ~15)); };
-        // bf16: 64 pieces per load, straight into LDS; piece c of row r lies at c ^ f(r).
-        constexpr int kDma = kPieces * 32 / 256;             // loads per wave and side
-        // codes: 16 bytes per load and lane, widened when they are put down.
-        constexpr int kCodeLoads = kCodes ? (2 * DT + 255) / 256 : 1;   // per lane and side: 32 rows of DT / 16 pieces over 256 lanes
-        u32x4 kc[kCodeLoads], vc[kCodeLoads];
-        float scale_in = 0.0f;
-        uint32_t valid_in = 0;
-        auto fetch = [&](int j0, int buf) {
-            int64_t first[2];
-            bool ok[2];
-#pragma unroll
-            for (int b = 0; b < 2; ++b) first[b] = base(j0, b, ok[b]);
-            valid_in = (ok[0] ? 0xFFFFu : 0u) | (ok[1] ? 0xFFFF0000u : 0u);
-            if (!kCodes) {
-#pragma unroll
-                for (int i = 0; i < kDma; ++i) {
-                    const int p0 = (wave * kDma + i) * 64, b = p0 / (16 * kPieces);   // a load's rows are of one half
-                    const int p = p0 + lane, r = p / kPieces, c = p % kPieces;
-                    const int from = row_at(j0, b, r & 15) * bytes;
-                    const int ck = (c ^ (r & 7)) * 16, cv = (c ^ ((r & kMaskV) << 1)) * 16;
-                    const char *k = static_cast<const char *>(a.c.k) + first[b] * bytes, *v = static_cast<const char *>(a.c.v) + first[b] * bytes;
-                    lds_dma16(reinterpret_cast<const u32x4 *>(k + (from + (ck < bytes ? ck : 0))),
-                              reinterpret_cast<u32x4 *>(lds[buf][0] + p0 * 16));
-                    lds_dma16(reinterpret_cast<const u32x4 *>(v + (from + (cv < bytes ? cv : 0))),
-                              reinterpret_cast<u32x4 *>(lds[buf][1] + p0 * 16));
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < kCodeLoads; ++i) {
-                    const int p = threadIdx.x + i * 256, r = (p / (DT / 16)) & 31, c = p % (DT / 16) * 16, b = r >> 4;
-                    const int64_t from = first[b] * bytes + row_at(j0, b, r & 15) * bytes + (c < bytes ? c : 0);
-                    kc[i] = ldg(reinterpret_cast<const u32x4 *>(static_cast<const char *>(a.c.k) + from));
-                    vc[i] = ldg(reinterpret_cast<const u32x4 *>(static_cast<const char *>(a.c.v) + from));
-                }
-                if (threadIdx.x < 64) {
-                    const int r = lane & 31;
-                    const int64_t from = first[r >> 4] + row_at(j0, r >> 4, r & 15);
-                    scale_in = (lane < 32 ? a.c.k_scale : a.c.v_scale)[from];
-                }
-            }
-        };
-        auto land = [&](int buf) {
-            if (!kCodes) {
-                wait_vm<0>();
-                return;
-            }
-#pragma unroll
-            for (int i = 0; i < kCodeLoads; ++i) {
-                const int p = threadIdx.x + i * 256, r = p / (DT / 16), c = p % (DT / 16) * 2;
-                if (DT == 64 && r >= 32) break;
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    *reinterpret_cast<u32x4 *>(lds[buf][0] + r * kRow + ((c + e) ^ (r & 7)) * 16) =
-                        e ? widen8<F>(kc[i].z, kc[i].w) : widen8<F>(kc[i].x, kc[i].y);
-                    *reinterpret_cast<u32x4 *>(lds[buf][1] + r * kRow + ((c + e) ^ ((r & kMaskV) << 1)) * 16) =
-                        e ? widen8<F>(vc[i].z, vc[i].w) : widen8<F>(vc[i].x, vc[i].y);
-                }
-            }
-            if (threadIdx.x < 64) lds_scale[buf][lane >> 5][lane & 31] = scale_in;
-        };
-        // Operand addresses within a buffer.
-        int at_k[2], at_v[8];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) at_k[x] = n * kRow + (((4 * x + g) ^ (n & 7)) << 4);
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-            const int key = 4 * g + (n >> 2);
-            at_v[x] = key * kRow + (((x ^ key) & kMaskV) << 5) + 8 * (n & 3);
-        }
-        look(k0);
-        fetch(k0, 0);
-        uint32_t valid = valid_in;
-        if (k0 + 32 < k1) look(k0 + 32);
-        land(0);
-        __syncthreads();
-        int buf = 0;
-        for (int j0 = k0; j0 < k1; j0 += 32, buf ^= 1) {
-            const bool more = j0 + 32 < k1;
-            if (more) {
-                fetch(j0 + 32, buf ^ 1);
-                look(min(j0 + 64, last));
-            }
-            if (j0 + 31 >= wlo && j0 < whi) {
-                const char *kb = lds[buf][0], *vb = lds[buf][1];
-                f32x4 sc[kNT][2];
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-#pragma unroll
-                    for (int t = 0; t < kNT; ++t) sc[t][b] = f32x4{0, 0, 0, 0};
-#pragma unroll
-                    for (int k = 0; k < kSteps; ++k) {
-                        const u32x4 kf = *reinterpret_cast<const u32x4 *>(kb + at_k[k & 1] + (k >> 1) * 128 + b * 16 * kRow);
-#pragma unroll
-                        for (int t = 0; t < kNT; ++t) sc[t][b] = mfma16(kf, qf[t][k], sc[t][b]);
-                    }
-                }
-                f32x4 vm[2];
-                if (kCodes) {
-#pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        const f32x4 ks = *reinterpret_cast<const f32x4 *>(&lds_scale[buf][0][16 * b + 4 * g]);
-                        vm[b] = *reinterpret_cast<const f32x4 *>(&lds_scale[buf][1][16 * b + 4 * g]);
-#pragma unroll
-                        for (int t = 0; t < kNT; ++t) sc[t][b] *= ks;
-                    }
-                }
-                u32x4 ph[kNT];
-#pragma unroll
-                for (int t = 0; t < kNT; ++t) {
-                    float x[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = sc[t][e >> 2][e & 3];
-                    const uint32_t vis = visible32(a, q, see[t], j0) & valid & bits(0, k1 - j0);
-                    if (__any(vis != 0xFFFFFFFFu)) {
-                        const uint32_t mine = vis >> (4 * g);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) x[e] = mine & (1u << (16 * (e >> 2) + (e & 3))) ? x[e] : kNegInf;
-                    }
-                    float top = x[0];
-#pragma unroll
-                    for (int e = 1; e < 8; ++e) top = fmaxf(top, x[e]);
-                    top = groups_max(top);
-                    top = top == kNegInf ? top : top * scale2;
-                    if (__any(top > m[t] + 8.0f)) {
-                        // The reference moves only when a score passes it by 2^8: sums stay in range.
-                        const float now = fmaxf(m[t], top), up = now == m[t] ? 1.0f : __builtin_amdgcn_exp2f(m[t] - now);
-                        m[t] = now;
-                        l[t] *= up;
-#pragma unroll
-                        for (int b = 0; b < kBlocks; ++b) o[t][b] *= up;
-                    }
-                    const float ref = m[t] == kNegInf ? 0.0f : m[t];
-                    float p[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[e], scale2, -ref));
-                        if (kCodes) {
-                            l[t] += p[e];
-                            p[e] = p[e] == 0.0f ? 0.0f : p[e] * vm[e >> 2][e & 3];
-                        }
-                    }
-                    ph[t] = u32x4{pack2(p[0], p[1]), pack2(p[2], p[3]), pack2(p[4], p[5]), pack2(p[6], p[7])};
-                    if (!kCodes) {
-                        // the sum of the weights as the product will use them
-                        constexpr uint32_t kOnes = 0x3F803F80u;
-                        l[t] = dot2(ph[t].x, kOnes, l[t]);
-                        l[t] = dot2(ph[t].y, kOnes, l[t]);
-                        l[t] = dot2(ph[t].z, kOnes, l[t]);
-                        l[t] = dot2(ph[t].w, kOnes, l[t]);
-                    }
-                }
-#pragma unroll
-                for (int b = 0; b < kBlocks; ++b) {
-                    const char *p = vb + at_v[b & 7] + (b >> 3) * 256;
-                    const u32x2 x = read_tr16(p), y = read_tr16(p + 16 * kRow);
-#pragma unroll
-                    for (int t = 0; t < kNT; ++t) o[t][b] = mfma16(u32x4{x.x, x.y, y.x, y.y}, ph[t], o[t][b]);
-                }
-            }
-            if (more) land(buf ^ 1);
-            valid = valid_in;
-            __syncthreads();
-        }
-    }
-
-    // Outputs: lane (n, g) holds elements 16 b + 4 g .. + 3 of row n.
-#pragma unroll
-    for (int t = 0; t < kNT; ++t) {
-        const int r = r0 + 16 * t + n, i = r / a.group;
+        const int r = r0 + 16 * t + n;
         l[t] = groups_sum(l[t]);
         float check = l[t] * 0.0f;
 #pragma unroll
@@ -313,15 +105,294 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(AttnJob a, Split sp, int t
             }
             if (sp.n_split > 1 && lane == 0) sp.ml[part + rr] = make_float2(mm, ll);
         }
-        (void)i;
     }
+}
+
+template <int F, int DT>
+__global__ __launch_bounds__(256, 2) void tile_kernel(TileArgs x) {
+    const AttnJob &a = x.a;
+    constexpr bool kCodes = F == kFmtInt8 || F == kFmtE4m3;
+    constexpr int kSteps = DT / 32, kBlocks = DT / 16;
+    constexpr int kRow = 2 * DT, kSide = 32 * kRow;          // LDS bytes of a row, of 32 keys
+    constexpr int kPieces = DT / 8;                          // 16-byte pieces of a row
+    constexpr int kMaskV = DT >= 128 ? 7 : 3;
+    // One LDS object: beside a second one the compiler waits for the loads into
+    // LDS that are still on their way before every read.
+    constexpr int kTail = kCodes ? 3 * kSide : 4 * kSide;
+    __shared__ __align__(16) char lds_all[kTail + 256 + 32];
+    char (*lds)[2][kSide] = reinterpret_cast<char (*)[2][kSide]>(lds_all);   // [buffer][K, V]; one buffer for codes
+    char *raw = lds_all + 2 * kSide;                                         // codes as fetched: K, then V
+    float (*lds_scale)[32] = reinterpret_cast<float (*)[32]>(lds_all + kTail);   // [K, V]
+    int (*range)[4] = reinterpret_cast<int (*)[4]>(lds_all + kTail + 256);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n = lane & 15, g = lane >> 4;
+    const Work work = work_of(x);
+    const int kvh = work.kvh, split = work.split, tile = work.tile, s = work.s;
+    const Seq q = seq_of(a, s);
+    const int rows = q.rows * a.group, d = a.c.d, r0 = tile * 128 + wave * kRowsPerWave;
+    if (tile * 128 >= rows) return;
+
+    u32x4 qf[kNT][kSteps];
+    f32x4 o[kNT][kBlocks];
+    float m[kNT], l[kNT];
+    int lo = 0x7FFFFFFF, hi = 0, flo = 0, fhi = 0x7FFFFFFF;   // some row sees [lo, hi), every row [flo, fhi)
+    const uint32_t sign = a.scale2 < 0.0f ? 0x80008000u : 0u;   // a negative scale goes into the queries
+    const float scale2 = fmaxf(fabsf(a.scale2), 0x1p-126f);   // not 0: -inf marks an unseen key
+#pragma unroll
+    for (int t = 0; t < kNT; ++t) {
+        const int r = r0 + 16 * t + n, i = r / a.group;
+        const bool on = r < rows;
+        const uint16_t *qp = static_cast<const uint16_t *>(a.q) + (size_t)(q.q0 + (on ? i : 0)) * a.ldq +
+                             (size_t)(kvh * a.group + (on ? r - i * a.group : 0)) * d;
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+            const int at = 32 * k + 8 * g;
+            qf[t][k] = u32x4{0, 0, 0, 0};
+            if (on && at < d) qf[t][k] = ldg(reinterpret_cast<const u32x4 *>(qp + at)) ^ sign;
+        }
+        const Sees see = sees(a, q, i);
+        if (on) {   // an unused column is never the reason to mask
+            lo = min(lo, see.tree ? min(see.lo, max(q.ctx, 0)) : see.lo);
+            hi = max(hi, see.tree ? q.kv : see.hi);
+            flo = max(flo, see.lo);
+            fhi = min(fhi, see.hi);
+        }
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b) o[t][b] = f32x4{0, 0, 0, 0};
+        m[t] = kNegInf, l[t] = 0.0f;
+    }
+#pragma unroll
+    for (int x = 1; x < 16; x <<= 1) {
+        lo = min(lo, __shfl_xor(lo, x));
+        hi = max(hi, __shfl_xor(hi, x));
+        flo = max(flo, __shfl_xor(flo, x));
+        fhi = min(fhi, __shfl_xor(fhi, x));
+    }
+    flo = __builtin_amdgcn_readfirstlane(flo);
+    fhi = __builtin_amdgcn_readfirstlane(fhi);
+    // Keys of this wave's rows, of the workgroup's, and the piece of them that is this workgroup's.
+    if (lane == 0) range[0][wave] = lo, range[1][wave] = hi;
+    __syncthreads();
+    const int wlo = __builtin_amdgcn_readfirstlane(lo), whi = __builtin_amdgcn_readfirstlane(hi);
+    lo = min(min(range[0][0], range[0][1]), min(range[0][2], range[0][3]));
+    hi = max(max(range[1][0], range[1][1]), max(range[1][2], range[1][3]));
+    lo = __builtin_amdgcn_readfirstlane(lo) & ~31;
+    hi = __builtin_amdgcn_readfirstlane(hi);
+    const int64_t c0 = (int64_t)lo + (int64_t)split * x.sp.chunk;
+    const int k0 = c0 < hi ? (int)c0 : hi, k1 = (int)min((int64_t)hi, c0 + x.sp.chunk), last = k1 - 1;
+
+    if (k0 < k1) {
+        const int32_t *table = a.c.table + (int64_t)s * a.c.max_pages;
+        const int shift = a.c.page_shift, pmask = (1 << shift) - 1, n_pages = a.c.n_pages;
+        const int bytes = d * (kCodes ? 1 : 2);              // of a cache row
+        const int64_t head = (int64_t)kvh << shift, pitch = (int64_t)a.c.n_kv << shift;   // rows: of this head in a page, of a page
+        int page[2];                                         // of the keys that are staged next
+        // Page numbers come from a register: lane i holds entry first_page + i of the
+        // table, read anew every 64 pages. A load per step would have to be waited
+        // for behind the step's own loads.
+        int first_page = -64, pages = 0;
+        auto look = [&](int j0) {
+            const int e0 = min(j0, last) >> shift, e1 = min(j0 + 16, last) >> shift;
+            if (e1 - first_page >= 64) {
+                first_page = e0;
+                pages = table[min(e0 + lane, last >> shift)];
+                __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
+            }
+            page[0] = __builtin_amdgcn_readlane(pages, e0 - first_page);
+            page[1] = __builtin_amdgcn_readlane(pages, e1 - first_page);
+        };
+        // The 16 keys of half b: element row of the first, and whether they have a page.
+        auto base = [&](int j0, int b, bool &ok) {
+            ok = (unsigned)page[b] < (unsigned)n_pages;
+            return (ok ? page[b] : 0) * pitch + head + (min(j0 + 16 * b, last) & pmask & ~15);
+        };
+        // Within a half: rows behind the last key read that key again.
+        auto row_at = [&](int j0, int b, int r) { return min(r, last - min(j0 + 16 * b, last & ~15)); };
+        // bf16: 64 pieces per load, straight into LDS; piece c of row r lies at c ^ f(r).
+        constexpr int kDma = kPieces * 32 / 256;             // loads per wave and side
+        // codes: as they lie, into a patch that the wave which fetched them widens from.
+        constexpr int kRaw = (DT + 127) / 128;               // loads per wave and side: 4 pieces of 64 pieces, DT / 16 per row
+        float scale_in = 0.0f;
+        uint32_t valid_in = 0;
+        auto fetch = [&](int j0, int buf) {
+            int64_t first[2];
+            bool ok[2];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) first[b] = base(j0, b, ok[b]);
+            valid_in = (ok[0] ? 0xFFFFu : 0u) | (ok[1] ? 0xFFFF0000u : 0u);
+            if (!kCodes) {
+                const bool whole = j0 + 32 <= k1;
+#pragma unroll
+                for (int i = 0; i < kDma; ++i) {
+                    // rows r0 .. of one half; lane: row r0 + dr, piece c
+                    const int p0 = (wave * kDma + i) * 64, b = p0 / (16 * kPieces), r0 = p0 / kPieces & 15;
+                    const int dr = lane / kPieces, c = lane % kPieces;
+                    const int key = (kDma * 64 / kPieces % 8 == 0 ? i * (64 / kPieces) : r0) + dr;   // r & 7 comes from its low bits
+                    const int ck = min((c ^ (key & 7)) * 16, bytes - 16), cv = min((c ^ ((key & kMaskV) << 1)) * 16, bytes - 16);
+                    const int64_t from = (first[b] + (whole ? r0 : 0)) * bytes;
+                    const int row = whole ? dr * bytes : row_at(j0, b, r0 + dr) * bytes;
+                    lds_dma16(reinterpret_cast<const u32x4 *>(static_cast<const char *>(a.c.k) + from + (row + ck)),
+                              reinterpret_cast<u32x4 *>(lds[buf][0] + p0 * 16));
+                    lds_dma16(reinterpret_cast<const u32x4 *>(static_cast<const char *>(a.c.v) + from + (row + cv)),
+                              reinterpret_cast<u32x4 *>(lds[buf][1] + p0 * 16));
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < kRaw; ++i) {
+                    const int p0 = (wave * kRaw + i) * 64, b = p0 / DT;      // 16 rows are DT pieces: a load's rows are of one half
+                    if (p0 >= 2 * DT) break;
+                    const int p = p0 + lane, r = p / (DT / 16) & 15, c = min(p % (DT / 16) * 16, bytes - 16);
+                    const int64_t from = first[b] * bytes;
+                    const int row = row_at(j0, b, r) * bytes + c;
+                    lds_dma16(reinterpret_cast<const u32x4 *>(static_cast<const char *>(a.c.k) + from + row),
+                              reinterpret_cast<u32x4 *>(raw + p0 * 16));
+                    lds_dma16(reinterpret_cast<const u32x4 *>(static_cast<const char *>(a.c.v) + from + row),
+                              reinterpret_cast<u32x4 *>(raw + 32 * DT + p0 * 16));
+                }
+                if (wave == 0) {
+                    const int r = lane & 31;
+                    const int64_t from = first[r >> 4] + row_at(j0, r >> 4, r & 15);
+                    scale_in = (lane < 32 ? a.c.k_scale : a.c.v_scale)[from];
+                }
+            }
+        };
+        auto land = [&]() {
+            wait_vm<0>();
+            if (!kCodes) return;
+#pragma unroll
+            for (int i = 0; i < kRaw; ++i) {
+                const int p0 = (wave * kRaw + i) * 64;
+                if (p0 >= 2 * DT) break;
+                const int p = p0 + lane, r = p / (DT / 16), c = p % (DT / 16) * 2;
+                const u32x4 k = *reinterpret_cast<const u32x4 *>(raw + p * 16), v = *reinterpret_cast<const u32x4 *>(raw + 32 * DT + p * 16);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    *reinterpret_cast<u32x4 *>(lds[0][0] + r * kRow + ((c + e) ^ (r & 7)) * 16) =
+                        e ? widen8<F>(k.z, k.w) : widen8<F>(k.x, k.y);
+                    *reinterpret_cast<u32x4 *>(lds[0][1] + r * kRow + ((c + e) ^ ((r & kMaskV) << 1)) * 16) =
+                        e ? widen8<F>(v.z, v.w) : widen8<F>(v.x, v.y);
+                }
+            }
+            if (wave == 0) lds_scale[lane >> 5][lane & 31] = scale_in;
+        };
+        // Operand addresses within a buffer.
+        int at_k[2], at_v[8];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) at_k[x] = n * kRow + (((4 * x + g) ^ (n & 7)) << 4);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+            const int key = 4 * g + (n >> 2);
+            at_v[x] = key * kRow + (((x ^ key) & kMaskV) << 5) + 8 * (n & 3);
+        }
+        look(k0);
+        fetch(k0, 0);
+        uint32_t valid = valid_in;
+        if (k0 + 32 < k1) look(k0 + 32);
+        if (!kCodes) land();
+        __syncthreads();
+        int buf = 0;
+        for (int j0 = k0; j0 < k1; j0 += 32) {
+            const bool more = j0 + 32 < k1;
+            if (kCodes) land();
+            valid = valid_in;
+            if (more) {
+                fetch(j0 + 32, buf ^ 1);
+                look(min(j0 + 64, last));
+            }
+            if (kCodes) __syncthreads();
+            if (j0 + 31 >= wlo && j0 < whi) {
+                const char *kb = lds[buf][0], *vb = lds[buf][1];
+                f32x4 sc[kNT][2];
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+#pragma unroll
+                    for (int t = 0; t < kNT; ++t) sc[t][b] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                    for (int k = 0; k < kSteps; ++k) {
+                        const u32x4 kf = *reinterpret_cast<const u32x4 *>(kb + at_k[k & 1] + (k >> 1) * 128 + b * 16 * kRow);
+#pragma unroll
+                        for (int t = 0; t < kNT; ++t) sc[t][b] = mfma16(kf, qf[t][k], sc[t][b]);
+                    }
+                }
+                f32x4 vm[2];
+                if (kCodes) {
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        const f32x4 ks = *reinterpret_cast<const f32x4 *>(&lds_scale[0][16 * b + 4 * g]);
+                        vm[b] = *reinterpret_cast<const f32x4 *>(&lds_scale[1][16 * b + 4 * g]);
+#pragma unroll
+                        for (int t = 0; t < kNT; ++t) sc[t][b] *= ks;
+                    }
+                }
+                u32x4 ph[kNT];
+                const bool all = j0 >= flo && j0 + 32 <= min(fhi, k1) && valid == 0xFFFFFFFFu;
+#pragma unroll
+                for (int t = 0; t < kNT; ++t) {
+                    float x[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = sc[t][e >> 2][e & 3];
+                    if (!all) {
+                        const uint32_t mine = (seen(argument_again<TileArgs>(), 16 * t, j0) & valid & bits(0, k1 - j0)) >> (4 * g);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) x[e] = mine & (1u << (16 * (e >> 2) + (e & 3))) ? x[e] : kNegInf;
+                    }
+                    float top = x[0];
+#pragma unroll
+                    for (int e = 1; e < 8; ++e) top = fmaxf(top, x[e]);
+                    top = groups_max(top);
+                    top = top == kNegInf ? top : top * scale2;
+                    if (__any(top > m[t] + 8.0f)) {
+                        // The reference moves only when a score passes it by 2^8: sums stay in range.
+                        const float now = fmaxf(m[t], top), up = now == m[t] ? 1.0f : __builtin_amdgcn_exp2f(m[t] - now);
+                        m[t] = now;
+                        l[t] *= up;
+#pragma unroll
+                        for (int b = 0; b < kBlocks; ++b) o[t][b] *= up;
+                    }
+                    const float ref = m[t] == kNegInf ? 0.0f : m[t];
+                    float p[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[e], scale2, -ref));
+                        if (kCodes) {
+                            l[t] += p[e];
+                            p[e] = p[e] == 0.0f ? 0.0f : p[e] * vm[e >> 2][e & 3];
+                        }
+                    }
+                    ph[t] = u32x4{pack2(p[0], p[1]), pack2(p[2], p[3]), pack2(p[4], p[5]), pack2(p[6], p[7])};
+                    if (!kCodes) {
+                        // the sum of the weights as the product will use them
+                        constexpr uint32_t kOnes = 0x3F803F80u;
+                        l[t] = dot2(ph[t].x, kOnes, l[t]);
+                        l[t] = dot2(ph[t].y, kOnes, l[t]);
+                        l[t] = dot2(ph[t].z, kOnes, l[t]);
+                        l[t] = dot2(ph[t].w, kOnes, l[t]);
+                    }
+                }
+#pragma unroll
+                for (int b = 0; b < kBlocks; ++b) {
+                    const char *p = vb + at_v[b & 7] + (b >> 3) * 256;
+                    const u32x2 x = read_tr16(p), y = read_tr16(p + 16 * kRow);
+#pragma unroll
+                    for (int t = 0; t < kNT; ++t) o[t][b] = mfma16(u32x4{x.x, x.y, y.x, y.y}, ph[t], o[t][b]);
+                }
+            }
+            if (!kCodes) {
+                if (more) land();
+                buf ^= 1;
+            }
+            __syncthreads();
+        }
+    }
+
+    finish<F, DT>(argument_again<TileArgs>(), o, m, l, k0, k1);
 }
 
 template <int F, int DT>
 void run(const AttnJob &a, const Split &sp, hipStream_t s) {
     const int tiles = (sp.rows + kTileRows - 1) / kTileRows;
     const int64_t blocks = (int64_t)a.c.n_seq * tiles * sp.n_split * a.c.n_kv;
-    hipLaunchKernelGGL((tile_kernel<F, DT>), dim3((unsigned)blocks), dim3(256), 0, s, a, sp, tiles);
+    hipLaunchKernelGGL((tile_kernel<F, DT>), dim3((unsigned)blocks), dim3(256), 0, s, TileArgs{a, sp, tiles});
 }
 
 template <int F>

@@ -98,6 +98,15 @@ struct Split {
     float2 *ml;
 };
 
+// The kernel's one argument, read from memory again: what only the end of a
+// kernel needs would otherwise hold scalar registers all through its loop.
+template <class T>
+__device__ __forceinline__ T argument_again() {
+    auto p = (const __attribute__((address_space(4))) char *)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    return *(const T *)p;
+}
+
 constexpr int kFewRows = 32;      // most query rows per key/value head of the few-row kernel
 constexpr int kMaxSplit = 64;     // one lane each in the join
 
