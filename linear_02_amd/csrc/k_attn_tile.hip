@@ -13,6 +13,7 @@ namespace wl {
 namespace {
 
 constexpr int kRowsPerWave = 32, kNT = kRowsPerWave / 16;
+constexpr int kAhead = 4;   // operands read ahead of the products
 
 struct TileArgs {
     AttnJob a;
@@ -183,6 +184,7 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(TileArgs x) {
 
     if (k0 < k1) {
         const int32_t *table = a.c.table + (int64_t)s * a.c.max_pages;
+        const char *kpool = static_cast<const char *>(a.c.k), *vpool = static_cast<const char *>(a.c.v);
         const int shift = a.c.page_shift, pmask = (1 << shift) - 1, n_pages = a.c.n_pages;
         const int bytes = d * (kCodes ? 1 : 2);              // of a cache row
         const int64_t head = (int64_t)kvh << shift, pitch = (int64_t)a.c.n_kv << shift;   // rows: of this head in a page, of a page
@@ -220,34 +222,35 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(TileArgs x) {
 #pragma unroll
             for (int b = 0; b < 2; ++b) first[b] = base(j0, b, ok[b]);
             valid_in = (ok[0] ? 0xFFFFu : 0u) | (ok[1] ? 0xFFFF0000u : 0u);
+            int ln = lane;
+            asm volatile("" : "+v"(ln));   // not kept through the loop either
             if (!kCodes) {
                 const bool whole = j0 + 32 <= k1;
+                const char *kp[2], *vp[2];
+#pragma unroll
+                for (int b = 0; b < 2; ++b) kp[b] = kpool + first[b] * bytes, vp[b] = vpool + first[b] * bytes;
+                const uint32_t to = lds_byte(lds_all) + buf * 2 * kSide;
 #pragma unroll
                 for (int i = 0; i < kDma; ++i) {
                     // rows r0 .. of one half; lane: row r0 + dr, piece c
                     const int p0 = (wave * kDma + i) * 64, b = p0 / (16 * kPieces), r0 = p0 / kPieces & 15;
-                    const int dr = lane / kPieces, c = lane % kPieces;
+                    const int dr = ln / kPieces, c = ln % kPieces;
                     const int key = (kDma * 64 / kPieces % 8 == 0 ? i * (64 / kPieces) : r0) + dr;   // r & 7 comes from its low bits
-                    const int ck = min((c ^ (key & 7)) * 16, bytes - 16), cv = min((c ^ ((key & kMaskV) << 1)) * 16, bytes - 16);
-                    const int64_t from = (first[b] + (whole ? r0 : 0)) * bytes;
-                    const int row = whole ? dr * bytes : row_at(j0, b, r0 + dr) * bytes;
-                    lds_dma16(reinterpret_cast<const u32x4 *>(static_cast<const char *>(a.c.k) + from + (row + ck)),
-                              reinterpret_cast<u32x4 *>(lds[buf][0] + p0 * 16));
-                    lds_dma16(reinterpret_cast<const u32x4 *>(static_cast<const char *>(a.c.v) + from + (row + cv)),
-                              reinterpret_cast<u32x4 *>(lds[buf][1] + p0 * 16));
+                    const uint32_t ck = min((c ^ (key & 7)) * 16, bytes - 16), cv = min((c ^ ((key & kMaskV) << 1)) * 16, bytes - 16);
+                    const uint32_t row = whole ? dr * bytes : row_at(j0, b, r0 + dr) * bytes, skip = whole ? r0 * bytes : 0;
+                    load_to_lds(kp[b] + skip, row + ck, to + p0 * 16);
+                    load_to_lds(vp[b] + skip, row + cv, to + kSide + p0 * 16);
                 }
             } else {
 #pragma unroll
                 for (int i = 0; i < kRaw; ++i) {
                     const int p0 = (wave * kRaw + i) * 64, b = p0 / DT;      // 16 rows are DT pieces: a load's rows are of one half
                     if (p0 >= 2 * DT) break;
-                    const int p = p0 + lane, r = p / (DT / 16) & 15, c = min(p % (DT / 16) * 16, bytes - 16);
+                    const int p = p0 + ln, r = p / (DT / 16) & 15, c = min(p % (DT / 16) * 16, bytes - 16);
                     const int64_t from = first[b] * bytes;
-                    const int row = row_at(j0, b, r) * bytes + c;
-                    lds_dma16(reinterpret_cast<const u32x4 *>(static_cast<const char *>(a.c.k) + from + row),
-                              reinterpret_cast<u32x4 *>(raw + p0 * 16));
-                    lds_dma16(reinterpret_cast<const u32x4 *>(static_cast<const char *>(a.c.v) + from + row),
-                              reinterpret_cast<u32x4 *>(raw + 32 * DT + p0 * 16));
+                    const uint32_t row = row_at(j0, b, r) * bytes + c;
+                    load_to_lds(kpool + from, row, lds_byte(raw) + p0 * 16);
+                    load_to_lds(vpool + from, row, lds_byte(raw) + 32 * DT + p0 * 16);
                 }
                 if (wave == 0) {
                     const int r = lane & 31;
@@ -257,7 +260,7 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(TileArgs x) {
             }
         };
         auto land = [&]() {
-            wait_vm<0>();
+            wait_loads();
             if (!kCodes) return;
 #pragma unroll
             for (int i = 0; i < kRaw; ++i) {
@@ -276,14 +279,8 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(TileArgs x) {
             if (wave == 0) lds_scale[lane >> 5][lane & 31] = scale_in;
         };
         // Operand addresses within a buffer.
-        int at_k[2], at_v[8];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) at_k[x] = n * kRow + (((4 * x + g) ^ (n & 7)) << 4);
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-            const int key = 4 * g + (n >> 2);
-            at_v[x] = key * kRow + (((x ^ key) & kMaskV) << 5) + 8 * (n & 3);
-        }
+        const int at_k = n * kRow + ((g ^ (n & 7)) << 4);    // piece 4 k + g: ^ (k << 6)
+        const int key_v = 4 * g + (n >> 2), at_v = key_v * kRow + ((key_v & kMaskV) << 5) + 8 * (n & 3);   // block b: ^ (b << 5)
         look(k0);
         fetch(k0, 0);
         uint32_t valid = valid_in;
@@ -301,7 +298,10 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(TileArgs x) {
             }
             if (kCodes) __syncthreads();
             if (j0 + 31 >= wlo && j0 < whi) {
-                const char *kb = lds[buf][0], *vb = lds[buf][1];
+                // Formed anew in every step: held in registers through the loop, the
+                // places of all operands would leave none to read ahead into.
+                int kb = at_k + buf * 2 * kSide, vb = at_v + buf * 2 * kSide + kSide;
+                asm volatile("" : "+v"(kb), "+v"(vb));
                 f32x4 sc[kNT][2];
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
@@ -309,10 +309,18 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(TileArgs x) {
                     for (int t = 0; t < kNT; ++t) sc[t][b] = f32x4{0, 0, 0, 0};
 #pragma unroll
                     for (int k = 0; k < kSteps; ++k) {
-                        const u32x4 kf = *reinterpret_cast<const u32x4 *>(kb + at_k[k & 1] + (k >> 1) * 128 + b * 16 * kRow);
+                        const u32x4 kf = *reinterpret_cast<const u32x4 *>(lds_all + (kb ^ ((k & 1) << 6)) + (k >> 1) * 128 + b * 16 * kRow);
 #pragma unroll
                         for (int t = 0; t < kNT; ++t) sc[t][b] = mfma16(kf, qf[t][k], sc[t][b]);
                     }
+                }
+                // Operand reads run kAhead ahead of the products: left to itself the
+                // compiler reads each operand right before its use.
+                __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
+#pragma unroll
+                for (int i = 0; i < 2 * kSteps; ++i) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, kNT, 0);
+                    if (i + kAhead < 2 * kSteps) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
                 }
                 f32x4 vm[2];
                 if (kCodes) {
@@ -371,10 +379,16 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(TileArgs x) {
                 }
 #pragma unroll
                 for (int b = 0; b < kBlocks; ++b) {
-                    const char *p = vb + at_v[b & 7] + (b >> 3) * 256;
+                    const char *p = lds_all + (vb ^ ((b & 7) << 5)) + (b >> 3) * 256;
                     const u32x2 x = read_tr16(p), y = read_tr16(p + 16 * kRow);
 #pragma unroll
                     for (int t = 0; t < kNT; ++t) o[t][b] = mfma16(u32x4{x.x, x.y, y.x, y.y}, ph[t], o[t][b]);
+                }
+                __builtin_amdgcn_sched_group_barrier(0x100, 2 * kAhead, 1);
+#pragma unroll
+                for (int i = 0; i < kBlocks; ++i) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, kNT, 1);
+                    if (i + kAhead < kBlocks) __builtin_amdgcn_sched_group_barrier(0x100, 2, 1);
                 }
             }
             if (!kCodes) {

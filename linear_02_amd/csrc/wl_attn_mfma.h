@@ -68,6 +68,18 @@ __device__ __forceinline__ u32x2 read_tr8(const void *lds) {
     return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr8_b64_v2i32((WL_LDS i32x2 *)lds));
 }
 
+// Each lane's 16 bytes at base + off (base the same in all lanes) into LDS byte
+// lds + 16 * lane. It writes no register, so nothing of it can be overwritten while
+// it is on its way; the wave waits with wait_loads before the barrier behind which
+// the bytes are read. Through the builtin the compiler takes such a load for one
+// that may finish out of order with LDS reads, and then drains every read of an
+// operand to 0 instead of counting.
+__device__ __forceinline__ void load_to_lds(const char *base, uint32_t off, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory", "m0");
+}
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ uint32_t lds_byte(const void *p) { return (uint32_t)(uintptr_t)(WL_LDS const char *)p; }
+
 // Bits [a, e) of 32.
 __device__ __forceinline__ uint32_t bits(int a, int e) {
     a = min(max(a, 0), 32), e = min(max(e, 0), 32);
