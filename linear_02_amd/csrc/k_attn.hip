@@ -78,7 +78,6 @@ struct Plan {
     Split sp;
 };
 
-constexpr int kWorkgroups = 512;   // wanted: two per CU
 constexpr int kMinChunk = 256;     // keys
 
 Plan plan_of(const AttnJob &a, bool f32) {

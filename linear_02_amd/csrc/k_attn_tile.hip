@@ -18,7 +18,8 @@ constexpr int kAhead = 4;   // operands read ahead of the products
 struct TileArgs {
     AttnJob a;
     Split sp;
-    int tiles;   // of 128 rows, per sequence and key/value head
+    int tiles;     // of 128 rows, per sequence and key/value head
+    int all_fit;   // whether all workgroups are on the card at once
 };
 
 // Which rows and keys a workgroup works on.
@@ -32,7 +33,11 @@ __device__ __forceinline__ Work work_of(const TileArgs &x) {
     u /= x.a.c.n_kv;
     w.split = u % x.sp.n_split;
     u /= x.sp.n_split;
-    w.tile = x.tiles - 1 - u % x.tiles;   // the longest rows first
+    // Under a causal mask later rows have more keys. The longest first, so that the
+    // short ones fill in; where all are on the card at once, two on a CU, the
+    // second half from the shortest up, so that a long and a short one share a CU.
+    const int i = u % x.tiles, half = (x.tiles + 1) / 2;
+    w.tile = x.all_fit && i >= half ? i - half : x.tiles - 1 - i;
     w.s = u / x.tiles;
     return w;
 }
@@ -117,6 +122,10 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(TileArgs x) {
     constexpr int kRow = 2 * DT, kSide = 32 * kRow;          // LDS bytes of a row, of 32 keys
     constexpr int kPieces = DT / 8;                          // 16-byte pieces of a row
     constexpr int kMaskV = DT >= 128 ? 7 : 3;
+    // LDS place of 16-byte piece c of a row: c ^ f(row), such that the 16 lanes that
+    // one pass of a read serves meet all 64 banks.
+    auto fk = [](int r) { return DT >= 128 ? r & 15 : (r >> 1) & 7; };
+    auto fv = [](int r) { return (r & kMaskV) << 1; };
     // One LDS object: beside a second one the compiler waits for the loads into
     // LDS that are still on their way before every read.
     constexpr int kTail = kCodes ? 3 * kSide : 4 * kSide;
@@ -184,11 +193,14 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(TileArgs x) {
 
     if (k0 < k1) {
         const int32_t *table = a.c.table + (int64_t)s * a.c.max_pages;
-        const char *kpool = static_cast<const char *>(a.c.k), *vpool = static_cast<const char *>(a.c.v);
         const int shift = a.c.page_shift, pmask = (1 << shift) - 1, n_pages = a.c.n_pages;
         const int bytes = d * (kCodes ? 1 : 2);              // of a cache row
         const int64_t head = (int64_t)kvh << shift, pitch = (int64_t)a.c.n_kv << shift;   // rows: of this head in a page, of a page
-        int page[2];                                         // of the keys that are staged next
+        const char *kpool = static_cast<const char *>(a.c.k) + head * bytes;
+        const int64_t to_v = static_cast<const char *>(a.c.v) - static_cast<const char *>(a.c.k), page_bytes = pitch * bytes;
+        // Keys come in halves of 16, each within one page. A wave fetches 8 rows: its half, its first row there.
+        const int half = wave >> 1, row0 = 8 * (wave & 1);
+        int page[2];                                         // of the keys that are fetched next
         // Page numbers come from a register: lane i holds entry first_page + i of the
         // table, read anew every 64 pages. A load per step would have to be waited
         // for behind the step's own loads.
@@ -203,58 +215,61 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(TileArgs x) {
             page[0] = __builtin_amdgcn_readlane(pages, e0 - first_page);
             page[1] = __builtin_amdgcn_readlane(pages, e1 - first_page);
         };
-        // The 16 keys of half b: element row of the first, and whether they have a page.
-        auto base = [&](int j0, int b, bool &ok) {
-            ok = (unsigned)page[b] < (unsigned)n_pages;
-            return (ok ? page[b] : 0) * pitch + head + (min(j0 + 16 * b, last) & pmask & ~15);
-        };
-        // Within a half: rows behind the last key read that key again.
+        auto has_page = [&](int b) { return (unsigned)page[b] < (unsigned)n_pages; };
+        // First of the 16 keys of half b, within its page. Rows behind the last key read that key again.
+        auto off_of = [&](int j0, int b) { return min(j0 + 16 * b, last) & pmask & ~15; };
         auto row_at = [&](int j0, int b, int r) { return min(r, last - min(j0 + 16 * b, last & ~15)); };
-        // bf16: 64 pieces per load, straight into LDS; piece c of row r lies at c ^ f(r).
+        // bf16: 64 pieces per load, straight to their places.
         constexpr int kDma = kPieces * 32 / 256;             // loads per wave and side
         // codes: as they lie, into a patch that the wave which fetched them widens from.
-        constexpr int kRaw = (DT + 127) / 128;               // loads per wave and side: 4 pieces of 64 pieces, DT / 16 per row
+        constexpr int kRaw = (DT + 127) / 128;               // loads per wave and side
         float scale_in = 0.0f;
         uint32_t valid_in = 0;
         auto fetch = [&](int j0, int buf) {
-            int64_t first[2];
-            bool ok[2];
-#pragma unroll
-            for (int b = 0; b < 2; ++b) first[b] = base(j0, b, ok[b]);
-            valid_in = (ok[0] ? 0xFFFFu : 0u) | (ok[1] ? 0xFFFF0000u : 0u);
+            valid_in = (has_page(0) ? 0xFFFFu : 0u) | (has_page(1) ? 0xFFFF0000u : 0u);
+            const int pg = half ? page[1] : page[0];
+            const char *kp = scalar(kpool + ((unsigned)pg < (unsigned)n_pages ? pg : 0) * page_bytes + off_of(j0, half) * bytes);
+            const char *vp = kp + to_v;
+            const bool whole = j0 + 32 <= k1;
             int ln = lane;
-            asm volatile("" : "+v"(ln));   // not kept through the loop either
+            asm volatile("" : "+v"(ln));   // what follows from it is not kept through the loop
             if (!kCodes) {
-                const bool whole = j0 + 32 <= k1;
-                const char *kp[2], *vp[2];
+                constexpr int kStep = 64 / kPieces;          // rows per load
+                const int dr = ln / kPieces, c = ln % kPieces;
+                const uint32_t to = lds_byte(lds_all) + buf * 2 * kSide + wave * 8 * kRow;
+                auto piece = [&](int i, bool v) {
+                    const int r = row0 + i * kStep + dr;
+                    return (uint32_t)min((c ^ (v ? fv(r) : fk(r))) * 16, bytes - 16);
+                };
+                if (whole) {
+                    const uint32_t at = (row0 + dr) * bytes;
 #pragma unroll
-                for (int b = 0; b < 2; ++b) kp[b] = kpool + first[b] * bytes, vp[b] = vpool + first[b] * bytes;
-                const uint32_t to = lds_byte(lds_all) + buf * 2 * kSide;
+                    for (int i = 0; i < kDma; ++i) {
+                        load_to_lds(kp, at + i * kStep * bytes + piece(i, false), to + i * 1024);
+                        load_to_lds(vp, at + i * kStep * bytes + piece(i, true), to + kSide + i * 1024);
+                    }
+                } else {
 #pragma unroll
-                for (int i = 0; i < kDma; ++i) {
-                    // rows r0 .. of one half; lane: row r0 + dr, piece c
-                    const int p0 = (wave * kDma + i) * 64, b = p0 / (16 * kPieces), r0 = p0 / kPieces & 15;
-                    const int dr = ln / kPieces, c = ln % kPieces;
-                    const int key = (kDma * 64 / kPieces % 8 == 0 ? i * (64 / kPieces) : r0) + dr;   // r & 7 comes from its low bits
-                    const uint32_t ck = min((c ^ (key & 7)) * 16, bytes - 16), cv = min((c ^ ((key & kMaskV) << 1)) * 16, bytes - 16);
-                    const uint32_t row = whole ? dr * bytes : row_at(j0, b, r0 + dr) * bytes, skip = whole ? r0 * bytes : 0;
-                    load_to_lds(kp[b] + skip, row + ck, to + p0 * 16);
-                    load_to_lds(vp[b] + skip, row + cv, to + kSide + p0 * 16);
+                    for (int i = 0; i < kDma; ++i) {
+                        const uint32_t at = row_at(j0, half, row0 + i * kStep + dr) * bytes;
+                        load_to_lds(kp, at + piece(i, false), to + i * 1024);
+                        load_to_lds(vp, at + piece(i, true), to + kSide + i * 1024);
+                    }
                 }
             } else {
+                // 8 rows of DT / 16 pieces
+                constexpr int kCodePieces = DT / 16;
 #pragma unroll
                 for (int i = 0; i < kRaw; ++i) {
-                    const int p0 = (wave * kRaw + i) * 64, b = p0 / DT;      // 16 rows are DT pieces: a load's rows are of one half
-                    if (p0 >= 2 * DT) break;
-                    const int p = p0 + ln, r = p / (DT / 16) & 15, c = min(p % (DT / 16) * 16, bytes - 16);
-                    const int64_t from = first[b] * bytes;
-                    const uint32_t row = row_at(j0, b, r) * bytes + c;
-                    load_to_lds(kpool + from, row, lds_byte(raw) + p0 * 16);
-                    load_to_lds(vpool + from, row, lds_byte(raw) + 32 * DT + p0 * 16);
+                    const int p = i * 64 + ln, c = min(p % kCodePieces * 16, bytes - 16);
+                    if (DT == 64 && ln >= 32) break;
+                    const uint32_t at = row_at(j0, half, row0 + p / kCodePieces) * bytes + c;
+                    load_to_lds(kp, at, lds_byte(raw) + (wave * 8 * kCodePieces + i * 64) * 16);
+                    load_to_lds(vp, at, lds_byte(raw) + 32 * DT + (wave * 8 * kCodePieces + i * 64) * 16);
                 }
                 if (wave == 0) {
-                    const int r = lane & 31;
-                    const int64_t from = first[r >> 4] + row_at(j0, r >> 4, r & 15);
+                    const int r = lane & 31, b = r >> 4, pg2 = b ? page[1] : page[0];
+                    const int64_t from = ((unsigned)pg2 < (unsigned)n_pages ? pg2 : 0) * pitch + head + off_of(j0, b) + row_at(j0, b, r & 15);
                     scale_in = (lane < 32 ? a.c.k_scale : a.c.v_scale)[from];
                 }
             }
@@ -262,24 +277,24 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(TileArgs x) {
         auto land = [&]() {
             wait_loads();
             if (!kCodes) return;
+            constexpr int kCodePieces = DT / 16;
 #pragma unroll
             for (int i = 0; i < kRaw; ++i) {
-                const int p0 = (wave * kRaw + i) * 64;
-                if (p0 >= 2 * DT) break;
-                const int p = p0 + lane, r = p / (DT / 16), c = p % (DT / 16) * 2;
+                if (DT == 64 && lane >= 32) break;
+                const int p = wave * 8 * kCodePieces + i * 64 + lane, r = p / kCodePieces, c = p % kCodePieces * 2;
                 const u32x4 k = *reinterpret_cast<const u32x4 *>(raw + p * 16), v = *reinterpret_cast<const u32x4 *>(raw + 32 * DT + p * 16);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    *reinterpret_cast<u32x4 *>(lds[0][0] + r * kRow + ((c + e) ^ (r & 7)) * 16) =
+                    *reinterpret_cast<u32x4 *>(lds[0][0] + r * kRow + ((c + e) ^ fk(r)) * 16) =
                         e ? widen8<F>(k.z, k.w) : widen8<F>(k.x, k.y);
-                    *reinterpret_cast<u32x4 *>(lds[0][1] + r * kRow + ((c + e) ^ ((r & kMaskV) << 1)) * 16) =
+                    *reinterpret_cast<u32x4 *>(lds[0][1] + r * kRow + ((c + e) ^ fv(r)) * 16) =
                         e ? widen8<F>(v.z, v.w) : widen8<F>(v.x, v.y);
                 }
             }
             if (wave == 0) lds_scale[lane >> 5][lane & 31] = scale_in;
         };
         // Operand addresses within a buffer.
-        const int at_k = n * kRow + ((g ^ (n & 7)) << 4);    // piece 4 k + g: ^ (k << 6)
+        const int at_k = n * kRow + ((g ^ fk(n)) << 4);      // piece 4 k + g: ^ (k << 6)
         const int key_v = 4 * g + (n >> 2), at_v = key_v * kRow + ((key_v & kMaskV) << 5) + 8 * (n & 3);   // block b: ^ (b << 5)
         look(k0);
         fetch(k0, 0);
@@ -309,7 +324,7 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(TileArgs x) {
                     for (int t = 0; t < kNT; ++t) sc[t][b] = f32x4{0, 0, 0, 0};
 #pragma unroll
                     for (int k = 0; k < kSteps; ++k) {
-                        const u32x4 kf = *reinterpret_cast<const u32x4 *>(lds_all + (kb ^ ((k & 1) << 6)) + (k >> 1) * 128 + b * 16 * kRow);
+                        const u32x4 kf = *reinterpret_cast<const u32x4 *>(lds_all + (kb ^ ((k & 3) << 6)) + (k >> 2) * 256 + b * 16 * kRow);
 #pragma unroll
                         for (int t = 0; t < kNT; ++t) sc[t][b] = mfma16(kf, qf[t][k], sc[t][b]);
                     }
@@ -406,7 +421,7 @@ template <int F, int DT>
 void run(const AttnJob &a, const Split &sp, hipStream_t s) {
     const int tiles = (sp.rows + kTileRows - 1) / kTileRows;
     const int64_t blocks = (int64_t)a.c.n_seq * tiles * sp.n_split * a.c.n_kv;
-    hipLaunchKernelGGL((tile_kernel<F, DT>), dim3((unsigned)blocks), dim3(256), 0, s, TileArgs{a, sp, tiles});
+    hipLaunchKernelGGL((tile_kernel<F, DT>), dim3((unsigned)blocks), dim3(256), 0, s, TileArgs{a, sp, tiles, blocks <= kWorkgroups});
 }
 
 template <int F>

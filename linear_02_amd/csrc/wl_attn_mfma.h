@@ -75,7 +75,13 @@ __device__ __forceinline__ u32x2 read_tr8(const void *lds) {
 // that may finish out of order with LDS reads, and then drains every read of an
 // operand to 0 instead of counting.
 __device__ __forceinline__ void load_to_lds(const char *base, uint32_t off, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory");
+}
+// A pointer that is the same in all lanes, in scalar registers.
+__device__ __forceinline__ const char *scalar(const char *p) {
+    const uint64_t v = (uint64_t)(uintptr_t)p;
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+    return (const char *)(uintptr_t)((uint64_t)hi << 32 | lo);
 }
 __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 __device__ __forceinline__ uint32_t lds_byte(const void *p) { return (uint32_t)(uintptr_t)(WL_LDS const char *)p; }
@@ -119,6 +125,7 @@ __device__ __forceinline__ T argument_again() {
     return *(const T *)p;
 }
 
+constexpr int kWorkgroups = 512;   // wanted: two per CU
 constexpr int kFewRows = 32;      // most query rows per key/value head of the few-row kernel
 constexpr int kMaxSplit = 64;     // one lane each in the join
 
