@@ -129,11 +129,11 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(TileArgs x) {
     // One LDS object: beside a second one the compiler waits for the loads into
     // LDS that are still on their way before every read.
     constexpr int kTail = kCodes ? 3 * kSide : 4 * kSide;
-    __shared__ __align__(16) char lds_all[kTail + 256 + 32];
+    __shared__ __align__(16) char lds_all[kTail + 512 + 32];
     char (*lds)[2][kSide] = reinterpret_cast<char (*)[2][kSide]>(lds_all);   // [buffer][K, V]; one buffer for codes
     char *raw = lds_all + 2 * kSide;                                         // codes as fetched: K, then V
-    float (*lds_scale)[32] = reinterpret_cast<float (*)[32]>(lds_all + kTail);   // [K, V]
-    int (*range)[4] = reinterpret_cast<int (*)[4]>(lds_all + kTail + 256);
+    float (*lds_scale)[2][32] = reinterpret_cast<float (*)[2][32]>(lds_all + kTail);   // [buffer][K, V]
+    int (*range)[4] = reinterpret_cast<int (*)[4]>(lds_all + kTail + 512);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
     const Work work = work_of(x);
@@ -223,7 +223,6 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(TileArgs x) {
         constexpr int kDma = kPieces * 32 / 256;             // loads per wave and side
         // codes: as they lie, into a patch that the wave which fetched them widens from.
         constexpr int kRaw = (DT + 127) / 128;               // loads per wave and side
-        float scale_in = 0.0f;
         uint32_t valid_in = 0;
         auto fetch = [&](int j0, int buf) {
             valid_in = (has_page(0) ? 0xFFFFu : 0u) | (has_page(1) ? 0xFFFF0000u : 0u);
@@ -267,11 +266,11 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(TileArgs x) {
                     load_to_lds(kp, at, lds_byte(raw) + (wave * 8 * kCodePieces + i * 64) * 16);
                     load_to_lds(vp, at, lds_byte(raw) + 32 * DT + (wave * 8 * kCodePieces + i * 64) * 16);
                 }
-                if (wave == 0) {
-                    const int r = lane & 31, b = r >> 4, pg2 = b ? page[1] : page[0];
-                    const int64_t from = ((unsigned)pg2 < (unsigned)n_pages ? pg2 : 0) * pitch + head + off_of(j0, b) + row_at(j0, b, r & 15);
-                    scale_in = (lane < 32 ? a.c.k_scale : a.c.v_scale)[from];
-                }
+                // 16 scales of K or V each
+                const char *scales = reinterpret_cast<const char *>(wave & 1 ? a.c.v_scale : a.c.k_scale);
+                const int64_t from = ((unsigned)pg < (unsigned)n_pages ? pg : 0) * pitch + head + off_of(j0, half);
+                if (ln < 16)
+                    load_to_lds4(scalar(scales + from * 4), row_at(j0, half, ln) * 4, lds_byte(lds_scale[buf][wave & 1] + 16 * half));
             }
         };
         auto land = [&]() {
@@ -291,7 +290,6 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(TileArgs x) {
                         e ? widen8<F>(v.z, v.w) : widen8<F>(v.x, v.y);
                 }
             }
-            if (wave == 0) lds_scale[lane >> 5][lane & 31] = scale_in;
         };
         // Operand addresses within a buffer.
         const int at_k = n * kRow + ((g ^ fk(n)) << 4);      // piece 4 k + g: ^ (k << 6)
@@ -315,7 +313,7 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(TileArgs x) {
             if (j0 + 31 >= wlo && j0 < whi) {
                 // Formed anew in every step: held in registers through the loop, the
                 // places of all operands would leave none to read ahead into.
-                int kb = at_k + buf * 2 * kSide, vb = at_v + buf * 2 * kSide + kSide;
+                int kb = at_k + (kCodes ? 0 : buf * 2 * kSide), vb = at_v + (kCodes ? 0 : buf * 2 * kSide) + kSide;
                 asm volatile("" : "+v"(kb), "+v"(vb));
                 f32x4 sc[kNT][2];
 #pragma unroll
@@ -337,12 +335,10 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(TileArgs x) {
                     __builtin_amdgcn_sched_group_barrier(0x008, kNT, 0);
                     if (i + kAhead < 2 * kSteps) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
                 }
-                f32x4 vm[2];
                 if (kCodes) {
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
-                        const f32x4 ks = *reinterpret_cast<const f32x4 *>(&lds_scale[0][16 * b + 4 * g]);
-                        vm[b] = *reinterpret_cast<const f32x4 *>(&lds_scale[1][16 * b + 4 * g]);
+                        const f32x4 ks = *reinterpret_cast<const f32x4 *>(&lds_scale[buf][0][16 * b + 4 * g]);
 #pragma unroll
                         for (int t = 0; t < kNT; ++t) sc[t][b] *= ks;
                     }
@@ -374,6 +370,11 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(TileArgs x) {
                     }
                     const float ref = m[t] == kNegInf ? 0.0f : m[t];
                     float p[8];
+                    f32x4 vm[2];
+                    if (kCodes) {
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) vm[b] = *reinterpret_cast<const f32x4 *>(&lds_scale[buf][1][16 * b + 4 * g]);
+                    }
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[e], scale2, -ref));
@@ -406,10 +407,8 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(TileArgs x) {
                     if (i + kAhead < kBlocks) __builtin_amdgcn_sched_group_barrier(0x100, 2, 1);
                 }
             }
-            if (!kCodes) {
-                if (more) land();
-                buf ^= 1;
-            }
+            if (!kCodes && more) land();
+            buf ^= 1;
             __syncthreads();
         }
     }

@@ -77,6 +77,10 @@ __device__ __forceinline__ u32x2 read_tr8(const void *lds) {
 __device__ __forceinline__ void load_to_lds(const char *base, uint32_t off, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory");
 }
+// The same with 4 bytes per lane.
+__device__ __forceinline__ void load_to_lds4(const char *base, uint32_t off, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory");
+}
 // A pointer that is the same in all lanes, in scalar registers.
 __device__ __forceinline__ const char *scalar(const char *p) {
     const uint64_t v = (uint64_t)(uintptr_t)p;
