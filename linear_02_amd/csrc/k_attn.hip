@@ -6,37 +6,6 @@ namespace wl {
 
 namespace {
 
-// A wave per query row and head.
-template <class E, int F>
-__global__ __launch_bounds__(256) void attn_rows_kernel(AttnJob a) {
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const int64_t unit = (int64_t)blockIdx.x * 4 + wave;
-    const int t = (int)(unit / a.n_q), h = (int)(unit % a.n_q);
-    if (t >= a.T) return;
-    int s = -1;
-    for (int c = 0; c < a.c.n_seq; ++c)
-        if (t >= a.q_start[c] && t < a.q_start[c + 1]) {
-            s = c;
-            break;
-        }
-    if (s < 0) return;
-    const Seq q = seq_of(a, s);
-    const int i = t - q.q0;
-    if (i >= q.rows) return;
-    float acc[4], m, l;
-    one_row<E, F>(a, q, i, h, 0, q.kv, acc, m, l);
-    if (4 * lane >= a.c.d) return;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc[e] = l == 0.0f ? 0.0f : acc[e] / l;
-    put4(static_cast<E *>(a.o) + (size_t)t * a.ldo + (size_t)h * a.c.d + 4 * lane, acc);
-}
-
-template <class E, int F>
-void run_rows(const AttnJob &a, hipStream_t s) {
-    const int64_t units = (int64_t)a.T * a.n_q;
-    hipLaunchKernelGGL((attn_rows_kernel<E, F>), dim3((unsigned)((units + 3) / 4)), dim3(256), 0, s, a);
-}
-
 // Joins the parts of every row: a wave per row, lane p weighs part p.
 template <class E>
 __global__ __launch_bounds__(256) void join_kernel(AttnJob a, Split sp) {
@@ -71,7 +40,7 @@ __global__ __launch_bounds__(256) void join_kernel(AttnJob a, Split sp) {
     put4(static_cast<E *>(a.o) + (size_t)(q.q0 + i) * a.ldo + (size_t)(kvh * a.group + r - i * a.group) * a.c.d + at, e);
 }
 
-enum Kind { kRows, kFew, kTile };
+enum Kind { kFew, kTile, kF32 };
 
 struct Plan {
     Kind kind;
@@ -83,14 +52,15 @@ constexpr int kMinChunk = 256;     // keys
 Plan plan_of(const AttnJob &a, bool f32) {
     Plan p{};
     p.sp.n_split = 1;
-    p.kind = f32 ? kRows : (int64_t)a.max_q * a.group > kFewRows ? kTile : kFew;
-    if (p.kind == kRows) return p;
+    p.kind = f32 ? kF32 : (int64_t)a.max_q * a.group > kFewRows ? kTile : kFew;
     p.sp.rows = a.max_q * a.group;
     // Most keys that the queries of one sequence see between them; pieces start at a multiple of 32.
     int64_t span = a.max_kv;
     if (a.mask == kMaskCausal && a.window && (int64_t)a.window + a.max_q < span) span = (int64_t)a.window + a.max_q;
     span += 31;
-    const int64_t units = (int64_t)a.c.n_seq * a.c.n_kv * (p.kind == kTile ? (p.sp.rows + kTileRows - 1) / kTileRows : 1);
+    const int64_t units = (int64_t)a.c.n_seq * a.c.n_kv * (p.kind == kTile  ? (p.sp.rows + kTileRows - 1) / kTileRows
+                                                          : p.kind == kF32 ? (p.sp.rows + kF32Rows - 1) / kF32Rows
+                                                                           : 1);
     int64_t chunk = (span * units + kWorkgroups - 1) / kWorkgroups;
     if (chunk < kMinChunk) chunk = kMinChunk;
     if (chunk < (span + kMaxSplit - 1) / kMaxSplit) chunk = (span + kMaxSplit - 1) / kMaxSplit;
@@ -113,24 +83,22 @@ size_t attention_scratch(const AttnJob &a, int fmt, bool f32) {
 
 hipError_t launch_attention(const AttnJob &a, int fmt, bool f32, void *ws, hipStream_t s) {
     Plan p = plan_of(a, f32);
-    if (p.kind != kRows) {
-        if (p.sp.n_split > 1) {
-            p.sp.part = static_cast<float *>(ws);
-            p.sp.ml = reinterpret_cast<float2 *>(p.sp.part + part_floats(a, p.sp) * a.c.d);
-        }
-        p.kind == kFew ? launch_few(a, fmt, p.sp, s) : launch_tile(a, fmt, p.sp, s);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess || p.sp.n_split == 1) return e;
-        const int64_t waves = (int64_t)a.c.n_seq * a.c.n_kv * p.sp.rows;
-        hipLaunchKernelGGL((join_kernel<uint16_t>), dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, s, a, p.sp);
-        return hipGetLastError();
+    if (p.sp.n_split > 1) {
+        p.sp.part = static_cast<float *>(ws);
+        p.sp.ml = reinterpret_cast<float2 *>(p.sp.part + part_floats(a, p.sp) * a.c.d);
     }
-    switch (fmt) {
-        case kFmtBf16: run_rows<uint16_t, kFmtBf16>(a, s); break;
-        case kFmtF32: run_rows<float, kFmtF32>(a, s); break;
-        case kFmtInt8: f32 ? run_rows<float, kFmtInt8>(a, s) : run_rows<uint16_t, kFmtInt8>(a, s); break;
-        default: f32 ? run_rows<float, kFmtE4m3>(a, s) : run_rows<uint16_t, kFmtE4m3>(a, s);
+    switch (p.kind) {
+        case kFew: launch_few(a, fmt, p.sp, s); break;
+        case kTile: launch_tile(a, fmt, p.sp, s); break;
+        default: launch_f32(a, fmt, p.sp, s);
     }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || p.sp.n_split == 1) return e;
+    const dim3 grid((unsigned)(((int64_t)a.c.n_seq * a.c.n_kv * p.sp.rows + 3) / 4));
+    if (f32)
+        hipLaunchKernelGGL((join_kernel<float>), grid, dim3(256), 0, s, a, p.sp);
+    else
+        hipLaunchKernelGGL((join_kernel<uint16_t>), grid, dim3(256), 0, s, a, p.sp);
     return hipGetLastError();
 }
 

@@ -134,8 +134,112 @@ constexpr int kFewRows = 32;      // most query rows per key/value head of the f
 constexpr int kMaxSplit = 64;     // one lane each in the join
 
 constexpr int kTileRows = 128;    // query rows per workgroup of the many-row kernel
+constexpr int kF32Rows = 64;      // of the fp32 kernel
 
 void launch_few(const AttnJob &a, int fmt, const Split &sp, hipStream_t s);
 void launch_tile(const AttnJob &a, int fmt, const Split &sp, hipStream_t s);
+void launch_f32(const AttnJob &a, int fmt, const Split &sp, hipStream_t s);
+
+// ---- kernels whose workgroups of four waves take tiles of 64 NT query rows -------
+
+struct TileArgs {
+    AttnJob a;
+    Split sp;
+    int tiles;     // of rows, per sequence and key/value head
+    int all_fit;   // whether all workgroups are on the card at once
+};
+
+// Which rows and keys a workgroup works on.
+struct Work {
+    int kvh, split, tile, s;
+};
+__device__ __forceinline__ Work work_of(const TileArgs &x) {
+    Work w;
+    int u = blockIdx.x;
+    w.kvh = u % x.a.c.n_kv;
+    u /= x.a.c.n_kv;
+    w.split = u % x.sp.n_split;
+    u /= x.sp.n_split;
+    // Under a causal mask later rows have more keys. The longest first, so that the
+    // short ones fill in; where all are on the card at once, two on a CU, the
+    // second half from the shortest up, so that a long and a short one share a CU.
+    const int i = u % x.tiles, half = (x.tiles + 1) / 2;
+    w.tile = x.all_fit && i >= half ? i - half : x.tiles - 1 - i;
+    w.s = u / x.tiles;
+    return w;
+}
+
+// Which of keys j0 .. j0 + 31 this lane's row of tile `first` (0 or 16) sees. Only
+// at the edges of what the wave's rows see, so from the arguments in memory.
+template <int NT>
+__device__ __forceinline__ uint32_t seen(const TileArgs &x, int first, int j0) {
+    const Work work = work_of(x);
+    const Seq q = seq_of(x.a, work.s);
+    const int r = (work.tile * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * 16 * NT + first + (threadIdx.x & 15);
+    return visible32(x.a, q, sees(x.a, q, r / x.a.group), j0);
+}
+
+// Writes a wave's outputs: lane (n, g) holds elements 16 b + 4 g .. + 3 of row n.
+template <class E, int F, int DT, int NT>
+__device__ __forceinline__ void finish(const TileArgs &x, f32x4 (&o)[NT][DT / 16], float (&m)[NT], float (&l)[NT], int k0, int k1) {
+    constexpr int kBlocks = DT / 16;
+    const AttnJob &a = x.a;
+    const Split &sp = x.sp;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15, g = lane >> 4;
+    const Work work = work_of(x);
+    const int kvh = work.kvh, split = work.split, tile = work.tile, s = work.s;
+    const Seq q = seq_of(a, s);
+    const int rows = q.rows * a.group, d = a.c.d, r0 = (tile * 4 + wave) * 16 * NT;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const int r = r0 + 16 * t + n;
+        l[t] = groups_sum(l[t]);
+        float check = l[t] * 0.0f;
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b)
+            if (16 * b < d) check += o[t][b].x * 0.0f + o[t][b].y * 0.0f + o[t][b].z * 0.0f + o[t][b].w * 0.0f;
+        // A row with an infinity or a NaN is done again key by key: one that it does
+        // not see may have got in as 0 * NaN.
+        uint64_t odd = __ballot(r < rows && check != 0.0f);
+        odd |= odd >> 32;
+        odd |= odd >> 16;
+        const uint32_t again = (uint32_t)odd & 0xFFFFu;
+        const int64_t part = ((int64_t)(s * (int64_t)a.c.n_kv + kvh) * sp.n_split + split) * sp.rows;
+        auto row_out = [&](int r) {
+            const int i = r / a.group;
+            return static_cast<E *>(a.o) + (size_t)(q.q0 + i) * a.ldo + (size_t)(kvh * a.group + r - i * a.group) * d;
+        };
+        if (r < rows && !(again >> n & 1u)) {
+            const float inv = l[t] == 0.0f ? 0.0f : 1.0f / l[t];
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b) {
+                const int at = 16 * b + 4 * g;
+                if (at >= d) break;
+                if (sp.n_split > 1) {
+                    *reinterpret_cast<f32x4 *>(sp.part + (part + r) * d + at) = o[t][b];
+                } else {
+                    const float v[4] = {o[t][b].x * inv, o[t][b].y * inv, o[t][b].z * inv, o[t][b].w * inv};
+                    put4(row_out(r) + at, v);
+                }
+            }
+            if (sp.n_split > 1 && g == 0) sp.ml[part + r] = make_float2(m[t], l[t]);
+        }
+        for (uint32_t left = again; left; left &= left - 1) {
+            const int rr = r0 + 16 * t + __ffs(left) - 1, ii = rr / a.group;
+            float acc[4], mm, ll;
+            one_row<E, F>(a, q, ii, kvh * a.group + rr - ii * a.group, k0, k1, acc, mm, ll);
+            if (4 * lane < d) {
+                if (sp.n_split > 1) {
+                    *reinterpret_cast<f32x4 *>(sp.part + (part + rr) * d + 4 * lane) = f32x4{acc[0], acc[1], acc[2], acc[3]};
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[e] = ll == 0.0f ? 0.0f : acc[e] / ll;
+                    put4(row_out(rr) + 4 * lane, acc);
+                }
+            }
+            if (sp.n_split > 1 && lane == 0) sp.ml[part + rr] = make_float2(mm, ll);
+        }
+    }
+}
 
 }  // namespace wl
