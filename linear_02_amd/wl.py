@@ -166,8 +166,17 @@ def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
 
 
+# The handle of a device's current stream, without building a Stream object.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _index(device: torch.device) -> int:
+    return device.index if device.index is not None else torch.cuda.current_device()
+
+
 def _stream(device: torch.device):
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    return ctypes.c_void_p(_raw_stream(_index(device)))
 
 
 def theta_to(th: dict, device) -> dict:
@@ -228,7 +237,7 @@ class Workspace:
     def get(self, device: torch.device, nbytes: int) -> torch.Tensor | None:
         if nbytes == 0:
             return None
-        key = (device.index, torch.cuda.current_stream(device).cuda_stream)
+        key = (device.index, _raw_stream(_index(device)))
         buf = self._bufs.get(key)
         if buf is None or buf.numel() < nbytes:
             buf = new_workspace(max(nbytes, 1 << 20), device)
@@ -463,34 +472,42 @@ class OpCall:
         return self._launch()
 
     def _launch(self):
+        stream = _raw_stream(self.device.index)
         if self.op != OP_ATTENTION:
-            _check(self.fn(self.args, _stream(self.device)))
-            return self.out
-        need = int(lib.wl_attention_workspace_bytes(self.args))
-        ws = self.ws if self.ws is not None else WORKSPACE.get(self.device, need)
-        _check(self.fn(self.args, _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _stream(self.device)))
+            status = self.fn(self.args, stream)
+        else:
+            need = lib.wl_attention_workspace_bytes(self.args)
+            ws = self.ws if self.ws is not None else WORKSPACE.get(self.device, need) if need else None
+            status = self.fn(self.args, _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), stream)
+        if status:
+            _check(status)
         return self.out
 
 
 def _tensor(t, name: str, like: torch.Tensor, dtype=None) -> None:
-    if t.device != like.device or not t.is_cuda:
+    if t.get_device() != like.get_device() or not t.is_cuda:
         raise ValueError(f"{name} must be on the device of the call's first tensor ({like.device})")
-    if t.dtype != (dtype or like.dtype):
+    if t.dtype is not (dtype or like.dtype):
         raise ValueError(f"{name} must be {dtype or like.dtype}")
 
 
 def _matrix(t, name: str, like: torch.Tensor, T: int, width: int) -> int:
     """Row stride of a [T][width] tensor whose rows are contiguous."""
-    _tensor(t, name, like)
-    if t.dim() != 2 or t.shape[0] != T or t.shape[1] != width or (width > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be [{T}][{width}] with contiguous rows")
-    return t.stride(0) if T > 1 else width
+    if t is not like:
+        _tensor(t, name, like)
+    if t.shape != (T, width):
+        raise ValueError(f"{name} must be [{T}][{width}]")
+    ld, one = t.stride()
+    if one != 1 and width > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return ld if T > 1 else width
 
 
 def _vector(t, name: str, like: torch.Tensor, n: int, dtype=None):
     if t is None:
         return None
-    _tensor(t, name, like, dtype)
+    if t.dtype is not (dtype or like.dtype) or t.get_device() != like.get_device():
+        _tensor(t, name, like, dtype)
     if t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous with {n} elements")
     return t.data_ptr()
@@ -509,7 +526,7 @@ def norm_call(x, y=None, post=None, pre=None, gate=None, eps: float = 1e-6, offs
     leave that output out (None)."""
     T, d = _first(x, "x").shape
     for name, t in (("x", x), ("y", y), ("x_out", x_out), ("n_out", n_out)):
-        if t is not None and (_matrix(t, name, x, T, d) != d or not t.is_contiguous()):
+        if t is not None and _matrix(t, name, x, T, d) != d:
             raise ValueError(f"{name} must be contiguous")
     gate_ld = 0
     if gate is not None:
@@ -582,7 +599,7 @@ def rope_call(q, k, pos, rope: Rope | None, d: int, q_norm=None, k_norm=None, ep
         n[i] = _heads(t, name, d)
         ld[i] = _matrix(t, name, first, T, n[i] * d)
         if outs[i] is None:
-            outs[i] = torch.empty(T, n[i] * d, dtype=t.dtype, device=t.device)
+            outs[i] = t.new_empty((T, n[i] * d))
         ldo[i] = _matrix(outs[i], name + "_out", first, T, n[i] * d)
     rot = None if rope is None else rope.struct(pos, T, first)
     args = RopeArgs(_ptr(q), _ptr(k), _vector(q_norm, "q_norm", first, d), _vector(k_norm, "k_norm", first, d),
@@ -647,7 +664,7 @@ def cache_write_call(cache: Cache, k, v, seq, slot, q=None, rope: Rope | None = 
         n_q = _heads(q, "q", c.d)
         ldq = _matrix(q, "q", k, T, n_q * c.d)
         if q_out is None:
-            q_out = torch.empty(T, n_q * c.d, dtype=q.dtype, device=q.device)
+            q_out = q.new_empty((T, n_q * c.d))
         ldo = _matrix(q_out, "q_out", k, T, n_q * c.d)
     rot = None if rope is None else rope.struct(pos, T, k)
     args = CacheWriteArgs(_at(c), k.data_ptr(), v.data_ptr(), _ptr(q), _vector(q_norm, "q_norm", k, c.d),
@@ -671,8 +688,7 @@ def cache_read_call(cache: Cache, seq, slot, dtype: torch.dtype | None = None, k
     c, T = cache.struct, seq.numel()
     if dtype is None:
         dtype = torch.float32 if cache.k.dtype == torch.float32 else torch.bfloat16
-    outs = [t if t is not None else torch.empty(T, c.n_kv * c.d, dtype=dtype, device=cache.k.device)
-            for t in (k_out, v_out)]
+    outs = [t if t is not None else cache.k.new_empty((T, c.n_kv * c.d), dtype=dtype) for t in (k_out, v_out)]
     first = _first(outs[0], "k_out")
     _tensor(first, "k_out", cache.k, dtype)
     args = CacheReadArgs(_at(c), _vector(seq, "seq", first, T, torch.int32), _vector(slot, "slot", first, T, torch.int32),
@@ -695,7 +711,7 @@ def attention_call(q, cache: Cache, q_start, kv_len, max_q: int, max_kv: int, sc
     n_q = _heads(q, "q", c.d)
     _tensor(cache.k, "the cache", q, cache.k.dtype)
     if o is None:
-        o = torch.empty(T, n_q * c.d, dtype=q.dtype, device=q.device)
+        o = q.new_empty((T, n_q * c.d))
     mask = mask or ("causal" if tree is None else "tree")
     if mask not in MASKS:
         raise ValueError(f"mask {mask!r} is not one of {sorted(MASKS)}")
