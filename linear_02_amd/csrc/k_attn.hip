@@ -47,7 +47,7 @@ struct Plan {
     Split sp;
 };
 
-constexpr int kMinChunk = 256;     // keys
+constexpr int kMinChunk = 128;     // keys: 32 for each of four waves
 
 Plan plan_of(const AttnJob &a, bool f32) {
     Plan p{};

@@ -36,228 +36,40 @@ struct Few {
     float m[NT], l[NT];
 };
 
-// Global addresses of 32 keys' rows for one lane, in two halves of 16 keys.
-struct KeyRows {
-    int64_t row[2];     // this lane's key (lane & 15)
-    int64_t first[2];   // the half's first key
-    uint32_t valid;     // bits of the keys that have a page
+struct FewArgs {
+    AttnJob a;
+    Split sp;
 };
 
-__device__ __forceinline__ KeyRows key_rows(const AttnJob &a, int s, int kvh, int j0, int last) {
-    KeyRows k;
-    k.valid = 0;
-    const int mask = (1 << a.c.page_shift) - 1;
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-        // Past the last key the last one is read again, so no load leaves the pages.
-        const int first = __builtin_amdgcn_readfirstlane(min(j0 + 16 * b, last));
-        const int mine = min(j0 + 16 * b + (int)(threadIdx.x & 15), last);
-        int page = a.c.table[(int64_t)s * a.c.max_pages + (first >> a.c.page_shift)];
-        const bool ok = (unsigned)page < (unsigned)a.c.n_pages;
-        if (ok) k.valid |= 0xFFFFu << (16 * b);
-        const int64_t at = ((int64_t)(ok ? page : 0) * a.c.n_kv + kvh) << a.c.page_shift;
-        k.row[b] = at + (mine & mask);
-        k.first[b] = at + (first & mask & ~15);
-    }
-    return k;
+// Which keys a workgroup works on.
+struct FewWork {
+    int kvh, split, s;
+};
+__device__ __forceinline__ FewWork work_of(const FewArgs &x) {
+    const int u = blockIdx.x / x.a.c.n_kv;
+    return {(int)blockIdx.x % x.a.c.n_kv, u % x.sp.n_split, u / x.sp.n_split};
 }
 
+// Which of keys j0 .. j0 + 31 this lane's row of tile t sees, for trees: from the
+// arguments in memory, at the few steps that reach the tree.
+__device__ __forceinline__ uint32_t few_seen(const FewArgs &x, int t, int j0) {
+    const Seq q = seq_of(x.a, work_of(x).s);
+    return visible32(x.a, q, sees(x.a, q, (16 * t + (threadIdx.x & 15)) / x.a.group), j0);
+}
+
+// Joins the four waves' outputs, 16 rows at a time: row n of a wave's patch holds
+// what it has of row n.
 template <int F, int DT, int NT>
-__global__ __launch_bounds__(256, (Few<F, DT, NT>::kPerCu)) void few_kernel(AttnJob a, Split sp) {
+__device__ __forceinline__ void join_waves(const FewArgs &args, const Seq &q, Few<F, DT, NT> &st, char *lds, int k0, int k1) {
     typedef Few<F, DT, NT> P;
-    constexpr bool kCodes = P::kCodes;
-    __shared__ __align__(16) char lds[kWaves * P::kPatch];
+    const AttnJob &a = args.a;
+    const Split &sp = args.sp;
     __shared__ float2 ml[kWaves][16];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int n = lane & 15, g = lane >> 4;
-    int u = blockIdx.x;
-    const int kvh = u % a.c.n_kv;
-    u /= a.c.n_kv;
-    const int split = u % sp.n_split, s = u / sp.n_split;
-    const Seq q = seq_of(a, s);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15, g = lane >> 4;
+    const FewWork work = work_of(args);
+    const int kvh = work.kvh, split = work.split, s = work.s;
     const int rows = q.rows * a.group, d = a.c.d;
-    if (rows == 0) return;
-
-    // Query rows of this lane's columns, and what they see.
-    P st;
-    Sees see[NT];
-    int lo = 0x7FFFFFFF, hi = 0;
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        const int r = 16 * t + n, i = r / a.group;
-        const bool on = r < rows;
-        const uint16_t *qp = static_cast<const uint16_t *>(a.q) + (size_t)(q.q0 + (on ? i : 0)) * a.ldq +
-                             (size_t)(kvh * a.group + (on ? r - i * a.group : 0)) * d;
-#pragma unroll
-        for (int k = 0; k < P::kSteps; ++k) {
-            const int at = kCodes ? 64 * (k >> 1) + 16 * g + 8 * (k & 1) : 32 * k + 8 * g;
-            st.q[t][k] = u32x4{0, 0, 0, 0};
-            if (on && at < d) st.q[t][k] = ldg(reinterpret_cast<const u32x4 *>(qp + at));
-        }
-        see[t] = sees(a, q, i);
-        if (on) {
-            lo = min(lo, see[t].tree ? min(see[t].lo, max(q.ctx, 0)) : see[t].lo);
-            hi = max(hi, see[t].tree ? q.kv : see[t].hi);
-        } else {
-            see[t] = Sees{0, 0x7FFFFFFF, nullptr};   // an unused column: never the reason to mask
-        }
-#pragma unroll
-        for (int b = 0; b < P::kBlocks; ++b) st.o[t][b] = f32x4{0, 0, 0, 0};
-        st.m[t] = kNegInf, st.l[t] = 0.0f;
-    }
-#pragma unroll
-    for (int x = 1; x < 16; x <<= 1) {
-        lo = min(lo, __shfl_xor(lo, x));
-        hi = max(hi, __shfl_xor(hi, x));
-    }
-    lo = __builtin_amdgcn_readfirstlane(lo) & ~31;
-    hi = __builtin_amdgcn_readfirstlane(hi);
-    // This workgroup's keys, and this wave's: a stretch of whole 32s.
-    const int64_t c0 = (int64_t)lo + (int64_t)split * sp.chunk;
-    const int w0 = c0 < hi ? (int)c0 : hi, w1 = (int)min((int64_t)hi, c0 + sp.chunk);
-    const int per = ((w1 - w0 + kWaves * 32 - 1) / (kWaves * 32)) * 32;
-    const int k0 = min(w0 + wave * per, w1), k1 = min(k0 + per, w1), last = k1 - 1;
-
     char *patch = lds + wave * P::kPatch;
-    if (k0 < k1) {
-        u32x4 kr[2][P::kLoads], vr[2][P::kLoads];
-        f32x4 ks[2], vs[2];
-        uint32_t valid;
-        auto load = [&](const void *pool, const KeyRows &k, u32x4 (&to)[2][P::kLoads]) {
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const char *row = static_cast<const char *>(pool) + k.row[b] * d * (kCodes ? 1 : 2);
-#pragma unroll
-                for (int i = 0; i < P::kLoads; ++i) {
-                    const int at = 64 * i + 16 * g;   // bytes
-                    to[b][i] = ldg(reinterpret_cast<const u32x4 *>(row + (at < d * (kCodes ? 1 : 2) ? at : 0)));
-                }
-            }
-        };
-        auto load_scale = [&](const float *pool, const KeyRows &k, f32x4 (&to)[2]) {
-#pragma unroll
-            for (int b = 0; b < 2; ++b) to[b] = ldg(reinterpret_cast<const f32x4 *>(pool + k.first[b] + 4 * g));
-        };
-        // LDS places. V row of key r: 16-byte piece c at c ^ f(r), so that the rows
-        // one transposing read takes together lie on different banks.
-        constexpr int kMask = DT >= 128 ? 7 : 3;
-        int put[2], get[8];
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            const int f = kCodes ? ((n & 3) | b << 2) & kMask : (n & kMask) << 1;
-            put[b] = (16 * b + n) * P::kRow + ((g ^ f) << 4);
-        }
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-            if (kCodes) {
-                const int e = n >> 1, key = 16 * (e >> 2) + 4 * g + (e & 3);
-                get[x] = key * P::kRow + (((x ^ e) & kMask) << 4) + 8 * (n & 1);
-            } else {
-                const int key = 4 * g + (n >> 2);
-                get[x] = key * P::kRow + (((x ^ key) & kMask) << 5) + 8 * (n & 3);
-            }
-        }
-        KeyRows at = key_rows(a, s, kvh, k0, last);
-        load(a.c.k, at, kr);
-        if (kCodes) load_scale(a.c.k_scale, at, ks);
-        load(a.c.v, at, vr);
-        if (kCodes) load_scale(a.c.v_scale, at, vs);
-        valid = at.valid;
-        for (int j0 = k0; j0 < k1; j0 += 32) {
-            const int next = j0 + 32 < k1 ? j0 + 32 : j0;
-            at = key_rows(a, s, kvh, next, last);
-            // scores
-            f32x4 sc[NT][2];
-#pragma unroll
-            for (int t = 0; t < NT; ++t) sc[t][0] = sc[t][1] = f32x4{0, 0, 0, 0};
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int k = 0; k < P::kSteps; ++k) {
-                    const u32x4 w = kr[b][kCodes ? k >> 1 : k];
-                    const u32x4 kf = kCodes ? (k & 1 ? widen8<F>(w.z, w.w) : widen8<F>(w.x, w.y)) : w;
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) sc[t][b] = mfma16(kf, st.q[t][k], sc[t][b]);
-                }
-            f32x4 mul[2] = {f32x4{a.scale2, a.scale2, a.scale2, a.scale2}, f32x4{a.scale2, a.scale2, a.scale2, a.scale2}};
-            if (kCodes) mul[0] *= ks[0], mul[1] *= ks[1];
-            load(a.c.k, at, kr);
-            if (kCodes) load_scale(a.c.k_scale, at, ks);
-            // V into the patch
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int i = 0; i < P::kLoads; ++i)
-                    *reinterpret_cast<u32x4 *>(patch + (put[b] ^ (i << 6))) = vr[b][i];
-            f32x4 vm[2];
-            if (kCodes) vm[0] = vs[0], vm[1] = vs[1];
-            load(a.c.v, at, vr);
-            if (kCodes) load_scale(a.c.v_scale, at, vs);
-            // weights
-            u32x4 ph[NT], pl[NT];
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const uint32_t vis = visible32(a, q, see[t], j0) & valid & bits(0, k1 - j0);
-                float x[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = sc[t][e >> 2][e & 3] * mul[e >> 2][e & 3];
-                if (__any(vis != 0xFFFFFFFFu)) {
-                    const uint32_t mine = vis >> (4 * g);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = mine & (1u << (16 * (e >> 2) + (e & 3))) ? x[e] : kNegInf;
-                }
-                float top = x[0];
-#pragma unroll
-                for (int e = 1; e < 8; ++e) top = fmaxf(top, x[e]);
-                top = groups_max(top);
-                if (__any(top > st.m[t] + 8.0f)) {
-                    // The reference moves only when a score passes it by 2^8: sums stay in range.
-                    const float now = fmaxf(st.m[t], top), up = now == st.m[t] ? 1.0f : __builtin_amdgcn_exp2f(st.m[t] - now);
-                    st.m[t] = now;
-                    st.l[t] *= up;
-#pragma unroll
-                    for (int b = 0; b < P::kBlocks; ++b) st.o[t][b] *= up;
-                }
-                const float ref = st.m[t] == kNegInf ? 0.0f : st.m[t];
-                float p[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    p[e] = __builtin_amdgcn_exp2f(x[e] - ref);
-                    st.l[t] += p[e];
-                    if (kCodes) p[e] = p[e] == 0.0f ? 0.0f : p[e] * vm[e >> 2][e & 3];
-                }
-                uint32_t h[4], r[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    h[e] = pack2(p[2 * e], p[2 * e + 1]);
-                    r[e] = pack2(p[2 * e] - bf16_f(h[e] & 0xFFFFu), p[2 * e + 1] - __uint_as_float(h[e] & 0xFFFF0000u));
-                }
-                ph[t] = u32x4{h[0], h[1], h[2], h[3]};
-                pl[t] = u32x4{r[0], r[1], r[2], r[3]};
-            }
-            // outputs
-#pragma unroll
-            for (int b = 0; b < P::kBlocks; ++b) {
-                u32x4 vf;
-                if (kCodes) {
-                    const u32x2 w = read_tr8(patch + get[b & 7] + (b >> 3) * 128);
-                    vf = widen8<F>(w.x, w.y);
-                } else {
-                    const char *p = patch + get[b & 7] + (b >> 3) * 256;
-                    const u32x2 x = read_tr16(p), y = read_tr16(p + 16 * P::kRow);
-                    vf = u32x4{x.x, x.y, y.x, y.y};
-                }
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    st.o[t][b] = mfma16(vf, ph[t], st.o[t][b]);
-                    st.o[t][b] = mfma16(vf, pl[t], st.o[t][b]);
-                }
-            }
-            valid = at.valid;
-        }
-    }
-
-    // Join the four waves, 16 rows at a time: row n of the patch holds the wave's output.
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         if (16 * t >= rows) break;
@@ -316,9 +128,246 @@ __global__ __launch_bounds__(256, (Few<F, DT, NT>::kPerCu)) void few_kernel(Attn
 }
 
 template <int F, int DT, int NT>
+__global__ __launch_bounds__(256, (Few<F, DT, NT>::kPerCu)) void few_kernel(FewArgs args) {
+    const AttnJob &a = args.a;
+    typedef Few<F, DT, NT> P;
+    constexpr bool kCodes = P::kCodes;
+    __shared__ __align__(16) char lds[kWaves * P::kPatch];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n = lane & 15, g = lane >> 4;
+    const FewWork work = work_of(args);
+    const int kvh = work.kvh, split = work.split, s = work.s;
+    const Seq q = seq_of(a, s);
+    const int rows = q.rows * a.group, d = a.c.d;
+    const bool tree = a.mask == kMaskTree;
+    if (rows == 0) return;
+
+    // Query rows of this lane's columns, and what they see.
+    P st;
+    int lo = 0x7FFFFFFF, hi = 0, flo = 0, fhi = 0x7FFFFFFF;   // some row sees [lo, hi), every row [flo, fhi)
+    int row_lo[NT], row_hi[NT];                              // this lane's rows; trees besides
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const int r = 16 * t + n, i = r / a.group;
+        const bool on = r < rows;
+        const uint16_t *qp = static_cast<const uint16_t *>(a.q) + (size_t)(q.q0 + (on ? i : 0)) * a.ldq +
+                             (size_t)(kvh * a.group + (on ? r - i * a.group : 0)) * d;
+#pragma unroll
+        for (int k = 0; k < P::kSteps; ++k) {
+            const int at = kCodes ? 64 * (k >> 1) + 16 * g + 8 * (k & 1) : 32 * k + 8 * g;
+            st.q[t][k] = u32x4{0, 0, 0, 0};
+            if (on && at < d) st.q[t][k] = ldg(reinterpret_cast<const u32x4 *>(qp + at));
+        }
+        const Sees see = sees(a, q, i);
+        if (on) {   // an unused column is never the reason to mask
+            lo = min(lo, see.tree ? min(see.lo, max(q.ctx, 0)) : see.lo);
+            hi = max(hi, see.tree ? q.kv : see.hi);
+            flo = max(flo, see.lo);
+            fhi = min(fhi, see.hi);
+        }
+        row_lo[t] = on ? see.lo : 0, row_hi[t] = on ? see.hi : 0x7FFFFFFF;
+#pragma unroll
+        for (int b = 0; b < P::kBlocks; ++b) st.o[t][b] = f32x4{0, 0, 0, 0};
+        st.m[t] = kNegInf, st.l[t] = 0.0f;
+    }
+#pragma unroll
+    for (int x = 1; x < 16; x <<= 1) {
+        lo = min(lo, __shfl_xor(lo, x));
+        hi = max(hi, __shfl_xor(hi, x));
+        flo = max(flo, __shfl_xor(flo, x));
+        fhi = min(fhi, __shfl_xor(fhi, x));
+    }
+    flo = __builtin_amdgcn_readfirstlane(flo);
+    fhi = __builtin_amdgcn_readfirstlane(fhi);
+    lo = __builtin_amdgcn_readfirstlane(lo) & ~31;
+    hi = __builtin_amdgcn_readfirstlane(hi);
+    // This workgroup's keys, and this wave's: a stretch of whole 32s.
+    const int64_t c0 = (int64_t)lo + (int64_t)split * args.sp.chunk;
+    const int w0 = c0 < hi ? (int)c0 : hi, w1 = (int)min((int64_t)hi, c0 + args.sp.chunk);
+    const int per = ((w1 - w0 + kWaves * 32 - 1) / (kWaves * 32)) * 32;
+    const int k0 = min(w0 + wave * per, w1), k1 = min(k0 + per, w1), last = k1 - 1;
+
+    char *patch = lds + wave * P::kPatch;
+    if (k0 < k1) {
+        u32x4 kr[2][P::kLoads], vr[2][P::kLoads];
+        f32x4 ks[2], vs[2];
+        uint32_t valid;
+        const int32_t *table = a.c.table + (int64_t)s * a.c.max_pages;
+        const int shift = a.c.page_shift, pmask = (1 << shift) - 1, n_pages = a.c.n_pages, bytes = d * (kCodes ? 1 : 2);
+        const int64_t head = (int64_t)kvh << shift, pitch = (int64_t)a.c.n_kv << shift;   // rows: of this head in a page, of a page
+        // Page numbers come from a register: lane i holds entry first_page + i of the
+        // table, read anew every 64 pages. A load per step would be waited for behind
+        // the keys and values that are on their way.
+        int first_page = -64, pages = 0;
+        // Where 32 keys lie, in two halves of 16, each within one page. Past the last
+        // key the last one is read again, so no load leaves the pages.
+        int64_t first[2];   // element row of the half's first key
+        uint32_t lane_at[2];   // bytes from there to this lane's key and piece
+        uint32_t valid_in;
+        auto look = [&](int j0) {
+            const int e0 = min(j0, last) >> shift, e1 = min(j0 + 16, last) >> shift;
+            if (e1 - first_page >= 64) {
+                first_page = e0;
+                pages = table[min(e0 + lane, last >> shift)];
+                __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
+            }
+            valid_in = 0;
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const int page = __builtin_amdgcn_readlane(pages, (b ? e1 : e0) - first_page), j = min(j0 + 16 * b, last);
+                const bool ok = (unsigned)page < (unsigned)n_pages;
+                if (ok) valid_in |= 0xFFFFu << (16 * b);
+                first[b] = (ok ? page : 0) * pitch + head + (j & pmask & ~15);
+                lane_at[b] = min(n, last - (j & ~15)) * bytes + 16 * g;
+            }
+        };
+        auto load = [&](const void *pool, u32x4 (&to)[2][P::kLoads]) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const char *row = scalar(static_cast<const char *>(pool) + first[b] * bytes);
+#pragma unroll
+                for (int i = 0; i < P::kLoads; ++i)
+                    to[b][i] = ldg(reinterpret_cast<const u32x4 *>(row + (lane_at[b] + (64 * i + 16 * g < bytes ? 64 * i : 0))));
+            }
+        };
+        auto load_scale = [&](const float *pool, f32x4 (&to)[2]) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) to[b] = ldg(reinterpret_cast<const f32x4 *>(pool + first[b] + 4 * g));
+        };
+        // LDS places. V row of key r: 16-byte piece c at c ^ f(r), so that the rows
+        // one transposing read takes together lie on different banks.
+        constexpr int kMask = DT >= 128 ? 7 : 3;
+        int put[2], get[8];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const int f = kCodes ? ((n & 3) | b << 2) & kMask : (n & kMask) << 1;
+            put[b] = (16 * b + n) * P::kRow + ((g ^ f) << 4);
+        }
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+            if (kCodes) {
+                const int e = n >> 1, key = 16 * (e >> 2) + 4 * g + (e & 3);
+                get[x] = key * P::kRow + (((x ^ e) & kMask) << 4) + 8 * (n & 1);
+            } else {
+                const int key = 4 * g + (n >> 2);
+                get[x] = key * P::kRow + (((x ^ key) & kMask) << 5) + 8 * (n & 3);
+            }
+        }
+        look(k0);
+        load(a.c.k, kr);
+        if (kCodes) load_scale(a.c.k_scale, ks);
+        load(a.c.v, vr);
+        if (kCodes) load_scale(a.c.v_scale, vs);
+        for (int j0 = k0; j0 < k1; j0 += 32) {
+            valid = valid_in;
+            look(min(j0 + 32, last & ~31));
+            // scores
+            f32x4 sc[NT][2];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) sc[t][0] = sc[t][1] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int k = 0; k < P::kSteps; ++k) {
+                    const u32x4 w = kr[b][kCodes ? k >> 1 : k];
+                    const u32x4 kf = kCodes ? (k & 1 ? widen8<F>(w.z, w.w) : widen8<F>(w.x, w.y)) : w;
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) sc[t][b] = mfma16(kf, st.q[t][k], sc[t][b]);
+                }
+            f32x4 mul[2] = {f32x4{a.scale2, a.scale2, a.scale2, a.scale2}, f32x4{a.scale2, a.scale2, a.scale2, a.scale2}};
+            if (kCodes) mul[0] *= ks[0], mul[1] *= ks[1];
+            load(a.c.k, kr);
+            if (kCodes) load_scale(a.c.k_scale, ks);
+            // V into the patch
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int i = 0; i < P::kLoads; ++i)
+                    *reinterpret_cast<u32x4 *>(patch + (put[b] ^ (i << 6))) = vr[b][i];
+            f32x4 vm[2];
+            if (kCodes) vm[0] = vs[0], vm[1] = vs[1];
+            load(a.c.v, vr);
+            if (kCodes) load_scale(a.c.v_scale, vs);
+            // weights
+            u32x4 ph[NT], pl[NT];
+            const bool all = j0 >= flo && j0 + 32 <= min(fhi, k1) && valid == 0xFFFFFFFFu;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                float x[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = sc[t][e >> 2][e & 3] * mul[e >> 2][e & 3];
+                if (!all) {
+                    uint32_t vis = bits(row_lo[t] - j0, row_hi[t] - j0);
+                    if (tree) vis = few_seen(argument_again<FewArgs>(), t, j0);
+                    const uint32_t mine = (vis & valid & bits(0, k1 - j0)) >> (4 * g);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = mine & (1u << (16 * (e >> 2) + (e & 3))) ? x[e] : kNegInf;
+                }
+                float top = x[0];
+#pragma unroll
+                for (int e = 1; e < 8; ++e) top = fmaxf(top, x[e]);
+                top = groups_max(top);
+                if (__any(top > st.m[t] + 8.0f)) {
+                    // The reference moves only when a score passes it by 2^8: sums stay in range.
+                    const float now = fmaxf(st.m[t], top), up = now == st.m[t] ? 1.0f : __builtin_amdgcn_exp2f(st.m[t] - now);
+                    st.m[t] = now;
+                    st.l[t] *= up;
+#pragma unroll
+                    for (int b = 0; b < P::kBlocks; ++b) st.o[t][b] *= up;
+                }
+                const float ref = st.m[t] == kNegInf ? 0.0f : st.m[t];
+                float p[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    p[e] = __builtin_amdgcn_exp2f(x[e] - ref);
+                    st.l[t] += p[e];
+                    if (kCodes) p[e] = p[e] == 0.0f ? 0.0f : p[e] * vm[e >> 2][e & 3];
+                }
+                uint32_t h[4], r[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    h[e] = pack2(p[2 * e], p[2 * e + 1]);
+                    r[e] = pack2(p[2 * e] - bf16_f(h[e] & 0xFFFFu), p[2 * e + 1] - __uint_as_float(h[e] & 0xFFFF0000u));
+                }
+                ph[t] = u32x4{h[0], h[1], h[2], h[3]};
+                pl[t] = u32x4{r[0], r[1], r[2], r[3]};
+            }
+            // outputs
+#pragma unroll
+            for (int b = 0; b < P::kBlocks; ++b) {
+                u32x4 vf;
+                if (kCodes) {
+                    const u32x2 w = read_tr8(patch + get[b & 7] + (b >> 3) * 128);
+                    vf = widen8<F>(w.x, w.y);
+                } else {
+                    const char *p = patch + get[b & 7] + (b >> 3) * 256;
+                    const u32x2 x = read_tr16(p), y = read_tr16(p + 16 * P::kRow);
+                    vf = u32x4{x.x, x.y, y.x, y.y};
+                }
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    st.o[t][b] = mfma16(vf, ph[t], st.o[t][b]);
+                    st.o[t][b] = mfma16(vf, pl[t], st.o[t][b]);
+                }
+            }
+            // Operand reads run ahead of the products.
+            constexpr int kReads = kCodes ? 1 : 2, kAhead = P::kBlocks < 8 ? P::kBlocks : 8;
+            __builtin_amdgcn_sched_group_barrier(0x100, kReads * kAhead, 0);
+#pragma unroll
+            for (int b = 0; b < P::kBlocks; ++b) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 2 * NT, 0);
+                if (b + kAhead < P::kBlocks) __builtin_amdgcn_sched_group_barrier(0x100, kReads, 0);
+            }
+        }
+    }
+
+    join_waves<F, DT, NT>(args, q, st, lds, k0, k1);
+}
+
+template <int F, int DT, int NT>
 void run(const AttnJob &a, const Split &sp, hipStream_t s) {
     const int64_t blocks = (int64_t)a.c.n_seq * sp.n_split * a.c.n_kv;
-    hipLaunchKernelGGL((few_kernel<F, DT, NT>), dim3((unsigned)blocks), dim3(256), 0, s, a, sp);
+    hipLaunchKernelGGL((few_kernel<F, DT, NT>), dim3((unsigned)blocks), dim3(256), 0, s, FewArgs{a, sp});
 }
 
 template <int F>
