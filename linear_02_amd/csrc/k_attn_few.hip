@@ -30,7 +30,7 @@ struct Few {
     static constexpr int kRow = kCodes ? DT : 2 * DT;   // bytes of a V row in LDS
     // Two workgroups per CU where 256 registers hold the 32 keys' K and V beside the outputs.
     static constexpr int kPerCu = DT == 256 && (NT == 2 || !kCodes) ? 1 : 2;
-    static constexpr int kPatch = 16 * DT * 4;          // LDS bytes per wave (V: 32 rows, at most this; outputs: 16 rows fp32)
+    static constexpr int kPatch = 64 * kRow > 64 * DT ? 64 * kRow : 64 * DT;   // LDS bytes per wave: 32 rows of V and of K, or 16 output rows fp32
     u32x4 q[NT][kSteps];
     f32x4 o[NT][kBlocks];
     float m[NT], l[NT];
@@ -202,7 +202,7 @@ __global__ __launch_bounds__(256, (Few<F, DT, NT>::kPerCu)) void few_kernel(FewA
         // Where 32 keys lie, in two halves of 16, each within one page. Past the last
         // key the last one is read again, so no load leaves the pages.
         int64_t first[2];   // element row of the half's first key
-        uint32_t lane_at[2];   // bytes from there to this lane's key and piece
+        uint32_t rows_in[2];   // rows of the half behind its first, to the last key
         uint32_t valid_in;
         auto look = [&](int j0) {
             const int e0 = min(j0, last) >> shift, e1 = min(j0 + 16, last) >> shift;
@@ -218,16 +218,21 @@ __global__ __launch_bounds__(256, (Few<F, DT, NT>::kPerCu)) void few_kernel(FewA
                 const bool ok = (unsigned)page < (unsigned)n_pages;
                 if (ok) valid_in |= 0xFFFFu << (16 * b);
                 first[b] = (ok ? page : 0) * pitch + head + (j & pmask & ~15);
-                lane_at[b] = min(n, last - (j & ~15)) * bytes + 16 * g;
+                rows_in[b] = last - (j & ~15);
             }
         };
+        // Whole rows by neighbouring lanes, and not kept in the caches: 64 bytes of 16
+        // rows each, as the score product takes them, cost a fifth of the bandwidth.
+        constexpr int kPieces = P::kRow / 16, kRows = 64 / kPieces;   // 16-byte pieces of a row, rows per load
+        const int my_row = lane / kPieces, my_piece = lane % kPieces;
         auto load = [&](const void *pool, u32x4 (&to)[2][P::kLoads]) {
+            const uint32_t c = min(my_piece * 16, bytes - 16);
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 const char *row = scalar(static_cast<const char *>(pool) + first[b] * bytes);
 #pragma unroll
                 for (int i = 0; i < P::kLoads; ++i)
-                    to[b][i] = ldg(reinterpret_cast<const u32x4 *>(row + (lane_at[b] + (64 * i + 16 * g < bytes ? 64 * i : 0))));
+                    to[b][i] = __builtin_nontemporal_load((const __attribute__((address_space(1))) u32x4 *)(row + (min((uint32_t)(i * kRows + my_row), rows_in[b]) * bytes + c)));
             }
         };
         auto load_scale = [&](const float *pool, f32x4 (&to)[2]) {
@@ -237,12 +242,19 @@ __global__ __launch_bounds__(256, (Few<F, DT, NT>::kPerCu)) void few_kernel(FewA
         // LDS places. V row of key r: 16-byte piece c at c ^ f(r), so that the rows
         // one transposing read takes together lie on different banks.
         constexpr int kMask = DT >= 128 ? 7 : 3;
-        int put[2], get[8];
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            const int f = kCodes ? ((n & 3) | b << 2) & kMask : (n & kMask) << 1;
-            put[b] = (16 * b + n) * P::kRow + ((g ^ f) << 4);
-        }
+        int get[8];
+        auto put = [&](int b, int i) {
+            const int r = i * kRows + my_row, f = kCodes ? ((r & 3) | b << 2) & kMask : (r & kMask) << 1;
+            return (16 * b + r) * P::kRow + ((my_piece ^ f) << 4);
+        };
+        // K piece c of row r at c ^ fk(r): the 16 rows of one pass of a read meet all banks.
+        constexpr int kShare = kPieces < 16 ? 16 / kPieces : 1;
+        auto fk = [&](int r) { return r / kShare & ((kPieces < 16 ? kPieces : 16) - 1); };
+        auto put_k = [&](int b, int i) {
+            const int r = i * kRows + my_row;
+            return 32 * P::kRow + (16 * b + r) * P::kRow + ((my_piece ^ fk(r)) << 4);
+        };
+        const int get_k = 32 * P::kRow + n * P::kRow + ((g ^ fk(n)) << 4);   // piece 4 i + g: ^ (i << 6)
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
             if (kCodes) {
@@ -262,28 +274,37 @@ __global__ __launch_bounds__(256, (Few<F, DT, NT>::kPerCu)) void few_kernel(FewA
             valid = valid_in;
             look(min(j0 + 32, last & ~31));
             // scores
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int i = 0; i < P::kLoads; ++i) *reinterpret_cast<u32x4 *>(patch + put_k(b, i)) = kr[b][i];
+            f32x4 kscale[2];
+            if (kCodes) kscale[0] = ks[0], kscale[1] = ks[1];
+            load(a.c.k, kr);
+            if (kCodes) load_scale(a.c.k_scale, ks);
             f32x4 sc[NT][2];
 #pragma unroll
             for (int t = 0; t < NT; ++t) sc[t][0] = sc[t][1] = f32x4{0, 0, 0, 0};
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int k = 0; k < P::kSteps; ++k) {
-                    const u32x4 w = kr[b][kCodes ? k >> 1 : k];
-                    const u32x4 kf = kCodes ? (k & 1 ? widen8<F>(w.z, w.w) : widen8<F>(w.x, w.y)) : w;
+                for (int i = 0; i < P::kLoads; ++i) {
+                    const u32x4 w = *reinterpret_cast<const u32x4 *>(patch + (get_k ^ ((i & 3) << 6)) + (i >> 2) * 256 + b * 16 * P::kRow);
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) sc[t][b] = mfma16(kf, st.q[t][k], sc[t][b]);
+                    for (int e = 0; e < (kCodes ? 2 : 1); ++e) {
+                        const u32x4 kf = kCodes ? (e ? widen8<F>(w.z, w.w) : widen8<F>(w.x, w.y)) : w;
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) sc[t][b] = mfma16(kf, st.q[t][kCodes ? 2 * i + e : i], sc[t][b]);
+                    }
                 }
             f32x4 mul[2] = {f32x4{a.scale2, a.scale2, a.scale2, a.scale2}, f32x4{a.scale2, a.scale2, a.scale2, a.scale2}};
-            if (kCodes) mul[0] *= ks[0], mul[1] *= ks[1];
-            load(a.c.k, kr);
-            if (kCodes) load_scale(a.c.k_scale, ks);
+            if (kCodes) mul[0] *= kscale[0], mul[1] *= kscale[1];
             // V into the patch
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
                 for (int i = 0; i < P::kLoads; ++i)
-                    *reinterpret_cast<u32x4 *>(patch + (put[b] ^ (i << 6))) = vr[b][i];
+                    *reinterpret_cast<u32x4 *>(patch + put(b, i)) = vr[b][i];
             f32x4 vm[2];
             if (kCodes) vm[0] = vs[0], vm[1] = vs[1];
             load(a.c.v, vr);
