@@ -44,24 +44,34 @@ enum Kind { kFew, kTile, kF32 };
 
 struct Plan {
     Kind kind;
+    int waves;   // per workgroup
     Split sp;
 };
 
 constexpr int kMinChunk = 128;     // keys: 32 for each of four waves
 
-Plan plan_of(const AttnJob &a, bool f32) {
+// Most query rows per key/value head of the few-row kernel. Above 16 it takes two
+// row tiles a wave, which at heads over 128 in bf16 does not fit its registers: 8
+// trees of 8 tokens and 4 heads over 8192 keys took 189 us so, 103 us in the tile
+// kernel; at 128 wide 55 and 58 us, in int8 at 256 wide 96 and 117 us.
+int few_rows(const AttnJob &a, int fmt) { return fmt == kFmtBf16 && a.c.d > 128 ? 16 : 32; }
+
+Plan plan_of(const AttnJob &a, int fmt, bool f32) {
     Plan p{};
     p.sp.n_split = 1;
-    p.kind = f32 ? kF32 : (int64_t)a.max_q * a.group > kFewRows ? kTile : kFew;
+    p.kind = f32 ? kF32 : (int64_t)a.max_q * a.group > few_rows(a, fmt) ? kTile : kFew;
     p.sp.rows = a.max_q * a.group;
+    // Codes are widened once per workgroup: eight waves where they hold all rows.
+    p.waves = p.kind == kTile && fmt != kFmtBf16 && p.sp.rows > 4 * kTileRows && p.sp.rows <= 8 * kTileRows ? 8 : 4;
     // Most keys that the queries of one sequence see between them; pieces start at a multiple of 32.
     int64_t span = a.max_kv;
     if (a.mask == kMaskCausal && a.window && (int64_t)a.window + a.max_q < span) span = (int64_t)a.window + a.max_q;
     span += 31;
-    const int64_t units = (int64_t)a.c.n_seq * a.c.n_kv * (p.kind == kTile  ? (p.sp.rows + kTileRows - 1) / kTileRows
+    const int64_t units = (int64_t)a.c.n_seq * a.c.n_kv * (p.kind == kTile  ? (p.sp.rows + p.waves * kTileRows - 1) / (p.waves * kTileRows)
                                                           : p.kind == kF32 ? (p.sp.rows + kF32Rows - 1) / kF32Rows
                                                                            : 1);
-    int64_t chunk = (span * units + kWorkgroups - 1) / kWorkgroups;
+    const int64_t want = p.waves == 8 ? kWorkgroups / 2 : kWorkgroups;
+    int64_t chunk = (span * units + want - 1) / want;
     if (chunk < kMinChunk) chunk = kMinChunk;
     if (chunk < (span + kMaxSplit - 1) / kMaxSplit) chunk = (span + kMaxSplit - 1) / kMaxSplit;
     chunk = (chunk + 127) / 128 * 128;
@@ -77,19 +87,19 @@ size_t part_floats(const AttnJob &a, const Split &sp) {
 }  // namespace
 
 size_t attention_scratch(const AttnJob &a, int fmt, bool f32) {
-    const Plan p = plan_of(a, f32);
+    const Plan p = plan_of(a, fmt, f32);
     return p.sp.n_split > 1 ? part_floats(a, p.sp) * (a.c.d + 2) * 4 : 0;
 }
 
 hipError_t launch_attention(const AttnJob &a, int fmt, bool f32, void *ws, hipStream_t s) {
-    Plan p = plan_of(a, f32);
+    Plan p = plan_of(a, fmt, f32);
     if (p.sp.n_split > 1) {
         p.sp.part = static_cast<float *>(ws);
         p.sp.ml = reinterpret_cast<float2 *>(p.sp.part + part_floats(a, p.sp) * a.c.d);
     }
     switch (p.kind) {
         case kFew: launch_few(a, fmt, p.sp, s); break;
-        case kTile: launch_tile(a, fmt, p.sp, s); break;
+        case kTile: launch_tile(a, fmt, p.sp, p.waves, s); break;
         default: launch_f32(a, fmt, p.sp, s);
     }
     const hipError_t e = hipGetLastError();

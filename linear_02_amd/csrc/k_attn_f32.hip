@@ -112,7 +112,7 @@ __global__ __launch_bounds__(256, 2) void f32_kernel(TileArgs x) {
                     sc = mfma4(kf.z, qf[j].z, sc);
                     sc = mfma4(kf.w, qf[j].w, sc);
                 }
-                const uint32_t vis = !paged ? 0u : seen<1>(x, 0, j0) & bits(0, k1 - j0);
+                const uint32_t vis = !paged ? 0u : seen<1, 4>(x, 0, j0) & bits(0, k1 - j0);
                 f32x4 vs{1, 1, 1, 1};
                 if (F != kFmtF32) {
                     sc *= *reinterpret_cast<const f32x4 *>(k_scale + 4 * g);
@@ -151,7 +151,7 @@ __global__ __launch_bounds__(256, 2) void f32_kernel(TileArgs x) {
             __syncthreads();
         }
     }
-    finish<float, F, DT, 1>(argument_again<TileArgs>(), o, m, l, k0, k1);
+    finish<float, F, DT, 1, 4>(argument_again<TileArgs>(), o, m, l, k0, k1);
 }
 
 template <int F, int DT>

@@ -30,6 +30,7 @@ struct Few {
     static constexpr int kRow = kCodes ? DT : 2 * DT;   // bytes of a V row in LDS
     // Two workgroups per CU where 256 registers hold the 32 keys' K and V beside the outputs.
     static constexpr int kPerCu = DT == 256 && (NT == 2 || !kCodes) ? 1 : 2;
+    static_assert(kCodes || DT < 256 || NT == 1, "32 rows of 256 and bf16 keys do not fit the registers");
     static constexpr int kPatch = 64 * kRow > 64 * DT ? 64 * kRow : 64 * DT;   // LDS bytes per wave: 32 rows of V and of K, or 16 output rows fp32
     u32x4 q[NT][kSteps];
     f32x4 o[NT][kBlocks];
@@ -224,7 +225,7 @@ __global__ __launch_bounds__(256, (Few<F, DT, NT>::kPerCu)) void few_kernel(FewA
         // Whole rows by neighbouring lanes, and not kept in the caches: 64 bytes of 16
         // rows each, as the score product takes them, cost a fifth of the bandwidth.
         constexpr int kPieces = P::kRow / 16, kRows = 64 / kPieces;   // 16-byte pieces of a row, rows per load
-        const int my_row = lane / kPieces, my_piece = lane % kPieces;
+        int my_row = lane / kPieces, my_piece = lane % kPieces;
         auto load = [&](const void *pool, u32x4 (&to)[2][P::kLoads]) {
             const uint32_t c = min(my_piece * 16, bytes - 16);
 #pragma unroll
@@ -272,6 +273,7 @@ __global__ __launch_bounds__(256, (Few<F, DT, NT>::kPerCu)) void few_kernel(FewA
         if (kCodes) load_scale(a.c.v_scale, vs);
         for (int j0 = k0; j0 < k1; j0 += 32) {
             valid = valid_in;
+            asm volatile("" : "+v"(my_row), "+v"(my_piece));   // places are formed anew, not held in registers
             look(min(j0 + 32, last & ~31));
             // scores
 #pragma unroll
@@ -371,14 +373,6 @@ __global__ __launch_bounds__(256, (Few<F, DT, NT>::kPerCu)) void few_kernel(FewA
                     st.o[t][b] = mfma16(vf, pl[t], st.o[t][b]);
                 }
             }
-            // Operand reads run ahead of the products.
-            constexpr int kReads = kCodes ? 1 : 2, kAhead = P::kBlocks < 8 ? P::kBlocks : 8;
-            __builtin_amdgcn_sched_group_barrier(0x100, kReads * kAhead, 0);
-#pragma unroll
-            for (int b = 0; b < P::kBlocks; ++b) {
-                __builtin_amdgcn_sched_group_barrier(0x008, 2 * NT, 0);
-                if (b + kAhead < P::kBlocks) __builtin_amdgcn_sched_group_barrier(0x100, kReads, 0);
-            }
         }
     }
 
@@ -398,8 +392,10 @@ void pick(const AttnJob &a, const Split &sp, hipStream_t s) {
         two ? run<F, 64, 2>(a, sp, s) : run<F, 64, 1>(a, sp, s);
     else if (a.c.d <= 128)
         two ? run<F, 128, 2>(a, sp, s) : run<F, 128, 1>(a, sp, s);
+    else if (F != kFmtBf16 && two)
+        run<F, F == kFmtBf16 ? 128 : 256, 2>(a, sp, s);
     else
-        two ? run<F, 256, 2>(a, sp, s) : run<F, 256, 1>(a, sp, s);
+        run<F, 256, 1>(a, sp, s);
 }
 
 }  // namespace

@@ -15,8 +15,8 @@ namespace {
 constexpr int kNT = 2;      // tiles of 16 query rows per wave
 constexpr int kAhead = 4;   // operands read ahead of the products
 
-template <int F, int DT>
-__global__ __launch_bounds__(256, 2) void tile_kernel(TileArgs x) {
+template <int F, int DT, int NW>
+__global__ __launch_bounds__(64 * NW, 2) void tile_kernel(TileArgs x) {
     const AttnJob &a = x.a;
     constexpr bool kCodes = F == kFmtInt8 || F == kFmtE4m3;
     constexpr int kSteps = DT / 32, kBlocks = DT / 16;
@@ -29,19 +29,20 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(TileArgs x) {
     auto fv = [](int r) { return (r & kMaskV) << 1; };
     // One LDS object: beside a second one the compiler waits for the loads into
     // LDS that are still on their way before every read.
-    constexpr int kTail = kCodes ? 3 * kSide : 4 * kSide;
-    __shared__ __align__(16) char lds_all[kTail + 512 + 32];
-    char (*lds)[2][kSide] = reinterpret_cast<char (*)[2][kSide]>(lds_all);   // [buffer][K, V]; one buffer for codes
-    char *raw = lds_all + 2 * kSide;                                         // codes as fetched: K, then V
-    float (*lds_scale)[2][32] = reinterpret_cast<float (*)[2][32]>(lds_all + kTail);   // [buffer][K, V]
-    int (*range)[4] = reinterpret_cast<int (*)[4]>(lds_all + kTail + 512);
+    constexpr bool kTwo = !kCodes || NW == 8;                // two buffers of keys and values, or one and more workgroups
+    constexpr int kRaw0 = (kTwo ? 4 : 2) * kSide, kTail = kRaw0 + (kCodes ? kSide : 0);
+    __shared__ __align__(16) char lds_all[kTail + 1024 + 8 * NW];
+    char (*lds)[2][kSide] = reinterpret_cast<char (*)[2][kSide]>(lds_all);   // [buffer][K, V]
+    char *raw = lds_all + kRaw0;                                             // codes as fetched: K, then V
+    float (*lds_scale)[2][32] = reinterpret_cast<float (*)[2][32]>(lds_all + kTail);   // [step % 4][K, V]
+    int (*range)[NW] = reinterpret_cast<int (*)[NW]>(lds_all + kTail + 1024);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
     const Work work = work_of(x);
     const int kvh = work.kvh, split = work.split, tile = work.tile, s = work.s;
     const Seq q = seq_of(a, s);
-    const int rows = q.rows * a.group, d = a.c.d, r0 = tile * kTileRows + wave * 16 * kNT;
-    if (tile * kTileRows >= rows) return;
+    const int rows = q.rows * a.group, d = a.c.d, r0 = (tile * NW + wave) * 16 * kNT;
+    if (tile * NW * 16 * kNT >= rows) return;
 
     u32x4 qf[kNT][kSteps];
     f32x4 o[kNT][kBlocks];
@@ -85,8 +86,8 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(TileArgs x) {
     if (lane == 0) range[0][wave] = lo, range[1][wave] = hi;
     __syncthreads();
     const int wlo = __builtin_amdgcn_readfirstlane(lo), whi = __builtin_amdgcn_readfirstlane(hi);
-    lo = min(min(range[0][0], range[0][1]), min(range[0][2], range[0][3]));
-    hi = max(max(range[1][0], range[1][1]), max(range[1][2], range[1][3]));
+#pragma unroll
+    for (int w = 0; w < NW; ++w) lo = min(lo, range[0][w]), hi = max(hi, range[1][w]);
     lo = __builtin_amdgcn_readfirstlane(lo) & ~31;
     hi = __builtin_amdgcn_readfirstlane(hi);
     const int64_t c0 = (int64_t)lo + (int64_t)split * x.sp.chunk;
@@ -99,8 +100,9 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(TileArgs x) {
         const int64_t head = (int64_t)kvh << shift, pitch = (int64_t)a.c.n_kv << shift;   // rows: of this head in a page, of a page
         const char *kpool = static_cast<const char *>(a.c.k) + head * bytes;
         const int64_t to_v = static_cast<const char *>(a.c.v) - static_cast<const char *>(a.c.k), page_bytes = pitch * bytes;
-        // Keys come in halves of 16, each within one page. A wave fetches 8 rows: its half, its first row there.
-        const int half = wave >> 1, row0 = 8 * (wave & 1);
+        // Keys come in halves of 16, each within one page. A wave fetches kMine rows: its half, its first row there.
+        constexpr int kMine = 32 / NW;
+        const int half = wave / (NW / 2), row0 = kMine * (wave % (NW / 2));
         int page[2];                                         // of the keys that are fetched next
         // Page numbers come from a register: lane i holds entry first_page + i of the
         // table, read anew every 64 pages. A load per step would have to be waited
@@ -121,11 +123,11 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(TileArgs x) {
         auto off_of = [&](int j0, int b) { return min(j0 + 16 * b, last) & pmask & ~15; };
         auto row_at = [&](int j0, int b, int r) { return min(r, last - min(j0 + 16 * b, last & ~15)); };
         // bf16: 64 pieces per load, straight to their places.
-        constexpr int kDma = kPieces * 32 / 256;             // loads per wave and side
+        constexpr int kDma = kPieces * kMine / 64;           // loads per wave and side
         // codes: as they lie, into a patch that the wave which fetched them widens from.
-        constexpr int kRaw = (DT + 127) / 128;               // loads per wave and side
+        constexpr int kCodePieces = DT / 16, kRaw = (kMine * kCodePieces + 63) / 64;   // pieces of a row; loads per wave and side
         uint32_t valid_in = 0;
-        auto fetch = [&](int j0, int buf) {
+        auto fetch = [&](int j0, int step) {
             valid_in = (has_page(0) ? 0xFFFFu : 0u) | (has_page(1) ? 0xFFFF0000u : 0u);
             const int pg = half ? page[1] : page[0];
             const char *kp = scalar(kpool + ((unsigned)pg < (unsigned)n_pages ? pg : 0) * page_bytes + off_of(j0, half) * bytes);
@@ -136,7 +138,7 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(TileArgs x) {
             if (!kCodes) {
                 constexpr int kStep = 64 / kPieces;          // rows per load
                 const int dr = ln / kPieces, c = ln % kPieces;
-                const uint32_t to = lds_byte(lds_all) + buf * 2 * kSide + wave * 8 * kRow;
+                const uint32_t to = lds_byte(lds_all) + (step & 1) * 2 * kSide + wave * kMine * kRow;
                 auto piece = [&](int i, bool v) {
                     const int r = row0 + i * kStep + dr;
                     return (uint32_t)min((c ^ (v ? fv(r) : fk(r))) * 16, bytes - 16);
@@ -157,37 +159,39 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(TileArgs x) {
                     }
                 }
             } else {
-                // 8 rows of DT / 16 pieces
-                constexpr int kCodePieces = DT / 16;
 #pragma unroll
                 for (int i = 0; i < kRaw; ++i) {
                     const int p = i * 64 + ln, c = min(p % kCodePieces * 16, bytes - 16);
-                    if (DT == 64 && ln >= 32) break;
+                    if (p >= kMine * kCodePieces) break;
                     const uint32_t at = row_at(j0, half, row0 + p / kCodePieces) * bytes + c;
-                    load_to_lds(kp, at, lds_byte(raw) + (wave * 8 * kCodePieces + i * 64) * 16);
-                    load_to_lds(vp, at, lds_byte(raw) + 32 * DT + (wave * 8 * kCodePieces + i * 64) * 16);
+                    load_to_lds(kp, at, lds_byte(raw) + (wave * kMine * kCodePieces + i * 64) * 16);
+                    load_to_lds(vp, at, lds_byte(raw) + 32 * DT + (wave * kMine * kCodePieces + i * 64) * 16);
                 }
-                // 16 scales of K or V each
-                const char *scales = reinterpret_cast<const char *>(wave & 1 ? a.c.v_scale : a.c.k_scale);
-                const int64_t from = ((unsigned)pg < (unsigned)n_pages ? pg : 0) * pitch + head + off_of(j0, half);
-                if (ln < 16)
-                    load_to_lds4(scalar(scales + from * 4), row_at(j0, half, ln) * 4, lds_byte(lds_scale[buf][wave & 1] + 16 * half));
+                // 16 scales of K or V each by four waves
+                if (wave < 4) {
+                    const int h = wave >> 1, pg = h ? page[1] : page[0];
+                    const char *scales = reinterpret_cast<const char *>(wave & 1 ? a.c.v_scale : a.c.k_scale);
+                    const int64_t from = ((unsigned)pg < (unsigned)n_pages ? pg : 0) * pitch + head + off_of(j0, h);
+                    if (ln < 16)
+                        load_to_lds4(scalar(scales + from * 4), row_at(j0, h, ln) * 4, lds_byte(lds_scale[step & 3][wave & 1] + 16 * h));
+                }
             }
         };
-        auto land = [&]() {
+        // What fetch(.., step) began is there; codes are widened into their buffer.
+        auto land = [&](int step) {
             wait_loads();
             if (!kCodes) return;
-            constexpr int kCodePieces = DT / 16;
+            char *to = lds_all + (kTwo ? (step & 1) * 2 * kSide : 0);
 #pragma unroll
             for (int i = 0; i < kRaw; ++i) {
-                if (DT == 64 && lane >= 32) break;
-                const int p = wave * 8 * kCodePieces + i * 64 + lane, r = p / kCodePieces, c = p % kCodePieces * 2;
+                if (i * 64 + lane >= kMine * kCodePieces) break;
+                const int p = wave * kMine * kCodePieces + i * 64 + lane, r = p / kCodePieces, c = p % kCodePieces * 2;
                 const u32x4 k = *reinterpret_cast<const u32x4 *>(raw + p * 16), v = *reinterpret_cast<const u32x4 *>(raw + 32 * DT + p * 16);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    *reinterpret_cast<u32x4 *>(lds[0][0] + r * kRow + ((c + e) ^ fk(r)) * 16) =
+                    *reinterpret_cast<u32x4 *>(to + r * kRow + ((c + e) ^ fk(r)) * 16) =
                         e ? widen8<F>(k.z, k.w) : widen8<F>(k.x, k.y);
-                    *reinterpret_cast<u32x4 *>(lds[0][1] + r * kRow + ((c + e) ^ fv(r)) * 16) =
+                    *reinterpret_cast<u32x4 *>(to + kSide + r * kRow + ((c + e) ^ fv(r)) * 16) =
                         e ? widen8<F>(v.z, v.w) : widen8<F>(v.x, v.y);
                 }
             }
@@ -195,26 +199,53 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(TileArgs x) {
         // Operand addresses within a buffer.
         const int at_k = n * kRow + ((g ^ fk(n)) << 4);      // piece 4 k + g: ^ (k << 6)
         const int key_v = 4 * g + (n >> 2), at_v = key_v * kRow + ((key_v & kMaskV) << 5) + 8 * (n & 3);   // block b: ^ (b << 5)
+        // Step n is fetched into buffer n % 2 while step n - 1 is worked on, and has
+        // landed for every wave behind the barrier at that step's end. Codes take one
+        // more step: fetched, then widened into their buffer. With eight waves the two
+        // that share a SIMD do that at opposite ends of a step, so that one widens
+        // while the other feeds the matrix cores; with four waves and one buffer it
+        // is done between two barriers, and the other workgroup of the CU goes on.
         look(k0);
         fetch(k0, 0);
-        uint32_t valid = valid_in;
+        uint32_t valid = valid_in, valid_next = 0;
         if (k0 + 32 < k1) look(k0 + 32);
-        if (!kCodes) land();
+        if (kTwo) land(0);
+        if (kCodes && kTwo && k0 + 32 < k1) {
+            fetch(k0 + 32, 1);
+            valid_next = valid_in;
+            look(min(k0 + 64, last));
+        }
         __syncthreads();
-        int buf = 0;
-        for (int j0 = k0; j0 < k1; j0 += 32) {
+        int step = 0;
+        for (int j0 = k0; j0 < k1; j0 += 32, ++step) {
             const bool more = j0 + 32 < k1;
-            if (kCodes) land();
-            valid = valid_in;
-            if (more) {
-                fetch(j0 + 32, buf ^ 1);
-                look(min(j0 + 64, last));
+            // Codes of the step after next, once the next step's are widened.
+            auto advance = [&]() {
+                if (!more) return;
+                land(step + 1);
+                if (j0 + 64 < k1) {
+                    fetch(j0 + 64, step + 2);
+                    look(min(j0 + 96, last));
+                }
+            };
+            if (kCodes && !kTwo) {
+                land(step);
+                valid = valid_in;
             }
-            if (kCodes) __syncthreads();
+            if (!(kCodes && kTwo)) {
+                if (more) {
+                    fetch(j0 + 32, step + 1);
+                    look(min(j0 + 64, last));
+                }
+            } else if (wave < 4) {
+                advance();
+            }
+            if (kCodes && !kTwo) __syncthreads();
             if (j0 + 31 >= wlo && j0 < whi) {
                 // Formed anew in every step: held in registers through the loop, the
                 // places of all operands would leave none to read ahead into.
-                int kb = at_k + (kCodes ? 0 : buf * 2 * kSide), vb = at_v + (kCodes ? 0 : buf * 2 * kSide) + kSide;
+                const int in = kTwo ? (step & 1) * 2 * kSide : 0;
+                int kb = at_k + in, vb = at_v + in + kSide;
                 asm volatile("" : "+v"(kb), "+v"(vb));
                 f32x4 sc[kNT][2];
 #pragma unroll
@@ -239,7 +270,7 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(TileArgs x) {
                 if (kCodes) {
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
-                        const f32x4 ks = *reinterpret_cast<const f32x4 *>(&lds_scale[buf][0][16 * b + 4 * g]);
+                        const f32x4 ks = *reinterpret_cast<const f32x4 *>(&lds_scale[step & 3][0][16 * b + 4 * g]);
 #pragma unroll
                         for (int t = 0; t < kNT; ++t) sc[t][b] *= ks;
                     }
@@ -252,7 +283,7 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(TileArgs x) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) x[e] = sc[t][e >> 2][e & 3];
                     if (!all) {
-                        const uint32_t mine = (seen<kNT>(argument_again<TileArgs>(), 16 * t, j0) & valid & bits(0, k1 - j0)) >> (4 * g);
+                        const uint32_t mine = (seen<kNT, NW>(argument_again<TileArgs>(), 16 * t, j0) & valid & bits(0, k1 - j0)) >> (4 * g);
 #pragma unroll
                         for (int e = 0; e < 8; ++e) x[e] = mine & (1u << (16 * (e >> 2) + (e & 3))) ? x[e] : kNegInf;
                     }
@@ -274,7 +305,7 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(TileArgs x) {
                     f32x4 vm[2];
                     if (kCodes) {
 #pragma unroll
-                        for (int b = 0; b < 2; ++b) vm[b] = *reinterpret_cast<const f32x4 *>(&lds_scale[buf][1][16 * b + 4 * g]);
+                        for (int b = 0; b < 2; ++b) vm[b] = *reinterpret_cast<const f32x4 *>(&lds_scale[step & 3][1][16 * b + 4 * g]);
                     }
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
@@ -308,39 +339,40 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(TileArgs x) {
                     if (i + kAhead < kBlocks) __builtin_amdgcn_sched_group_barrier(0x100, 2, 1);
                 }
             }
-            if (!kCodes && more) land();
-            buf ^= 1;
+            if (!kCodes && more) land(step + 1);
+            if (kCodes && kTwo && wave >= 4) advance();
+            if (kTwo) valid = kCodes ? valid_next : valid_in, valid_next = valid_in;
             __syncthreads();
         }
     }
 
-    finish<uint16_t, F, DT, kNT>(argument_again<TileArgs>(), o, m, l, k0, k1);
+    finish<uint16_t, F, DT, kNT, NW>(argument_again<TileArgs>(), o, m, l, k0, k1);
 }
 
-template <int F, int DT>
+template <int F, int DT, int NW>
 void run(const AttnJob &a, const Split &sp, hipStream_t s) {
-    const int tiles = (sp.rows + kTileRows - 1) / kTileRows;
+    const int per = NW * 16 * kNT, tiles = (sp.rows + per - 1) / per;
     const int64_t blocks = (int64_t)a.c.n_seq * tiles * sp.n_split * a.c.n_kv;
-    hipLaunchKernelGGL((tile_kernel<F, DT>), dim3((unsigned)blocks), dim3(256), 0, s, TileArgs{a, sp, tiles, blocks <= kWorkgroups});
+    hipLaunchKernelGGL((tile_kernel<F, DT, NW>), dim3((unsigned)blocks), dim3(64 * NW), 0, s, TileArgs{a, sp, tiles, blocks <= kWorkgroups});
 }
 
-template <int F>
+template <int F, int NW>
 void pick(const AttnJob &a, const Split &sp, hipStream_t s) {
     if (a.c.d <= 64)
-        run<F, 64>(a, sp, s);
+        run<F, 64, NW>(a, sp, s);
     else if (a.c.d <= 128)
-        run<F, 128>(a, sp, s);
+        run<F, 128, NW>(a, sp, s);
     else
-        run<F, 256>(a, sp, s);
+        run<F, 256, NW>(a, sp, s);
 }
 
 }  // namespace
 
-void launch_tile(const AttnJob &a, int fmt, const Split &sp, hipStream_t s) {
+void launch_tile(const AttnJob &a, int fmt, const Split &sp, int waves, hipStream_t s) {
     switch (fmt) {
-        case kFmtBf16: pick<kFmtBf16>(a, sp, s); break;
-        case kFmtInt8: pick<kFmtInt8>(a, sp, s); break;
-        default: pick<kFmtE4m3>(a, sp, s);
+        case kFmtBf16: pick<kFmtBf16, 4>(a, sp, s); break;
+        case kFmtInt8: waves == 8 ? pick<kFmtInt8, 8>(a, sp, s) : pick<kFmtInt8, 4>(a, sp, s); break;
+        default: waves == 8 ? pick<kFmtE4m3, 8>(a, sp, s) : pick<kFmtE4m3, 4>(a, sp, s);
     }
 }
 

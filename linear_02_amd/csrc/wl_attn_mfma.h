@@ -130,14 +130,13 @@ __device__ __forceinline__ T argument_again() {
 }
 
 constexpr int kWorkgroups = 512;   // wanted: two per CU
-constexpr int kFewRows = 32;      // most query rows per key/value head of the few-row kernel
 constexpr int kMaxSplit = 64;     // one lane each in the join
 
-constexpr int kTileRows = 128;    // query rows per workgroup of the many-row kernel
+constexpr int kTileRows = 32;     // query rows per wave of the many-row kernel
 constexpr int kF32Rows = 64;      // of the fp32 kernel
 
 void launch_few(const AttnJob &a, int fmt, const Split &sp, hipStream_t s);
-void launch_tile(const AttnJob &a, int fmt, const Split &sp, hipStream_t s);
+void launch_tile(const AttnJob &a, int fmt, const Split &sp, int waves, hipStream_t s);
 void launch_f32(const AttnJob &a, int fmt, const Split &sp, hipStream_t s);
 
 // ---- kernels whose workgroups of four waves take tiles of 64 NT query rows -------
@@ -171,16 +170,16 @@ __device__ __forceinline__ Work work_of(const TileArgs &x) {
 
 // Which of keys j0 .. j0 + 31 this lane's row of tile `first` (0 or 16) sees. Only
 // at the edges of what the wave's rows see, so from the arguments in memory.
-template <int NT>
+template <int NT, int NW>
 __device__ __forceinline__ uint32_t seen(const TileArgs &x, int first, int j0) {
     const Work work = work_of(x);
     const Seq q = seq_of(x.a, work.s);
-    const int r = (work.tile * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * 16 * NT + first + (threadIdx.x & 15);
+    const int r = (work.tile * NW + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * 16 * NT + first + (threadIdx.x & 15);
     return visible32(x.a, q, sees(x.a, q, r / x.a.group), j0);
 }
 
 // Writes a wave's outputs: lane (n, g) holds elements 16 b + 4 g .. + 3 of row n.
-template <class E, int F, int DT, int NT>
+template <class E, int F, int DT, int NT, int NW>
 __device__ __forceinline__ void finish(const TileArgs &x, f32x4 (&o)[NT][DT / 16], float (&m)[NT], float (&l)[NT], int k0, int k1) {
     constexpr int kBlocks = DT / 16;
     const AttnJob &a = x.a;
@@ -189,7 +188,7 @@ __device__ __forceinline__ void finish(const TileArgs &x, f32x4 (&o)[NT][DT / 16
     const Work work = work_of(x);
     const int kvh = work.kvh, split = work.split, tile = work.tile, s = work.s;
     const Seq q = seq_of(a, s);
-    const int rows = q.rows * a.group, d = a.c.d, r0 = (tile * 4 + wave) * 16 * NT;
+    const int rows = q.rows * a.group, d = a.c.d, r0 = (tile * NW + wave) * 16 * NT;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         const int r = r0 + 16 * t + n;
