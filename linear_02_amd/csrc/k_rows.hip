@@ -42,12 +42,22 @@ __device__ __forceinline__ void load4(const float *p, float *v) {
     const f32x4 w = ldg(reinterpret_cast<const f32x4 *>(p));
     v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
 }
-__device__ __forceinline__ void store4(uint16_t *p, const float *v) {
-    *reinterpret_cast<u32x2 *>(p) =
-        u32x2{f_bf16(v[0]) | (uint32_t)f_bf16(v[1]) << 16, f_bf16(v[2]) | (uint32_t)f_bf16(v[3]) << 16};
+// S: past the caches.
+template <bool S, class V>
+__device__ __forceinline__ void put(V *p, V v) {
+    if (S)
+        __builtin_nontemporal_store(v, p);
+    else
+        *p = v;
 }
+template <bool S = false>
+__device__ __forceinline__ void store4(uint16_t *p, const float *v) {
+    put<S>(reinterpret_cast<u32x2 *>(p),
+           u32x2{f_bf16(v[0]) | (uint32_t)f_bf16(v[1]) << 16, f_bf16(v[2]) | (uint32_t)f_bf16(v[3]) << 16});
+}
+template <bool S = false>
 __device__ __forceinline__ void store4(float *p, const float *v) {
-    *reinterpret_cast<f32x4 *>(p) = f32x4{v[0], v[1], v[2], v[3]};
+    put<S>(reinterpret_cast<f32x4 *>(p), f32x4{v[0], v[1], v[2], v[3]});
 }
 
 __device__ __forceinline__ uint32_t swap16(uint32_t v) { return __builtin_amdgcn_ds_swizzle(v, 0x401F); }   // lane ^ 16
@@ -244,7 +254,9 @@ __device__ __forceinline__ void cache8(const void *pool, int64_t at, float *v) {
     }
 }
 
-template <class E, int F, int L>
+// S: the results go past the caches (8191 rows of 16 heads of 256 out of an e4m3
+// cache, 101 MB: 25.2 us without, 20.1 us with).
+template <class E, int F, int L, bool S>
 __global__ __launch_bounds__(kThreads) void read_kernel(ReadJob a) {
     constexpr int HW = 64 / L;
     const int lane = threadIdx.x & 63, j = lane & (L - 1), sub = lane / L;
@@ -270,8 +282,8 @@ __global__ __launch_bounds__(kThreads) void read_kernel(ReadJob a) {
             for (int e = 0; e < 8; ++e) v[e] *= s;
         }
         out += (size_t)t * (is_k ? a.ldk : a.ldv) + (size_t)hc * d + 8 * j;
-        store4(out, v);
-        store4(out + 4, v + 4);
+        store4<S>(out, v);
+        store4<S>(out + 4, v + 4);
     }
 }
 
@@ -296,14 +308,20 @@ void run_rows(const RowsJob &a, hipStream_t s) {
     }
 }
 
-template <class E, int F>
+template <class E, int F, bool S>
 void run_read(const ReadJob &a, hipStream_t s) {
     const dim3 g = grid_of(a.T, a.waves), b(kThreads);
     switch (lanes_of(a.c.d)) {
-        case 8: hipLaunchKernelGGL((read_kernel<E, F, 8>), g, b, 0, s, a); break;
-        case 16: hipLaunchKernelGGL((read_kernel<E, F, 16>), g, b, 0, s, a); break;
-        default: hipLaunchKernelGGL((read_kernel<E, F, 32>), g, b, 0, s, a);
+        case 8: hipLaunchKernelGGL((read_kernel<E, F, 8, S>), g, b, 0, s, a); break;
+        case 16: hipLaunchKernelGGL((read_kernel<E, F, 16, S>), g, b, 0, s, a); break;
+        default: hipLaunchKernelGGL((read_kernel<E, F, 32, S>), g, b, 0, s, a);
     }
+}
+
+template <class E, int F>
+void run_read(const ReadJob &a, hipStream_t s) {
+    const size_t written = (size_t)a.T * a.c.n_kv * a.c.d * sizeof(E) * ((a.k_out != nullptr) + (a.v_out != nullptr));
+    written > kStreamBytes ? run_read<E, F, true>(a, s) : run_read<E, F, false>(a, s);
 }
 
 }  // namespace

@@ -7,6 +7,10 @@
 
 namespace wl {
 
+// Results larger than this are stored past the caches (twice the L2 of one XCD):
+// they would push out what the call still reads.
+constexpr size_t kStreamBytes = (size_t)8 << 20;
+
 // ---- norms (k_norm.hip) -----------------------------------------------------
 constexpr int kNormMaxD = 32768;
 
@@ -39,7 +43,8 @@ struct RowsJob {
     const int32_t *seq, *slot;
     CacheRef c;
     int T, n_q, n_k, n_v, d, ldq, ldk, ldv, ldq_out, ldk_out;
-    int rot, interleaved, waves;   // waves: per token
+    int rot, interleaved;
+    int waves;   // per token, set by the launch
     float turn_scale, eps, offset;
 };
 hipError_t launch_rows(RowsJob a, int fmt, bool f32, hipStream_t stream);
@@ -48,7 +53,8 @@ struct ReadJob {
     const int32_t *seq, *slot;
     CacheRef c;
     void *k_out, *v_out;
-    int T, ldk, ldv, waves;
+    int T, ldk, ldv;
+    int waves;   // per token, set by the launch
 };
 hipError_t launch_cache_read(ReadJob a, int fmt, bool f32, hipStream_t stream);
 
