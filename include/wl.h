@@ -274,6 +274,7 @@ wl_status wl_step_destroy(wl_step step);
  *     them. It is a multiple of 8 and at least the row's width.
  *   - An output may be exactly one of its call's inputs where that is stated
  *     (same pointer, same ld); any other overlap is WL_ERR_INVALID_ARG.
+ *   - T is at most 2^24.
  *   - Index arrays (positions, sequences, slots, lengths, page table) are device
  *     int32, read when the work runs, so a recorded step follows them. The host
  *     cannot check them; the kernels do, as stated at each operation, and never
@@ -419,7 +420,7 @@ wl_status wl_cache_read(const wl_cache_read_args *a, void *hip_stream);
  *             sequence s's, rows outside every sequence are left as they were
  *   kv_len    device int32 [n_seq]: keys of the sequence, the new tokens' last.
  *             Query i of m has its own key in slot kv_len - m + i.
- *   max_q, max_kv  the largest q_start[s+1] - q_start[s] and kv_len[s]: these fix
+ *   max_q, max_kv  (max_kv <= 2^30) the largest q_start[s+1] - q_start[s] and kv_len[s]: these fix
  *             the launch. Queries beyond max_q get no result, keys beyond max_kv
  *             (or beyond max_pages page) are not seen.
  *   mask      WL_ATTN_CAUSAL  query i sees the slots up to its own
@@ -435,9 +436,11 @@ wl_status wl_cache_read(const wl_cache_read_args *a, void *hip_stream);
  * A query that sees no key, or whose every score is -inf, gives zeros. A key
  * that a query does not see has no influence on it, whatever it holds; the same
  * goes for slots from kv_len on. n_q is a multiple of n_kv.
- * Products of bf16 tensors run on the matrix cores with fp32 sums; weights are
- * rounded to bf16 for the second product and their sum is taken of the rounded
- * ones (bf16 caches); dtype f32 is fp32 throughout.
+ * Products of bf16 tensors run on the matrix cores with fp32 sums. For the
+ * second product a weight (times its key's v_scale, in the quantised formats) is
+ * rounded to bf16, with the remainder as a second bf16 where there are few rows
+ * per key/value head (single tokens, small trees); a bf16 cache's weights are
+ * summed as rounded. dtype f32 is fp32 throughout.
  *   ws   ws_bytes >= wl_attention_workspace_bytes(a), prepared as the other
  *        operations' (its first WL_SYNC_BYTES are not touched, so that one
  *        workspace serves a whole layer); NULL is accepted where that is 0 */

@@ -44,7 +44,8 @@ enum Kind { kFew, kTile, kF32 };
 
 struct Plan {
     Kind kind;
-    int waves;   // per workgroup
+    int waves;       // per workgroup
+    int64_t units;   // workgroups before the keys are divided
     Split sp;
 };
 
@@ -75,6 +76,7 @@ Plan plan_of(const AttnJob &a, int fmt, bool f32) {
     if (chunk < kMinChunk) chunk = kMinChunk;
     if (chunk < (span + kMaxSplit - 1) / kMaxSplit) chunk = (span + kMaxSplit - 1) / kMaxSplit;
     chunk = (chunk + 127) / 128 * 128;
+    p.units = units;
     p.sp.chunk = (int)(chunk < (1 << 30) ? chunk : (1 << 30));
     p.sp.n_split = (int)((span + chunk - 1) / chunk);
     return p;
@@ -85,6 +87,11 @@ size_t part_floats(const AttnJob &a, const Split &sp) {
 }
 
 }  // namespace
+
+int64_t attention_workgroups(const AttnJob &a, int fmt, bool f32) {
+    const Plan p = plan_of(a, fmt, f32);
+    return p.units * p.sp.n_split;
+}
 
 size_t attention_scratch(const AttnJob &a, int fmt, bool f32) {
     const Plan p = plan_of(a, fmt, f32);

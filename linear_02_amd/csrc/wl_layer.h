@@ -71,6 +71,7 @@ struct AttnJob {
     float scale2;   // scale * log2(e): scores are kept as powers of two
 };
 hipError_t launch_attention(const AttnJob &a, int fmt, bool f32, void *ws, hipStream_t stream);
+int64_t attention_workgroups(const AttnJob &a, int fmt, bool f32);
 // Bytes of scratch the launch needs.
 size_t attention_scratch(const AttnJob &a, int fmt, bool f32);
 

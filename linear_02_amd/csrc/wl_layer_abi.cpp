@@ -22,6 +22,9 @@ static_assert(WL_ATTN_CAUSAL == wl::kMaskCausal && WL_ATTN_TREE == wl::kMaskTree
 namespace {
 
 const int64_t kMaxElems = (int64_t)1 << 31;
+const int32_t kMaxTokens = 1 << 24;        // a wave each stays inside a launch's 2^32 threads
+const int32_t kMaxKeys = 1 << 30;          // key numbers stay in int32 a few tiles past the last
+const int64_t kMaxWorkgroups = 1 << 23;
 
 wl_status check_dtype(int32_t dtype) {
     if (dtype != WL_DTYPE_BF16 && dtype != WL_DTYPE_F32)
@@ -44,6 +47,7 @@ wl_status check_rows(const void *p, int32_t T, int64_t width, int32_t ld, const 
     if (ld < width || ld % 8)
         return fail(WL_ERR_INVALID_ARG, "%s: ld=%d must be a multiple of 8 and at least %lld", name, ld, (long long)width);
     if ((int64_t)T * ld >= kMaxElems) return fail(WL_ERR_INVALID_ARG, "%s spans 2^31 or more elements", name);
+    if (T > kMaxTokens) return fail(WL_ERR_UNSUPPORTED, "T=%d exceeds %d", T, kMaxTokens);
     return WL_OK;
 }
 
@@ -149,6 +153,7 @@ wl_status check_attention(const wl_attention_args *a, wl::AttnJob *job) {
     const wl_cache *c = a->cache;
     if (a->T < 0 || a->max_q < 0 || a->max_kv < 0)
         return fail(WL_ERR_INVALID_ARG, "T=%d, max_q=%d or max_kv=%d is negative", a->T, a->max_q, a->max_kv);
+    if (a->max_kv > kMaxKeys) return fail(WL_ERR_UNSUPPORTED, "max_kv=%d exceeds %d", a->max_kv, kMaxKeys);
     if (a->n_q < 1 || a->n_q % c->n_kv)
         return fail(WL_ERR_INVALID_ARG, "n_q=%d is not a positive multiple of n_kv=%d", a->n_q, c->n_kv);
     if (a->mask < WL_ATTN_CAUSAL || a->mask > WL_ATTN_FULL) return fail(WL_ERR_INVALID_ARG, "mask=%d is unknown", a->mask);
@@ -196,6 +201,10 @@ wl_status check_attention(const wl_attention_args *a, wl::AttnJob *job) {
     j.window = a->window;
     j.tree_words = a->tree_words;
     j.scale2 = (float)(a->scale * 1.4426950408889634);   // log2(e)
+    const int64_t blocks = wl::attention_workgroups(j, c->format, a->dtype == WL_DTYPE_F32);
+    if (blocks > kMaxWorkgroups)
+        return fail(WL_ERR_UNSUPPORTED, "n_seq=%d, n_kv=%d and max_q=%d ask for %lld workgroups, more than %lld", c->n_seq, c->n_kv,
+                    a->max_q, (long long)blocks, (long long)kMaxWorkgroups);
     *job = j;
     return WL_OK;
 }

@@ -460,10 +460,11 @@ class OpCall:
     """A checked call of one operation: ``out`` are its outputs, ``launch`` runs it
     on the current stream of its device. Keeps its tensors alive."""
 
-    __slots__ = ("op", "args", "out", "device", "fn", "ws", "keep")
+    __slots__ = ("op", "args", "out", "device", "fn", "ws", "keep", "used")
 
     def __init__(self, op, fn, args, out, device, keep, ws=None):
         self.op, self.fn, self.args, self.out, self.device, self.keep, self.ws = op, fn, args, out, device, keep, ws
+        self.used = None   # the shared workspace of the last launch: a captured one still needs it
 
     def launch(self):
         if self.device.index != torch.cuda.current_device():
@@ -478,6 +479,7 @@ class OpCall:
         else:
             need = lib.wl_attention_workspace_bytes(self.args)
             ws = self.ws if self.ws is not None else WORKSPACE.get(self.device, need) if need else None
+            self.used = ws
             status = self.fn(self.args, _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), stream)
         if status:
             _check(status)

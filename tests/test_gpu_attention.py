@@ -27,9 +27,9 @@ class Batch:
     """Sequences with the given earlier keys and new tokens over a shuffled cache
     whose unused slots and pages hold NaN."""
 
-    def __init__(self, wl, ctx, rows, hq, hkv, d, page, fmt, seed=0, extra=0, wide=0):
+    def __init__(self, wl, ctx, rows, hq, hkv, d, page, fmt, seed=0, extra=0, wide=0, dtype=None):
         g = torch.Generator().manual_seed(seed)
-        dtype = F32 if fmt == F32 else BF
+        dtype = dtype or (F32 if fmt == F32 else BF)
         self.ctx, self.rows = ctx, rows
         lens = [c + r for c, r in zip(ctx, rows)]
         need = [max(1, -(-n // page)) for n in lens]
@@ -219,6 +219,38 @@ def test_pages_that_are_none(wl, fmt):
         b = Batch(wl, [100, 90], rows, 4, 2, 64, 16, fmt, seed=5)
         b.cache.table[0, 2], b.cache.table[1, 0], b.cache.table[0, 5] = -1, b.cache.k.shape[0], 1 << 30
         b.check(wl)
+
+
+@pytest.mark.parametrize("fmt", [I8, E4])
+def test_fp32_queries_over_codes(wl, fmt):
+    for ctx, rows, hq, hkv, d, page in (([70, 0], [1, 90], 4, 2, 96, 16), ([1500], [3], 4, 1, 256, 64), ([40], [5], 2, 2, 16, 32)):
+        Batch(wl, ctx, rows, hq, hkv, d, page, fmt, seed=12, dtype=F32).check(wl, window=60)
+
+
+@pytest.mark.parametrize("fmt", [BF, I8, F32])
+@pytest.mark.parametrize("rows", [[2, 0, 1, 0], [60, 0, 41, 0]])
+def test_idle_sequences(wl, rows, fmt):
+    """Sequences of the batch without new tokens, with and without keys."""
+    b = Batch(wl, [30, 40, 100, 0], rows, 8, 4, 64, 16, fmt, seed=13, extra=1)
+    b.check(wl)
+    b.check(wl, mask="full")
+
+
+@pytest.mark.parametrize("fmt", [BF, E4, F32])
+@pytest.mark.parametrize("scale", [0.0, -0.3, 1.5])
+def test_scales(wl, scale, fmt):
+    """No scale, a negative one, and one whose scores make the running maximum climb."""
+    for ctx, rows, d in (([300, 20], [1, 3], 128), ([200], [150], 64), ([90], [40], 256)):
+        b = Batch(wl, ctx, rows, 4, 2, d, 16, fmt, seed=14)
+        b.scale = scale
+        b.check(wl)
+
+
+def test_pages_shared_by_sequences(wl):
+    """A common first page: both sequences read it."""
+    b = Batch(wl, [60, 60], [1, 1], 4, 2, 64, 16, BF, seed=15)
+    b.cache.table[1, :2] = b.cache.table[0, :2]
+    b.check(wl)
 
 
 def test_limits_of_the_launch(wl):

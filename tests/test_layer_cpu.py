@@ -145,6 +145,20 @@ def test_attention_refuses(wl, bad, status):
     assert wl.lib.wl_attention_workspace_bytes(ctypes.byref(a)) == 0
 
 
+def test_sizes_beyond_a_launch_are_refused(wl):
+    a = struct(wl.NormArgs, **(NORM | dict(T=(1 << 24) + 1, d=8, gate_ld=8, x_out=P[26], n_out=None)))
+    assert wl.lib.wl_norm_residual(ctypes.byref(a), None) == 2 and b"T=" in wl.lib.wl_last_error()
+    c = cache(wl, n_kv=1, d=16)
+    w = write_args(wl, c, T=(1 << 24) + 1, n_q=0, ldk=16, ldv=16)
+    assert wl.lib.wl_cache_write(ctypes.byref(w), None) == 2
+    a = attention_args(wl, cache(wl), max_kv=(1 << 30) + 1)
+    assert wl.lib.wl_attention(ctypes.byref(a), P[20], 1 << 40, None) == 2
+    big = cache(wl, n_seq=1 << 23)                             # 2^23 sequences of 2 key/value heads
+    a = attention_args(wl, big, q_start=P[24], kv_len=P[28])
+    assert wl.lib.wl_attention(ctypes.byref(a), P[20], 1 << 40, None) == 2
+    assert b"workgroups" in wl.lib.wl_last_error()
+
+
 def test_step_ops_refuse(wl):
     ops = (wl.StepOp * 1)()
     h = ctypes.c_void_p()
