@@ -49,7 +49,10 @@ struct Plan {
     Split sp;
 };
 
-constexpr int kMinChunk = 128;     // keys: 32 for each of four waves
+// Fewest keys of a piece. In us for 128, 256, 512 (bf16, 256 wide): one token of 4
+// heads over 4096 keys 23.5, 21.5, 22.8; 128 tokens of 4 heads over 4096 keys 38.3,
+// 34.3, 41.0; 512 tokens of 4 heads alone 25.8, 28.2, 36.6.
+constexpr int kMinChunk = 256;
 
 // Most query rows per key/value head of the few-row kernel. Above 16 it takes two
 // row tiles a wave, which at heads over 128 in bf16 does not fit its registers: 8
@@ -71,11 +74,16 @@ Plan plan_of(const AttnJob &a, int fmt, bool f32) {
     const int64_t units = (int64_t)a.c.n_seq * a.c.n_kv * (p.kind == kTile  ? (p.sp.rows + p.waves * kTileRows - 1) / (p.waves * kTileRows)
                                                           : p.kind == kF32 ? (p.sp.rows + kF32Rows - 1) / kF32Rows
                                                                            : 1);
-    const int64_t want = p.waves == 8 ? kWorkgroups / 2 : kWorkgroups;
+    // Enough pieces for every place on the card, one or two workgroups per CU; twice
+    // as many where the sequences alone take more than half of the places, since
+    // their lengths may be uneven.
+    const bool one_per_cu = p.waves == 8 || (p.kind == kFew && fmt == kFmtBf16 && a.c.d > 128);
+    const int64_t places = one_per_cu ? kWorkgroups / 2 : kWorkgroups;
+    const int64_t want = p.kind == kFew && 2 * units > places ? 2 * places : places;
     int64_t chunk = (span * units + want - 1) / want;
     if (chunk < kMinChunk) chunk = kMinChunk;
     if (chunk < (span + kMaxSplit - 1) / kMaxSplit) chunk = (span + kMaxSplit - 1) / kMaxSplit;
-    chunk = (chunk + 127) / 128 * 128;
+    chunk = (chunk + 127) / 128 * 128;   // whole 32s for each of four waves
     p.units = units;
     p.sp.chunk = (int)(chunk < (1 << 30) ? chunk : (1 << 30));
     p.sp.n_split = (int)((span + chunk - 1) / chunk);
