@@ -1,17 +1,23 @@
 // Attention with few query rows per key/value head (single tokens, small trees):
-// at most 32 rows, a row being a new token and one of the query heads that share
-// the key/value head.
+// at most 32 rows (16 over bf16 keys wider than 128), a row being a new token and
+// one of the query heads that share the key/value head.
 //
 // Bound by reading the keys and values once. Every wave works alone on a stretch
-// of keys, 32 at a time, with no barrier in its loop: K comes from global memory
-// straight into the registers of the score product (a key's row is the operand
-// row, 64 contiguous bytes per four lanes), V through a patch of LDS of the wave's
-// own that the transposing reads turn. The next 32 keys' loads are issued as soon
-// as the registers are free, so 32 keys of K and V per wave are under way while
-// the present ones are worked on. The matrix cores do 16 rows for the price of
-// one, so the weights are fed as a bf16 head plus a bf16 remainder and lose
-// nothing. The four waves of a workgroup join their outputs in LDS; workgroups
-// that divide a long sequence leave partial outputs that a second launch joins.
+// of keys, 32 at a time, with no barrier in its loop: K and V come as whole rows,
+// past the caches, into registers and from there into a patch of LDS of the wave's
+// own, where K is read as the operand of the score product and V through the
+// transposing reads. The next 32 keys' loads are issued as soon as the registers
+// are free, so 32 keys of K and V per wave are under way while the present ones are
+// worked on. The matrix cores do 16 rows for the price of one, so the weights are
+// fed as a bf16 head plus a bf16 remainder and lose nothing. The four waves of a
+// workgroup join their outputs in LDS; workgroups that divide a long sequence
+// leave partial outputs that a second launch joins.
+//
+// 32 streams of 2048 to 8192 keys, 32 query and 8 key/value heads of 256, one token
+// each: bf16 226 us (1.37 GB, 6.1 TB/s), int8 136 us, e4m3 130 us (0.69 GB, 5.3 TB/s);
+// a large copy moves 5.1 TB/s. Reading K straight into operand layout (16 rows x 64
+// bytes per load) gave 278 and 169 us; V alone as whole rows 262 and 146, both
+// 227 and 136.
 #include "wl_attn_mfma.h"
 
 namespace wl {

@@ -5,7 +5,19 @@
 // share every key that is staged; its four waves hold 32 rows each. Keys and
 // values pass through LDS 32 at a time, in two buffers: while the waves work on
 // one, the next 32 are on their way into the other. Queries, scores, weights and
-// outputs stay in registers from the first key to the last.
+// outputs stay in registers from the first key to the last, which at heads of 256
+// fills them: 128 for outputs, 64 for queries, 16 for scores, the rest for
+// operands on their way. Two workgroups share a CU, so that one's softmax and
+// barriers fall into the other's products.
+// int8 and e4m3 keys are widened to bf16 between two barriers (one workgroup's
+// widening under the other's products), or with 129 to 256 rows, as larger trees
+// have, by eight waves that share the widened keys.
+//
+// Bound by the issue of matrix products and of the softmax between them: 2048
+// tokens over 4000 keys, 32 query and 8 key/value heads of 256, causal: bf16
+// 204 us (201 GFLOP, 985 TFLOP/s; a large library product reaches 1335), e4m3
+// 266 us; 8192 over 8192 in bf16 989 us (1112 TFLOP/s). 48-token trees of 4
+// sequences over up to 16384 int8 keys: 183 us.
 #include "wl_attn_mfma.h"
 
 namespace wl {
