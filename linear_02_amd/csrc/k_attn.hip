@@ -11,14 +11,16 @@ template <class E>
 __global__ __launch_bounds__(256) void join_kernel(AttnJob a, Split sp) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int64_t w = (int64_t)blockIdx.x * 4 + wave;
-    const int64_t unit = w / sp.rows;
-    const int r = (int)(w - unit * sp.rows), s = (int)(unit / a.c.n_kv), kvh = (int)(unit % a.c.n_kv);
+    const int64_t per = (int64_t)a.max_q * a.group, unit = w / per;
+    const int r = (int)(w - unit * per), s = (int)(unit / a.c.n_kv), kvh = (int)(unit % a.c.n_kv);
     if (s >= a.c.n_seq) return;
     const Seq q = seq_of(a, s);
     if (r >= q.rows * a.group) return;
-    const int64_t first = unit * sp.n_split * sp.rows + r;
+    const int tile = r / sp.tile_rows;
+    const Parts parts = parts_of(a, sp, s, tile);
+    const int64_t first = part_row(a, sp, parts.first, kvh, tile, r), next = (int64_t)a.c.n_kv * sp.rows;
     float2 v = make_float2(kNegInf, 0.0f);
-    if (lane < sp.n_split) v = sp.ml[first + (int64_t)lane * sp.rows];
+    if (lane < parts.n) v = sp.ml[first + lane * next];
     float m = v.x;
 #pragma unroll
     for (int x = 1; x < 64; x <<= 1) m = fmaxf(m, __shfl_xor(m, x));
@@ -26,10 +28,10 @@ __global__ __launch_bounds__(256) void join_kernel(AttnJob a, Split sp) {
     const float l = wave_sum(up == 0.0f ? 0.0f : up * v.y);
     const int at = 4 * lane;
     f32x4 sum{0, 0, 0, 0};
-    for (int p = 0; p < sp.n_split; ++p) {
+    for (int p = 0; p < parts.n; ++p) {
         const float u = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(up), p));
         if (u == 0.0f) continue;
-        if (at < a.c.d) sum += *reinterpret_cast<const f32x4 *>(sp.part + (first + (int64_t)p * sp.rows) * a.c.d + at) * u;
+        if (at < a.c.d) sum += *reinterpret_cast<const f32x4 *>(sp.part + (first + p * next) * a.c.d + at) * u;
     }
     if (at >= a.c.d) return;
     const int i = r / a.group;
@@ -44,15 +46,15 @@ enum Kind { kFew, kTile, kF32 };
 
 struct Plan {
     Kind kind;
-    int waves;       // per workgroup
-    int64_t units;   // workgroups before the keys are divided
+    int waves;          // per workgroup
+    int64_t items;      // as in Split, which holds it if it is within a launch's limits
     Split sp;
 };
 
 // Fewest keys of a piece. In us for 128, 256, 512 (bf16, 256 wide): one token of 4
 // heads over 4096 keys 23.5, 21.5, 22.8; 128 tokens of 4 heads over 4096 keys 38.3,
 // 34.3, 41.0; 512 tokens of 4 heads alone 25.8, 28.2, 36.6.
-constexpr int kMinChunk = 256;
+static_assert(kMinChunk == 256, "measured as above");
 
 // Most query rows per key/value head of the few-row kernel. Above 16 it takes two
 // row tiles a wave, which at heads over 128 in bf16 does not fit its registers: 8
@@ -62,18 +64,18 @@ int few_rows(const AttnJob &a, int fmt) { return fmt == kFmtBf16 && a.c.d > 128 
 
 Plan plan_of(const AttnJob &a, int fmt, bool f32) {
     Plan p{};
-    p.sp.n_split = 1;
     p.kind = f32 ? kF32 : (int64_t)a.max_q * a.group > few_rows(a, fmt) ? kTile : kFew;
-    p.sp.rows = a.max_q * a.group;
+    const int64_t rows = a.max_q > 0 ? (int64_t)a.max_q * a.group : 1;
     // Codes are widened once per workgroup: eight waves where they hold all rows.
-    p.waves = p.kind == kTile && fmt != kFmtBf16 && p.sp.rows > 4 * kTileRows && p.sp.rows <= 8 * kTileRows ? 8 : 4;
+    p.waves = p.kind == kTile && fmt != kFmtBf16 && rows > 4 * kTileRows && rows <= 8 * kTileRows ? 8 : 4;
     // Most keys that the queries of one sequence see between them; pieces start at a multiple of 32.
     int64_t span = a.max_kv;
     if (a.mask == kMaskCausal && a.window && (int64_t)a.window + a.max_q < span) span = (int64_t)a.window + a.max_q;
     span += 31;
-    const int64_t units = (int64_t)a.c.n_seq * a.c.n_kv * (p.kind == kTile  ? (p.sp.rows + p.waves * kTileRows - 1) / (p.waves * kTileRows)
-                                                          : p.kind == kF32 ? (p.sp.rows + kF32Rows - 1) / kF32Rows
-                                                                           : 1);
+    p.sp.tile_rows = p.kind == kTile ? p.waves * kTileRows : p.kind == kF32 ? kF32Rows : (int)rows;
+    p.sp.rows = (int)(rows < p.sp.tile_rows ? rows : p.sp.tile_rows);
+    p.sp.tiles = (int)((rows + p.sp.tile_rows - 1) / p.sp.tile_rows);
+    const int64_t all_tiles = (int64_t)a.c.n_seq * p.sp.tiles, units = all_tiles * a.c.n_kv;
     // Enough pieces for every place on the card, one or two workgroups per CU; twice
     // as many where the sequences alone take more than half of the places, since
     // their lengths may be uneven.
@@ -83,34 +85,48 @@ Plan plan_of(const AttnJob &a, int fmt, bool f32) {
     int64_t chunk = (span * units + want - 1) / want;
     if (chunk < kMinChunk) chunk = kMinChunk;
     if (chunk < (span + kMaxSplit - 1) / kMaxSplit) chunk = (span + kMaxSplit - 1) / kMaxSplit;
-    chunk = (chunk + 127) / 128 * 128;   // whole 32s for each of four waves
-    p.units = units;
+    p.sp.step = p.kind == kFew ? 128 : 32;   // whole 32s, for each of four waves if they divide a piece
+    chunk = (chunk + 127) / 128 * 128;
     p.sp.chunk = (int)(chunk < (1 << 30) ? chunk : (1 << 30));
     p.sp.n_split = (int)((span + chunk - 1) / chunk);
+    p.items = all_tiles * p.sp.n_split;
+    p.sp.want = (int)want, p.sp.places = (int)places;
+    // Sequences differ in length, and max_kv is often what they may reach one day:
+    // the device divides them by their lengths, up to 64, a lane each. 8 sequences of
+    // 2048 keys, one token, 32 and 8 heads of 256: 27 us whether max_kv is 2048 or
+    // 131072 (in pieces of max_kv: 27 and 47 us); one of 4096 keys, 4 heads: 21 us (20
+    // and 45); 4 trees over 9201 to 16336 int8 keys: 157 us (183).
+    if (p.sp.n_split > 1 && a.c.n_seq <= 64) {
+        p.sp.planned = 1;
+        const int64_t most = (span + kMinChunk - 1) / kMinChunk;
+        p.sp.n_split = (int)(most < kMaxSplit ? most : kMaxSplit);
+        p.items = all_tiles * p.sp.n_split;
+        if (want / a.c.n_kv + all_tiles < p.items) p.items = want / a.c.n_kv + all_tiles;
+    }
+    p.sp.all_fit = p.items * a.c.n_kv <= kWorkgroups;
+    p.sp.items = (int)(p.items < (1 << 30) ? p.items : (1 << 30));
     return p;
 }
 
-size_t part_floats(const AttnJob &a, const Split &sp) {
-    return (size_t)a.c.n_seq * a.c.n_kv * sp.n_split * sp.rows;
-}
+size_t part_rows(const AttnJob &a, const Plan &p) { return (size_t)p.items * a.c.n_kv * p.sp.rows; }
 
 }  // namespace
 
 int64_t attention_workgroups(const AttnJob &a, int fmt, bool f32) {
     const Plan p = plan_of(a, fmt, f32);
-    return p.units * p.sp.n_split;
+    return p.items * a.c.n_kv;
 }
 
 size_t attention_scratch(const AttnJob &a, int fmt, bool f32) {
     const Plan p = plan_of(a, fmt, f32);
-    return p.sp.n_split > 1 ? part_floats(a, p.sp) * (a.c.d + 2) * 4 : 0;
+    return p.sp.n_split > 1 ? part_rows(a, p) * (a.c.d + 2) * 4 : 0;
 }
 
 hipError_t launch_attention(const AttnJob &a, int fmt, bool f32, void *ws, hipStream_t s) {
     Plan p = plan_of(a, fmt, f32);
     if (p.sp.n_split > 1) {
         p.sp.part = static_cast<float *>(ws);
-        p.sp.ml = reinterpret_cast<float2 *>(p.sp.part + part_floats(a, p.sp) * a.c.d);
+        p.sp.ml = reinterpret_cast<float2 *>(p.sp.part + part_rows(a, p) * a.c.d);
     }
     switch (p.kind) {
         case kFew: launch_few(a, fmt, p.sp, s); break;
@@ -119,7 +135,7 @@ hipError_t launch_attention(const AttnJob &a, int fmt, bool f32, void *ws, hipSt
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.sp.n_split == 1) return e;
-    const dim3 grid((unsigned)(((int64_t)a.c.n_seq * a.c.n_kv * p.sp.rows + 3) / 4));
+    const dim3 grid((unsigned)(((int64_t)a.c.n_seq * a.c.n_kv * a.max_q * a.group + 3) / 4));
     if (f32)
         hipLaunchKernelGGL((join_kernel<float>), grid, dim3(256), 0, s, a, p.sp);
     else

@@ -28,9 +28,11 @@ __global__ __launch_bounds__(256, 2) void f32_kernel(TileArgs x) {
     int(*range)[4] = reinterpret_cast<int(*)[4]>(lds + 2 * kSide + 128);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
-    const Work work = work_of(x);
-    const int kvh = work.kvh, split = work.split, tile = work.tile, s = work.s;
-    const Seq q = seq_of(a, s);
+    const int kvh = (int)blockIdx.x % a.c.n_kv;
+    Seq q;
+    const Work work = work_of(a, x.sp, (int)blockIdx.x / a.c.n_kv, q);
+    const int tile = work.tile, s = work.s;
+    if (s < 0) return;
     const int rows = q.rows * a.group, d = a.c.d, r = (tile * 4 + wave) * 16 + n;
     if (tile * kF32Rows >= rows) return;
 
@@ -64,8 +66,8 @@ __global__ __launch_bounds__(256, 2) void f32_kernel(TileArgs x) {
     hi = max(max(range[1][0], range[1][1]), max(range[1][2], range[1][3]));
     lo = __builtin_amdgcn_readfirstlane(lo) & ~31;
     hi = __builtin_amdgcn_readfirstlane(hi);
-    const int64_t c0 = (int64_t)lo + (int64_t)split * x.sp.chunk;
-    const int k0 = c0 < hi ? (int)c0 : hi, k1 = (int)min((int64_t)hi, c0 + x.sp.chunk), last = k1 - 1;
+    const int64_t c0 = (int64_t)lo + work.from;
+    const int k0 = c0 < hi ? (int)c0 : hi, k1 = (int)min((int64_t)hi, c0 + work.chunk), last = k1 - 1;
 
     if (k0 < k1) {
         const int32_t *table = a.c.table + (int64_t)s * a.c.max_pages;
@@ -112,7 +114,7 @@ __global__ __launch_bounds__(256, 2) void f32_kernel(TileArgs x) {
                     sc = mfma4(kf.z, qf[j].z, sc);
                     sc = mfma4(kf.w, qf[j].w, sc);
                 }
-                const uint32_t vis = !paged ? 0u : seen<1, 4>(x, 0, j0) & bits(0, k1 - j0);
+                const uint32_t vis = !paged ? 0u : seen<1, 4>(x, work, 0, j0) & bits(0, k1 - j0);
                 f32x4 vs{1, 1, 1, 1};
                 if (F != kFmtF32) {
                     sc *= *reinterpret_cast<const f32x4 *>(k_scale + 4 * g);
@@ -151,14 +153,12 @@ __global__ __launch_bounds__(256, 2) void f32_kernel(TileArgs x) {
             __syncthreads();
         }
     }
-    finish<float, F, DT, 1, 4>(argument_again<TileArgs>(), o, m, l, k0, k1);
+    finish<float, F, DT, 1, 4>(argument_again<TileArgs>(), work, o, m, l, k0, k1);
 }
 
 template <int F, int DT>
 void run(const AttnJob &a, const Split &sp, hipStream_t s) {
-    const int tiles = (sp.rows + kF32Rows - 1) / kF32Rows;
-    const int64_t blocks = (int64_t)a.c.n_seq * tiles * sp.n_split * a.c.n_kv;
-    hipLaunchKernelGGL((f32_kernel<F, DT>), dim3((unsigned)blocks), dim3(256), 0, s, TileArgs{a, sp, tiles, blocks <= kWorkgroups});
+    hipLaunchKernelGGL((f32_kernel<F, DT>), dim3((unsigned)sp.items * a.c.n_kv), dim3(256), 0, s, TileArgs{a, sp});
 }
 
 template <int F>

@@ -43,38 +43,23 @@ struct Few {
     float m[NT], l[NT];
 };
 
-struct FewArgs {
-    AttnJob a;
-    Split sp;
-};
-
-// Which keys a workgroup works on.
-struct FewWork {
-    int kvh, split, s;
-};
-__device__ __forceinline__ FewWork work_of(const FewArgs &x) {
-    const int u = blockIdx.x / x.a.c.n_kv;
-    return {(int)blockIdx.x % x.a.c.n_kv, u % x.sp.n_split, u / x.sp.n_split};
-}
-
 // Which of keys j0 .. j0 + 31 this lane's row of tile t sees, for trees: from the
 // arguments in memory, at the few steps that reach the tree.
-__device__ __forceinline__ uint32_t few_seen(const FewArgs &x, int t, int j0) {
-    const Seq q = seq_of(x.a, work_of(x).s);
+__device__ __forceinline__ uint32_t few_seen(const TileArgs &x, int s, int t, int j0) {
+    const Seq q = seq_of(x.a, s);
     return visible32(x.a, q, sees(x.a, q, (16 * t + (threadIdx.x & 15)) / x.a.group), j0);
 }
 
 // Joins the four waves' outputs, 16 rows at a time: row n of a wave's patch holds
 // what it has of row n.
 template <int F, int DT, int NT>
-__device__ __forceinline__ void join_waves(const FewArgs &args, const Seq &q, Few<F, DT, NT> &st, char *lds, int k0, int k1) {
+__device__ __forceinline__ void join_waves(const TileArgs &args, const Work &work, const Seq &q, Few<F, DT, NT> &st, char *lds, int k0, int k1) {
     typedef Few<F, DT, NT> P;
     const AttnJob &a = args.a;
     const Split &sp = args.sp;
     __shared__ float2 ml[kWaves][16];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15, g = lane >> 4;
-    const FewWork work = work_of(args);
-    const int kvh = work.kvh, split = work.split, s = work.s;
+    const int kvh = (int)blockIdx.x % a.c.n_kv;
     const int rows = q.rows * a.group, d = a.c.d;
     char *patch = lds + wave * P::kPatch;
 #pragma unroll
@@ -118,7 +103,7 @@ __device__ __forceinline__ void join_waves(const FewArgs &args, const Seq &q, Fe
                 sum += *reinterpret_cast<const f32x4 *>(lds + w * P::kPatch + (c * DT + at) * 4) * up;
             }
             if (sp.n_split > 1) {
-                const int64_t row = ((int64_t)(s * (int64_t)a.c.n_kv + kvh) * sp.n_split + split) * sp.rows + r;
+                const int64_t row = part_row(a, sp, work.part, kvh, 0, r);
                 *reinterpret_cast<f32x4 *>(sp.part + row * d + at) = sum;
                 if (at == 0) sp.ml[row] = make_float2(m, l);
             } else {
@@ -135,16 +120,18 @@ __device__ __forceinline__ void join_waves(const FewArgs &args, const Seq &q, Fe
 }
 
 template <int F, int DT, int NT>
-__global__ __launch_bounds__(256, (Few<F, DT, NT>::kPerCu)) void few_kernel(FewArgs args) {
+__global__ __launch_bounds__(256, (Few<F, DT, NT>::kPerCu)) void few_kernel(TileArgs args) {
     const AttnJob &a = args.a;
     typedef Few<F, DT, NT> P;
     constexpr bool kCodes = P::kCodes;
     __shared__ __align__(16) char lds[kWaves * P::kPatch];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
-    const FewWork work = work_of(args);
-    const int kvh = work.kvh, split = work.split, s = work.s;
-    const Seq q = seq_of(a, s);
+    const int kvh = (int)blockIdx.x % a.c.n_kv;
+    Seq q;
+    const Work work = work_of(a, args.sp, (int)blockIdx.x / a.c.n_kv, q);
+    const int s = work.s;
+    if (s < 0) return;
     const int rows = q.rows * a.group, d = a.c.d;
     const bool tree = a.mask == kMaskTree;
     if (rows == 0) return;
@@ -189,8 +176,8 @@ __global__ __launch_bounds__(256, (Few<F, DT, NT>::kPerCu)) void few_kernel(FewA
     lo = __builtin_amdgcn_readfirstlane(lo) & ~31;
     hi = __builtin_amdgcn_readfirstlane(hi);
     // This workgroup's keys, and this wave's: a stretch of whole 32s.
-    const int64_t c0 = (int64_t)lo + (int64_t)split * args.sp.chunk;
-    const int w0 = c0 < hi ? (int)c0 : hi, w1 = (int)min((int64_t)hi, c0 + args.sp.chunk);
+    const int64_t c0 = (int64_t)lo + work.from;
+    const int w0 = c0 < hi ? (int)c0 : hi, w1 = (int)min((int64_t)hi, c0 + work.chunk);
     const int per = ((w1 - w0 + kWaves * 32 - 1) / (kWaves * 32)) * 32;
     const int k0 = min(w0 + wave * per, w1), k1 = min(k0 + per, w1), last = k1 - 1;
 
@@ -327,7 +314,7 @@ __global__ __launch_bounds__(256, (Few<F, DT, NT>::kPerCu)) void few_kernel(FewA
                 for (int e = 0; e < 8; ++e) x[e] = sc[t][e >> 2][e & 3] * mul[e >> 2][e & 3];
                 if (!all) {
                     uint32_t vis = bits(row_lo[t] - j0, row_hi[t] - j0);
-                    if (tree) vis = few_seen(argument_again<FewArgs>(), t, j0);
+                    if (tree) vis = few_seen(argument_again<TileArgs>(), s, t, j0);
                     const uint32_t mine = (vis & valid & bits(0, k1 - j0)) >> (4 * g);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) x[e] = mine & (1u << (16 * (e >> 2) + (e & 3))) ? x[e] : kNegInf;
@@ -382,13 +369,12 @@ __global__ __launch_bounds__(256, (Few<F, DT, NT>::kPerCu)) void few_kernel(FewA
         }
     }
 
-    join_waves<F, DT, NT>(args, q, st, lds, k0, k1);
+    join_waves<F, DT, NT>(args, work, q, st, lds, k0, k1);
 }
 
 template <int F, int DT, int NT>
 void run(const AttnJob &a, const Split &sp, hipStream_t s) {
-    const int64_t blocks = (int64_t)a.c.n_seq * sp.n_split * a.c.n_kv;
-    hipLaunchKernelGGL((few_kernel<F, DT, NT>), dim3((unsigned)blocks), dim3(256), 0, s, FewArgs{a, sp});
+    hipLaunchKernelGGL((few_kernel<F, DT, NT>), dim3((unsigned)sp.items * a.c.n_kv), dim3(256), 0, s, TileArgs{a, sp});
 }
 
 template <int F>

@@ -16,8 +16,8 @@
 // Bound by the issue of matrix products and of the softmax between them: 2048
 // tokens over 4000 keys, 32 query and 8 key/value heads of 256, causal: bf16
 // 204 us (201 GFLOP, 985 TFLOP/s; a large library product reaches 1335), e4m3
-// 266 us; 8192 over 8192 in bf16 989 us (1112 TFLOP/s). 48-token trees of 4
-// sequences over up to 16384 int8 keys: 183 us.
+// 271 us; 8192 over 8192 in bf16 989 us (1112 TFLOP/s). Trees of up to 48 tokens of
+// 4 sequences over up to 16384 int8 keys: 157 us.
 #include "wl_attn_mfma.h"
 
 namespace wl {
@@ -53,9 +53,11 @@ __global__ __launch_bounds__(64 * NW, 2) void tile_kernel(TileArgs x) {
     int (*range)[NW] = reinterpret_cast<int (*)[NW]>(lds_all + kTail + 1024);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
-    const Work work = work_of(x);
-    const int kvh = work.kvh, split = work.split, tile = work.tile, s = work.s;
-    const Seq q = seq_of(a, s);
+    const int kvh = (int)blockIdx.x % a.c.n_kv;
+    Seq q;
+    const Work work = work_of(a, x.sp, (int)blockIdx.x / a.c.n_kv, q);
+    const int tile = work.tile, s = work.s;
+    if (s < 0) return;
     const int rows = q.rows * a.group, d = a.c.d, r0 = (tile * NW + wave) * 16 * kNT;
     if (tile * NW * 16 * kNT >= rows) return;
 
@@ -105,8 +107,8 @@ __global__ __launch_bounds__(64 * NW, 2) void tile_kernel(TileArgs x) {
     for (int w = 0; w < NW; ++w) lo = min(lo, range[0][w]), hi = max(hi, range[1][w]);
     lo = __builtin_amdgcn_readfirstlane(lo) & ~31;
     hi = __builtin_amdgcn_readfirstlane(hi);
-    const int64_t c0 = (int64_t)lo + (int64_t)split * x.sp.chunk;
-    const int k0 = c0 < hi ? (int)c0 : hi, k1 = (int)min((int64_t)hi, c0 + x.sp.chunk), last = k1 - 1;
+    const int64_t c0 = (int64_t)lo + work.from;
+    const int k0 = c0 < hi ? (int)c0 : hi, k1 = (int)min((int64_t)hi, c0 + work.chunk), last = k1 - 1;
 
     if (k0 < k1) {
         const int32_t *table = a.c.table + (int64_t)s * a.c.max_pages;
@@ -303,7 +305,7 @@ __global__ __launch_bounds__(64 * NW, 2) void tile_kernel(TileArgs x) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) x[e] = sc[t][e >> 2][e & 3];
                     if (!all) {
-                        const uint32_t mine = (seen<kNT, NW>(argument_again<TileArgs>(), 16 * t, j0) & valid & bits(0, k1 - j0)) >> (4 * g);
+                        const uint32_t mine = (seen<kNT, NW>(argument_again<TileArgs>(), work, 16 * t, j0) & valid & bits(0, k1 - j0)) >> (4 * g);
 #pragma unroll
                         for (int e = 0; e < 8; ++e) x[e] = mine & (1u << (16 * (e >> 2) + (e & 3))) ? x[e] : kNegInf;
                     }
@@ -368,14 +370,12 @@ __global__ __launch_bounds__(64 * NW, 2) void tile_kernel(TileArgs x) {
         }
     }
 
-    finish<uint16_t, F, DT, kNT, NW>(argument_again<TileArgs>(), o, m, l, k0, k1);
+    finish<uint16_t, F, DT, kNT, NW>(argument_again<TileArgs>(), work, o, m, l, k0, k1);
 }
 
 template <int F, int DT, int NW>
 void run(const AttnJob &a, const Split &sp, hipStream_t s) {
-    const int per = NW * 16 * kNT, tiles = (sp.rows + per - 1) / per;
-    const int64_t blocks = (int64_t)a.c.n_seq * tiles * sp.n_split * a.c.n_kv;
-    hipLaunchKernelGGL((tile_kernel<F, DT, NW>), dim3((unsigned)blocks), dim3(64 * NW), 0, s, TileArgs{a, sp, tiles, blocks <= kWorkgroups});
+    hipLaunchKernelGGL((tile_kernel<F, DT, NW>), dim3((unsigned)sp.items * a.c.n_kv), dim3(64 * NW), 0, s, TileArgs{a, sp});
 }
 
 template <int F, int NW>

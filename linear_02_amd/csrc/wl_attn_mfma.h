@@ -110,12 +110,23 @@ __device__ __forceinline__ uint32_t visible32(const AttnJob &a, const Seq &q, co
     return r | (x & bits(q.ctx - j0 > 0 ? q.ctx - j0 : 0, q.kv - j0));
 }
 
-// How the keys of a call are divided: every sequence and key/value head has
-// n_split pieces of `chunk` keys, counted from the first key any of its queries
-// sees. part: [unit][n_split][rows][d] unnormalised outputs, ml: the same without
+// How the work of a call is divided. A workgroup takes a tile of one sequence's
+// query rows, of one key/value head, over all its keys or a piece of them, counted
+// from the first key that a row of the tile sees. Pieces are of `chunk` keys, or
+// (planned) of a length that the workgroups derive from the lengths of all
+// sequences, which only the device knows.
+// part: [tile and piece][head][rows][d] unnormalised outputs; ml: the same without
 // [d], the reference maximum (power of two) and sum of each row.
 struct Split {
-    int n_split, chunk, rows;
+    int n_split;      // most pieces of a tile's keys; 1: undivided
+    int planned;      // whether the device chooses them
+    int chunk;        // keys of a piece, not planned
+    int step;         // a piece is a multiple of so many keys
+    int want, places; // workgroups wanted, workgroups that run at once
+    int tiles;        // of rows, most of a sequence
+    int tile_rows, rows;   // rows of a tile, rows kept of one (fewer if no sequence has so many)
+    int items;        // tiles and pieces at most, over all sequences
+    int all_fit;      // whether all workgroups are on the card at once
     float *part;
     float2 *ml;
 };
@@ -130,7 +141,6 @@ __device__ __forceinline__ T argument_again() {
 }
 
 constexpr int kWorkgroups = 512;   // wanted: two per CU
-constexpr int kMaxSplit = 64;     // one lane each in the join
 
 constexpr int kTileRows = 32;     // query rows per wave of the many-row kernel
 constexpr int kF32Rows = 64;      // of the fp32 kernel
@@ -144,35 +154,137 @@ void launch_f32(const AttnJob &a, int fmt, const Split &sp, hipStream_t s);
 struct TileArgs {
     AttnJob a;
     Split sp;
-    int tiles;     // of rows, per sequence and key/value head
-    int all_fit;   // whether all workgroups are on the card at once
 };
 
-// Which rows and keys a workgroup works on.
+// Which rows and keys a workgroup works on: keys from + 0 .. chunk - 1 behind the
+// first that a row sees. s < 0: none. part: place of its partial outputs.
 struct Work {
-    int kvh, split, tile, s;
+    int s, tile, part, from, chunk;
 };
-__device__ __forceinline__ Work work_of(const TileArgs &x) {
+
+// The lengths that a plan divides: this lane's sequence.
+struct Lengths {
+    int keys, tiles;   // keys that a tile's rows see at most, tiles of rows
+    Seq q;
+};
+__device__ __forceinline__ Lengths lengths_of(const AttnJob &a, const Split &sp, int lane) {
+    Lengths v{0, 0, seq_of(a, min(lane, a.c.n_seq - 1))};
+    if (lane >= a.c.n_seq || v.q.rows == 0) return v;
+    v.tiles = sp.tiles == 1 ? 1 : (unsigned)(v.q.rows * a.group + sp.tile_rows - 1) / sp.tile_rows;
+    v.keys = v.q.kv;
+    if (a.mask == kMaskCausal && a.window) v.keys = (int)min((int64_t)v.keys, (int64_t)a.window + v.q.rows + 31);
+    return v;
+}
+
+constexpr int kMinChunk = 256;     // fewest keys of a piece
+constexpr int kMaxSplit = 64;      // most pieces: one lane each in the join
+constexpr float kPieceCost = 96;   // of beginning and ending a piece, in keys
+
+// Keys of a piece at up to 64 sequences, a lane each: of 64 lengths, from that which
+// gives as many pieces as are wanted to three times that, the one with the least
+// time, rounds of workgroups x the time of one. Never shorter than the first, so
+// that there are at most want / n_kv + (all tiles) pieces; where 2^29 cuts it short,
+// no sequence has more than two.
+__device__ __forceinline__ int chunk_of(const AttnJob &a, const Split &sp, const Lengths &v, int lane) {
+    const float heads = (float)a.c.n_kv;
+    const float ideal = wave_sum((float)v.keys * (float)v.tiles) * heads * __builtin_amdgcn_rcpf((float)sp.want) * 1.0001f + 1.0f;
+    const float at = ideal * (1.0f + (float)lane * (1.0f / 32));
+    const int mine = max(((int)fminf(at, 0x1p29f) & -sp.step) + sp.step, kMinChunk);
+    const float inv = __builtin_amdgcn_rcpf((float)mine);
+    float pieces = 0.0f;
+    for (int j = 0; j < a.c.n_seq; ++j) {
+        const float keys = (float)__builtin_amdgcn_readlane(v.keys, j), tiles = (float)__builtin_amdgcn_readlane(v.tiles, j);
+        pieces += tiles * __builtin_ceilf(keys * inv);
+    }
+    const float cost = __builtin_ceilf(pieces * heads * __builtin_amdgcn_rcpf((float)sp.places) * (1.0f - 0x1p-20f)) * ((float)mine + kPieceCost);
+    float best = -cost;
+    best = fmaxf(best, dpp<0xB1>(best));    // quad_perm [1,0,3,2]
+    best = fmaxf(best, dpp<0x4E>(best));    // quad_perm [2,3,0,1]
+    best = fmaxf(best, dpp<0x141>(best));   // row_half_mirror
+    best = fmaxf(best, dpp<0x140>(best));   // row_mirror
+    best = groups_max(best);
+    const uint64_t which = __ballot(best == -cost);
+    return __builtin_amdgcn_readlane(mine, which ? __ffsll((unsigned long long)which) - 1 : 0);
+}
+
+// Pieces of this lane's sequence: never more than the keys over chunk rounded up
+// (the factor makes up for the reciprocal's error), and at least 1 if there are keys.
+__device__ __forceinline__ int pieces_of(const Lengths &v, int chunk) {
+    return (int)fminf(__builtin_ceilf((float)v.keys * __builtin_amdgcn_rcpf((float)chunk) * (1.0f - 0x1p-20f)), kMaxSplit);
+}
+
+__device__ __forceinline__ Work find_work(const AttnJob &a, const Split &sp, int i, Seq &q) {
     Work w;
-    int u = blockIdx.x;
-    w.kvh = u % x.a.c.n_kv;
-    u /= x.a.c.n_kv;
-    w.split = u % x.sp.n_split;
-    u /= x.sp.n_split;
-    // Under a causal mask later rows have more keys. The longest first, so that the
-    // short ones fill in; where all are on the card at once, two on a CU, the
-    // second half from the shortest up, so that a long and a short one share a CU.
-    const int i = u % x.tiles, half = (x.tiles + 1) / 2;
-    w.tile = x.all_fit && i >= half ? i - half : x.tiles - 1 - i;
-    w.s = u / x.tiles;
+    if (!sp.planned) {
+        const int split = i % sp.n_split, u = i / sp.n_split;
+        // Under a causal mask later rows have more keys. The longest first, so that the
+        // short ones fill in; where all are on the card at once, two on a CU, the
+        // second half from the shortest up, so that a long and a short one share a CU.
+        const int t = u % sp.tiles, half = (sp.tiles + 1) / 2;
+        w.tile = sp.all_fit && t >= half ? t - half : sp.tiles - 1 - t;
+        w.s = u / sp.tiles;
+        w.part = (w.s * sp.tiles + w.tile) * sp.n_split + split;
+        w.chunk = sp.chunk;
+        w.from = split * sp.chunk;
+        q = seq_of(a, w.s);
+        return w;
+    }
+    const int lane = threadIdx.x & 63;
+    const Lengths v = lengths_of(a, sp, lane);
+    const int n = pieces_of(v, chunk_of(a, sp, v, lane)), all = n * v.tiles;
+    int first = 0;
+    w.s = -1;
+    for (int j = 0; j < a.c.n_seq; ++j) {
+        const int here = __builtin_amdgcn_readlane(all, j);
+        if (i < first + here) {
+            w.s = j;
+            break;
+        }
+        first += here;
+    }
+    if (w.s < 0) return w;
+    const int pieces = __builtin_amdgcn_readlane(n, w.s), keys = __builtin_amdgcn_readlane(v.keys, w.s);
+    const int t = sp.tiles == 1 ? 0 : (unsigned)(i - first) / pieces, split = i - first - t * pieces;
+    w.tile = __builtin_amdgcn_readlane(v.tiles, w.s) - 1 - t;
+    w.part = first + w.tile * pieces + split;
+    w.chunk = (int)((unsigned)(keys + pieces - 1) / pieces + sp.step - 1) & -sp.step;   // all pieces alike
+    q = {w.s, __builtin_amdgcn_readlane(v.q.q0, w.s), __builtin_amdgcn_readlane(v.q.rows, w.s), __builtin_amdgcn_readlane(v.q.m, w.s),
+         __builtin_amdgcn_readlane(v.q.kv, w.s), __builtin_amdgcn_readlane(v.q.ctx, w.s)};
+    w.from = split * w.chunk;
     return w;
+}
+
+// Work of the i-th tile and piece of a call, in scalar registers.
+__device__ __forceinline__ Work work_of(const AttnJob &a, const Split &sp, int i, Seq &q) {
+    const Work w = find_work(a, sp, i, q);
+    return {__builtin_amdgcn_readfirstlane(w.s), __builtin_amdgcn_readfirstlane(w.tile), __builtin_amdgcn_readfirstlane(w.part),
+            __builtin_amdgcn_readfirstlane(w.from), __builtin_amdgcn_readfirstlane(w.chunk)};
+}
+
+// Where the pieces of a tile lie, for the join: n from `first` on.
+struct Parts {
+    int first, n;
+};
+__device__ __forceinline__ Parts parts_of(const AttnJob &a, const Split &sp, int s, int tile) {
+    if (!sp.planned) return {(s * sp.tiles + tile) * sp.n_split, sp.n_split};
+    const int lane = threadIdx.x & 63;
+    const Lengths v = lengths_of(a, sp, lane);
+    const int n = pieces_of(v, chunk_of(a, sp, v, lane)), all = n * v.tiles;
+    int first = 0;
+    for (int j = 0; j < s; ++j) first += __builtin_amdgcn_readlane(all, j);
+    const int pieces = __builtin_amdgcn_readlane(n, s);
+    return {first + tile * pieces, pieces};
+}
+
+// Row r of a sequence in the partial outputs.
+__device__ __forceinline__ int64_t part_row(const AttnJob &a, const Split &sp, int part, int kvh, int tile, int r) {
+    return ((int64_t)part * a.c.n_kv + kvh) * sp.rows + r - tile * sp.tile_rows;
 }
 
 // Which of keys j0 .. j0 + 31 this lane's row of tile `first` (0 or 16) sees. Only
 // at the edges of what the wave's rows see, so from the arguments in memory.
 template <int NT, int NW>
-__device__ __forceinline__ uint32_t seen(const TileArgs &x, int first, int j0) {
-    const Work work = work_of(x);
+__device__ __forceinline__ uint32_t seen(const TileArgs &x, const Work &work, int first, int j0) {
     const Seq q = seq_of(x.a, work.s);
     const int r = (work.tile * NW + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * 16 * NT + first + (threadIdx.x & 15);
     return visible32(x.a, q, sees(x.a, q, r / x.a.group), j0);
@@ -180,13 +292,12 @@ __device__ __forceinline__ uint32_t seen(const TileArgs &x, int first, int j0) {
 
 // Writes a wave's outputs: lane (n, g) holds elements 16 b + 4 g .. + 3 of row n.
 template <class E, int F, int DT, int NT, int NW>
-__device__ __forceinline__ void finish(const TileArgs &x, f32x4 (&o)[NT][DT / 16], float (&m)[NT], float (&l)[NT], int k0, int k1) {
+__device__ __forceinline__ void finish(const TileArgs &x, const Work &work, f32x4 (&o)[NT][DT / 16], float (&m)[NT], float (&l)[NT], int k0, int k1) {
     constexpr int kBlocks = DT / 16;
     const AttnJob &a = x.a;
     const Split &sp = x.sp;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15, g = lane >> 4;
-    const Work work = work_of(x);
-    const int kvh = work.kvh, split = work.split, tile = work.tile, s = work.s;
+    const int kvh = (int)blockIdx.x % a.c.n_kv, tile = work.tile, s = work.s;
     const Seq q = seq_of(a, s);
     const int rows = q.rows * a.group, d = a.c.d, r0 = (tile * NW + wave) * 16 * NT;
 #pragma unroll
@@ -203,7 +314,7 @@ __device__ __forceinline__ void finish(const TileArgs &x, f32x4 (&o)[NT][DT / 16
         odd |= odd >> 32;
         odd |= odd >> 16;
         const uint32_t again = (uint32_t)odd & 0xFFFFu;
-        const int64_t part = ((int64_t)(s * (int64_t)a.c.n_kv + kvh) * sp.n_split + split) * sp.rows;
+        const int64_t part = part_row(a, sp, work.part, kvh, tile, 0);
         auto row_out = [&](int r) {
             const int i = r / a.group;
             return static_cast<E *>(a.o) + (size_t)(q.q0 + i) * a.ldo + (size_t)(kvh * a.group + r - i * a.group) * d;

@@ -357,3 +357,25 @@ def test_far_pages_of_a_large_pool(wl):
         o = wl.wl_attention(torch.cat((q, q)), c, ints([0, rows, 2 * rows]), ints([n, n]), rows, n, d ** -0.5)
         torch.cuda.synchronize()
         assert torch.equal(o[:rows], o[rows:]) and torch.isfinite(o).all() and (o != 0).any()
+
+
+@pytest.mark.parametrize("fmt", [BF, I8, F32])
+@pytest.mark.parametrize("rows, n_seq", [(1, 64), (1, 65), (5, 7), (40, 3), (40, 64), (70, 2)])
+def test_uneven_sequences_far_below_the_limit(wl, rows, n_seq, fmt):
+    """Lengths from one key to thousands, some sequences idle, and a max_kv that none
+    of them comes near: pieces follow the lengths, up to 64 sequences."""
+    g = torch.Generator().manual_seed(rows * 100 + n_seq)
+    ctx = [int(v) for v in torch.randint(0, 300, (n_seq,), generator=g)]
+    ctx[n_seq // 2], ctx[-1] = 2900, 0
+    new = [0 if i % 5 == 4 else 1 + int(torch.randint(0, rows, (1,), generator=g)) for i in range(n_seq)]
+    b = Batch(wl, ctx, new, 4, 1, 128, 16, fmt)
+    b.check(wl)
+    tree, pos = b.tree()
+    b.check(wl, "tree", mask="tree", tree=tree, q_pos=pos)
+    b.check(wl, "window", window=600)
+    # a longer page table, whose further entries are no pages
+    c = b.cache
+    table = torch.nn.functional.pad(c.table, (0, (1 << 16) - c.table.shape[1]), value=-1)
+    b.cache = wl.Cache(c.k, c.v, table, c.k_scale, c.v_scale)
+    b.max_q, b.max_kv = rows, 1 << 20
+    b.check(wl, "max_kv of a million")
