@@ -95,7 +95,7 @@ Plan plan_of(const AttnJob &a, int fmt, bool f32) {
     // the device divides them by their lengths, up to 64, a lane each. 8 sequences of
     // 2048 keys, one token, 32 and 8 heads of 256: 27 us whether max_kv is 2048 or
     // 131072 (in pieces of max_kv: 27 and 47 us); one of 4096 keys, 4 heads: 21 us (20
-    // and 45); 4 trees over 9201 to 16336 int8 keys: 157 us (183).
+    // and 45); 4 trees over 9201 to 16336 int8 keys: 157 us (183; 131 since their rows are shared alike).
     if (p.sp.n_split > 1 && a.c.n_seq <= 64) {
         p.sp.planned = 1;
         const int64_t most = (span + kMinChunk - 1) / kMinChunk;

@@ -33,7 +33,8 @@ __global__ __launch_bounds__(256, 2) void f32_kernel(TileArgs x) {
     const Work work = work_of(a, x.sp, (int)blockIdx.x / a.c.n_kv, q);
     const int tile = work.tile, s = work.s;
     if (s < 0) return;
-    const int rows = q.rows * a.group, d = a.c.d, r = (tile * 4 + wave) * 16 + n;
+    auto rows_of = [](int tile, int) { return WaveRows{(tile * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * 16, 1}; };
+    const int rows = q.rows * a.group, d = a.c.d, r = rows_of(tile, 0).first + n;
     if (tile * kF32Rows >= rows) return;
 
     // Queries of this lane's row: elements 16 j + 4 g .. + 3 are those of step (j, e).
@@ -114,7 +115,7 @@ __global__ __launch_bounds__(256, 2) void f32_kernel(TileArgs x) {
                     sc = mfma4(kf.z, qf[j].z, sc);
                     sc = mfma4(kf.w, qf[j].w, sc);
                 }
-                const uint32_t vis = !paged ? 0u : seen<1, 4>(x, work, 0, j0) & bits(0, k1 - j0);
+                const uint32_t vis = !paged ? 0u : seen(x, work, rows_of, 0, j0) & bits(0, k1 - j0);
                 f32x4 vs{1, 1, 1, 1};
                 if (F != kFmtF32) {
                     sc *= *reinterpret_cast<const f32x4 *>(k_scale + 4 * g);
@@ -153,7 +154,7 @@ __global__ __launch_bounds__(256, 2) void f32_kernel(TileArgs x) {
             __syncthreads();
         }
     }
-    finish<float, F, DT, 1, 4>(argument_again<TileArgs>(), work, o, m, l, k0, k1);
+    finish<float, F, DT, 1>(argument_again<TileArgs>(), work, rows_of, o, m, l, k0, k1);
 }
 
 template <int F, int DT>

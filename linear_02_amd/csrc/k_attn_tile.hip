@@ -2,7 +2,7 @@
 //
 // A workgroup takes 128 query rows of one key/value head, a row being a new token
 // and one of the query heads that share the key/value head, so that those heads
-// share every key that is staged; its four waves hold 32 rows each. Keys and
+// share every key that is staged; its four waves hold up to 32 each. Keys and
 // values pass through LDS 32 at a time, in two buffers: while the waves work on
 // one, the next 32 are on their way into the other. Queries, scores, weights and
 // outputs stay in registers from the first key to the last, which at heads of 256
@@ -17,14 +17,19 @@
 // tokens over 4000 keys, 32 query and 8 key/value heads of 256, causal: bf16
 // 204 us (201 GFLOP, 985 TFLOP/s; a large library product reaches 1335), e4m3
 // 271 us; 8192 over 8192 in bf16 989 us (1112 TFLOP/s). Trees of up to 48 tokens of
-// 4 sequences over up to 16384 int8 keys: 157 us.
+// 4 sequences over up to 16384 int8 keys: 131 us.
 #include "wl_attn_mfma.h"
 
 namespace wl {
 
 namespace {
 
-constexpr int kNT = 2;      // tiles of 16 query rows per wave
+constexpr int kNT = 2;      // tiles of 16 query rows per wave, at most
+
+template <int N>
+struct Tiles {
+    static constexpr int n = N;
+};
 
 template <int F, int DT, int NW>
 __global__ __launch_bounds__(64 * NW, 2) void tile_kernel(TileArgs x) {
@@ -58,8 +63,23 @@ __global__ __launch_bounds__(64 * NW, 2) void tile_kernel(TileArgs x) {
     const Work work = work_of(a, x.sp, (int)blockIdx.x / a.c.n_kv, q);
     const int tile = work.tile, s = work.s;
     if (s < 0) return;
-    const int rows = q.rows * a.group, d = a.c.d, r0 = (tile * NW + wave) * 16 * kNT;
+    const int rows = q.rows * a.group, d = a.c.d;
     if (tile * NW * 16 * kNT >= rows) return;
+    // The four SIMDs share the rows alike: 16 for each of the first four waves, as
+    // many for each of the next four, and so on, up to 32 per wave. With 32 per wave
+    // from the first on, two SIMDs had twice the work at 192 rows, and the trees above
+    // took 157 us; at 48 rows only two SIMDs had any (8 trees of 12 tokens over up to
+    // 8192 int8 keys: 89, now 74 us). bf16 keys come as fast as memory gives them at so
+    // few rows (97 and 94 us), and prompts lose 1 % to the second loop.
+    auto rows_of = [](int tile, int rows) {
+        const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), tile0 = tile * NW * 16 * kNT;
+        if (!kCodes) return WaveRows{tile0 + 16 * kNT * w, kNT};
+        const int all = (rows - tile0 + 15) / 16, early = all > NW ? 2 : 1;
+        if (NW == 4 || w < 4) return WaveRows{tile0 + 16 * w * early, early};
+        const int late = all > 12 ? 2 : 1;
+        return WaveRows{tile0 + 16 * (4 * early + (w - 4) * late), late};
+    };
+    const int r0 = rows_of(tile, rows).first, nt = rows_of(tile, rows).tiles;
 
     u32x4 qf[kNT][kSteps];
     f32x4 o[kNT][kBlocks];
@@ -70,7 +90,7 @@ __global__ __launch_bounds__(64 * NW, 2) void tile_kernel(TileArgs x) {
 #pragma unroll
     for (int t = 0; t < kNT; ++t) {
         const int r = r0 + 16 * t + n, i = r / a.group;
-        const bool on = r < rows;
+        const bool on = t < nt && r < rows;
         const uint16_t *qp = static_cast<const uint16_t *>(a.q) + (size_t)(q.q0 + (on ? i : 0)) * a.ldq +
                              (size_t)(kvh * a.group + (on ? r - i * a.group : 0)) * d;
 #pragma unroll
@@ -216,6 +236,113 @@ __global__ __launch_bounds__(64 * NW, 2) void tile_kernel(TileArgs x) {
         // Operand addresses within a buffer.
         const int at_k = n * kRow + ((g ^ fk(n)) << 4);      // piece 4 k + g: ^ (k << 6)
         const int key_v = 4 * g + (n >> 2), at_v = key_v * kRow + ((key_v & kMaskV) << 5) + 8 * (n & 3);   // block b: ^ (b << 5)
+        // 32 keys for the first N tiles of this wave's rows.
+        auto attend = [&](auto tiles, const int &j0, const int &step, const uint32_t &valid) {
+            constexpr int N = decltype(tiles)::n;
+            // Formed anew in every step: held in registers through the loop, the
+            // places of all operands would leave none to read ahead into.
+            const int in = kTwo ? (step & 1) * 2 * kSide : 0;
+            int kb = at_k + in, vb = at_v + in + kSide;
+            asm volatile("" : "+v"(kb), "+v"(vb));
+            // The products at a higher wave priority than the softmax between them: the
+            // other wave of the SIMD does its softmax meanwhile (and the compiler keeps the
+            // phases apart: 322 -> 294 us for the prompt above in e4m3).
+            __builtin_amdgcn_s_setprio(1);
+            f32x4 sc[N][2];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+#pragma unroll
+                for (int t = 0; t < N; ++t) sc[t][b] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int k = 0; k < kSteps; ++k) {
+                    const u32x4 kf = *reinterpret_cast<const u32x4 *>(lds_all + (kb ^ ((k & 3) << 6)) + (k >> 2) * 256 + b * 16 * kRow);
+#pragma unroll
+                    for (int t = 0; t < N; ++t) sc[t][b] = mfma16(kf, qf[t][k], sc[t][b]);
+                }
+            }
+            // Operand reads run kAhead ahead of the products: left to itself the
+            // compiler reads each operand right before its use.
+            __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
+#pragma unroll
+            for (int i = 0; i < 2 * kSteps; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x008, N, 0);
+                if (i + kAhead < 2 * kSteps) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            }
+            __builtin_amdgcn_s_setprio(0);
+            if (kCodes) {
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const f32x4 ks = *reinterpret_cast<const f32x4 *>(&lds_scale[step & 3][0][16 * b + 4 * g]);
+#pragma unroll
+                    for (int t = 0; t < N; ++t) sc[t][b] *= ks;
+                }
+            }
+            u32x4 ph[N];
+            const bool all = j0 >= flo && j0 + 32 <= min(fhi, k1) && valid == 0xFFFFFFFFu;
+#pragma unroll
+            for (int t = 0; t < N; ++t) {
+                float x[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = sc[t][e >> 2][e & 3];
+                if (!all) {
+                    const uint32_t mine = (seen(argument_again<TileArgs>(), work, rows_of, t, j0) & valid & bits(0, k1 - j0)) >> (4 * g);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = mine & (1u << (16 * (e >> 2) + (e & 3))) ? x[e] : kNegInf;
+                }
+                float top = x[0];
+#pragma unroll
+                for (int e = 1; e < 8; ++e) top = fmaxf(top, x[e]);
+                top = groups_max(top);
+                top = top == kNegInf ? top : top * scale2;
+                if (__any(top > m[t] + 8.0f)) {
+                    // The reference moves only when a score passes it by 2^8: sums stay in range.
+                    const float now = fmaxf(m[t], top), up = now == m[t] ? 1.0f : __builtin_amdgcn_exp2f(m[t] - now);
+                    m[t] = now;
+                    l[t] *= up;
+#pragma unroll
+                    for (int b = 0; b < kBlocks; ++b) o[t][b] *= up;
+                }
+                const float ref = m[t] == kNegInf ? 0.0f : m[t];
+                float p[8];
+                f32x4 vm[2];
+                if (kCodes) {
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) vm[b] = *reinterpret_cast<const f32x4 *>(&lds_scale[step & 3][1][16 * b + 4 * g]);
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[e], scale2, -ref));
+                    if (kCodes) {
+                        l[t] += p[e];
+                        p[e] = p[e] == 0.0f ? 0.0f : p[e] * vm[e >> 2][e & 3];
+                    }
+                }
+                ph[t] = u32x4{pack2(p[0], p[1]), pack2(p[2], p[3]), pack2(p[4], p[5]), pack2(p[6], p[7])};
+                if (!kCodes) {
+                    // the sum of the weights as the product will use them
+                    constexpr uint32_t kOnes = 0x3F803F80u;
+                    l[t] = dot2(ph[t].x, kOnes, l[t]);
+                    l[t] = dot2(ph[t].y, kOnes, l[t]);
+                    l[t] = dot2(ph[t].z, kOnes, l[t]);
+                    l[t] = dot2(ph[t].w, kOnes, l[t]);
+                }
+            }
+            __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b) {
+                const char *p = lds_all + (vb ^ ((b & 7) << 5)) + (b >> 3) * 256;
+                const u32x2 x = read_tr16(p), y = read_tr16(p + 16 * kRow);
+#pragma unroll
+                for (int t = 0; t < N; ++t) o[t][b] = mfma16(u32x4{x.x, x.y, y.x, y.y}, ph[t], o[t][b]);
+            }
+            __builtin_amdgcn_sched_group_barrier(0x100, 2 * kAhead, 1);
+#pragma unroll
+            for (int i = 0; i < kBlocks; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x008, N, 1);
+                if (i + kAhead < kBlocks) __builtin_amdgcn_sched_group_barrier(0x100, 2, 1);
+            }
+            __builtin_amdgcn_s_setprio(0);
+        };
         // Step n is fetched into buffer n % 2 while step n - 1 is worked on, and has
         // landed for every wave behind the barrier at that step's end. Codes take one
         // more step: fetched, then widened into their buffer. With eight waves the two
@@ -233,144 +360,50 @@ __global__ __launch_bounds__(64 * NW, 2) void tile_kernel(TileArgs x) {
             look(min(k0 + 64, last));
         }
         __syncthreads();
-        int step = 0;
-        for (int j0 = k0; j0 < k1; j0 += 32, ++step) {
-            const bool more = j0 + 32 < k1;
-            // Codes of the step after next, once the next step's are widened.
-            auto advance = [&]() {
-                if (!more) return;
-                land(step + 1);
-                if (j0 + 64 < k1) {
-                    fetch(j0 + 64, step + 2);
-                    look(min(j0 + 96, last));
+        // Waves of a workgroup with one and with two tiles walk in loops of their own and
+        // meet at every barrier: each loop has the same ones, as often.
+        auto walk = [&](auto tiles) {
+            int step = 0;
+            for (int j0 = k0; j0 < k1; j0 += 32, ++step) {
+                const bool more = j0 + 32 < k1;
+                // Codes of the step after next, once the next step's are widened.
+                auto advance = [&]() {
+                    if (!more) return;
+                    land(step + 1);
+                    if (j0 + 64 < k1) {
+                        fetch(j0 + 64, step + 2);
+                        look(min(j0 + 96, last));
+                    }
+                };
+                if (kCodes && !kTwo) {
+                    land(step);
+                    valid = valid_in;
                 }
-            };
-            if (kCodes && !kTwo) {
-                land(step);
-                valid = valid_in;
+                if (!(kCodes && kTwo)) {
+                    if (more) {
+                        fetch(j0 + 32, step + 1);
+                        look(min(j0 + 64, last));
+                    }
+                } else if (wave < 4) {
+                    advance();
+                }
+                if (kCodes && !kTwo) __syncthreads();
+                if (j0 + 31 >= wlo && j0 < whi) {
+                    attend(tiles, j0, step, valid);
+                }
+                if (!kCodes && more) land(step + 1);
+                if (kCodes && kTwo && wave >= 4) advance();
+                if (kTwo) valid = kCodes ? valid_next : valid_in, valid_next = valid_in;
+                __syncthreads();
             }
-            if (!(kCodes && kTwo)) {
-                if (more) {
-                    fetch(j0 + 32, step + 1);
-                    look(min(j0 + 64, last));
-                }
-            } else if (wave < 4) {
-                advance();
-            }
-            if (kCodes && !kTwo) __syncthreads();
-            if (j0 + 31 >= wlo && j0 < whi) {
-                // Formed anew in every step: held in registers through the loop, the
-                // places of all operands would leave none to read ahead into.
-                const int in = kTwo ? (step & 1) * 2 * kSide : 0;
-                int kb = at_k + in, vb = at_v + in + kSide;
-                asm volatile("" : "+v"(kb), "+v"(vb));
-                // The products at a higher wave priority than the softmax between them: the
-                // other wave of the SIMD does its softmax meanwhile (and the compiler keeps the
-                // phases apart: 322 -> 294 us for the prompt above in e4m3).
-                __builtin_amdgcn_s_setprio(1);
-                f32x4 sc[kNT][2];
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-#pragma unroll
-                    for (int t = 0; t < kNT; ++t) sc[t][b] = f32x4{0, 0, 0, 0};
-#pragma unroll
-                    for (int k = 0; k < kSteps; ++k) {
-                        const u32x4 kf = *reinterpret_cast<const u32x4 *>(lds_all + (kb ^ ((k & 3) << 6)) + (k >> 2) * 256 + b * 16 * kRow);
-#pragma unroll
-                        for (int t = 0; t < kNT; ++t) sc[t][b] = mfma16(kf, qf[t][k], sc[t][b]);
-                    }
-                }
-                // Operand reads run kAhead ahead of the products: left to itself the
-                // compiler reads each operand right before its use.
-                __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
-#pragma unroll
-                for (int i = 0; i < 2 * kSteps; ++i) {
-                    __builtin_amdgcn_sched_group_barrier(0x008, kNT, 0);
-                    if (i + kAhead < 2 * kSteps) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-                }
-                __builtin_amdgcn_s_setprio(0);
-                if (kCodes) {
-#pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        const f32x4 ks = *reinterpret_cast<const f32x4 *>(&lds_scale[step & 3][0][16 * b + 4 * g]);
-#pragma unroll
-                        for (int t = 0; t < kNT; ++t) sc[t][b] *= ks;
-                    }
-                }
-                u32x4 ph[kNT];
-                const bool all = j0 >= flo && j0 + 32 <= min(fhi, k1) && valid == 0xFFFFFFFFu;
-#pragma unroll
-                for (int t = 0; t < kNT; ++t) {
-                    float x[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = sc[t][e >> 2][e & 3];
-                    if (!all) {
-                        const uint32_t mine = (seen<kNT, NW>(argument_again<TileArgs>(), work, 16 * t, j0) & valid & bits(0, k1 - j0)) >> (4 * g);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) x[e] = mine & (1u << (16 * (e >> 2) + (e & 3))) ? x[e] : kNegInf;
-                    }
-                    float top = x[0];
-#pragma unroll
-                    for (int e = 1; e < 8; ++e) top = fmaxf(top, x[e]);
-                    top = groups_max(top);
-                    top = top == kNegInf ? top : top * scale2;
-                    if (__any(top > m[t] + 8.0f)) {
-                        // The reference moves only when a score passes it by 2^8: sums stay in range.
-                        const float now = fmaxf(m[t], top), up = now == m[t] ? 1.0f : __builtin_amdgcn_exp2f(m[t] - now);
-                        m[t] = now;
-                        l[t] *= up;
-#pragma unroll
-                        for (int b = 0; b < kBlocks; ++b) o[t][b] *= up;
-                    }
-                    const float ref = m[t] == kNegInf ? 0.0f : m[t];
-                    float p[8];
-                    f32x4 vm[2];
-                    if (kCodes) {
-#pragma unroll
-                        for (int b = 0; b < 2; ++b) vm[b] = *reinterpret_cast<const f32x4 *>(&lds_scale[step & 3][1][16 * b + 4 * g]);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[e], scale2, -ref));
-                        if (kCodes) {
-                            l[t] += p[e];
-                            p[e] = p[e] == 0.0f ? 0.0f : p[e] * vm[e >> 2][e & 3];
-                        }
-                    }
-                    ph[t] = u32x4{pack2(p[0], p[1]), pack2(p[2], p[3]), pack2(p[4], p[5]), pack2(p[6], p[7])};
-                    if (!kCodes) {
-                        // the sum of the weights as the product will use them
-                        constexpr uint32_t kOnes = 0x3F803F80u;
-                        l[t] = dot2(ph[t].x, kOnes, l[t]);
-                        l[t] = dot2(ph[t].y, kOnes, l[t]);
-                        l[t] = dot2(ph[t].z, kOnes, l[t]);
-                        l[t] = dot2(ph[t].w, kOnes, l[t]);
-                    }
-                }
-                __builtin_amdgcn_s_setprio(1);
-#pragma unroll
-                for (int b = 0; b < kBlocks; ++b) {
-                    const char *p = lds_all + (vb ^ ((b & 7) << 5)) + (b >> 3) * 256;
-                    const u32x2 x = read_tr16(p), y = read_tr16(p + 16 * kRow);
-#pragma unroll
-                    for (int t = 0; t < kNT; ++t) o[t][b] = mfma16(u32x4{x.x, x.y, y.x, y.y}, ph[t], o[t][b]);
-                }
-                __builtin_amdgcn_sched_group_barrier(0x100, 2 * kAhead, 1);
-#pragma unroll
-                for (int i = 0; i < kBlocks; ++i) {
-                    __builtin_amdgcn_sched_group_barrier(0x008, kNT, 1);
-                    if (i + kAhead < kBlocks) __builtin_amdgcn_sched_group_barrier(0x100, 2, 1);
-                }
-                __builtin_amdgcn_s_setprio(0);
-            }
-            if (!kCodes && more) land(step + 1);
-            if (kCodes && kTwo && wave >= 4) advance();
-            if (kTwo) valid = kCodes ? valid_next : valid_in, valid_next = valid_in;
-            __syncthreads();
-        }
+        };
+        if (!kCodes || nt == kNT)
+            walk(Tiles<kNT>());
+        else
+            walk(Tiles<1>());
     }
 
-    finish<uint16_t, F, DT, kNT, NW>(argument_again<TileArgs>(), work, o, m, l, k0, k1);
+    finish<uint16_t, F, DT, kNT>(argument_again<TileArgs>(), work, rows_of, o, m, l, k0, k1);
 }
 
 template <int F, int DT, int NW>

@@ -281,27 +281,35 @@ __device__ __forceinline__ int64_t part_row(const AttnJob &a, const Split &sp, i
     return ((int64_t)part * a.c.n_kv + kvh) * sp.rows + r - tile * sp.tile_rows;
 }
 
-// Which of keys j0 .. j0 + 31 this lane's row of tile `first` (0 or 16) sees. Only
+// Rows of a wave: `tiles` tiles of 16 from `first` on.
+struct WaveRows {
+    int first, tiles;
+};
+
+// Which of keys j0 .. j0 + 31 this lane's row of the wave's tile t sees. Only
 // at the edges of what the wave's rows see, so from the arguments in memory.
-template <int NT, int NW>
-__device__ __forceinline__ uint32_t seen(const TileArgs &x, const Work &work, int first, int j0) {
+template <class R>
+__device__ __forceinline__ uint32_t seen(const TileArgs &x, const Work &work, R rows_of, int t, int j0) {
     const Seq q = seq_of(x.a, work.s);
-    const int r = (work.tile * NW + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * 16 * NT + first + (threadIdx.x & 15);
+    const int r = rows_of(work.tile, q.rows * x.a.group).first + 16 * t + (threadIdx.x & 15);
     return visible32(x.a, q, sees(x.a, q, r / x.a.group), j0);
 }
 
 // Writes a wave's outputs: lane (n, g) holds elements 16 b + 4 g .. + 3 of row n.
-template <class E, int F, int DT, int NT, int NW>
-__device__ __forceinline__ void finish(const TileArgs &x, const Work &work, f32x4 (&o)[NT][DT / 16], float (&m)[NT], float (&l)[NT], int k0, int k1) {
+template <class E, int F, int DT, int NT, class R>
+__device__ __forceinline__ void finish(const TileArgs &x, const Work &work, R rows_of, f32x4 (&o)[NT][DT / 16], float (&m)[NT], float (&l)[NT], int k0, int k1) {
     constexpr int kBlocks = DT / 16;
     const AttnJob &a = x.a;
     const Split &sp = x.sp;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15, g = lane >> 4;
+    const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
     const int kvh = (int)blockIdx.x % a.c.n_kv, tile = work.tile, s = work.s;
     const Seq q = seq_of(a, s);
-    const int rows = q.rows * a.group, d = a.c.d, r0 = (tile * NW + wave) * 16 * NT;
+    const int rows = q.rows * a.group, d = a.c.d;
+    const WaveRows mine = rows_of(tile, rows);
+    const int r0 = mine.first;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
+        if (t >= mine.tiles) break;
         const int r = r0 + 16 * t + n;
         l[t] = groups_sum(l[t]);
         float check = l[t] * 0.0f;
