@@ -57,14 +57,14 @@ struct Plan {
 static_assert(kMinChunk == 256, "measured as above");
 
 // Most query rows per key/value head of the few-row kernel. Above 16 it takes two
-// row tiles a wave, which at heads over 128 in bf16 does not fit its registers: 8
-// trees of 8 tokens and 4 heads over 8192 keys took 189 us so, 103 us in the tile
-// kernel; at 128 wide 55 and 58 us, in int8 at 256 wide 96 and 117 us.
-int few_rows(const AttnJob &a, int fmt) { return fmt == kFmtBf16 && a.c.d > 128 ? 16 : 32; }
+// row tiles a wave, which at heads over 128 fill or pass its registers: 8 trees of 8
+// tokens and 4 heads over up to 8192 keys of 256 took 189 us so in bf16 and 92 in
+// int8, 103 and 75 us in the tile kernel; at 128 wide 57 and 58 us, 45 and 55 us.
+int few_rows(const AttnJob &a) { return a.c.d > 128 ? 16 : 32; }
 
 Plan plan_of(const AttnJob &a, int fmt, bool f32) {
     Plan p{};
-    p.kind = f32 ? kF32 : (int64_t)a.max_q * a.group > few_rows(a, fmt) ? kTile : kFew;
+    p.kind = f32 ? kF32 : (int64_t)a.max_q * a.group > few_rows(a) ? kTile : kFew;
     const int64_t rows = a.max_q > 0 ? (int64_t)a.max_q * a.group : 1;
     // Codes are widened once per workgroup: eight waves where they hold all rows.
     p.waves = p.kind == kTile && fmt != kFmtBf16 && rows > 4 * kTileRows && rows <= 8 * kTileRows ? 8 : 4;

@@ -1,5 +1,5 @@
 // Attention with few query rows per key/value head (single tokens, small trees):
-// at most 32 rows (16 over bf16 keys wider than 128), a row being a new token and
+// at most 32 rows (16 of heads wider than 128), a row being a new token and
 // one of the query heads that share the key/value head.
 //
 // Bound by reading the keys and values once. Every wave works alone on a stretch
@@ -35,8 +35,8 @@ struct Few {
     static constexpr int kBlocks = DT / 16;             // 16-wide blocks of the output
     static constexpr int kRow = kCodes ? DT : 2 * DT;   // bytes of a V row in LDS
     // Two workgroups per CU where 256 registers hold the 32 keys' K and V beside the outputs.
-    static constexpr int kPerCu = DT == 256 && (NT == 2 || !kCodes) ? 1 : 2;
-    static_assert(kCodes || DT < 256 || NT == 1, "32 rows of 256 and bf16 keys do not fit the registers");
+    static constexpr int kPerCu = DT == 256 && !kCodes ? 1 : 2;
+    static_assert(DT < 256 || NT == 1, "32 rows of 256 do not fit the registers");
     static constexpr int kPatch = 64 * kRow > 64 * DT ? 64 * kRow : 64 * DT;   // LDS bytes per wave: 32 rows of V and of K, or 16 output rows fp32
     u32x4 q[NT][kSteps];
     f32x4 o[NT][kBlocks];
@@ -384,8 +384,6 @@ void pick(const AttnJob &a, const Split &sp, hipStream_t s) {
         two ? run<F, 64, 2>(a, sp, s) : run<F, 64, 1>(a, sp, s);
     else if (a.c.d <= 128)
         two ? run<F, 128, 2>(a, sp, s) : run<F, 128, 1>(a, sp, s);
-    else if (F != kFmtBf16 && two)
-        run<F, F == kFmtBf16 ? 128 : 256, 2>(a, sp, s);
     else
         run<F, 256, 1>(a, sp, s);
 }
