@@ -153,3 +153,85 @@ def test_step_of_other_operations(wl):
     with pytest.raises(wl.WlError) as e:
         wl.LayerStep([rope, bad])
     assert "call 1" in str(e.value)
+
+
+def attended(wl, g, n_seq, keys):
+    """One token each of n_seq sequences over a filled cache: cache, queries, lengths
+    and an attention that divides its keys."""
+    cache = wl.new_cache(n_seq * keys // 64, 1, 64, D, torch.arange(n_seq * keys // 64, dtype=torch.int32, device=DEV).view(n_seq, -1))
+    T = n_seq * keys
+    k, v = (torch.randn(T, D, generator=g).to(torch.bfloat16).to(DEV) for _ in range(2))
+    at = torch.arange(T, dtype=torch.int32, device=DEV)
+    wl.wl_cache_write(cache, k, v, at // keys, at % keys)
+    q = torch.randn(n_seq, 4 * D, generator=g).to(torch.bfloat16).to(DEV)
+    lens = ints([keys - 100 * s for s in range(n_seq)])
+    att = wl.attention_call(q, cache, ints(list(range(n_seq + 1))), lens, 1, keys, D ** -0.5)
+    return cache, q, lens, att
+
+
+def test_step_with_divided_attention_beside_projections(wl):
+    """One workspace for a projection and attentions that leave partial outputs in it."""
+    g = torch.Generator().manual_seed(11)
+    theta = inputs.theta(g, 4 * D, 4 * D, 32)
+    dev = wl.theta_to(theta, DEV)
+    cache, q, lens, att = attended(wl, g, 3, 2048)
+    assert wl.lib.wl_attention_workspace_bytes(att.args) > wl.SYNC_BYTES
+    y = torch.empty(3, 4 * D, dtype=torch.bfloat16, device=DEV)
+    again = wl.attention_call(y, cache, ints([0, 1, 2, 3]), lens, 1, 2048, D ** -0.5)
+    step = wl.LayerStep([att, (wl.OP_LINEAR, [dev], att.out, y), again])
+    for it in range(4):
+        q.copy_(torch.randn(3, 4 * D, generator=g).to(torch.bfloat16))
+        lens -= it
+        step.launch()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in (att.out, y, again.out)]
+        att.launch()
+        wl.wl_linear(dev, att.out, y=y)
+        again.launch()
+        torch.cuda.synchronize()
+        for a, b, what in zip(got, (att.out, y, again.out), ("first", "projection", "second")):
+            assert torch.equal(a, b), (it, what)
+        want, slack = ref.attention(q, cache, ints([0, 1, 2, 3]), lens, D ** -0.5)
+        ref.assert_near(att.out, want, slack, "first")
+        want, slack = ref.attention(y, cache, ints([0, 1, 2, 3]), lens, D ** -0.5)
+        ref.assert_near(again.out, want, slack, "second")
+    step.close()
+
+
+def test_two_streams_at_once(wl):
+    """Attentions with divided keys, norms and cache reads on two streams, each with
+    buffers of its own: the same bits as alone."""
+    g = torch.Generator().manual_seed(12)
+    work, alone = [], []
+    for n_seq in (2, 5):
+        cache, q, _, att = attended(wl, g, n_seq, 4096)
+        n = wl.norm_call(q)
+        slots = torch.arange(n_seq, dtype=torch.int32, device=DEV)
+        work.append([n, att, wl.cache_read_call(cache, slots, slots * 700)])
+    torch.cuda.synchronize()
+    for calls in work:
+        for c in calls:
+            c.launch()
+        torch.cuda.synchronize()
+        alone.append([[t.clone() for t in outputs(c)] for c in calls])
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        for calls in work:
+            for c in calls:
+                for t in outputs(c):
+                    t.fill_(7)
+        torch.cuda.synchronize()
+        for i in range(3):
+            for calls, s in zip(work, streams):
+                with torch.cuda.stream(s):
+                    calls[i].launch()
+        torch.cuda.synchronize()
+        for calls, want in zip(work, alone):
+            for c, w in zip(calls, want):
+                for a, b in zip(outputs(c), w):
+                    assert torch.equal(a, b)
+
+
+def outputs(call):
+    out = call.out if isinstance(call.out, (tuple, list)) else [call.out]
+    return [t for t in out if t is not None]
