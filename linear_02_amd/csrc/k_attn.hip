@@ -46,7 +46,7 @@ enum Kind { kFew, kTile, kF32 };
 
 struct Plan {
     Kind kind;
-    int waves;          // per workgroup
+    int waves, tiles;   // per workgroup, tiles of query rows per wave
     int64_t items;      // as in Split, which holds it if it is within a launch's limits
     Split sp;
 };
@@ -66,13 +66,21 @@ Plan plan_of(const AttnJob &a, int fmt, bool f32) {
     Plan p{};
     p.kind = f32 ? kF32 : (int64_t)a.max_q * a.group > few_rows(a) ? kTile : kFew;
     const int64_t rows = a.max_q > 0 ? (int64_t)a.max_q * a.group : 1;
-    // Codes are widened once per workgroup: eight waves where they hold all rows.
-    p.waves = p.kind == kTile && fmt != kFmtBf16 && rows > 4 * kTileRows && rows <= 8 * kTileRows ? 8 : 4;
     // Most keys that the queries of one sequence see between them; pieces start at a multiple of 32.
     int64_t span = a.max_kv;
     if (a.mask == kMaskCausal && a.window && (int64_t)a.window + a.max_q < span) span = (int64_t)a.window + a.max_q;
     span += 31;
-    p.sp.tile_rows = p.kind == kTile ? p.waves * kTileRows : p.kind == kF32 ? kF32Rows : (int)rows;
+    // One tile a wave, with its exact weights, for 64 rows, and for calls whose tiles of
+    // 64 rows in pieces of kMinChunk keys fit the card about twice: with two tiles much of
+    // it would be idle. Prompts of 512 tokens in bf16, 4 heads over 1 of 256: 28.1 us with
+    // two, 23.5 with one; 32 over 8: 41.5 and 38.9; 4 trees of 60 tokens over 2000 keys,
+    // int8, 128 wide: 45.9 and 42.1. (2 x 256 tokens over 4000 keys, 4096 such pieces: 66
+    // with either; prompts of thousands read each key half as often with two.)
+    const int64_t pieces = (int64_t)a.c.n_seq * a.c.n_kv * ((rows + 4 * kTileRows - 1) / (4 * kTileRows)) * ((span + kMinChunk - 1) / kMinChunk);
+    p.tiles = rows > 4 * kTileRows && pieces > 2 * kWorkgroups ? 2 : 1;
+    // Codes are widened once per workgroup: eight waves where they hold all rows.
+    p.waves = p.tiles == 2 && fmt != kFmtBf16 && rows > 8 * kTileRows && rows <= 16 * kTileRows && p.kind == kTile ? 8 : 4;
+    p.sp.tile_rows = p.kind == kTile ? p.waves * p.tiles * kTileRows : p.kind == kF32 ? kF32Rows : (int)rows;
     p.sp.rows = (int)(rows < p.sp.tile_rows ? rows : p.sp.tile_rows);
     p.sp.tiles = (int)((rows + p.sp.tile_rows - 1) / p.sp.tile_rows);
     const int64_t all_tiles = (int64_t)a.c.n_seq * p.sp.tiles, units = all_tiles * a.c.n_kv;
@@ -130,7 +138,7 @@ hipError_t launch_attention(const AttnJob &a, int fmt, bool f32, void *ws, hipSt
     }
     switch (p.kind) {
         case kFew: launch_few(a, fmt, p.sp, s); break;
-        case kTile: launch_tile(a, fmt, p.sp, p.waves, s); break;
+        case kTile: launch_tile(a, fmt, p.sp, p.waves, p.tiles, s); break;
         default: launch_f32(a, fmt, p.sp, s);
     }
     const hipError_t e = hipGetLastError();

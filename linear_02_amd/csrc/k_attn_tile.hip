@@ -24,14 +24,13 @@ namespace wl {
 
 namespace {
 
-constexpr int kNT = 2;      // tiles of 16 query rows per wave, at most
-
 template <int N>
 struct Tiles {
     static constexpr int n = N;
 };
 
-template <int F, int DT, int NW>
+// kNT: tiles of 16 query rows per wave, at most.
+template <int F, int DT, int NW, int kNT>
 __global__ __launch_bounds__(64 * NW, 2) void tile_kernel(TileArgs x) {
     const AttnJob &a = x.a;
     constexpr bool kCodes = F == kFmtInt8 || F == kFmtE4m3;
@@ -42,7 +41,10 @@ __global__ __launch_bounds__(64 * NW, 2) void tile_kernel(TileArgs x) {
     // Operands read ahead of the products. 2048 tokens over 4000 keys, 32 heads of
     // 256, in us for 2, 3, 4, 6: bf16 213, 207, 208, 260; e4m3 266, 295, 294, 323 (the
     // registers that more would take are not there).
-    constexpr int kAhead = kCodes ? 2 : 3;
+    constexpr int kAhead = kNT == 1 ? 4 : kCodes ? 2 : 3;
+    // With one tile there are registers and time for the weights as a bf16 head plus a
+    // bf16 remainder, which lose nothing.
+    constexpr bool kExact = kNT == 1;
     // LDS place of 16-byte piece c of a row: c ^ f(row), such that the 16 lanes that
     // one pass of a read serves meet all 64 banks.
     auto fk = [](int r) { return DT >= 128 ? r & 15 : (r >> 1) & 7; };
@@ -73,7 +75,7 @@ __global__ __launch_bounds__(64 * NW, 2) void tile_kernel(TileArgs x) {
     // few rows (97 and 94 us), and prompts lose 1 % to the second loop.
     auto rows_of = [](int tile, int rows) {
         const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), tile0 = tile * NW * 16 * kNT;
-        if (!kCodes) return WaveRows{tile0 + 16 * kNT * w, kNT};
+        if (!kCodes || kNT == 1) return WaveRows{tile0 + 16 * kNT * w, kNT};
         const int all = (rows - tile0 + 15) / 16, early = all > NW ? 2 : 1;
         if (NW == 4 || w < 4) return WaveRows{tile0 + 16 * w * early, early};
         const int late = all > 12 ? 2 : 1;
@@ -277,7 +279,7 @@ __global__ __launch_bounds__(64 * NW, 2) void tile_kernel(TileArgs x) {
                     for (int t = 0; t < N; ++t) sc[t][b] *= ks;
                 }
             }
-            u32x4 ph[N];
+            u32x4 ph[N], pl[N];
             const bool all = j0 >= flo && j0 + 32 <= min(fhi, k1) && valid == 0xFFFFFFFFu;
 #pragma unroll
             for (int t = 0; t < N; ++t) {
@@ -312,13 +314,17 @@ __global__ __launch_bounds__(64 * NW, 2) void tile_kernel(TileArgs x) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[e], scale2, -ref));
-                    if (kCodes) {
-                        l[t] += p[e];
-                        p[e] = p[e] == 0.0f ? 0.0f : p[e] * vm[e >> 2][e & 3];
-                    }
+                    if (kCodes || kExact) l[t] += p[e];
+                    if (kCodes) p[e] = p[e] == 0.0f ? 0.0f : p[e] * vm[e >> 2][e & 3];
                 }
                 ph[t] = u32x4{pack2(p[0], p[1]), pack2(p[2], p[3]), pack2(p[4], p[5]), pack2(p[6], p[7])};
-                if (!kCodes) {
+                if (kExact) {
+                    uint32_t r[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        r[e] = pack2(p[2 * e] - bf16_f(ph[t][e] & 0xFFFFu), p[2 * e + 1] - __uint_as_float(ph[t][e] & 0xFFFF0000u));
+                    pl[t] = u32x4{r[0], r[1], r[2], r[3]};
+                } else if (!kCodes) {
                     // the sum of the weights as the product will use them
                     constexpr uint32_t kOnes = 0x3F803F80u;
                     l[t] = dot2(ph[t].x, kOnes, l[t]);
@@ -333,12 +339,15 @@ __global__ __launch_bounds__(64 * NW, 2) void tile_kernel(TileArgs x) {
                 const char *p = lds_all + (vb ^ ((b & 7) << 5)) + (b >> 3) * 256;
                 const u32x2 x = read_tr16(p), y = read_tr16(p + 16 * kRow);
 #pragma unroll
-                for (int t = 0; t < N; ++t) o[t][b] = mfma16(u32x4{x.x, x.y, y.x, y.y}, ph[t], o[t][b]);
+                for (int t = 0; t < N; ++t) {
+                    o[t][b] = mfma16(u32x4{x.x, x.y, y.x, y.y}, ph[t], o[t][b]);
+                    if (kExact) o[t][b] = mfma16(u32x4{x.x, x.y, y.x, y.y}, pl[t], o[t][b]);
+                }
             }
             __builtin_amdgcn_sched_group_barrier(0x100, 2 * kAhead, 1);
 #pragma unroll
             for (int i = 0; i < kBlocks; ++i) {
-                __builtin_amdgcn_sched_group_barrier(0x008, N, 1);
+                __builtin_amdgcn_sched_group_barrier(0x008, kExact ? 2 * N : N, 1);
                 if (i + kAhead < kBlocks) __builtin_amdgcn_sched_group_barrier(0x100, 2, 1);
             }
             __builtin_amdgcn_s_setprio(0);
@@ -397,7 +406,7 @@ __global__ __launch_bounds__(64 * NW, 2) void tile_kernel(TileArgs x) {
                 __syncthreads();
             }
         };
-        if (!kCodes || nt == kNT)
+        if (!kCodes || kNT == 1 || nt == kNT)
             walk(Tiles<kNT>());
         else
             walk(Tiles<1>());
@@ -406,28 +415,38 @@ __global__ __launch_bounds__(64 * NW, 2) void tile_kernel(TileArgs x) {
     finish<uint16_t, F, DT, kNT>(argument_again<TileArgs>(), work, rows_of, o, m, l, k0, k1);
 }
 
-template <int F, int DT, int NW>
+template <int F, int DT, int NW, int NT>
 void run(const AttnJob &a, const Split &sp, hipStream_t s) {
-    hipLaunchKernelGGL((tile_kernel<F, DT, NW>), dim3((unsigned)sp.items * a.c.n_kv), dim3(64 * NW), 0, s, TileArgs{a, sp});
+    hipLaunchKernelGGL((tile_kernel<F, DT, NW, NT>), dim3((unsigned)sp.items * a.c.n_kv), dim3(64 * NW), 0, s, TileArgs{a, sp});
 }
 
-template <int F, int NW>
+template <int F, int NW, int NT>
 void pick(const AttnJob &a, const Split &sp, hipStream_t s) {
     if (a.c.d <= 64)
-        run<F, 64, NW>(a, sp, s);
+        run<F, 64, NW, NT>(a, sp, s);
     else if (a.c.d <= 128)
-        run<F, 128, NW>(a, sp, s);
+        run<F, 128, NW, NT>(a, sp, s);
     else
-        run<F, 256, NW>(a, sp, s);
+        run<F, 256, NW, NT>(a, sp, s);
+}
+
+template <int F>
+void pick(const AttnJob &a, const Split &sp, int waves, int tiles, hipStream_t s) {
+    if (tiles == 1)
+        pick<F, 4, 1>(a, sp, s);
+    else if (waves == 8)
+        pick<F, F == kFmtBf16 ? 4 : 8, 2>(a, sp, s);
+    else
+        pick<F, 4, 2>(a, sp, s);
 }
 
 }  // namespace
 
-void launch_tile(const AttnJob &a, int fmt, const Split &sp, int waves, hipStream_t s) {
+void launch_tile(const AttnJob &a, int fmt, const Split &sp, int waves, int tiles, hipStream_t s) {
     switch (fmt) {
-        case kFmtBf16: pick<kFmtBf16, 4>(a, sp, s); break;
-        case kFmtInt8: waves == 8 ? pick<kFmtInt8, 8>(a, sp, s) : pick<kFmtInt8, 4>(a, sp, s); break;
-        default: waves == 8 ? pick<kFmtE4m3, 8>(a, sp, s) : pick<kFmtE4m3, 4>(a, sp, s);
+        case kFmtBf16: pick<kFmtBf16>(a, sp, waves, tiles, s); break;
+        case kFmtInt8: pick<kFmtInt8>(a, sp, waves, tiles, s); break;
+        default: pick<kFmtE4m3>(a, sp, waves, tiles, s);
     }
 }
 
