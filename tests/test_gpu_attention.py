@@ -27,6 +27,8 @@ class Batch:
     """Sequences with the given earlier keys and new tokens over a shuffled cache
     whose unused slots and pages hold NaN."""
 
+    far = False   # whether max_kv is a large limit, as a recorded step has it
+
     def __init__(self, wl, ctx, rows, hq, hkv, d, page, fmt, seed=0, extra=0, wide=0, dtype=None):
         g = torch.Generator().manual_seed(seed)
         dtype = dtype or (F32 if fmt == F32 else BF)
@@ -56,6 +58,10 @@ class Batch:
         self.q = q[:, wide:]
         self.max_q, self.max_kv, self.scale = max(max(rows), 1), max(max(lens), 1), d ** -0.5
         self.g = g
+        if self.far:
+            self.max_kv = 1 << 18
+            table = torch.nn.functional.pad(c.table, (0, self.max_kv // page - c.table.shape[1]), value=-1)
+            self.cache = wl.Cache(c.k, c.v, table, c.k_scale, c.v_scale)
 
     def tree(self):
         """A random tree per sequence: (words, positions)."""
@@ -379,3 +385,43 @@ def test_uneven_sequences_far_below_the_limit(wl, rows, n_seq, fmt):
     b.cache = wl.Cache(c.k, c.v, table, c.k_scale, c.v_scale)
     b.max_q, b.max_kv = rows, 1 << 20
     b.check(wl, "max_kv of a million")
+
+
+@pytest.fixture
+def far(monkeypatch):
+    """A max_kv at which calls of more than 64 rows per head are taken to be large:
+    32 rows per wave, and eight waves at 129 to 256 rows over int8 and e4m3."""
+    monkeypatch.setattr(Batch, "far", True)
+
+
+@pytest.mark.parametrize("fmt", [BF, I8, E4, F32])
+@pytest.mark.parametrize("case", [c for c in range(len(CASES)) if max(CASES[c][1]) > 1 and not CASES[c][6]])
+def test_causal_under_a_large_limit(wl, far, case, fmt):
+    test_causal(wl, case, fmt)
+
+
+@pytest.mark.parametrize("fmt", [BF, I8, E4, F32])
+@pytest.mark.parametrize("d, rows, hq", [(64, [70, 1, 64], 4), (128, [24, 25, 3], 8), (256, [64, 33, 0], 3), (256, [90, 30, 100], 2),
+                                         (96, [256, 17, 129], 1), (256, [48, 31, 35], 4), (256, [40, 200, 16], 1)])
+def test_shares_of_the_rows(wl, far, d, rows, hq, fmt):
+    """Rows of a head from a wave's to several workgroups', by sequences that differ."""
+    print(f"attention rows {rows} {hq} {d} {fmt}", flush=True)
+    b = Batch(wl, [33, 400, 77], rows, hq, 1, d, 32, fmt, seed=21, extra=1)
+    b.check(wl)
+    words, pos = b.tree()
+    b.check(wl, "tree", tree=words, q_pos=pos, window=60)
+    b.check(wl, "full", mask="full")
+
+
+@pytest.mark.parametrize("fmt", [BF, I8, E4, F32])
+def test_unseen_and_absent_keys_under_a_large_limit(wl, far, fmt):
+    for rows in ([150, 40], [100, 3], [60, 60]):
+        test_nan_and_infinity_of_unseen_keys(wl, fmt, rows)
+    test_pages_that_are_none(wl, fmt)
+    test_queries_without_keys(wl, fmt)
+
+
+@pytest.mark.parametrize("fmt", [BF, E4, F32])
+@pytest.mark.parametrize("scale", [0.0, -0.3, 1.5])
+def test_scales_under_a_large_limit(wl, far, scale, fmt):
+    test_scales(wl, scale, fmt)
