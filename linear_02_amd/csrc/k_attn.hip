@@ -76,7 +76,7 @@ Plan plan_of(const AttnJob &a, int fmt, bool f32) {
     // two, 23.5 with one; 32 over 8: 41.5 and 38.9; 4 trees of 60 tokens over 2000 keys,
     // int8, 128 wide: 45.9 and 42.1. (2 x 256 tokens over 4000 keys, 4096 such pieces: 66
     // with either; prompts of thousands read each key half as often with two.)
-    const int64_t pieces = (int64_t)a.c.n_seq * a.c.n_kv * ((rows + 4 * kTileRows - 1) / (4 * kTileRows)) * ((span + kMinChunk - 1) / kMinChunk);
+    const double pieces = (double)a.c.n_seq * a.c.n_kv * ((rows + 4 * kTileRows - 1) / (4 * kTileRows)) * ((span + kMinChunk - 1) / kMinChunk);
     p.tiles = rows > 4 * kTileRows && pieces > 2 * kWorkgroups ? 2 : 1;
     // Codes are widened once per workgroup: eight waves where they hold all rows.
     p.waves = p.tiles == 2 && fmt != kFmtBf16 && rows > 8 * kTileRows && rows <= 16 * kTileRows && p.kind == kTile ? 8 : 4;
@@ -103,7 +103,7 @@ Plan plan_of(const AttnJob &a, int fmt, bool f32) {
     // the device divides them by their lengths, up to 64, a lane each. 8 sequences of
     // 2048 keys, one token, 32 and 8 heads of 256: 27 us whether max_kv is 2048 or
     // 131072 (in pieces of max_kv: 27 and 47 us); one of 4096 keys, 4 heads: 21 us (20
-    // and 45); 4 trees over 9201 to 16336 int8 keys: 157 us (183; 131 since their rows are shared alike).
+    // and 45); 4 trees over 9201 to 16336 int8 keys: 157 us (183).
     if (p.sp.n_split > 1 && a.c.n_seq <= 64) {
         p.sp.planned = 1;
         const int64_t most = (span + kMinChunk - 1) / kMinChunk;

@@ -2,8 +2,8 @@
 //
 // A workgroup takes 128 query rows of one key/value head, a row being a new token
 // and one of the query heads that share the key/value head, so that those heads
-// share every key that is staged; its four waves hold up to 32 each. Keys and
-// values pass through LDS 32 at a time, in two buffers: while the waves work on
+// share every key that is staged; its four waves hold up to 32 each. (64 rows, 16 a
+// wave, where a head has no more or the card would be half idle.) Keys and values pass through LDS 32 at a time, in two buffers: while the waves work on
 // one, the next 32 are on their way into the other. Queries, scores, weights and
 // outputs stay in registers from the first key to the last, which at heads of 256
 // fills them: 128 for outputs, 64 for queries, 16 for scores, the rest for
@@ -16,8 +16,8 @@
 // Bound by the issue of matrix products and of the softmax between them: 2048
 // tokens over 4000 keys, 32 query and 8 key/value heads of 256, causal: bf16
 // 204 us (201 GFLOP, 985 TFLOP/s; a large library product reaches 1335), e4m3
-// 271 us; 8192 over 8192 in bf16 989 us (1112 TFLOP/s). Trees of up to 48 tokens of
-// 4 sequences over up to 16384 int8 keys: 131 us.
+// 270 us; 8192 over 8192 in bf16 989 us (1112 TFLOP/s). Trees of up to 48 tokens of
+// 4 sequences over up to 16384 int8 keys: 128 us and 10 for the join.
 #include "wl_attn_mfma.h"
 
 namespace wl {
