@@ -2,8 +2,9 @@
 //
 // A workgroup takes 128 query rows of one key/value head, a row being a new token
 // and one of the query heads that share the key/value head, so that those heads
-// share every key that is staged; its four waves hold up to 32 each. (64 rows, 16 a
-// wave, where a head has no more or the card would be half idle.) Keys and values pass through LDS 32 at a time, in two buffers: while the waves work on
+// share every key that is staged; its four waves hold up to 32 each. (64 rows, 16
+// a wave, where a head has no more or the card would be half idle.) Keys and
+// values pass through LDS 32 at a time, in two buffers: while the waves work on
 // one, the next 32 are on their way into the other. Queries, scores, weights and
 // outputs stay in registers from the first key to the last, which at heads of 256
 // fills them: 128 for outputs, 64 for queries, 16 for scores, the rest for
