@@ -54,7 +54,9 @@ struct Plan {
 // Fewest keys of a piece. In us for 128, 256, 512 (bf16, 256 wide): one token of 4
 // heads over 4096 keys 23.5, 21.5, 22.8; 128 tokens of 4 heads over 4096 keys 38.3,
 // 34.3, 41.0; 512 tokens of 4 heads alone 25.8, 28.2, 36.6.
-static_assert(kMinChunk == 256, "measured as above");
+// In fp32, where a step of 16 keys is long, for 32, 64, 128, 256: one token of 4 heads
+// over 1000 keys 27, 30, 40, 63; 8 tokens of 32 heads over up to 1024 keys 42, 42, 46, 67.
+constexpr int kMinChunk = 256, kMinChunkF32 = 64;
 
 // Most query rows per key/value head of the few-row kernel. Above 16 it takes two
 // row tiles a wave, which at heads over 128 fill or pass its registers: 8 trees of 8
@@ -91,10 +93,11 @@ Plan plan_of(const AttnJob &a, int fmt, bool f32) {
     const int64_t places = one_per_cu ? kWorkgroups / 2 : kWorkgroups;
     const int64_t want = p.kind == kFew && 2 * units > places ? 2 * places : places;
     int64_t chunk = (span * units + want - 1) / want;
-    if (chunk < kMinChunk) chunk = kMinChunk;
+    p.sp.least = p.kind == kF32 ? kMinChunkF32 : kMinChunk;
+    if (chunk < p.sp.least) chunk = p.sp.least;
     if (chunk < (span + kMaxSplit - 1) / kMaxSplit) chunk = (span + kMaxSplit - 1) / kMaxSplit;
     p.sp.step = p.kind == kFew ? 128 : 32;   // whole 32s, for each of four waves if they divide a piece
-    chunk = (chunk + 127) / 128 * 128;
+    chunk = (chunk + p.sp.step - 1) / p.sp.step * p.sp.step;
     p.sp.chunk = (int)(chunk < (1 << 30) ? chunk : (1 << 30));
     p.sp.n_split = (int)((span + chunk - 1) / chunk);
     p.items = all_tiles * p.sp.n_split;
@@ -106,7 +109,7 @@ Plan plan_of(const AttnJob &a, int fmt, bool f32) {
     // and 45); 4 trees over 9201 to 16336 int8 keys: 157 us (183).
     if (p.sp.n_split > 1 && a.c.n_seq <= 64) {
         p.sp.planned = 1;
-        const int64_t most = (span + kMinChunk - 1) / kMinChunk;
+        const int64_t most = (span + p.sp.least - 1) / p.sp.least;
         p.sp.n_split = (int)(most < kMaxSplit ? most : kMaxSplit);
         p.items = all_tiles * p.sp.n_split;
         if (want / a.c.n_kv + all_tiles < p.items) p.items = want / a.c.n_kv + all_tiles;

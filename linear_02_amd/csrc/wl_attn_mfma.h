@@ -121,7 +121,7 @@ struct Split {
     int n_split;      // most pieces of a tile's keys; 1: undivided
     int planned;      // whether the device chooses them
     int chunk;        // keys of a piece, not planned
-    int step;         // a piece is a multiple of so many keys
+    int step, least;  // a piece is a multiple of so many keys, and at least so many
     int want, places; // workgroups wanted, workgroups that run at once
     int tiles;        // of rows, most of a sequence
     int tile_rows, rows;   // rows of a tile, rows kept of one (fewer if no sequence has so many)
@@ -176,7 +176,6 @@ __device__ __forceinline__ Lengths lengths_of(const AttnJob &a, const Split &sp,
     return v;
 }
 
-constexpr int kMinChunk = 256;     // fewest keys of a piece
 constexpr int kMaxSplit = 64;      // most pieces: one lane each in the join
 constexpr float kPieceCost = 96;   // of beginning and ending a piece, in keys
 
@@ -189,7 +188,7 @@ __device__ __forceinline__ int chunk_of(const AttnJob &a, const Split &sp, const
     const float heads = (float)a.c.n_kv;
     const float ideal = wave_sum((float)v.keys * (float)v.tiles) * heads * __builtin_amdgcn_rcpf((float)sp.want) * 1.0001f + 1.0f;
     const float at = ideal * (1.0f + (float)lane * (1.0f / 32));
-    const int mine = max(((int)fminf(at, 0x1p29f) & -sp.step) + sp.step, kMinChunk);
+    const int mine = max(((int)fminf(at, 0x1p29f) & -sp.step) + sp.step, sp.least);
     const float inv = __builtin_amdgcn_rcpf((float)mine);
     float pieces = 0.0f;
     for (int j = 0; j < a.c.n_seq; ++j) {
