@@ -185,6 +185,8 @@ constexpr float kPieceCost = 96;   // of beginning and ending a piece, in keys
 // that there are at most want / n_kv + (all tiles) pieces; where 2^29 cuts it short,
 // no sequence has more than two.
 __device__ __forceinline__ int chunk_of(const AttnJob &a, const Split &sp, const Lengths &v, int lane) {
+#pragma clang fp contract(off)
+    // The kernels and the join have to come to the same bits: nothing is fused here.
     const float heads = (float)a.c.n_kv;
     const float ideal = wave_sum((float)v.keys * (float)v.tiles) * heads * __builtin_amdgcn_rcpf((float)sp.want) * 1.0001f + 1.0f;
     const float at = ideal * (1.0f + (float)lane * (1.0f / 32));
@@ -209,6 +211,7 @@ __device__ __forceinline__ int chunk_of(const AttnJob &a, const Split &sp, const
 // Pieces of this lane's sequence: never more than the keys over chunk rounded up
 // (the factor makes up for the reciprocal's error), and at least 1 if there are keys.
 __device__ __forceinline__ int pieces_of(const Lengths &v, int chunk) {
+#pragma clang fp contract(off)
     return (int)fminf(__builtin_ceilf((float)v.keys * __builtin_amdgcn_rcpf((float)chunk) * (1.0f - 0x1p-20f)), kMaxSplit);
 }
 
