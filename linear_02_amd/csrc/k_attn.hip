@@ -24,8 +24,11 @@ __global__ __launch_bounds__(256) void join_kernel(AttnJob a, Split sp) {
     float m = v.x;
 #pragma unroll
     for (int x = 1; x < 64; x <<= 1) m = fmaxf(m, __shfl_xor(m, x));
-    const float up = v.x == kNegInf && v.y == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(v.x - m);
-    const float l = wave_sum(up == 0.0f ? 0.0f : up * v.y);
+    // A piece without visible keys weighs nothing. One whose sum is NaN (a visible key's
+    // score is) makes the row NaN, however far its maximum is below the others': a
+    // piece of nothing but NaN has none at all.
+    const float up = v.x == kNegInf && v.y == 0.0f ? 0.0f : v.y != v.y ? v.y : __builtin_amdgcn_exp2f(v.x - m);
+    const float l = wave_sum(up * v.y);
     const int at = 4 * lane;
     f32x4 sum{0, 0, 0, 0};
     for (int p = 0; p < parts.n; ++p) {

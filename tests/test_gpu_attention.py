@@ -425,3 +425,29 @@ def test_unseen_and_absent_keys_under_a_large_limit(wl, far, fmt):
 @pytest.mark.parametrize("scale", [0.0, -0.3, 1.5])
 def test_scales_under_a_large_limit(wl, far, scale, fmt):
     test_scales(wl, scale, fmt)
+
+
+@pytest.mark.parametrize("fmt, d, keys, bad", [
+    (F32, 64, 129, [128]), (BF, 256, 513, [512]), (I8, 128, 513, [512]), (E4, 256, 513, [512]),   # the newest key, alone in its piece
+    (F32, 128, 192, range(64, 128)), (BF, 128, 768, range(256, 512)), (I8, 64, 768, range(0, 256)),   # a piece of NaN between others
+    (F32, 128, 300, [70]), (BF, 64, 2000, [300]), (E4, 128, 5000, [4999])])                       # one of many
+@pytest.mark.parametrize("limit", [0, 1 << 16])
+def test_visible_nan_reaches_the_output_through_the_join(wl, fmt, d, keys, bad, limit):
+    """One token over divided keys: a NaN in a visible key makes every score of the row's
+    softmax NaN, whatever the other pieces hold and however large their scores are."""
+    print(f"attention NaN {fmt} {d} {keys} {limit}", flush=True)
+    for loud in (1.0, 300.0):
+        b = Batch(wl, [keys - 1], [1], 4, 1, d, 16, fmt, seed=31)
+        b.max_kv, b.scale = max(limit, keys), b.scale * loud
+        if limit:
+            table = torch.nn.functional.pad(b.cache.table, (0, limit // 16 - b.cache.table.shape[1]), value=-1)
+            b.cache = wl.Cache(b.cache.k, b.cache.v, table, b.cache.k_scale, b.cache.v_scale)
+        assert wl.lib.wl_attention_workspace_bytes(wl.attention_call(b.q, b.cache, b.q_start, b.kv_len, 1, b.max_kv, 1.0).args), "undivided"
+        o = b.run(wl)
+        torch.cuda.synchronize()
+        assert torch.isfinite(o).all()
+        k = torch.full((len(bad), d), float("nan"), dtype=b.q.dtype, device=DEV)
+        wl.wl_cache_write(b.cache, k, torch.ones_like(k), ints([0] * len(bad)), ints(list(bad)))
+        o = b.run(wl)
+        torch.cuda.synchronize()
+        assert torch.isnan(o).all(), loud
