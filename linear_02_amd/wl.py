@@ -416,7 +416,7 @@ class Step:
                 raise ValueError(f"call {i}: {len(thetas)} thetas for op {op}")
             T = _io(x, int(thetas[0]["d_in"]), thetas[0]["W0"].dtype)
             structs = [make_theta(t) for t in thetas]
-            self._keep += [structs, thetas, x, y]
+            self._keep += [structs, [dict(t) for t in thetas], x, y]   # the thetas are the caller's to reuse
             arr[i].op = op
             for j, st in enumerate(structs):
                 arr[i].th[j] = ctypes.pointer(st)
@@ -574,8 +574,10 @@ class Rope:
 
     def struct(self, pos, T: int, like: torch.Tensor):
         f = _vector(self.freq, "freq", like, self.freq.numel(), torch.float64)
-        return Rotary(f, _vector(pos, "pos", like, T, torch.int32), 2 * self.freq.numel(),
-                      ROPE_INTERLEAVED if self.interleaved else ROPE_HALF, self.scale)
+        rot = Rotary(f, _vector(pos, "pos", like, T, torch.int32), 2 * self.freq.numel(),
+                     ROPE_INTERLEAVED if self.interleaved else ROPE_HALF, self.scale)
+        rot.freq_tensor = self.freq
+        return rot
 
 
 def _at(struct) -> int | None:
@@ -607,7 +609,7 @@ def rope_call(q, k, pos, rope: Rope | None, d: int, q_norm=None, k_norm=None, ep
     args = RopeArgs(_ptr(q), _ptr(k), _vector(q_norm, "q_norm", first, d), _vector(k_norm, "k_norm", first, d),
                     _ptr(outs[0]), _ptr(outs[1]), _at(rot), T, n[0], n[1], d, ld[0], ld[1], ldo[0], ldo[1],
                     _CODES[first.dtype], eps, offset)
-    return OpCall(OP_ROPE, lib.wl_rope, args, tuple(outs), first.device, (q, k, pos, rope, rot, q_norm, k_norm))
+    return OpCall(OP_ROPE, lib.wl_rope, args, tuple(outs), first.device, (q, k, pos, rot, q_norm, k_norm))
 
 
 def wl_rope(q, k, pos, rope, d, **kw):
@@ -642,6 +644,7 @@ class Cache:
         self.k, self.v, self.table, self.k_scale, self.v_scale = k, v, table, k_scale, v_scale
         self.struct = CacheStruct(k.data_ptr(), v.data_ptr(), scales[0], scales[1], table.data_ptr(), n_pages, page,
                                   n_kv, d, table.shape[0], table.shape[1], CACHE_FORMATS[k.dtype])
+        self.struct.tensors = k, v, table, k_scale, v_scale   # what it points into, for calls that hold it
 
 
 def new_cache(n_pages: int, n_kv: int, page: int, d: int, table: torch.Tensor, dtype=torch.bfloat16) -> Cache:
@@ -674,7 +677,7 @@ def cache_write_call(cache: Cache, k, v, seq, slot, q=None, rope: Rope | None = 
                           _vector(slot, "slot", k, T, torch.int32), _at(rot), T, n_q, _matrix(k, "k", k, T, width),
                           _matrix(v, "v", k, T, width), ldq, ldo, _CODES[k.dtype], eps, offset)
     return OpCall(OP_CACHE_WRITE, lib.wl_cache_write, args, q_out, k.device,
-                  (cache, k, v, seq, slot, q, rope, rot, pos, q_norm, k_norm))
+                  (c, k, v, seq, slot, q, rot, pos, q_norm, k_norm))
 
 
 def wl_cache_write(cache, k, v, seq, slot, **kw):
@@ -696,7 +699,7 @@ def cache_read_call(cache: Cache, seq, slot, dtype: torch.dtype | None = None, k
     args = CacheReadArgs(_at(c), _vector(seq, "seq", first, T, torch.int32), _vector(slot, "slot", first, T, torch.int32),
                          outs[0].data_ptr(), outs[1].data_ptr(), T, _matrix(outs[0], "k_out", first, T, c.n_kv * c.d),
                          _matrix(outs[1], "v_out", first, T, c.n_kv * c.d), _CODES[dtype])
-    return OpCall(OP_CACHE_READ, lib.wl_cache_read, args, tuple(outs), first.device, (cache, seq, slot))
+    return OpCall(OP_CACHE_READ, lib.wl_cache_read, args, tuple(outs), first.device, (c, seq, slot))
 
 
 def wl_cache_read(cache, seq, slot, **kw):
@@ -732,7 +735,7 @@ def attention_call(q, cache: Cache, q_start, kv_len, max_q: int, max_kv: int, sc
                          _vector(tree, "tree", q, T * words, torch.int32), _vector(q_pos, "q_pos", q, T, torch.int32),
                          T, n_q, _matrix(q, "q", q, T, n_q * c.d), _matrix(o, "o", q, T, n_q * c.d), max_q, max_kv,
                          MASKS[mask], window, words, _CODES[q.dtype], scale)
-    return OpCall(OP_ATTENTION, lib.wl_attention, args, o, q.device, (q, cache, q_start, kv_len, tree, q_pos), ws)
+    return OpCall(OP_ATTENTION, lib.wl_attention, args, o, q.device, (q, c, q_start, kv_len, tree, q_pos), ws)
 
 
 def wl_attention(q, cache, q_start, kv_len, max_q, max_kv, scale, **kw):
@@ -748,14 +751,18 @@ class LayerStep(Step):
     def __init__(self, calls, ws: torch.Tensor | None = None):
         n = len(calls)
         ops = (StepOp * n)()
-        self._keep = [calls]
+        # What the graph's addresses point into: the list, the calls and the thetas are the
+        # caller's to reuse.
+        self._keep = []
         device = None
         for i, call in enumerate(calls):
             if isinstance(call, OpCall):
                 ops[i].op, ops[i].args = call.op, ctypes.addressof(call.args)
                 device = call.device
+                self._keep.append((call.args, call.out, call.keep))
                 continue
             op, thetas, x, y = call
+            self._keep += [x, y, [dict(t) for t in thetas]]
             if len(thetas) != (1 if op == OP_LINEAR else 3):
                 raise ValueError(f"call {i}: {len(thetas)} thetas for op {op}")
             c = Call()

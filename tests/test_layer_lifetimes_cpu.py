@@ -1,0 +1,126 @@
+"""What the binding keeps alive: device memory whose addresses calls, steps and captured
+graphs hold. Without a GPU, by weak references to host tensors in their place."""
+from __future__ import annotations
+
+import ctypes
+import gc
+import weakref
+
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def wl():
+    import os
+
+    from linear_02_amd import build
+    if not os.path.exists(build.LIBRARY):
+        build.build()
+    from linear_02_amd import wl as mod
+    return mod
+
+
+@pytest.fixture
+def no_device(wl, monkeypatch):
+    """Steps are checked and made on the host alone; rows of x without a look at its device."""
+    for f in ("wl_step_create", "wl_step_create_ops"):
+        monkeypatch.setattr(wl.lib, f, lambda *a: 0)
+    monkeypatch.setattr(wl, "_io", lambda x, *a: x.shape[0])
+
+
+def bf16(*shape):
+    return torch.zeros(shape, dtype=torch.bfloat16)
+
+
+def theta():
+    return dict(W0=bf16(64, 64), s=torch.ones(64), U=bf16(64, 4), V=bf16(64, 4), d_in=64, d_out=64, r=4)
+
+
+def watch(*tensors):
+    return [weakref.ref(t) for t in tensors]
+
+
+def alive(refs):
+    gc.collect()
+    return [r() is not None for r in refs]
+
+
+def norm(wl):
+    x, out = bf16(4, 64), bf16(4, 64)
+    args = wl.NormArgs(x=x.data_ptr(), n_out=out.data_ptr(), T=4, d=64)
+    return wl.OpCall(wl.OP_NORM, None, args, (None, out), torch.device("cuda", 0), (x,)), watch(x, out)
+
+
+def test_a_layer_step_outlives_the_list_it_was_made_from(wl, no_device):
+    call, refs = norm(wl)
+    th, x, y = theta(), bf16(4, 64), bf16(4, 64)
+    refs += watch(x, y, th["W0"], th["s"], th["U"], th["V"])
+    thetas = [th]
+    calls = [call, (wl.OP_LINEAR, thetas, x, y)]
+    step = wl.LayerStep(calls, ws=torch.zeros(1, dtype=torch.uint8))
+    args = ctypes.addressof(call.args)
+    calls.clear(), thetas.clear(), th.clear()
+    call.args = call.out = call.keep = None
+    del call, x, y
+    assert all(alive(refs))
+    assert args in [ctypes.addressof(a) for k in step._keep if isinstance(k, tuple) for a in k if isinstance(a, ctypes.Structure)]
+    del step
+    assert not any(alive(refs))
+
+
+def test_a_step_outlives_the_thetas_it_was_made_from(wl, no_device):
+    th, x, y = theta(), bf16(4, 64), bf16(4, 64)
+    refs = watch(x, y, th["W0"], th["s"], th["U"], th["V"])
+    thetas = [th]
+    calls = [(wl.OP_LINEAR, thetas, x, y)]
+    step = wl.Step(calls, ws=torch.zeros(1, dtype=torch.uint8))
+    calls.clear(), thetas.clear(), th.clear()
+    del x, y
+    assert all(alive(refs))
+    del step
+    assert not any(alive(refs))
+
+
+class OnDevice:
+    """A host tensor that says it is on the device."""
+
+    def __init__(self, t):
+        self.t = t
+
+    is_cuda, device = True, torch.device("cuda", 0)
+
+    def get_device(self):
+        return 0
+
+    def new_empty(self, *a, **kw):
+        return OnDevice(self.t.new_empty(*a, **kw))
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+def test_calls_keep_the_cache_and_frequencies_they_were_made_with(wl):
+    def dev(*shape, dtype=torch.bfloat16):
+        return OnDevice(torch.zeros(shape, dtype=dtype))
+
+    k, v, table = dev(2, 1, 16, 64), dev(2, 1, 16, 64), dev(1, 2, dtype=torch.int32)
+    freq = dev(32, dtype=torch.float64)
+    refs = watch(k, v, table, freq)
+    cache, rope = wl.Cache(k, v, table), wl.Rope(freq)
+    i32 = dict(dtype=torch.int32)
+    row = dev(3, 64)
+    calls = [wl.cache_write_call(cache, row, dev(3, 64), dev(3, **i32), dev(3, **i32), q=dev(3, 64), rope=rope),
+             wl.cache_read_call(cache, dev(3, **i32), dev(3, **i32)),
+             wl.attention_call(row, cache, dev(2, **i32), dev(1, **i32), 3, 3, 1.0),
+             wl.rope_call(row, None, dev(3, **i32), rope, 64)]
+    cache.k = cache.v = cache.table = rope.freq = None
+    struct = ctypes.addressof(cache.struct)
+    assert [c.args.cache == struct for c in calls[:3]] == [True] * 3
+    del k, v, table, freq, cache, rope
+    for _ in range(3):                      # each of the three that hold the cache, alone at last
+        assert all(alive(refs))
+        calls.pop(0)
+    assert alive(refs) == [False, False, False, True]
+    calls.clear()
+    assert not any(alive(refs))
