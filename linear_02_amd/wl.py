@@ -144,6 +144,9 @@ def _load(path: str = LIBRARY) -> ctypes.CDLL:
     lib.wl_step_ops_workspace_bytes.restype = sz
     lib.wl_step_create_ops.argtypes = [ctypes.POINTER(StepOp), i32, vp, sz, ctypes.POINTER(vp)]
     lib.wl_step_create_ops.restype = ctypes.c_int
+    # Of the HIP runtime that the library is linked to.
+    lib.hipStreamGetCaptureInfo.argtypes = [vp, ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_ulonglong)]
+    lib.hipStreamGetCaptureInfo.restype = ctypes.c_int
     lib.wl_workspace_init.argtypes = [vp, sz, vp]
     lib.wl_workspace_init.restype = ctypes.c_int
     lib.wl_sync_bytes.argtypes = []
@@ -177,6 +180,15 @@ def _index(device: torch.device) -> int:
 
 def _stream(device: torch.device):
     return ctypes.c_void_p(_raw_stream(_index(device)))
+
+
+def _capture(stream: int) -> int | None:
+    """Id of the graph capture that a stream is part of, None if it is in none."""
+    if not stream:
+        return None   # the default stream cannot be captured
+    status, ident = ctypes.c_int(0), ctypes.c_ulonglong(0)
+    lib.hipStreamGetCaptureInfo(stream, ctypes.byref(status), ctypes.byref(ident))
+    return ident.value if status.value == 1 else None
 
 
 def theta_to(th: dict, device) -> dict:
@@ -219,30 +231,53 @@ def workspace_init(ws: torch.Tensor) -> None:
 def new_workspace(nbytes: int, device) -> torch.Tensor:
     """A projection workspace of at least nbytes (and at least the sync area),
     prepared by wl_workspace_init."""
-    device = torch.device(device)
-    ws = torch.empty(max(int(nbytes), SYNC_BYTES), dtype=torch.uint8, device=device)
+    ws = _bytes(max(int(nbytes), SYNC_BYTES), torch.device(device))
     workspace_init(ws)
     return ws
+
+
+def _bytes(nbytes: int, device: torch.device) -> torch.Tensor:
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
 class Workspace:
     """A device workspace per (device, stream) that grows on demand, prepared by
     wl_workspace_init when allocated.
 
-    Calls on one stream run in order, so they can share one workspace."""
+    Calls on one stream run in order, so they can share one workspace. Calls that a
+    graph capture records share one of that capture's own, allocated and prepared
+    within it: under torch.cuda.graph its memory is the graph's, so that no later
+    call can replace it, and no replay finds it prepared by another graph alone or in
+    use by one (pass ``ws`` to a call to leave the preparing out of the graph)."""
 
     def __init__(self):
         self._bufs: dict = {}
+        self._captured: dict = {}   # the capture that a stream was last in, its workspace
 
     def get(self, device: torch.device, nbytes: int) -> torch.Tensor | None:
         if nbytes == 0:
             return None
-        key = (device.index, _raw_stream(_index(device)))
-        buf = self._bufs.get(key)
+        stream = _raw_stream(_index(device))
+        key, capture = (device.index, stream), _capture(stream)
+        if capture is None:
+            buf = self._bufs.get(key)
+        else:
+            of, buf = self._captured.pop(key, (None, None))
+            buf = buf if of == capture else None
         if buf is None or buf.numel() < nbytes:
             buf = new_workspace(max(nbytes, 1 << 20), device)
+        if capture is None:
             self._bufs[key] = buf
+        else:
+            self._captured[key] = capture, buf
         return buf
+
+    def scratch(self, device: torch.device, nbytes: int) -> torch.Tensor | None:
+        """get() for a call that leaves the sync area alone: in a capture, memory of the
+        graph's for this call, with nothing to prepare."""
+        if nbytes and _capture(_raw_stream(_index(device))) is not None:
+            return _bytes(nbytes, device)
+        return self.get(device, nbytes)
 
 
 WORKSPACE = Workspace()
@@ -460,11 +495,10 @@ class OpCall:
     """A checked call of one operation: ``out`` are its outputs, ``launch`` runs it
     on the current stream of its device. Keeps its tensors alive."""
 
-    __slots__ = ("op", "args", "out", "device", "fn", "ws", "keep", "used")
+    __slots__ = ("op", "args", "out", "device", "fn", "ws", "keep")
 
     def __init__(self, op, fn, args, out, device, keep, ws=None):
         self.op, self.fn, self.args, self.out, self.device, self.keep, self.ws = op, fn, args, out, device, keep, ws
-        self.used = None   # the shared workspace of the last launch: a captured one still needs it
 
     def launch(self):
         if self.device.index != torch.cuda.current_device():
@@ -478,8 +512,7 @@ class OpCall:
             status = self.fn(self.args, stream)
         else:
             need = lib.wl_attention_workspace_bytes(self.args)
-            ws = self.ws if self.ws is not None else WORKSPACE.get(self.device, need) if need else None
-            self.used = ws
+            ws = self.ws if self.ws is not None else WORKSPACE.scratch(self.device, need)
             status = self.fn(self.args, _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), stream)
         if status:
             _check(status)

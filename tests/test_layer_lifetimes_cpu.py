@@ -124,3 +124,69 @@ def test_calls_keep_the_cache_and_frequencies_they_were_made_with(wl):
     assert alive(refs) == [False, False, False, True]
     calls.clear()
     assert not any(alive(refs))
+
+
+@pytest.fixture
+def streams(wl, monkeypatch):
+    """Host memory for workspaces, on a stream and in a capture of the test's choice."""
+    class At:
+        stream, capture, prepared = 1, None, 0
+
+    def prepared(nbytes, device):
+        At.prepared += 1
+        return torch.empty(nbytes, dtype=torch.uint8)
+
+    monkeypatch.setattr(wl, "_raw_stream", lambda index: At.stream)
+    monkeypatch.setattr(wl, "_capture", lambda stream: At.capture, raising=False)
+    monkeypatch.setattr(wl, "_bytes", lambda n, device: torch.empty(n, dtype=torch.uint8), raising=False)
+    monkeypatch.setattr(wl, "new_workspace", prepared)
+    return At
+
+
+CUDA0 = torch.device("cuda", 0)
+
+
+def test_a_capture_has_a_workspace_of_its_own(wl, streams):
+    w = wl.Workspace()
+    eager = w.get(CUDA0, 1000)
+    assert w.get(CUDA0, 500) is eager and streams.prepared == 1
+    streams.capture = 7
+    first = w.get(CUDA0, 1000)
+    assert first is not eager and streams.prepared == 2        # prepared by a node of the graph
+    assert w.get(CUDA0, 900) is first and streams.prepared == 2
+    streams.stream = 2                                         # another stream in the same capture
+    beside = w.get(CUDA0, 1000)
+    assert beside is not first and streams.prepared == 3
+    streams.stream, streams.capture = 1, 8                     # another graph on the same stream
+    second = w.get(CUDA0, 1000)
+    assert second is not first and streams.prepared == 4
+    large = w.get(CUDA0, 1 << 21)
+    assert large.numel() >= 1 << 21 and w.get(CUDA0, 1000) is large
+    streams.capture = None
+    assert w.get(CUDA0, 1000) is eager and streams.prepared == 5
+
+
+def test_captured_attention_takes_memory_of_its_graph(wl, streams):
+    got = []
+
+    def launched(args, ws, nbytes, stream):
+        got.append((ws, nbytes))
+        return 0
+
+    cache = wl.CacheStruct(k=1 << 20, v=1 << 30, table=1 << 34, n_pages=64, page=64, n_kv=1, d=64, n_seq=1, max_pages=64)
+    args = wl.AttentionArgs(cache=ctypes.addressof(cache), q=1 << 35, o=1 << 36, q_start=1 << 37, kv_len=1 << 38, T=1, n_q=1, ldq=64,
+                            ldo=64, max_q=1, max_kv=4096, scale=1.0)
+    need = int(wl.lib.wl_attention_workspace_bytes(args))
+    assert need > 0
+    call = wl.OpCall(wl.OP_ATTENTION, launched, args, None, CUDA0, ())
+    shared = wl.WORKSPACE.get(CUDA0, need)
+    prepared = streams.prepared
+    call._launch()
+    assert got[-1][0] == shared.data_ptr() and streams.prepared == prepared
+    streams.capture = 3
+    call._launch()
+    assert got[-1][0] != shared.data_ptr() and got[-1][1] >= need and streams.prepared == prepared
+    call.ws = torch.empty(need, dtype=torch.uint8)
+    call._launch()
+    assert got[-1][0] == call.ws.data_ptr()
+    wl.WORKSPACE._bufs.pop((0, streams.stream))
