@@ -438,9 +438,13 @@ wl_status wl_cache_read(const wl_cache_read_args *a, void *hip_stream);
  * goes for slots from kv_len on. n_q is a multiple of n_kv.
  * Products of bf16 tensors run on the matrix cores with fp32 sums. For the
  * second product a weight (times its key's v_scale, in the quantised formats) is
- * rounded to bf16, with the remainder as a second bf16 where there are few rows
- * per key/value head (single tokens, small trees); a bf16 cache's weights are
- * summed as rounded. dtype f32 is fp32 throughout.
+ * rounded to bf16 (2^-8 of it at most), with the remainder as a second bf16 (then
+ * 2^-16) where a call is small: with rows = max_q n_q / n_kv, where rows <= 64 or
+ * n_seq n_kv ceil(rows / 64) <= 32. Without the remainder, a bf16 cache's weights
+ * are summed as rounded too. dtype f32 is fp32 throughout.
+ * max_kv does not change what is rounded; the order of the fp32 sums follows the
+ * division of the keys, which depends on max_kv and on all sequences' lengths, so
+ * that a query's last bits may differ with the batch it is in.
  *   ws   ws_bytes >= wl_attention_workspace_bytes(a), prepared as the other
  *        operations' (its first WL_SYNC_BYTES are not touched, so that one
  *        workspace serves a whole layer); NULL is accepted where that is 0 */

@@ -50,6 +50,7 @@ enum Kind { kFew, kTile, kF32 };
 struct Plan {
     Kind kind;
     int waves, tiles;   // per workgroup, tiles of query rows per wave
+    bool exact;         // of the tile kernel: weights with their remainder
     int64_t items;      // as in Split, which holds it if it is within a launch's limits
     Split sp;
 };
@@ -67,6 +68,20 @@ constexpr int kMinChunk = 256, kMinChunkF32 = 64;
 // int8, 103 and 75 us in the tile kernel; at 128 wide 57 and 58 us, 45 and 55 us.
 int few_rows(const AttnJob &a) { return a.c.d > 128 ? 16 : 32; }
 
+// Tiles of query rows per wave, and what the weights keep. Which of the two precisions a
+// call has follows from its rows alone, not from max_kv: the remainder is kept for up to
+// 64 rows per head, and up to this many tiles of 64 rows over all sequences and key/value
+// heads, where the card has time for it (one tile a wave). In us, one tile with remainders
+// against two without, heads of 256: 8 tiles over 512, 4096, 16384 keys in bf16 21, 29, 51
+// and 26, 33, 50; 32 over 512, 4096 in int8 27, 43 and 34, 49; 24 over 2048, 16384 in int8
+// 32, 83 and 42, 68; 64 over 128, 1024, 8192 in bf16 13, 30, 72 and 19, 34, 62; 256 over
+// 512, 2048, 8192 38, 69, 206 and 40, 59, 139.
+constexpr int kExactTiles = 32;
+// Beyond, one tile a wave without remainders where the tiles of 64 rows in pieces of
+// kMinChunk keys fit the card about twice, since with two much of it would be idle: 256
+// tiles over 512 keys as above 36 us with one, 40 with two; 64 over 1024 29 and 34.
+constexpr int kOneTilePieces = 2 * kWorkgroups;
+
 Plan plan_of(const AttnJob &a, int fmt, bool f32) {
     Plan p{};
     p.kind = f32 ? kF32 : (int64_t)a.max_q * a.group > few_rows(a) ? kTile : kFew;
@@ -75,14 +90,9 @@ Plan plan_of(const AttnJob &a, int fmt, bool f32) {
     int64_t span = a.max_kv;
     if (a.mask == kMaskCausal && a.window && (int64_t)a.window + a.max_q < span) span = (int64_t)a.window + a.max_q;
     span += 31;
-    // One tile a wave, with its exact weights, for 64 rows, and for calls whose tiles of
-    // 64 rows in pieces of kMinChunk keys fit the card about twice: with two tiles much of
-    // it would be idle. Prompts of 512 tokens in bf16, 4 heads over 1 of 256: 28.1 us with
-    // two, 23.5 with one; 32 over 8: 41.5 and 38.9; 4 trees of 60 tokens over 2000 keys,
-    // int8, 128 wide: 45.9 and 42.1. (2 x 256 tokens over 4000 keys, 4096 such pieces: 66
-    // with either; prompts of thousands read each key half as often with two.)
-    const double pieces = (double)a.c.n_seq * a.c.n_kv * ((rows + 4 * kTileRows - 1) / (4 * kTileRows)) * ((span + kMinChunk - 1) / kMinChunk);
-    p.tiles = rows > 4 * kTileRows && pieces > 2 * kWorkgroups ? 2 : 1;
+    const int64_t small = (int64_t)a.c.n_seq * a.c.n_kv * ((rows + 4 * kTileRows - 1) / (4 * kTileRows));   // tiles of 64 rows
+    p.exact = rows <= 4 * kTileRows || small <= kExactTiles;
+    p.tiles = !p.exact && (double)small * ((span + kMinChunk - 1) / kMinChunk) > kOneTilePieces ? 2 : 1;
     // Codes are widened once per workgroup: eight waves where they hold all rows.
     p.waves = p.tiles == 2 && fmt != kFmtBf16 && rows > 8 * kTileRows && rows <= 16 * kTileRows && p.kind == kTile ? 8 : 4;
     p.sp.tile_rows = p.kind == kTile ? p.waves * p.tiles * kTileRows : p.kind == kF32 ? kF32Rows : (int)rows;
@@ -144,7 +154,7 @@ hipError_t launch_attention(const AttnJob &a, int fmt, bool f32, void *ws, hipSt
     }
     switch (p.kind) {
         case kFew: launch_few(a, fmt, p.sp, s); break;
-        case kTile: launch_tile(a, fmt, p.sp, p.waves, p.tiles, s); break;
+        case kTile: launch_tile(a, fmt, p.sp, p.waves, p.tiles, p.exact, s); break;
         default: launch_f32(a, fmt, p.sp, s);
     }
     const hipError_t e = hipGetLastError();

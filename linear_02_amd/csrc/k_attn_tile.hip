@@ -3,7 +3,7 @@
 // A workgroup takes 128 query rows of one key/value head, a row being a new token
 // and one of the query heads that share the key/value head, so that those heads
 // share every key that is staged; its four waves hold up to 32 each. (64 rows, 16
-// a wave, where a head has no more or the card would be half idle.) Keys and
+// a wave, where a head has no more or the call is small.) Keys and
 // values pass through LDS 32 at a time, in two buffers: while the waves work on
 // one, the next 32 are on their way into the other. Queries, scores, weights and
 // outputs stay in registers from the first key to the last, which at heads of 256
@@ -30,8 +30,9 @@ struct Tiles {
     static constexpr int n = N;
 };
 
-// kNT: tiles of 16 query rows per wave, at most.
-template <int F, int DT, int NW, int kNT>
+// kNT: tiles of 16 query rows per wave, at most. kExact: weights as a bf16 head plus a
+// bf16 remainder, 16 bits of them, for which one tile leaves registers; else as one bf16.
+template <int F, int DT, int NW, int kNT, bool kExact>
 __global__ __launch_bounds__(64 * NW, 2) void tile_kernel(TileArgs x) {
     const AttnJob &a = x.a;
     constexpr bool kCodes = F == kFmtInt8 || F == kFmtE4m3;
@@ -43,9 +44,7 @@ __global__ __launch_bounds__(64 * NW, 2) void tile_kernel(TileArgs x) {
     // 256, in us for 2, 3, 4, 6: bf16 213, 207, 208, 260; e4m3 266, 295, 294, 323 (the
     // registers that more would take are not there).
     constexpr int kAhead = kNT == 1 ? 4 : kCodes ? 2 : 3;
-    // With one tile there are registers and time for the weights as a bf16 head plus a
-    // bf16 remainder, which lose nothing.
-    constexpr bool kExact = kNT == 1;
+    static_assert(!kExact || kNT == 1, "two tiles leave no registers for the remainders");
     // LDS place of 16-byte piece c of a row: c ^ f(row), such that the 16 lanes that
     // one pass of a read serves meet all 64 banks.
     auto fk = [](int r) { return DT >= 128 ? r & 15 : (r >> 1) & 7; };
@@ -416,38 +415,38 @@ __global__ __launch_bounds__(64 * NW, 2) void tile_kernel(TileArgs x) {
     finish<uint16_t, F, DT, kNT>(argument_again<TileArgs>(), work, rows_of, o, m, l, k0, k1);
 }
 
-template <int F, int DT, int NW, int NT>
+template <int F, int DT, int NW, int NT, bool EX>
 void run(const AttnJob &a, const Split &sp, hipStream_t s) {
-    hipLaunchKernelGGL((tile_kernel<F, DT, NW, NT>), dim3((unsigned)sp.items * a.c.n_kv), dim3(64 * NW), 0, s, TileArgs{a, sp});
+    hipLaunchKernelGGL((tile_kernel<F, DT, NW, NT, EX>), dim3((unsigned)sp.items * a.c.n_kv), dim3(64 * NW), 0, s, TileArgs{a, sp});
 }
 
-template <int F, int NW, int NT>
+template <int F, int NW, int NT, bool EX>
 void pick(const AttnJob &a, const Split &sp, hipStream_t s) {
     if (a.c.d <= 64)
-        run<F, 64, NW, NT>(a, sp, s);
+        run<F, 64, NW, NT, EX>(a, sp, s);
     else if (a.c.d <= 128)
-        run<F, 128, NW, NT>(a, sp, s);
+        run<F, 128, NW, NT, EX>(a, sp, s);
     else
-        run<F, 256, NW, NT>(a, sp, s);
+        run<F, 256, NW, NT, EX>(a, sp, s);
 }
 
 template <int F>
-void pick(const AttnJob &a, const Split &sp, int waves, int tiles, hipStream_t s) {
+void pick(const AttnJob &a, const Split &sp, int waves, int tiles, bool exact, hipStream_t s) {
     if (tiles == 1)
-        pick<F, 4, 1>(a, sp, s);
+        exact ? pick<F, 4, 1, true>(a, sp, s) : pick<F, 4, 1, false>(a, sp, s);
     else if (waves == 8)
-        pick<F, F == kFmtBf16 ? 4 : 8, 2>(a, sp, s);
+        pick<F, F == kFmtBf16 ? 4 : 8, 2, false>(a, sp, s);
     else
-        pick<F, 4, 2>(a, sp, s);
+        pick<F, 4, 2, false>(a, sp, s);
 }
 
 }  // namespace
 
-void launch_tile(const AttnJob &a, int fmt, const Split &sp, int waves, int tiles, hipStream_t s) {
+void launch_tile(const AttnJob &a, int fmt, const Split &sp, int waves, int tiles, bool exact, hipStream_t s) {
     switch (fmt) {
-        case kFmtBf16: pick<kFmtBf16>(a, sp, waves, tiles, s); break;
-        case kFmtInt8: pick<kFmtInt8>(a, sp, waves, tiles, s); break;
-        default: pick<kFmtE4m3>(a, sp, waves, tiles, s);
+        case kFmtBf16: pick<kFmtBf16>(a, sp, waves, tiles, exact, s); break;
+        case kFmtInt8: pick<kFmtInt8>(a, sp, waves, tiles, exact, s); break;
+        default: pick<kFmtE4m3>(a, sp, waves, tiles, exact, s);
     }
 }
 

@@ -146,7 +146,7 @@ constexpr int kTileRows = 16;     // query rows of a tile of the many-row kernel
 constexpr int kF32Rows = 64;      // of the fp32 kernel
 
 void launch_few(const AttnJob &a, int fmt, const Split &sp, hipStream_t s);
-void launch_tile(const AttnJob &a, int fmt, const Split &sp, int waves, int tiles, hipStream_t s);
+void launch_tile(const AttnJob &a, int fmt, const Split &sp, int waves, int tiles, bool exact, hipStream_t s);
 void launch_f32(const AttnJob &a, int fmt, const Split &sp, hipStream_t s);
 
 // ---- kernels whose workgroups of four waves take tiles of 64 NT query rows -------
