@@ -82,12 +82,14 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void norm_kernel(Nor
     const E *gate = static_cast<const E *>(a.gate) + (size_t)t * a.gate_ld;
     const E *post = static_cast<const E *>(a.post), *pre = static_cast<const E *>(a.pre);
 
+    const float pre_offset = a.pre ? a.offset : 0.0f;   // an absent weight is 1, whatever the offset
+
     float r[NP][8], p[NP][8], g[NP][8], wp[NP][8], wn[NP][8];
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
         const int at = (tid + i * kThreads) * 8;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) r[i][e] = p[i][e] = 0.0f, g[i][e] = 1.0f, wp[i][e] = wn[i][e] = 1.0f - a.offset;
+        for (int e = 0; e < 8; ++e) r[i][e] = p[i][e] = 0.0f, g[i][e] = wp[i][e] = wn[i][e] = 1.0f;
         if (at >= a.d) continue;
         load8(x + at, r[i]);
         if (a.y) load8(y + at, p[i]);
@@ -126,7 +128,7 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void norm_kernel(Nor
         if (a.x_out) store8<S>(xo + at, r[i]);
         if (a.n_out) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) r[i][e] *= inv * (wn[i][e] + a.offset);
+            for (int e = 0; e < 8; ++e) r[i][e] *= inv * (wn[i][e] + pre_offset);
             store8<S>(no + at, r[i]);
         }
     }

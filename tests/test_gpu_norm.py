@@ -113,3 +113,16 @@ def test_graph_and_stream(wl):
         call.launch()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, call.out))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("offset", [3e7, -0.3, 1.0])
+def test_an_absent_weight_is_one(wl, dtype, offset):
+    """Without weights the offset has no part: n is the bare norm for any offset."""
+    x, y = draw(1, 5, 1152, dtype=dtype), draw(2, 5, 1152, dtype=dtype)
+    z = ref.f64(x) + ref.f64(y)
+    inv = 1 / (z.square().mean(1, keepdim=True) + 1e-6).sqrt()
+    xo, no = wl.wl_norm_residual(x, y=y, offset=offset)
+    torch.cuda.synchronize()
+    ref.assert_near(no, z * inv, 2 * ref.CHAIN * ref.EPS32 * (ref.f64(x).abs() + ref.f64(y).abs()) * inv, "n")
+    assert torch.equal(no, wl.wl_norm_residual(x, y=y)[1])
