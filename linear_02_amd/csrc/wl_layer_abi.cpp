@@ -24,7 +24,7 @@ namespace {
 const int64_t kMaxElems = (int64_t)1 << 31;
 const int32_t kMaxTokens = 1 << 24;        // a wave each stays inside a launch's 2^32 threads
 const int32_t kMaxKeys = 1 << 30;          // key numbers stay in int32 a few tiles past the last
-const int64_t kMaxWorkgroups = 1 << 23;
+const int64_t kMaxWorkgroups = (1 << 23) - 1;   // of up to 512 threads: fewer than 2^32 in a launch
 
 wl_status check_dtype(int32_t dtype) {
     if (dtype != WL_DTYPE_BF16 && dtype != WL_DTYPE_F32)

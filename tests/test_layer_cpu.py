@@ -159,6 +159,15 @@ def test_sizes_beyond_a_launch_are_refused(wl):
     assert b"workgroups" in wl.lib.wl_last_error()
 
 
+def test_two_to_the_32_threads_are_refused(wl):
+    """2^23 workgroups of eight waves, which codes at 129 to 256 rows per head take."""
+    c = cache(wl, n_kv=1, d=16, n_seq=1 << 23, max_pages=1, format=2, k=1 << 36, v=1 << 37, k_scale=1 << 38, v_scale=1 << 39,
+              table=1 << 40)
+    a = attention_args(wl, c, q=1 << 41, o=1 << 42, q_start=1 << 43, kv_len=1 << 44, T=200, max_q=200, n_q=1, ldq=16, ldo=16)
+    assert wl.lib.wl_attention(ctypes.byref(a), None, 0, None) == 2, wl.lib.wl_last_error()
+    assert b"workgroups" in wl.lib.wl_last_error()
+
+
 def test_step_ops_refuse(wl):
     ops = (wl.StepOp * 1)()
     h = ctypes.c_void_p()
