@@ -14,6 +14,7 @@ dtype of W0 picks the variant).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -180,6 +181,13 @@ def _index(device: torch.device) -> int:
 
 def _stream(device: torch.device):
     return ctypes.c_void_p(_raw_stream(_index(device)))
+
+
+def _on(device: torch.device):
+    """Context in which a device is the current one."""
+    if device.index is None or device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
 
 
 def _capture(stream: int) -> int | None:
@@ -431,6 +439,12 @@ def abi_version() -> int:
     return int(lib.wl_abi_version())
 
 
+def _one_device(device: torch.device | None, other: torch.device, i: int) -> torch.device:
+    if device is not None and other != device:
+        raise ValueError(f"call {i} is on {other}, those before it on {device}")
+    return other
+
+
 class Step:
     """A decode step: a fixed list of calls that the library records once into a
     HIP graph (wl_step_create) and launches with one call.
@@ -456,24 +470,30 @@ class Step:
             for j, st in enumerate(structs):
                 arr[i].th[j] = ctypes.pointer(st)
             arr[i].x, arr[i].y, arr[i].T = _ptr(x), _ptr(y), T
-            device = x.device
+            device = _one_device(device, x.device, i)
         need = int(lib.wl_step_workspace_bytes(arr, n))
         if need == 0:
             raise ValueError("invalid calls for a step")
-        self.ws = ws if ws is not None else new_workspace(need, device)
-        self.device = device
+        self._create(lambda *a: lib.wl_step_create(arr, n, STEP_GROUP_SHARED_W0 if group_shared_w0 else 0, *a), need, ws, device)
+
+    def _create(self, make, need: int, ws: torch.Tensor | None, device: torch.device) -> None:
+        """make(workspace, its bytes, handle) on the calls' device."""
         h = ctypes.c_void_p()
-        _check(lib.wl_step_create(arr, n, STEP_GROUP_SHARED_W0 if group_shared_w0 else 0, _ptr(self.ws),
-                                  self.ws.numel() * self.ws.element_size(), ctypes.byref(h)))
+        with _on(device):
+            self.ws = ws if ws is not None else new_workspace(need, device)
+            self.device = device
+            _check(make(_ptr(self.ws), self.ws.numel() * self.ws.element_size(), ctypes.byref(h)))
         self.handle = h
 
     def launch(self) -> None:
-        _check(lib.wl_step_launch(self.handle, _stream(self.device)))
+        with _on(self.device):
+            _check(lib.wl_step_launch(self.handle, _stream(self.device)))
 
     def close(self) -> None:
         if getattr(self, "handle", None) is not None and self.handle.value:
-            torch.cuda.current_stream(self.device).synchronize()
-            lib.wl_step_destroy(self.handle)
+            with _on(self.device):
+                torch.cuda.current_stream(self.device).synchronize()
+                lib.wl_step_destroy(self.handle)
         self.handle = None
 
     def __del__(self):
@@ -791,7 +811,7 @@ class LayerStep(Step):
         for i, call in enumerate(calls):
             if isinstance(call, OpCall):
                 ops[i].op, ops[i].args = call.op, ctypes.addressof(call.args)
-                device = call.device
+                device = _one_device(device, call.device, i)
                 self._keep.append((call.args, call.out, call.keep))
                 continue
             op, thetas, x, y = call
@@ -805,12 +825,8 @@ class LayerStep(Step):
                 c.th[j] = ctypes.pointer(st)
             self._keep += [structs, c]
             ops[i].op, ops[i].args = op, ctypes.addressof(c)
-            device = x.device
+            device = _one_device(device, x.device, i)
         need = int(lib.wl_step_ops_workspace_bytes(ops, n))
         if need == 0:
             raise ValueError("invalid calls for a step")
-        self.ws = ws if ws is not None else new_workspace(need, device)
-        self.device = device
-        h = ctypes.c_void_p()
-        _check(lib.wl_step_create_ops(ops, n, _ptr(self.ws), self.ws.numel() * self.ws.element_size(), ctypes.byref(h)))
-        self.handle = h
+        self._create(lambda *a: lib.wl_step_create_ops(ops, n, *a), need, ws, device)

@@ -49,7 +49,7 @@ def alive(refs):
 def norm(wl):
     x, out = bf16(4, 64), bf16(4, 64)
     args = wl.NormArgs(x=x.data_ptr(), n_out=out.data_ptr(), T=4, d=64)
-    return wl.OpCall(wl.OP_NORM, None, args, (None, out), torch.device("cuda", 0), (x,)), watch(x, out)
+    return wl.OpCall(wl.OP_NORM, None, args, (None, out), x.device, (x,)), watch(x, out)
 
 
 def test_a_layer_step_outlives_the_list_it_was_made_from(wl, no_device):
@@ -190,3 +190,47 @@ def test_captured_attention_takes_memory_of_its_graph(wl, streams):
     call._launch()
     assert got[-1][0] == call.ws.data_ptr()
     wl.WORKSPACE._bufs.pop((0, streams.stream))
+
+
+class Elsewhere:
+    """A tensor of another device."""
+
+    def __init__(self, t, index):
+        self.t, self.device = t, torch.device("cuda", index)
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+def test_a_step_is_made_and_launched_on_its_calls_device(wl, no_device, monkeypatch):
+    """One device per step, which need not be the current one."""
+    at, seen = [0], []
+
+    class On:
+        def __init__(self, device):
+            self.index = device.index
+
+        def __enter__(self):
+            at.append(self.index)
+
+        def __exit__(self, *a):
+            at.pop()
+
+    monkeypatch.setattr(wl.torch.cuda, "current_device", lambda: at[-1])
+    monkeypatch.setattr(wl.torch.cuda, "device", On)
+    monkeypatch.setattr(wl, "_raw_stream", lambda index: index)
+    for f in ("wl_step_create", "wl_step_create_ops", "wl_step_launch"):
+        monkeypatch.setattr(wl.lib, f, lambda *a, f=f: seen.append((f, at[-1])) or 0)
+    ws = torch.zeros(1, dtype=torch.uint8)
+
+    def calls(*indexes):
+        return [(wl.OP_LINEAR, [theta()], Elsewhere(bf16(4, 64), i), bf16(4, 64)) for i in indexes]
+
+    for make, f in ((wl.Step, "wl_step_create"), (wl.LayerStep, "wl_step_create_ops")):
+        for index in (0, 1):
+            make(calls(index, index), ws=ws).launch()
+            assert seen == [(f, index), ("wl_step_launch", index)] and at == [0]
+            seen.clear()
+        with pytest.raises(ValueError, match="call 1"):
+            make(calls(0, 1), ws=ws)
+        assert not seen
