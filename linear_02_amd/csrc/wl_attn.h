@@ -130,6 +130,7 @@ __device__ void one_row(const AttnJob &a, const Seq &q, int i, int h, int j0, in
         const float p = __builtin_amdgcn_exp2f(s - (n == kNegInf ? 0.0f : n));
         m = n;
         l = l * up + p;
+        if (l != l) break;   // the row is NaN, whatever follows
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[e] = acc[e] * up + (p != 0.0f ? p * (vs * w[e]) : 0.0f);
     }

@@ -451,3 +451,20 @@ def test_visible_nan_reaches_the_output_through_the_join(wl, fmt, d, keys, bad, 
         o = b.run(wl)
         torch.cuda.synchronize()
         assert torch.isnan(o).all(), loud
+
+
+@pytest.mark.parametrize("fmt", [BF, E4, F32])
+def test_queries_of_nan_are_not_walked_key_by_key(wl, fmt):
+    """A prompt of NaN ends with the first key that each row sees: a wave would walk 16
+    rows one after the other, a quarter of a microsecond a key, 15 ms in all."""
+    b = Batch(wl, [0], [4096], 4, 1, 64, 64, fmt, seed=32)
+    b.q[5:].fill_(float("nan"))
+    for _ in range(2):
+        start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        torch.cuda.synchronize()
+        start.record()
+        o = b.run(wl)
+        end.record()
+        torch.cuda.synchronize()
+    assert torch.isnan(o[5:]).all() and torch.isfinite(o[:5]).all()
+    assert start.elapsed_time(end) < 2
