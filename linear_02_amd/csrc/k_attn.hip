@@ -65,7 +65,7 @@ constexpr int kMinChunk = 256, kMinChunkF32 = 64;
 // Most query rows per key/value head of the few-row kernel. Above 16 it takes two
 // row tiles a wave, which at heads over 128 fill or pass its registers: 8 trees of 8
 // tokens and 4 heads over up to 8192 keys of 256 took 189 us so in bf16 and 92 in
-// int8, 103 and 75 us in the tile kernel; at 128 wide 57 and 58 us, 45 and 55 us.
+// int8, 97 and 77 us in the tile kernel; at 128 wide 57 and 58 us, 45 and 55 us.
 int few_rows(const AttnJob &a) { return a.c.d > 128 ? 16 : 32; }
 
 // Tiles of query rows per wave, and what the weights keep. Which of the two precisions a
@@ -117,9 +117,10 @@ Plan plan_of(const AttnJob &a, int fmt, bool f32) {
     p.sp.want = (int)want, p.sp.places = (int)places;
     // Sequences differ in length, and max_kv is often what they may reach one day:
     // the device divides them by their lengths, up to 64, a lane each. 8 sequences of
-    // 2048 keys, one token, 32 and 8 heads of 256: 27 us whether max_kv is 2048 or
-    // 131072 (in pieces of max_kv: 27 and 47 us); one of 4096 keys, 4 heads: 21 us (20
-    // and 45); 4 trees over 9201 to 16336 int8 keys: 157 us (183).
+    // 2048 keys, one token, 32 and 8 heads of 256: 28 us whether max_kv is 2048 or
+    // 131072 (in pieces of max_kv: 27 and 47 us); one of 4096 keys, 4 heads: 20 us (20
+    // and 45). 64 sequences of up to 2048 keys, 4 heads over 1: 37 us under either; 65,
+    // which are divided by max_kv, 45 and 70.
     if (p.sp.n_split > 1 && a.c.n_seq <= 64) {
         p.sp.planned = 1;
         const int64_t most = (span + p.sp.least - 1) / p.sp.least;

@@ -9,7 +9,7 @@
 // transposing reads. The next 32 keys' loads are issued as soon as the registers
 // are free, so 32 keys of K and V per wave are under way while the present ones are
 // worked on. The matrix cores do 16 rows for the price of one, so the weights are
-// fed as a bf16 head plus a bf16 remainder and lose nothing. The four waves of a
+// fed as a bf16 head plus a bf16 remainder, off by 2^-16 at most. The four waves of a
 // workgroup join their outputs in LDS; workgroups that divide a long sequence
 // leave partial outputs that a second launch joins.
 //

@@ -256,7 +256,8 @@ class Workspace:
     graph capture records share one of that capture's own, allocated and prepared
     within it: under torch.cuda.graph its memory is the graph's, so that no later
     call can replace it, and no replay finds it prepared by another graph alone or in
-    use by one (pass ``ws`` to a call to leave the preparing out of the graph)."""
+    use by one. Pass ``ws`` to a call to leave the preparing out of the graph, and in a
+    capture that is not torch's, whose graph owns no memory."""
 
     def __init__(self):
         self._bufs: dict = {}
@@ -450,7 +451,7 @@ class Step:
     HIP graph (wl_step_create) and launches with one call.
 
     calls: (op, thetas, x, y) tuples, op one of OP_LINEAR (one theta), OP_QKV
-    (Q, K, V), OP_MLP (gate, up, down); device tensors, which must stay alive
+    (Q, K, V), OP_MLP (gate, up, down); tensors of one device, which must stay alive
     while the step exists (the step keeps references). group_shared_w0 launches
     calls that share their first theta's W0 back to back (independent calls
     only)."""
