@@ -439,7 +439,7 @@ wl_status wl_cache_read(const wl_cache_read_args *a, void *hip_stream);
  * Products of bf16 tensors run on the matrix cores with fp32 sums. For the
  * second product a weight (times its key's v_scale, in the quantised formats) is
  * rounded to bf16 (2^-8 of it at most), with the remainder as a second bf16 (then
- * 2^-16) where a call is small: with rows = max_q n_q / n_kv, where rows <= 64 or
+ * 2^-16) where a call is small: with rows = min(max_q, T) n_q / n_kv, rows <= 64 or
  * n_seq n_kv ceil(rows / 64) <= 32. Without the remainder, a bf16 cache's weights
  * are summed as rounded too. dtype f32 is fp32 throughout.
  * max_kv does not change what is rounded; the order of the fp32 sums follows the
