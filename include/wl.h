@@ -463,6 +463,178 @@ typedef struct {
 size_t wl_attention_workspace_bytes(const wl_attention_args *a);
 wl_status wl_attention(const wl_attention_args *a, void *ws, size_t ws_bytes, void *hip_stream);
 
+/* ---------------------------------------------------------------------------
+ * Around a batch of a serving step: which rows and pages it has, a cache of
+ * latent vectors with the attention over it, and which drafted tokens stay.
+ * Conventions as above.
+ */
+
+/* Plans the next step's batch on the device: gives pages to the sequences that
+ * grow, takes them back from those that were cut, and maps the batch's rows.
+ * For every sequence s in order, with `past` keys in the cache and `n_new` tokens
+ * to add (negative numbers count as 0):
+ *   want = ceil((past + n_new) / page) pages. s is served if want <= max_pages,
+ *          if the stack has the pages that it and the sequences before it lack
+ *          (one that lacks none is not held up by them), and if its rows and those
+ *          before it are T at most.
+ *   served       pages held .. want - 1 come from the top of the stack; n_new rows
+ *   not served   no pages, no rows; kv_len = past
+ *   pages behind ceil(kv_len / page) go back onto the stack, where the next call
+ *   finds them, and leave the table (-1)
+ * State, kept from call to call (in and out):
+ *   table       [n_seq][max_pages], a cache's page table
+ *   held        [n_seq] pages in the sequence's row of it
+ *   free_pages  [n_pages] a stack of page numbers, -1 above the top
+ *   n_free      [1] its height
+ * Written, as wl_cache_write and wl_attention read them:
+ *   q_start [n_seq + 1], kv_len [n_seq] (past + n_new where served)
+ *   seq, slot  [T] of every row: slots past .. past + n_new - 1 of a sequence, -1
+ *              behind the last sequence's rows. With T == 0 (pages only) they may be
+ *              NULL.
+ * A sequence is dropped by past = n_new = 0, a slot of the batch filled anew by
+ * giving its numbers. All int32. page as in wl_cache; n_seq at most 65536.
+ *   ws   ws_bytes >= wl_batch_plan_workspace_bytes(a) (its first WL_SYNC_BYTES are
+ *        not touched); NULL is accepted where that is 0 */
+typedef struct {
+    int32_t *table, *held, *free_pages, *n_free;
+    const int32_t *past, *n_new;
+    int32_t *q_start, *kv_len, *seq, *slot;
+    int32_t T, n_seq, max_pages, n_pages, page;
+} wl_batch_plan_args;
+size_t wl_batch_plan_workspace_bytes(const wl_batch_plan_args *a);
+wl_status wl_batch_plan(const wl_batch_plan_args *a, void *ws, size_t ws_bytes, void *hip_stream);
+
+/* A paged cache of latent vectors: one row a token, shared by all heads, with a
+ * latent vector c and a rotated key r.
+ *   rows    [n_pages][page] rows, 16-byte aligned:
+ *             WL_CACHE_BF16, WL_CACHE_F32  `latent` + `rot` elements
+ *             WL_CACHE_E4M3  `latent` e4m3 codes, then `rot` bf16 elements
+ *   scale   fp32 [n_pages][page] of the codes, 16-byte aligned (WL_CACHE_E4M3 only);
+ *           scales and codes as in wl_cache
+ *   table   as in wl_cache
+ * latent: 128, 256 or 512; rot: 32 or 64; page as in wl_cache. dtype bf16 goes with
+ * bf16 and e4m3 caches, f32 with f32 ones (else WL_ERR_UNSUPPORTED, as is
+ * WL_CACHE_INT8). The pool may hold more than 2^31 elements. */
+typedef struct {
+    void *rows;
+    float *scale;
+    const int32_t *table;
+    int32_t n_pages, page, latent, rot, n_seq, max_pages, format;
+} wl_latent_cache;
+
+/* Writes tokens into the cache: the latent normalised, the key rotated, and Q
+ * rotated beside them, in one launch.
+ *   c        [T] rows of latent + rot: a token's latent and its key
+ *   norm     [latent] or NULL: latent -> rms(latent) (norm + offset)
+ *   seq, slot  as in wl_cache_write
+ *   q, q_out [T] rows of n_q heads of nope + rot, of which the last rot are rotated;
+ *            q_out may be q; n_q == 0: no Q. nope: a multiple of 8, at most 256
+ *   rotary   NULL: no rotation; else its rot is the cache's. Its pos may be NULL:
+ *            the slots are the positions
+ * Skipped tokens, and tokens of one seq and slot, as in wl_cache_write. */
+typedef struct {
+    const wl_latent_cache *cache;
+    const void *c, *norm, *q;
+    void *q_out;
+    const int32_t *seq, *slot;
+    const wl_rotary *rotary;
+    int32_t T, n_q, nope, ldc, ldq, ldq_out, dtype;
+    float eps, offset;
+} wl_latent_write_args;
+wl_status wl_latent_write(const wl_latent_write_args *a, void *hip_stream);
+
+/* Reads tokens back: out [T] rows of latent + rot, as dtype. Tokens without a place
+ * leave their rows as they were. */
+typedef struct {
+    const wl_latent_cache *cache;
+    const int32_t *seq, *slot;
+    void *out;
+    int32_t T, ld, dtype;
+} wl_latent_read_args;
+wl_status wl_latent_read(const wl_latent_read_args *a, void *hip_stream);
+
+/* Attention of new tokens over the latent cache, which holds them already. Head h
+ * has its own keys and values of every row (c_j, r_j):
+ *   k_j = [ W_h^K c_j ; r_j ],  v_j = W_h^V c_j,  o = sum_j w_j v_j,
+ *   w = softmax_j( scale q . k_j )  over the visible keys j
+ *   q     [T] rows of n_q heads of nope + rot
+ *   w     [n_q][nope + value][latent]: W_h^K, then W_h^V of every head (the weight of
+ *         a projection from latent to n_q (nope + value), as wl_materialize_weff
+ *         writes it). NULL: q and o are in the latent space, nope = value = latent,
+ *         W_h^K = W_h^V = 1
+ *   o     [T] rows of n_q heads of value
+ *   nope, value  multiples of 32, at most 256 (with w)
+ *   q_start, kv_len, tree, q_pos, T, max_q, max_kv, mask, window, tree_words, scale
+ *         as in wl_attention, and the same rules for rows outside every sequence,
+ *         queries that see no key and keys that a query does not see
+ *   form  WL_LATENT_ABSORBED  q is taken to the latent space, W_h^K^T q, and attends
+ *                             there; W_h^V is applied to the outputs
+ *         WL_LATENT_EXPANDED  keys and values are formed once in the workspace.
+ *                             With w, bf16 tensors, nope and value both 64 or both
+ *                             128 only (else WL_ERR_UNSUPPORTED)
+ *         WL_LATENT_AUTO      the one that takes less time: expanded for prompts
+ * Numerics in bf16: q in the latent space, outputs there before W_h^V, expanded keys
+ * and values and the weights of the second product are each rounded to bf16 once;
+ * sums are fp32. dtype f32 is fp32 throughout.
+ *   ws   ws_bytes >= wl_latent_attention_workspace_bytes(a), as in wl_attention */
+enum { WL_LATENT_AUTO = 0, WL_LATENT_ABSORBED = 1, WL_LATENT_EXPANDED = 2 };
+typedef struct {
+    const wl_latent_cache *cache;
+    const void *q, *w;
+    void *o;
+    const int32_t *q_start, *kv_len;
+    const uint32_t *tree;
+    const int32_t *q_pos;
+    int32_t T, n_q, nope, value, ldq, ldo, max_q, max_kv, mask, window, tree_words, dtype, form;
+    float scale;
+} wl_latent_attention_args;
+size_t wl_latent_attention_workspace_bytes(const wl_latent_attention_args *a);
+wl_status wl_latent_attention(const wl_latent_attention_args *a, void *ws, size_t ws_bytes, void *hip_stream);
+
+/* Which drafted tokens stay, and the token behind them, so that the answer is
+ * distributed as the target's own. Row 0 of a sequence is its last known token, the
+ * others are drafted ones; row r of `target` is the target's distribution of the token
+ * that follows row r.
+ *   target, draft  [T] rows of `vocab`, ld apart (any ld >= vocab), 16-byte aligned;
+ *                  WL_VERIFY_LOGITS: p = softmax(x / temperature);
+ *                  WL_VERIFY_PROBABILITIES: p = x, negative and NaN as 0
+ *                  (a NaN logit counts as -inf)
+ *   token    int32 [T]; q_start as in wl_attention, rows outside every sequence are
+ *            left as they were; at most max_q rows of a sequence, 1 <= max_q <= 1024
+ *   parent   int32 [T] or NULL: the row, within its sequence, that a drafted row follows
+ *            (an earlier one, else the row is out of reach); NULL: the row before it
+ *   u        fp32 [T][2] in [0, 1), 8-byte aligned
+ *   temperature  fp32 [n_seq] or NULL (all 1); 0 or less: greedy, p is 1 at the largest
+ *            entry of the row, the first of equal ones, and `draft` is not read
+ * A draw with u from weights w is the first x with sum_(y <= x) w(y) > u sum w.
+ * draft == NULL (drafts that were not drawn, trees of them):
+ *   at row r the next token is drawn from p_r with u[r][1]; while a row that follows r
+ *   holds it, the first of these is next
+ * draft (row r: the distribution that row r + 1 was drawn from; parent NULL):
+ *   row r + 1 stays if u[r][0] draft_r(d) < p_r(d), d its token; behind the last row
+ *   that stays, the next token is drawn with u[r][1] from max(p_r - draft_r, 0), or
+ *   from p_r if no row was refused or nothing is left
+ * Written, for a sequence of m rows in its rows of out and path:
+ *   out    the tokens that stay, then the new one, then -1; a row without any weight
+ *          gives -1 as the new one
+ *   path   or NULL: the rows, within the sequence, whose keys stay: 0, then those of
+ *          the tokens that stay, then -1
+ *   n_out  [n_seq] tokens in out (those that stay + 1; 0 without rows)
+ *   len    or NULL: [n_seq], n_out is added (the keys that stay, as `past` of wl_batch_plan)
+ * Sums are fp64. dtype: of target and draft. vocab >= 1.
+ *   ws   ws_bytes >= wl_verify_drafts_workspace_bytes(a), its first WL_SYNC_BYTES not
+ *        touched */
+enum { WL_VERIFY_LOGITS = 0, WL_VERIFY_PROBABILITIES = 1 };
+typedef struct {
+    const void *target, *draft;
+    const int32_t *token, *q_start, *parent;
+    const float *u, *temperature;
+    int32_t *out, *path, *n_out, *len;
+    int32_t T, n_seq, vocab, ld_target, ld_draft, max_q, kind, dtype;
+} wl_verify_args;
+size_t wl_verify_drafts_workspace_bytes(const wl_verify_args *a);
+wl_status wl_verify_drafts(const wl_verify_args *a, void *ws, size_t ws_bytes, void *hip_stream);
+
 /* Steps of whole layers: wl_step_create for a list that mixes projection calls
  * with the operations above, so that a decode step of a model is one graph.
  *   op    WL_OP_LINEAR, WL_OP_QKV, WL_OP_MLP: args is a wl_call (whose op says
@@ -470,7 +642,9 @@ wl_status wl_attention(const wl_attention_args *a, void *ws, size_t ws_bytes, vo
  * Launched and destroyed as any step; positions, slots, lengths, page tables are
  * read at each launch, max_q and max_kv are fixed here (give the largest that
  * the step will meet). Every operation is checked as by its own entry point. */
-enum { WL_OP_NORM = 3, WL_OP_ROPE = 4, WL_OP_CACHE_WRITE = 5, WL_OP_CACHE_READ = 6, WL_OP_ATTENTION = 7 };
+enum { WL_OP_NORM = 3, WL_OP_ROPE = 4, WL_OP_CACHE_WRITE = 5, WL_OP_CACHE_READ = 6, WL_OP_ATTENTION = 7,
+       WL_OP_BATCH_PLAN = 16, WL_OP_LATENT_WRITE = 17, WL_OP_LATENT_READ = 18, WL_OP_LATENT_ATTENTION = 19,
+       WL_OP_VERIFY_DRAFTS = 20 };
 typedef struct {
     int32_t op;
     const void *args;

@@ -962,6 +962,22 @@ wl_status check_calls(const wl_call *calls, int32_t n_calls) {
     return WL_OK;
 }
 
+bool known_op(int32_t op) {
+    return (op >= WL_OP_LINEAR && op <= WL_OP_ATTENTION) || (op >= WL_OP_BATCH_PLAN && op <= WL_OP_VERIFY_DRAFTS);
+}
+
+// Workspace bytes of an operation other than the projections; 0 for invalid arguments too.
+size_t op_bytes(const wl_step_op &o) {
+    switch (o.op) {
+        case WL_OP_ATTENTION: return wl_attention_workspace_bytes(static_cast<const wl_attention_args *>(o.args));
+        case WL_OP_BATCH_PLAN: return wl_batch_plan_workspace_bytes(static_cast<const wl_batch_plan_args *>(o.args));
+        case WL_OP_LATENT_ATTENTION:
+            return wl_latent_attention_workspace_bytes(static_cast<const wl_latent_attention_args *>(o.args));
+        case WL_OP_VERIFY_DRAFTS: return wl_verify_drafts_workspace_bytes(static_cast<const wl_verify_args *>(o.args));
+        default: return 0;
+    }
+}
+
 wl_status run_op(const wl_step_op &o, void *ws, size_t ws_bytes, hipStream_t s) {
     switch (o.op) {
         case WL_OP_NORM: return wl_norm_residual(static_cast<const wl_norm_args *>(o.args), s);
@@ -969,6 +985,12 @@ wl_status run_op(const wl_step_op &o, void *ws, size_t ws_bytes, hipStream_t s) 
         case WL_OP_CACHE_WRITE: return wl_cache_write(static_cast<const wl_cache_write_args *>(o.args), s);
         case WL_OP_CACHE_READ: return wl_cache_read(static_cast<const wl_cache_read_args *>(o.args), s);
         case WL_OP_ATTENTION: return wl_attention(static_cast<const wl_attention_args *>(o.args), ws, ws_bytes, s);
+        case WL_OP_BATCH_PLAN: return wl_batch_plan(static_cast<const wl_batch_plan_args *>(o.args), ws, ws_bytes, s);
+        case WL_OP_LATENT_WRITE: return wl_latent_write(static_cast<const wl_latent_write_args *>(o.args), s);
+        case WL_OP_LATENT_READ: return wl_latent_read(static_cast<const wl_latent_read_args *>(o.args), s);
+        case WL_OP_LATENT_ATTENTION:
+            return wl_latent_attention(static_cast<const wl_latent_attention_args *>(o.args), ws, ws_bytes, s);
+        case WL_OP_VERIFY_DRAFTS: return wl_verify_drafts(static_cast<const wl_verify_args *>(o.args), ws, ws_bytes, s);
         default: return run_call(*static_cast<const wl_call *>(o.args), ws, ws_bytes, s);
     }
 }
@@ -1077,13 +1099,13 @@ size_t wl_step_ops_workspace_bytes(const wl_step_op *ops, int32_t n_ops) {
     // A step without projections or split attention still needs a workspace pointer.
     size_t most = WL_SYNC_BYTES;
     for (int i = 0; i < n_ops; ++i) {
-        if (!ops[i].args || ops[i].op < WL_OP_LINEAR || ops[i].op > WL_OP_ATTENTION) return 0;
+        if (!ops[i].args || !known_op(ops[i].op)) return 0;
         size_t b = 0;
         if (ops[i].op <= WL_OP_MLP) {
             const wl_call *c = static_cast<const wl_call *>(ops[i].args);
             if (c->op != ops[i].op || (b = wl_step_workspace_bytes(c, 1)) == 0) return 0;
-        } else if (ops[i].op == WL_OP_ATTENTION) {
-            b = wl_attention_workspace_bytes(static_cast<const wl_attention_args *>(ops[i].args));
+        } else {
+            b = op_bytes(ops[i]);
         }
         most = b > most ? b : most;
     }
@@ -1098,7 +1120,7 @@ wl_status wl_step_create_ops(const wl_step_op *ops, int32_t n_ops, void *ws, siz
         return fail(WL_ERR_INVALID_ARG, "n_ops=%d is outside [1, %d]", n_ops, kMaxStepCalls);
     for (int i = 0; i < n_ops; ++i) {
         if (!ops[i].args) return fail(WL_ERR_INVALID_ARG, "op %d: args is NULL", i);
-        if (ops[i].op < WL_OP_LINEAR || ops[i].op > WL_OP_ATTENTION)
+        if (!known_op(ops[i].op))
             return fail(WL_ERR_INVALID_ARG, "op %d: op=%d is unknown", i, ops[i].op);
         if (ops[i].op <= WL_OP_MLP) {
             const wl_call *c = static_cast<const wl_call *>(ops[i].args);

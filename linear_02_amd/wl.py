@@ -60,6 +60,11 @@ STEP_GROUP_SHARED_W0 = 1
 
 # The operations between the projections: norms, rotary positions, cache, attention.
 OP_NORM, OP_ROPE, OP_CACHE_WRITE, OP_CACHE_READ, OP_ATTENTION = 3, 4, 5, 6, 7
+# Those around a batch of a serving step: its plan, the latent cache, verification.
+OP_BATCH_PLAN, OP_LATENT_WRITE, OP_LATENT_READ, OP_LATENT_ATTENTION, OP_VERIFY_DRAFTS = 16, 17, 18, 19, 20
+LATENT_FORMS = {"auto": 0, "absorbed": 1, "expanded": 2}
+VERIFY_LOGITS, VERIFY_PROBABILITIES = 0, 1
+VERIFY_ROWS = 1024   # most rows of a sequence in wl_verify_drafts
 ROPE_HALF, ROPE_INTERLEAVED = 0, 1
 ROPE_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "parts": 3}
 MASKS = {"causal": 0, "tree": 1, "full": 2}
@@ -83,6 +88,16 @@ CacheWriteArgs = _struct("CacheWriteArgs", "cache k v q q_weight k_weight q_out 
 CacheReadArgs = _struct("CacheReadArgs", "cache seq slot k_out v_out", "T ldk ldv dtype")
 AttentionArgs = _struct("AttentionArgs", "cache q o q_start kv_len tree q_pos",
                         "T n_q ldq ldo max_q max_kv mask window tree_words dtype", "scale")
+BatchPlanArgs = _struct("BatchPlanArgs", "table held free_pages n_free past n_new q_start kv_len seq slot",
+                        "T n_seq max_pages n_pages page")
+LatentCacheStruct = _struct("LatentCacheStruct", "rows scale table", "n_pages page latent rot n_seq max_pages format")
+LatentWriteArgs = _struct("LatentWriteArgs", "cache c norm q q_out seq slot rotary", "T n_q nope ldc ldq ldq_out dtype",
+                          "eps offset")
+LatentReadArgs = _struct("LatentReadArgs", "cache seq slot out", "T ld dtype")
+LatentAttentionArgs = _struct("LatentAttentionArgs", "cache q w o q_start kv_len tree q_pos",
+                              "T n_q nope value ldq ldo max_q max_kv mask window tree_words dtype form", "scale")
+VerifyArgs = _struct("VerifyArgs", "target draft token q_start parent u temperature out path n_out len",
+                     "T n_seq vocab ld_target ld_draft max_q kind dtype")
 
 
 class StepOp(ctypes.Structure):
@@ -131,8 +146,15 @@ def _load(path: str = LIBRARY) -> ctypes.CDLL:
     lib.wl_step_destroy.argtypes = [vp]
     lib.wl_step_destroy.restype = ctypes.c_int
     for name, args in (("wl_norm_residual", NormArgs), ("wl_rope", RopeArgs), ("wl_cache_write", CacheWriteArgs),
-                       ("wl_cache_read", CacheReadArgs)):
+                       ("wl_cache_read", CacheReadArgs), ("wl_latent_write", LatentWriteArgs),
+                       ("wl_latent_read", LatentReadArgs)):
         getattr(lib, name).argtypes = [ctypes.POINTER(args), vp]
+        getattr(lib, name).restype = ctypes.c_int
+    for name, args in (("wl_batch_plan", BatchPlanArgs), ("wl_latent_attention", LatentAttentionArgs),
+                       ("wl_verify_drafts", VerifyArgs)):
+        getattr(lib, name + "_workspace_bytes").argtypes = [ctypes.POINTER(args)]
+        getattr(lib, name + "_workspace_bytes").restype = sz
+        getattr(lib, name).argtypes = [ctypes.POINTER(args), vp, sz, vp]
         getattr(lib, name).restype = ctypes.c_int
     lib.wl_rope_frequencies.argtypes = [i32, ctypes.c_double, i32] + [ctypes.c_double] * 4 + \
         [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_float)]
@@ -512,6 +534,12 @@ class Step:
 # in the same tensors) or recorded with others in a LayerStep.
 
 
+# Workspace bytes of the operations that take a workspace.
+_WORKSPACE_BYTES = {OP_ATTENTION: lib.wl_attention_workspace_bytes, OP_BATCH_PLAN: lib.wl_batch_plan_workspace_bytes,
+                    OP_LATENT_ATTENTION: lib.wl_latent_attention_workspace_bytes,
+                    OP_VERIFY_DRAFTS: lib.wl_verify_drafts_workspace_bytes}
+
+
 class OpCall:
     """A checked call of one operation: ``out`` are its outputs, ``launch`` runs it
     on the current stream of its device. Keeps its tensors alive."""
@@ -529,10 +557,11 @@ class OpCall:
 
     def _launch(self):
         stream = _raw_stream(self.device.index)
-        if self.op != OP_ATTENTION:
+        need_of = _WORKSPACE_BYTES.get(self.op)
+        if need_of is None:
             status = self.fn(self.args, stream)
         else:
-            need = lib.wl_attention_workspace_bytes(self.args)
+            need = need_of(self.args)
             ws = self.ws if self.ws is not None else WORKSPACE.scratch(self.device, need)
             status = self.fn(self.args, _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), stream)
         if status:
@@ -795,6 +824,239 @@ def attention_call(q, cache: Cache, q_start, kv_len, max_q: int, max_kv: int, sc
 def wl_attention(q, cache, q_start, kv_len, max_q, max_kv, scale, **kw):
     """softmax(scale q k) v of the tokens over the cache; see attention_call."""
     return attention_call(q, cache, q_start, kv_len, max_q, max_kv, scale, **kw).launch()
+
+
+# ---- around a batch of a serving step ---------------------------------------------
+
+
+class Pages:
+    """The pages of a cache's sequences, as wl_batch_plan keeps them on the device:
+    table int32 [n_seq][max_pages], held int32 [n_seq] pages of every row of it, free
+    int32 [n_pages] (a stack, -1 above its top) and its height n_free int32 [1], of
+    pages of ``page`` tokens. ``table`` is the cache's own."""
+
+    __slots__ = ("table", "held", "free", "n_free", "page")
+
+    def __init__(self, table, held, free, n_free, page: int):
+        if table.dtype != torch.int32 or table.dim() != 2 or not table.is_contiguous() or not table.is_cuda:
+            raise ValueError("table must be a contiguous int32 [n_seq][max_pages] device tensor")
+        _vector(held, "held", table, table.shape[0])
+        _vector(free, "free", table, free.numel())
+        _vector(n_free, "n_free", table, 1)
+        self.table, self.held, self.free, self.n_free, self.page = table, held, free, n_free, page
+
+
+def new_pages(n_seq: int, max_pages: int, n_pages: int, page: int, device="cuda") -> Pages:
+    """Pages of n_seq empty sequences, all of 0 .. n_pages - 1 free (the lowest first)."""
+    i32 = dict(dtype=torch.int32, device=device)
+    return Pages(torch.full((n_seq, max_pages), -1, **i32), torch.zeros(n_seq, **i32),
+                 torch.arange(n_pages - 1, -1, -1, **i32), torch.full((1,), n_pages, **i32), page)
+
+
+def batch_plan_call(pages: Pages, past, n_new, T: int, q_start=None, kv_len=None, seq=None, slot=None,
+                    ws: torch.Tensor | None = None) -> OpCall:
+    """wl_batch_plan as an OpCall; out = (q_start, kv_len, seq, slot) of a batch of T rows."""
+    t = pages.table
+    n_seq, max_pages = t.shape
+    q_start = t.new_empty(n_seq + 1) if q_start is None else q_start
+    kv_len = t.new_empty(n_seq) if kv_len is None else kv_len
+    seq = t.new_empty(T) if seq is None else seq
+    slot = t.new_empty(T) if slot is None else slot
+    args = BatchPlanArgs(t.data_ptr(), pages.held.data_ptr(), pages.free.data_ptr(), pages.n_free.data_ptr(),
+                         _vector(past, "past", t, n_seq), _vector(n_new, "n_new", t, n_seq),
+                         _vector(q_start, "q_start", t, n_seq + 1), _vector(kv_len, "kv_len", t, n_seq),
+                         _vector(seq, "seq", t, T), _vector(slot, "slot", t, T), T, n_seq, max_pages,
+                         pages.free.numel(), pages.page)
+    return OpCall(OP_BATCH_PLAN, lib.wl_batch_plan, args, (q_start, kv_len, seq, slot), t.device,
+                  (t, pages.held, pages.free, pages.n_free, past, n_new), ws)
+
+
+def wl_batch_plan(pages, past, n_new, T, **kw):
+    """(q_start, kv_len, seq, slot) of the next batch: n_new tokens behind past keys of
+    every sequence, in T rows; pages are given and taken back. See batch_plan_call."""
+    return batch_plan_call(pages, past, n_new, T, **kw).launch()
+
+
+class LatentCache:
+    """A paged cache of latent vectors: rows [n_pages][page][latent + rot] (bf16 or
+    fp32), or uint8 [n_pages][page][latent + 2 rot] (e4m3 codes, then the key in bf16)
+    with fp32 scale [n_pages][page]; table int32 [n_seq][max_pages] of page numbers."""
+
+    __slots__ = ("rows", "table", "scale", "latent", "rot", "struct")
+
+    def __init__(self, rows, table, latent: int, rot: int, scale=None):
+        codes = rows.dtype == torch.uint8
+        if not (codes or rows.dtype in _CODES) or rows.dim() != 3 or not rows.is_contiguous() or not rows.is_cuda:
+            raise ValueError("rows must be a contiguous [n_pages][page][width] device tensor of bf16, fp32 or uint8")
+        if rows.shape[2] != latent + (2 * rot if codes else rot):
+            raise ValueError(f"rows must be {latent + (2 * rot if codes else rot)} wide")
+        _tensor(table, "table", rows, torch.int32)
+        if table.dim() != 2 or not table.is_contiguous():
+            raise ValueError("table must be a contiguous [n_seq][max_pages] tensor")
+        if codes and (scale is None or scale.shape != rows.shape[:2]):
+            raise ValueError("scale must be [n_pages][page]")
+        self.rows, self.table, self.scale, self.latent, self.rot = rows, table, scale, latent, rot
+        self.struct = LatentCacheStruct(
+            rows.data_ptr(), _vector(scale, "scale", rows, scale.numel(), torch.float32) if codes else None,
+            table.data_ptr(), rows.shape[0], rows.shape[1], latent, rot, table.shape[0], table.shape[1],
+            CACHE_FORMATS[torch.float8_e4m3fn] if codes else CACHE_FORMATS[rows.dtype])
+        self.struct.tensors = rows, table, scale   # what it points into, for calls that hold it
+
+    @property
+    def dtype(self) -> torch.dtype:
+        """Of the tensors that go with it."""
+        return torch.float32 if self.rows.dtype == torch.float32 else torch.bfloat16
+
+
+def new_latent_cache(n_pages: int, page: int, latent: int, rot: int, table: torch.Tensor,
+                     dtype=torch.bfloat16) -> LatentCache:
+    """A LatentCache of uninitialised pages on the table's device; dtype bf16, fp32 or
+    float8_e4m3fn."""
+    if dtype not in (torch.bfloat16, torch.float32, torch.float8_e4m3fn):
+        raise ValueError("dtype must be bf16, fp32 or float8_e4m3fn")
+    codes = dtype == torch.float8_e4m3fn
+    rows = torch.empty(n_pages, page, latent + (2 * rot if codes else rot), dtype=torch.uint8 if codes else dtype,
+                       device=table.device)
+    scale = torch.empty(n_pages, page, dtype=torch.float32, device=table.device) if codes else None
+    return LatentCache(rows, table, latent, rot, scale)
+
+
+def latent_write_call(cache: LatentCache, c, seq, slot, q=None, n_q: int = 0, rope: Rope | None = None, pos=None,
+                      norm=None, eps: float = 1e-6, offset: float = 0.0, q_out=None) -> OpCall:
+    """wl_latent_write as an OpCall; out = q_out (None without q). c: [T][latent + rot];
+    q: [T] rows of n_q heads, of which the last rot elements are rotated. pos None: the
+    slots are the positions."""
+    s = cache.struct
+    T = _first(c, "c").shape[0]
+    _tensor(cache.rows, "the cache", c, cache.rows.dtype)
+    nope = ldq = ldo = 0
+    if q is not None:
+        if n_q < 1 or q.dim() != 2 or q.shape[1] % n_q or q.shape[1] // n_q < s.rot:
+            raise ValueError(f"q must be a matrix of n_q heads of at least {s.rot}")
+        nope = q.shape[1] // n_q - s.rot
+        ldq = _matrix(q, "q", c, T, q.shape[1])
+        if q_out is None:
+            q_out = q.new_empty(q.shape)
+        ldo = _matrix(q_out, "q_out", c, T, q.shape[1])
+    elif n_q:
+        raise ValueError("n_q goes with q")
+    rot = None if rope is None else rope.struct(pos, T, c)
+    args = LatentWriteArgs(_at(s), c.data_ptr(), _vector(norm, "norm", c, s.latent), _ptr(q), _ptr(q_out),
+                           _vector(seq, "seq", c, T, torch.int32), _vector(slot, "slot", c, T, torch.int32), _at(rot), T,
+                           n_q, nope, _matrix(c, "c", c, T, s.latent + s.rot), ldq, ldo, _CODES[c.dtype], eps, offset)
+    return OpCall(OP_LATENT_WRITE, lib.wl_latent_write, args, q_out, c.device, (s, c, norm, q, seq, slot, rot, pos))
+
+
+def wl_latent_write(cache, c, seq, slot, **kw):
+    """Writes the tokens' latents (normalised by ``norm``) and keys (rotated) into the
+    cache, q rotated beside them; returns the rotated q, or None. See latent_write_call."""
+    return latent_write_call(cache, c, seq, slot, **kw).launch()
+
+
+def latent_read_call(cache: LatentCache, seq, slot, out=None) -> OpCall:
+    """wl_latent_read as an OpCall; out = [T][latent + rot] of cache.dtype. Rows of
+    tokens without a place in the cache keep what it held (a new one is uninitialised)."""
+    s, T = cache.struct, seq.numel()
+    out = cache.rows.new_empty((T, s.latent + s.rot), dtype=cache.dtype) if out is None else _first(out, "out")
+    _tensor(out, "out", cache.rows, cache.dtype)
+    args = LatentReadArgs(_at(s), _vector(seq, "seq", out, T, torch.int32), _vector(slot, "slot", out, T, torch.int32),
+                          out.data_ptr(), T, _matrix(out, "out", out, T, s.latent + s.rot), _CODES[out.dtype])
+    return OpCall(OP_LATENT_READ, lib.wl_latent_read, args, out, out.device, (s, seq, slot))
+
+
+def wl_latent_read(cache, seq, slot, **kw):
+    """The rows of the tokens at (seq, slot), read back from the cache."""
+    return latent_read_call(cache, seq, slot, **kw).launch()
+
+
+def latent_attention_call(q, cache: LatentCache, w, q_start, kv_len, max_q: int, max_kv: int, scale: float,
+                          mask: str | None = None, window: int = 0, tree=None, q_pos=None, form: str = "auto", o=None,
+                          ws: torch.Tensor | None = None) -> OpCall:
+    """wl_latent_attention as an OpCall; out = o. q: [T] rows of heads of nope + rot; w:
+    [n_q][nope + value][latent], or None, where q's heads are latent + rot wide and o's
+    latent. mask, window, tree, q_pos as in attention_call; form "auto", "absorbed" or
+    "expanded"."""
+    s = cache.struct
+    T = _first(q, "q").shape[0]
+    _tensor(cache.rows, "the cache", q, cache.rows.dtype)
+    if w is None:
+        n_q, nope, value = _heads(q, "q", s.latent + s.rot), s.latent, s.latent
+    else:
+        _tensor(w, "w", q)
+        if w.dim() != 3 or not w.is_contiguous() or w.shape[2] != s.latent:
+            raise ValueError(f"w must be a contiguous [n_q][nope + value][{s.latent}] tensor")
+        n_q = w.shape[0]
+        if n_q < 1 or q.shape[1] % n_q:
+            raise ValueError(f"q must be a matrix of {n_q} heads")
+        nope = q.shape[1] // n_q - s.rot
+        value = w.shape[1] - nope
+        if nope < 1 or value < 1:
+            raise ValueError(f"q's heads of {q.shape[1] // n_q} do not go with w's {w.shape[1]} rows a head")
+    if o is None:
+        o = q.new_empty((T, n_q * value))
+    mask = mask or ("causal" if tree is None else "tree")
+    if mask not in MASKS:
+        raise ValueError(f"mask {mask!r} is not one of {sorted(MASKS)}")
+    if form not in LATENT_FORMS:
+        raise ValueError(f"form {form!r} is not one of {sorted(LATENT_FORMS)}")
+    if (tree is None) == (mask == "tree"):
+        raise ValueError("tree goes with mask='tree'")
+    words = 0
+    if tree is not None:
+        if tree.dim() != 2 or tree.shape[0] != T:
+            raise ValueError(f"tree must be [{T}][words]")
+        words = tree.shape[1]
+    elif q_pos is not None:
+        raise ValueError("q_pos goes with mask='tree'")
+    n_seq = s.n_seq
+    args = LatentAttentionArgs(
+        _at(s), q.data_ptr(), _ptr(w), o.data_ptr(), _vector(q_start, "q_start", q, n_seq + 1, torch.int32),
+        _vector(kv_len, "kv_len", q, n_seq, torch.int32), _vector(tree, "tree", q, T * words, torch.int32),
+        _vector(q_pos, "q_pos", q, T, torch.int32), T, n_q, nope, value, _matrix(q, "q", q, T, n_q * (nope + s.rot)),
+        _matrix(o, "o", q, T, n_q * value), max_q, max_kv, MASKS[mask], window, words, _CODES[q.dtype],
+        LATENT_FORMS[form], scale)
+    return OpCall(OP_LATENT_ATTENTION, lib.wl_latent_attention, args, o, q.device,
+                  (q, s, w, q_start, kv_len, tree, q_pos), ws)
+
+
+def wl_latent_attention(q, cache, w, q_start, kv_len, max_q, max_kv, scale, **kw):
+    """softmax(scale q k) v of the tokens over the latent cache, every head's keys and
+    values formed from its rows by w; see latent_attention_call."""
+    return latent_attention_call(q, cache, w, q_start, kv_len, max_q, max_kv, scale, **kw).launch()
+
+
+def verify_drafts_call(target, token, q_start, u, draft=None, parent=None, temperature=None, probabilities: bool = False,
+                       max_q: int = VERIFY_ROWS, length=None, out=None, n_out=None, path=None,
+                       ws: torch.Tensor | None = None) -> OpCall:
+    """wl_verify_drafts as an OpCall; out = (out, n_out, path). target, draft: [T][vocab]
+    logits, or probabilities; token int32 [T]; q_start int32 [n_seq + 1]; u fp32 [T][2];
+    parent int32 [T] for trees; temperature fp32 [n_seq] (0: greedy); length int32
+    [n_seq]: n_out is added to it."""
+    T, vocab = _first(target, "target").shape
+    n_seq = q_start.numel() - 1
+    lds = [0, 0]
+    for i, (t, name) in enumerate(((target, "target"), (draft, "draft"))):
+        if t is not None:
+            lds[i] = _matrix(t, name, target, T, vocab)
+    out = token.new_empty(T) if out is None else out
+    n_out = token.new_empty(n_seq) if n_out is None else n_out
+    path = token.new_empty(T) if path is None else path
+    i32, f32 = torch.int32, torch.float32
+    args = VerifyArgs(target.data_ptr(), _ptr(draft), _vector(token, "token", target, T, i32),
+                      _vector(q_start, "q_start", target, n_seq + 1, i32), _vector(parent, "parent", target, T, i32),
+                      _vector(u, "u", target, 2 * T, f32), _vector(temperature, "temperature", target, n_seq, f32),
+                      _vector(out, "out", target, T, i32), _vector(path, "path", target, T, i32),
+                      _vector(n_out, "n_out", target, n_seq, i32), _vector(length, "length", target, n_seq, i32), T, n_seq,
+                      vocab, lds[0], lds[1], max_q, VERIFY_PROBABILITIES if probabilities else VERIFY_LOGITS,
+                      _CODES[target.dtype])
+    return OpCall(OP_VERIFY_DRAFTS, lib.wl_verify_drafts, args, (out, n_out, path), target.device,
+                  (target, draft, token, q_start, parent, u, temperature, length), ws)
+
+
+def wl_verify_drafts(target, token, q_start, u, **kw):
+    """(out, n_out, path): of every sequence the drafted tokens that stay and the one
+    behind them, how many, and their rows; see verify_drafts_call."""
+    return verify_drafts_call(target, token, q_start, u, **kw).launch()
 
 
 class LayerStep(Step):
