@@ -1,0 +1,482 @@
+// Attention of latent queries on the matrix cores, over bf16 and e4m3 rows.
+//
+// All heads share a row, and a row is key and value at once: a workgroup takes a tile
+// of (token, head) rows and brings every cache row once into LDS, 32 at a time, where
+// its first `latent` elements serve both products. Queries, scores, weights and outputs
+// stay in registers from the first key to the last; at a latent of 512 that is 128 of
+// outputs and 72 of queries for every 16 rows a wave has.
+//   many rows  four waves of 32 rows share a tile of keys (one wave per SIMD, which
+//              then has 512 registers): an operand read from LDS serves two products
+//   64 rows    four waves of 16 rows, two workgroups per CU
+//   32 rows    two pairs of waves, each pair with keys of its own
+//   16 rows    every wave with keys of its own, which it fetches for itself and waits
+//              for alone; joined in LDS at the end
+// Rows of e4m3 stay codes in LDS and are widened as operands: half the LDS traffic, and
+// the vector units have the time beside the products.
+#include "wl_latent.h"
+
+namespace wl {
+
+namespace {
+
+// The tile in LDS: rows of kP pieces of 16 bytes, with place for 64 rotated elements.
+// kP is 8 modulo 16 (0 for 256 bytes of codes), so that neighbouring rows start half of
+// the banks apart; piece c of row r lies at c ^ swizzle(r), and at c ^ (r & 7) in the
+// rotated part. Every pass of the operands' reads (16 rows and one piece of a key
+// operand; 8 rows and 32 bytes of a transposing read; rows 0 .. 7 and 16 .. 23 and 16
+// bytes of an 8-bit one) then meets all 64 banks once.
+template <int F, int L>
+struct Tile {
+    static constexpr bool kCodes = F == kFmtE4m3;
+    static constexpr int kLatent = kCodes ? L / 16 : L / 8;   // pieces of the latent
+    static constexpr int kP = kLatent + 8, kRow = 16 * kP;
+    static constexpr int kBytes = 32 * kRow;
+    static constexpr int kLoads = 16 * kP / 64;               // of 16 rows
+    static __device__ __forceinline__ int swizzle(int r) { return ((r & 15) ^ (r >> 1 & 8)) & (kLatent - 1); }
+};
+
+// kNT: tiles of 16 rows per wave. kRW x kKW waves: over rows, and over keys. kExact: queries'
+// and weights' remainders are multiplied too.
+template <int F, int L, int kNT, int kRW, int kKW, bool kExact>
+__global__ __launch_bounds__(256, kNT == 1 && kKW == 1 ? 2 : 1) void latent_kernel(CoreArgs x) {
+    typedef Tile<F, L> T;
+    constexpr bool kCodes = T::kCodes;
+    constexpr int kSteps = L / 32, kBlocks = L / 16, kRow = T::kRow;
+    constexpr int kBuffers = kKW == 4 ? 1 : 2;
+    constexpr int kScales = kCodes ? kKW * 2 * 32 * 4 : 0;    // [group][step % 2][32]
+    constexpr int kTiles = kKW * kBuffers * T::kBytes, kJoin = kKW > 1 ? 4 * kBlocks * 1024 : 0;
+    constexpr int kMain = kTiles + kScales > kJoin ? kTiles + kScales : kJoin;
+    __shared__ __align__(16) char lds_all[kMain + 512];
+    int (*range)[4] = reinterpret_cast<int (*)[4]>(lds_all + kMain);                   // [lo, hi][wave]
+    const AttnJob &a = x.a;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n = lane & 15, g = lane >> 4;
+    const int rw = wave % kRW, kw = wave / kRW;
+    Seq q;
+    const Work work = work_of(a, x.sp, (int)blockIdx.x, q);
+    const int tile = work.tile, s = work.s;
+    if (s < 0) return;
+    const int rows = q.rows * a.group, R = x.rot;
+    constexpr int kRows = 16 * kNT * kRW;
+    if (tile * kRows >= rows) return;
+    auto rows_of = [](int tile, int) {
+        const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % kRW;
+        return WaveRows{tile * kRows + 16 * kNT * w, kNT};
+    };
+    const int r0 = rows_of(tile, rows).first;
+
+    u32x4 qf[kNT][kSteps + 2], ql[kExact ? kNT : 1][kExact ? kSteps : 1];
+    f32x4 o[kNT][kBlocks];
+    float m[kNT], l[kNT];
+    int lo = 0x7FFFFFFF, hi = 0, flo = 0, fhi = 0x7FFFFFFF;   // some row sees [lo, hi), every row [flo, fhi)
+    const uint32_t sign = a.scale2 < 0.0f ? 0x80008000u : 0u;   // a negative scale goes into the queries
+    const float scale2 = fmaxf(fabsf(a.scale2), 0x1p-126f);   // not 0: -inf marks an unseen key
+#pragma unroll
+    for (int t = 0; t < kNT; ++t) {
+        const int r = r0 + 16 * t + n, i = r / a.group;
+        const bool on = r < rows;
+        const int64_t at = (int64_t)(q.q0 + (on ? i : 0)) * a.ldq + (int64_t)(on ? r - i * a.group : 0) * (L + R) + 8 * g;
+        if (!kExact) {
+            const uint16_t *qp = static_cast<const uint16_t *>(a.q) + at;
+#pragma unroll
+            for (int k = 0; k < kSteps + 2; ++k) {
+                qf[t][k] = u32x4{0, 0, 0, 0};
+                if (on && 32 * k < L + R) qf[t][k] = ldg(reinterpret_cast<const u32x4 *>(qp + 32 * k)) ^ sign;
+            }
+        } else {
+            // fp32 queries: a bf16 head and a bf16 remainder; the rotated part is exact in bf16.
+            const float *qp = static_cast<const float *>(a.q) + at;
+#pragma unroll
+            for (int k = 0; k < kSteps + 2; ++k) {
+                f32x4 v[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+                if (on && 32 * k < L + R)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) v[e] = ldg(reinterpret_cast<const f32x4 *>(qp + 32 * k + 4 * e));
+                uint32_t h[4], w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float v0 = v[e >> 1][2 * (e & 1)], v1 = v[e >> 1][2 * (e & 1) + 1];
+                    h[e] = pack2(v0, v1);
+                    w[e] = pack2(v0 - bf16_f(h[e] & 0xFFFFu), v1 - __uint_as_float(h[e] & 0xFFFF0000u));
+                }
+                qf[t][k] = u32x4{h[0], h[1], h[2], h[3]} ^ sign;
+                if (k < kSteps) ql[t][k] = u32x4{w[0], w[1], w[2], w[3]} ^ sign;
+            }
+        }
+        const Sees see = sees(a, q, i);
+        if (on) {   // an unused column is never the reason to mask
+            lo = min(lo, see.tree ? min(see.lo, max(q.ctx, 0)) : see.lo);
+            hi = max(hi, see.tree ? q.kv : see.hi);
+            flo = max(flo, see.lo);
+            fhi = min(fhi, see.hi);
+        }
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b) o[t][b] = f32x4{0, 0, 0, 0};
+        m[t] = kNegInf, l[t] = 0.0f;
+    }
+#pragma unroll
+    for (int y = 1; y < 16; y <<= 1) {
+        lo = min(lo, __shfl_xor(lo, y));
+        hi = max(hi, __shfl_xor(hi, y));
+        flo = max(flo, __shfl_xor(flo, y));
+        fhi = min(fhi, __shfl_xor(fhi, y));
+    }
+    flo = __builtin_amdgcn_readfirstlane(flo);
+    fhi = __builtin_amdgcn_readfirstlane(fhi);
+    if (lane == 0) range[0][wave] = lo, range[1][wave] = hi;
+    __syncthreads();
+    const int wlo = __builtin_amdgcn_readfirstlane(lo), whi = __builtin_amdgcn_readfirstlane(hi);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) lo = min(lo, range[0][w]), hi = max(hi, range[1][w]);
+    lo = __builtin_amdgcn_readfirstlane(lo) & ~31;
+    hi = __builtin_amdgcn_readfirstlane(hi);
+    const int64_t c0 = (int64_t)lo + work.from;
+    const int k0 = c0 < hi ? (int)c0 : hi, k1 = (int)min((int64_t)hi, c0 + work.chunk), last = k1 - 1;
+
+    if (k0 < k1) {
+        const int32_t *table = a.c.table + (int64_t)s * a.c.max_pages;
+        const int shift = a.c.page_shift, pmask = (1 << shift) - 1, n_pages = a.c.n_pages;
+        const int pieces = kCodes ? (L + 2 * R) / 16 : (L + R) / 8, bytes = 16 * pieces;   // of a cache row
+        const int64_t page_bytes = (int64_t)bytes << shift;
+        // Keys come in halves of 16, each within one page; a wave fetches kHalves of them, or part of one.
+        constexpr int kHalves = kRW == 1 ? 2 : 1, kMine = T::kLoads * 2 / kRW / kHalves;   // loads of a half
+        const int half0 = kRW == 1 ? 0 : rw / (kRW / 2), load0 = kRW == 4 ? rw % 2 * kMine : 0;
+        int page[2];
+        int first_page = -64, entries = 0;   // lane i holds entry first_page + i of the table
+        auto look = [&](int j0) {
+            const int e0 = min(j0, last) >> shift, e1 = min(j0 + 16, last) >> shift;
+            if (e1 - first_page >= 64) {
+                first_page = e0;
+                entries = table[min(e0 + lane, last >> shift)];
+                __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
+            }
+            page[0] = __builtin_amdgcn_readlane(entries, e0 - first_page);
+            page[1] = __builtin_amdgcn_readlane(entries, e1 - first_page);
+        };
+        auto has_page = [&](int b) { return (unsigned)page[b] < (unsigned)n_pages; };
+        uint32_t valid_in = 0;
+        auto fetch = [&](int j0, int step) {
+            valid_in = (has_page(0) ? 0xFFFFu : 0u) | (has_page(1) ? 0xFFFF0000u : 0u);
+            const uint32_t to = lds_byte(lds_all) + (kw * kBuffers + (kBuffers == 2 ? step & 1 : 0)) * T::kBytes;
+            int ln = lane;
+            asm volatile("" : "+v"(ln));   // what follows from it is not kept through the loop
+#pragma unroll
+            for (int hh = 0; hh < kHalves; ++hh) {
+                const int half = half0 + hh, jh = j0 + 16 * half;
+                const int pg = half ? page[1] : page[0], off = min(jh, last) & pmask & ~15;
+                const int most = last - min(jh, last & ~15);   // rows behind the last key read that key again
+                const char *from = scalar(static_cast<const char *>(a.c.k) + ((unsigned)pg < (unsigned)n_pages ? pg : 0) * page_bytes + (int64_t)off * bytes);
+#pragma unroll
+                for (int i = 0; i < kMine; ++i) {
+                    const int p = (load0 + i) * 64 + ln, r = (unsigned)p / (unsigned)T::kP, c = p - r * T::kP;
+                    const int piece = c < T::kLatent ? c ^ T::swizzle(16 * half + r) : T::kLatent + ((c - T::kLatent) ^ (r & 7));
+                    load_to_lds(from, min(r, most) * bytes + min(piece, pieces - 1) * 16, to + half * 16 * kRow + (load0 + i) * 1024);
+                }
+                if (kCodes && rw == (kRW == 1 ? 0 : kRW / 2 * half)) {
+                    const char *sc = scalar(reinterpret_cast<const char *>(a.c.k_scale + (((int64_t)((unsigned)pg < (unsigned)n_pages ? pg : 0) << shift) + off)));
+                    if (ln < 16) load_to_lds4(sc, min(ln, most) * 4, lds_byte(lds_all) + kTiles + ((kw * 2 + (step & 1)) * 32 + 16 * half) * 4);
+                }
+            }
+        };
+        // Eight elements of a key operand: piece (in eights of elements) c of row r.
+        auto key8 = [&](const char *row, int r, int c) {
+            if (kCodes)
+                return [](u32x2 w) { return widen8<kFmtE4m3>(w.x, w.y); }(*reinterpret_cast<const u32x2 *>(row + ((c >> 1 ^ T::swizzle(r)) << 4) + 8 * (c & 1)));
+            return *reinterpret_cast<const u32x4 *>(row + ((c ^ T::swizzle(r)) << 4));
+        };
+        const int key_v = 4 * g + (n >> 2), key_c = n < 8 ? 4 * g + (n >> 1) : 16 + 4 * g + ((n - 8) >> 1);
+        auto attend = [&](const int &j0, const int &step, const uint32_t &valid) {
+            const char *in = lds_all + (kw * kBuffers + (kBuffers == 2 ? step & 1 : 0)) * T::kBytes;
+            const float *scales = reinterpret_cast<const float *>(lds_all + kTiles) + (kw * 2 + (step & 1)) * 32;
+            int nn = n, gg = g;
+            asm volatile("" : "+v"(nn), "+v"(gg));   // places are formed anew in every step
+            f32x4 sc[kNT][2];
+            __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const int r = 16 * b + nn;
+                const char *row = in + r * kRow;
+#pragma unroll
+                for (int t = 0; t < kNT; ++t) sc[t][b] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int k = 0; k < kSteps; ++k) {
+                    const u32x4 kf = key8(row, r, 4 * k + gg);
+#pragma unroll
+                    for (int t = 0; t < kNT; ++t) {
+                        sc[t][b] = mfma16(kf, qf[t][k], sc[t][b]);
+                        if (kExact) sc[t][b] = mfma16(kf, ql[t][k], sc[t][b]);
+                    }
+                }
+                if (kCodes) {
+                    const f32x4 ks = *reinterpret_cast<const f32x4 *>(scales + 16 * b + 4 * g);
+#pragma unroll
+                    for (int t = 0; t < kNT; ++t) sc[t][b] *= ks;
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    if (32 * k >= R) break;
+                    const u32x4 kf = *reinterpret_cast<const u32x4 *>(row + ((T::kLatent + ((4 * k + gg) ^ (r & 7))) << 4));
+#pragma unroll
+                    for (int t = 0; t < kNT; ++t) sc[t][b] = mfma16(kf, qf[t][kSteps + k], sc[t][b]);
+                }
+            }
+            __builtin_amdgcn_s_setprio(0);
+            u32x4 ph[kNT], pl[kNT];
+            const bool all = j0 >= flo && j0 + 32 <= min(fhi, k1) && valid == 0xFFFFFFFFu;
+#pragma unroll
+            for (int t = 0; t < kNT; ++t) {
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = sc[t][e >> 2][e & 3];
+                if (!all) {
+                    const CoreArgs again = argument_again<CoreArgs>();
+                    const Seq qq = seq_of(again.a, work.s);
+                    const int r = rows_of(work.tile, 0).first + 16 * t + (threadIdx.x & 15);
+                    const uint32_t mine = (visible32(again.a, qq, sees(again.a, qq, r / again.a.group), j0) & valid & bits(0, k1 - j0)) >> (4 * g);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] = mine & (1u << (16 * (e >> 2) + (e & 3))) ? v[e] : kNegInf;
+                }
+                float top = v[0];
+#pragma unroll
+                for (int e = 1; e < 8; ++e) top = fmaxf(top, v[e]);
+                top = groups_max(top);
+                top = top == kNegInf ? top : top * scale2;
+                if (__any(top > m[t] + 8.0f)) {
+                    // The reference moves only when a score passes it by 2^8: sums stay in range.
+                    const float now = fmaxf(m[t], top), up = now == m[t] ? 1.0f : __builtin_amdgcn_exp2f(m[t] - now);
+                    m[t] = now;
+                    l[t] *= up;
+#pragma unroll
+                    for (int b = 0; b < kBlocks; ++b) o[t][b] *= up;
+                }
+                const float ref = m[t] == kNegInf ? 0.0f : m[t];
+                float p[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(v[e], scale2, -ref));
+                    if (kCodes || kExact) l[t] += p[e];
+                }
+                if (kCodes) {
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        const f32x4 vs = *reinterpret_cast<const f32x4 *>(scales + 16 * b + 4 * g);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) p[4 * b + e] = p[4 * b + e] == 0.0f ? 0.0f : p[4 * b + e] * vs[e];
+                    }
+                }
+                ph[t] = u32x4{pack2(p[0], p[1]), pack2(p[2], p[3]), pack2(p[4], p[5]), pack2(p[6], p[7])};
+                if (kExact) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        w[e] = pack2(p[2 * e] - bf16_f(ph[t][e] & 0xFFFFu), p[2 * e + 1] - __uint_as_float(ph[t][e] & 0xFFFF0000u));
+                    pl[t] = u32x4{w[0], w[1], w[2], w[3]};
+                } else if (!kCodes) {
+                    // the sum of the weights as the product will use them
+                    constexpr uint32_t kOnes = 0x3F803F80u;
+                    l[t] = dot2(ph[t].x, kOnes, l[t]);
+                    l[t] = dot2(ph[t].y, kOnes, l[t]);
+                    l[t] = dot2(ph[t].z, kOnes, l[t]);
+                    l[t] = dot2(ph[t].w, kOnes, l[t]);
+                }
+            }
+            __builtin_amdgcn_s_setprio(1);
+            int kv = kCodes ? key_c : key_v, nv = n;
+            asm volatile("" : "+v"(kv), "+v"(nv));
+            const char *row = in + kv * kRow;
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b) {
+                u32x4 vf;
+                if (kCodes) {
+                    const u32x2 w = read_tr8(row + ((b ^ T::swizzle(kv)) << 4) + 8 * (nv & 1));
+                    vf = widen8<kFmtE4m3>(w.x, w.y);
+                } else {
+                    // rows kv and 16 + kv, whose swizzles differ in bit 3
+                    const int c = (2 * b + (nv >> 1 & 1)) ^ T::swizzle(kv);
+                    const u32x2 u = read_tr16(row + (c << 4) + 8 * (nv & 1)), w = read_tr16(row + 16 * kRow + ((c ^ 8) << 4) + 8 * (nv & 1));
+                    vf = u32x4{u.x, u.y, w.x, w.y};
+                }
+#pragma unroll
+                for (int t = 0; t < kNT; ++t) {
+                    o[t][b] = mfma16(vf, ph[t], o[t][b]);
+                    if (kExact) o[t][b] = mfma16(vf, pl[t], o[t][b]);
+                }
+            }
+            __builtin_amdgcn_s_setprio(0);
+        };
+        if (kKW < 4) {
+            // A group's tile of step n is fetched into buffer n % 2 while that of step n - 1 is
+            // worked on. All groups take as many steps, and meet at the same barriers.
+            constexpr int kStride = 32 * kKW;
+            const int steps = (k1 - k0 + kStride - 1) / kStride;
+            auto at = [&](int step) { return k0 + (step * kKW + kw) * 32; };
+            uint32_t valid = 0;
+            look(min(at(0), last));
+            if (at(0) < k1) fetch(at(0), 0);
+            valid = valid_in;
+            wait_loads();
+            __syncthreads();
+            for (int step = 0; step < steps; ++step) {
+                const int j0 = at(step), next = j0 + kStride;
+                if (next < k1) {
+                    look(next);
+                    fetch(next, step + 1);
+                }
+                if (j0 < k1 && j0 + 31 >= wlo && j0 < whi) attend(j0, step, valid);
+                valid = valid_in;
+                wait_loads();
+                __syncthreads();
+            }
+        } else {
+            // The wave's own keys, 32 of every 128: nothing to meet for.
+            for (int j0 = k0 + 32 * kw; j0 < k1; j0 += 128) {
+                look(j0);
+                fetch(j0, 0);
+                wait_loads();
+                if (j0 + 31 >= wlo && j0 < whi) attend(j0, 0, valid_in);
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // read before the next rows come in
+            }
+            __syncthreads();
+        }
+    }
+
+    // Outputs, of a piece of the keys or of all: normalised, in bf16, with the reference and the sum
+    // of a piece.
+    const CoreArgs y = argument_again<CoreArgs>();
+    const AttnJob &b = y.a;
+    const Split &sp = y.sp;
+    const Seq qq = seq_of(b, s);
+    auto place = [&](int r) {
+        const int i = r / b.group;
+        return sp.n_split > 1 ? reinterpret_cast<uint16_t *>(sp.part) + part_row(b, sp, work.part, 0, tile, r) * L
+                              : static_cast<uint16_t *>(b.o) + (size_t)(qq.q0 + i) * b.ldo + (size_t)(r - i * b.group) * L;
+    };
+    auto put_stat = [&](int r, float mm, float ll) {
+        if (sp.n_split > 1) sp.ml[part_row(b, sp, work.part, 0, tile, r)] = make_float2(mm, ll);
+    };
+    // A row with an infinity or a NaN is done again key by key: one that it does not see may
+    // have got in as 0 * NaN.
+    auto redo = [&](uint32_t again, int first) {
+        for (uint32_t left = again; left; left &= left - 1) {
+            const int rr = first + __ffs(left) - 1, ii = rr / b.group;
+            float acc[8], mm, ll;
+            latent_row<typename std::conditional<kExact, float, uint16_t>::type, F>(b, y.rot, qq, ii, rr - ii * b.group, k0, k1, acc, mm, ll);
+            if (8 * lane < L) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) acc[e] = ll == 0.0f ? 0.0f : acc[e] / ll;
+                put4(place(rr) + 8 * lane, acc);
+                put4(place(rr) + 8 * lane + 4, acc + 4);
+            }
+            if (lane == 0) put_stat(rr, mm, ll);
+        }
+    };
+    auto odd_rows = [&](int t) {
+        float check = l[t] * 0.0f;
+#pragma unroll
+        for (int c = 0; c < kBlocks; ++c) check += o[t][c].x * 0.0f + o[t][c].y * 0.0f + o[t][c].z * 0.0f + o[t][c].w * 0.0f;
+        uint64_t odd = __ballot(r0 + 16 * t + n < rows && check != 0.0f);
+        odd |= odd >> 32;
+        odd |= odd >> 16;
+        return (uint32_t)odd & 0xFFFFu;
+    };
+    if constexpr (kKW == 1) {
+#pragma unroll
+        for (int t = 0; t < kNT; ++t) {
+            const int r = r0 + 16 * t + n;
+            l[t] = groups_sum(l[t]);
+            const uint32_t again = odd_rows(t);
+            if (r < rows && !(again >> n & 1u)) {
+                const float inv = l[t] == 0.0f ? 0.0f : 1.0f / l[t];
+                uint16_t *to = place(r) + 4 * g;
+#pragma unroll
+                for (int c = 0; c < kBlocks; ++c) {
+                    const float v[4] = {o[t][c].x * inv, o[t][c].y * inv, o[t][c].z * inv, o[t][c].w * inv};
+                    put4(to + 16 * c, v);
+                }
+                if (g == 0) put_stat(r, m[t], l[t]);
+            }
+            redo(again, r0 + 16 * t);
+        }
+    } else {
+        // The groups' outputs meet in LDS, each wave joins a part of the columns.
+        constexpr int kOwn = kBlocks / kKW;
+        static_assert(kNT == 1, "waves over keys have one tile of rows");
+        l[0] = groups_sum(l[0]);
+        uint32_t again = odd_rows(0);
+        f32x4 *mine = reinterpret_cast<f32x4 *>(lds_all);
+#pragma unroll
+        for (int c = 0; c < kBlocks; ++c) mine[(wave * kBlocks + c) * 64 + lane] = o[0][c];
+        if (g == 0) reinterpret_cast<float *>(range)[wave * 16 + n] = m[0];
+        __syncthreads();
+        float ms[kKW], top = kNegInf;
+#pragma unroll
+        for (int w = 0; w < kKW; ++w) {
+            ms[w] = reinterpret_cast<const float *>(range)[(w * kRW + rw) * 16 + n];
+            top = fmaxf(top, ms[w]);
+        }
+        __syncthreads();
+        if (g == 0) reinterpret_cast<float *>(range)[wave * 16 + n] = l[0];
+        __syncthreads();
+        float sum = 0.0f, up[kKW];
+#pragma unroll
+        for (int w = 0; w < kKW; ++w) {
+            up[w] = ms[w] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(ms[w] - top);
+            sum += up[w] * reinterpret_cast<const float *>(range)[(w * kRW + rw) * 16 + n];
+        }
+        __syncthreads();
+        if (lane == 0) reinterpret_cast<uint32_t *>(range)[wave] = again;
+        __syncthreads();
+        again = 0;
+#pragma unroll
+        for (int w = 0; w < kKW; ++w) again |= reinterpret_cast<const uint32_t *>(range)[w * kRW + rw];
+        again = __builtin_amdgcn_readfirstlane(again);
+        const int r = r0 + n;
+        if (r < rows && !(again >> n & 1u)) {
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            uint16_t *to = place(r) + 4 * g;
+#pragma unroll
+            for (int c = 0; c < kOwn; ++c) {
+                const int at = kw * kOwn + c;
+                f32x4 v{0, 0, 0, 0};
+#pragma unroll
+                for (int w = 0; w < kKW; ++w) v += mine[((w * kRW + rw) * kBlocks + at) * 64 + lane] * up[w];
+                const float e[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
+                put4(to + 16 * at, e);
+            }
+            if (kw == 0 && g == 0) put_stat(r, top, sum);
+        }
+        if (kw == 0) redo(again, r0);
+    }
+}
+
+template <int F, int L>
+void run(const CoreArgs &x, const CoreKind &k, unsigned blocks, hipStream_t s) {
+    const dim3 g(blocks), b(256);
+    if (k.tiles == 2)
+        hipLaunchKernelGGL((latent_kernel<F, L, 2, 4, 1, false>), g, b, 0, s, x);
+    else if (k.row_waves == 4)
+        hipLaunchKernelGGL((latent_kernel<F, L, 1, 4, 1, false>), g, b, 0, s, x);
+    else if (k.row_waves == 2)
+        hipLaunchKernelGGL((latent_kernel<F, L, 1, 2, 2, false>), g, b, 0, s, x);
+    else if (k.exact)
+        hipLaunchKernelGGL((latent_kernel<F, L, 1, 1, 4, true>), g, b, 0, s, x);
+    else
+        hipLaunchKernelGGL((latent_kernel<F, L, 1, 1, 4, false>), g, b, 0, s, x);
+}
+
+template <int F>
+void run(const CoreArgs &x, const CoreKind &k, unsigned blocks, hipStream_t s) {
+    switch (x.a.c.d) {
+        case 128: run<F, 128>(x, k, blocks, s); break;
+        case 256: run<F, 256>(x, k, blocks, s); break;
+        default: run<F, 512>(x, k, blocks, s);
+    }
+}
+
+}  // namespace
+
+void launch_latent_tile(const CoreArgs &x, int fmt, const CoreKind &k, unsigned blocks, hipStream_t s) {
+    fmt == kFmtE4m3 ? run<kFmtE4m3>(x, k, blocks, s) : run<kFmtBf16>(x, k, blocks, s);
+}
+
+}  // namespace wl

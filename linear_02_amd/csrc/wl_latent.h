@@ -17,6 +17,20 @@ struct CoreArgs {
     int rot;
 };
 
+// Which kernel: tiles of 16 rows per wave, waves over rows (the others over keys), whether
+// queries are fp32 and multiplied with their remainders.
+struct CoreKind {
+    int tiles, row_waves;
+    bool exact;
+};
+void launch_latent_tile(const CoreArgs &x, int fmt, const CoreKind &k, unsigned blocks, hipStream_t s);
+
+// Products of every token and head (k_latent_heads.hip): into the latent space (out: bf16, or
+// fp32), and out of it, with the join of divided keys.
+void launch_absorb(const LatentJob &a, void *out, bool f32_out, hipStream_t s);
+void launch_up(const LatentJob &a, const CoreArgs &x, hipStream_t s);
+void launch_join(const CoreArgs &x, hipStream_t s);
+
 // Bytes of a cache row.
 template <int F>
 __device__ __forceinline__ int latent_row_bytes(int latent, int rot) {

@@ -274,7 +274,8 @@ def test_missing_pages(wl):
 def test_unseen_keys_have_no_influence(wl, fmt):
     """NaN and infinities in rows that no query sees, or that some do not see."""
     b = Batch(wl, [(70, 4), (33, 1)], 9, fmt=fmt, seed=11)
-    clean = b.run(wl, window=20, form="absorbed")
+    clean = b.check(wl, "clean", window=20, form="absorbed")
+    ref, slack = serve_ref.latent_attention(b.q, b.cache, b.w, i32(b.starts), i32(b.lens), b.scale, window=20)
     last = [b.cache.table[s, (n - 1) // 16].item() for s, n in enumerate(b.lens)]
     bad = float("nan")
     rows = b.cache.rows
@@ -292,7 +293,9 @@ def test_unseen_keys_have_no_influence(wl, fmt):
     # the last key of sequence 0 is seen by its last query alone
     as_bad(rows[last[0], (b.lens[0] - 1) % 16])
     o = b.run(wl, window=20, form="absorbed")
-    assert o[3].isnan().all() and torch.equal(o[:3], clean[:3]) and torch.equal(o[4:], clean[4:])
+    assert o[3].isnan().all() and torch.equal(o[4:], clean[4:])
+    # the others share its tile of keys: summed anew, in another order, within the same bar
+    layer_ref.assert_near(o[:3], ref[:3], slack[:3], "rows beside one that sees it")
 
 
 def test_weightless_keys_of_minus_infinity(wl):
