@@ -19,20 +19,19 @@ namespace wl {
 
 namespace {
 
-// The tile in LDS: rows of kP pieces of 16 bytes, with place for 64 rotated elements.
-// kP is 8 modulo 16 (0 for 256 bytes of codes), so that neighbouring rows start half of
-// the banks apart; piece c of row r lies at c ^ swizzle(r), and at c ^ (r & 7) in the
-// rotated part. Every pass of the operands' reads (16 rows and one piece of a key
-// operand; 8 rows and 32 bytes of a transposing read; rows 0 .. 7 and 16 .. 23 and 16
-// bytes of an 8-bit one) then meets all 64 banks once.
+// The tile in LDS: 32 rows of the latent, kLatent pieces of 16 bytes each, then 32 rows of 8
+// pieces of the key. Piece c of row r lies at c ^ turn(r) (c ^ (r / 2 % 8) of the key), so that
+// every pass of the operands' reads meets all 64 banks once: 16 rows and one piece of a key
+// operand; 8 rows and two pieces of a transposing read; rows 0 .. 7 and 16 .. 23 and one piece
+// of an 8-bit one. (128 wide codes have half a row of banks, and two passes.)
 template <int F, int L>
 struct Tile {
     static constexpr bool kCodes = F == kFmtE4m3;
-    static constexpr int kLatent = kCodes ? L / 16 : L / 8;   // pieces of the latent
-    static constexpr int kP = kLatent + 8, kRow = 16 * kP;
-    static constexpr int kBytes = 32 * kRow;
-    static constexpr int kLoads = 16 * kP / 64;               // of 16 rows
-    static __device__ __forceinline__ int swizzle(int r) { return ((r & 15) ^ (r >> 1 & 8)) & (kLatent - 1); }
+    static constexpr int kLatent = kCodes ? L / 16 : L / 8;
+    static constexpr int kRow = 16 * kLatent, kKeys = 32 * kRow, kBytes = kKeys + 32 * 128;
+    static constexpr int kLoads = 16 * kLatent / 64;          // of the latents of 16 rows
+    static constexpr int kPer = 64 / kLatent;                 // rows of a load
+    static __device__ __forceinline__ int turn(int r) { return ((r & 7) << 1 | ((r >> 3 ^ r >> 4) & 1)) & (kLatent - 1); }
 };
 
 // kNT: tiles of 16 rows per wave. kRW x kKW waves: over rows, and over keys. kExact: queries'
@@ -41,7 +40,7 @@ template <int F, int L, int kNT, int kRW, int kKW, bool kExact>
 __global__ __launch_bounds__(256, kNT == 1 && kKW == 1 ? 2 : 1) void latent_kernel(CoreArgs x) {
     typedef Tile<F, L> T;
     constexpr bool kCodes = T::kCodes;
-    constexpr int kSteps = L / 32, kBlocks = L / 16, kRow = T::kRow;
+    constexpr int kSteps = L / 32, kBlocks = L / 16;
     constexpr int kBuffers = kKW == 4 ? 1 : 2;
     constexpr int kScales = kCodes ? kKW * 2 * 32 * 4 : 0;    // [group][step % 2][32]
     constexpr int kTiles = kKW * kBuffers * T::kBytes, kJoin = kKW > 1 ? 4 * kBlocks * 1024 : 0;
@@ -65,9 +64,20 @@ __global__ __launch_bounds__(256, kNT == 1 && kKW == 1 ? 2 : 1) void latent_kern
     };
     const int r0 = rows_of(tile, rows).first;
 
+    // With one wave per SIMD, outputs live in accumulation registers. Said where paths meet and where
+    // anything but a product writes them: else the compiler moves all of them there and back in every step.
+    auto keep = [](f32x4 &v) {
+        if (kNT == 2 || kKW > 1) asm volatile("" : "+a"(v));
+    };
     u32x4 qf[kNT][kSteps + 2], ql[kExact ? kNT : 1][kExact ? kSteps : 1];
     f32x4 o[kNT][kBlocks];
     float m[kNT], l[kNT];
+    auto keep_all = [&]() {
+#pragma unroll
+        for (int t = 0; t < kNT; ++t)
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b) keep(o[t][b]);
+    };
     int lo = 0x7FFFFFFF, hi = 0, flo = 0, fhi = 0x7FFFFFFF;   // some row sees [lo, hi), every row [flo, fhi)
     const uint32_t sign = a.scale2 < 0.0f ? 0x80008000u : 0u;   // a negative scale goes into the queries
     const float scale2 = fmaxf(fabsf(a.scale2), 0x1p-126f);   // not 0: -inf marks an unseen key
@@ -111,7 +121,10 @@ __global__ __launch_bounds__(256, kNT == 1 && kKW == 1 ? 2 : 1) void latent_kern
             fhi = min(fhi, see.hi);
         }
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b) o[t][b] = f32x4{0, 0, 0, 0};
+        for (int b = 0; b < kBlocks; ++b) {
+            o[t][b] = f32x4{0, 0, 0, 0};
+            keep(o[t][b]);
+        }
         m[t] = kNegInf, l[t] = 0.0f;
     }
 #pragma unroll
@@ -138,9 +151,10 @@ __global__ __launch_bounds__(256, kNT == 1 && kKW == 1 ? 2 : 1) void latent_kern
         const int shift = a.c.page_shift, pmask = (1 << shift) - 1, n_pages = a.c.n_pages;
         const int pieces = kCodes ? (L + 2 * R) / 16 : (L + R) / 8, bytes = 16 * pieces;   // of a cache row
         const int64_t page_bytes = (int64_t)bytes << shift;
-        // Keys come in halves of 16, each within one page; a wave fetches kHalves of them, or part of one.
-        constexpr int kHalves = kRW == 1 ? 2 : 1, kMine = T::kLoads * 2 / kRW / kHalves;   // loads of a half
-        const int half0 = kRW == 1 ? 0 : rw / (kRW / 2), load0 = kRW == 4 ? rw % 2 * kMine : 0;
+        // Keys come in halves of 16, each within one page; a wave fetches kHalves of them, or half of one.
+        constexpr int kHalves = kRW == 1 ? 2 : 1, kShare = kRW == 4 ? 2 : 1;
+        constexpr int kMine = T::kLoads / kShare, kMineKeys = 2 / kShare;                  // loads of a half
+        const int half0 = kRW == 1 ? 0 : rw / (kRW / 2), share = kRW == 4 ? rw % 2 : 0;
         int page[2];
         int first_page = -64, entries = 0;   // lane i holds entry first_page + i of the table
         auto look = [&](int j0) {
@@ -166,11 +180,26 @@ __global__ __launch_bounds__(256, kNT == 1 && kKW == 1 ? 2 : 1) void latent_kern
                 const int pg = half ? page[1] : page[0], off = min(jh, last) & pmask & ~15;
                 const int most = last - min(jh, last & ~15);   // rows behind the last key read that key again
                 const char *from = scalar(static_cast<const char *>(a.c.k) + ((unsigned)pg < (unsigned)n_pages ? pg : 0) * page_bytes + (int64_t)off * bytes);
+                const int sub = ln / T::kLatent, c = ln % T::kLatent, first = share * kMine * T::kPer;
+                const uint32_t lds_to = to + half * 16 * T::kRow + share * kMine * 1024;
+                const uint32_t turned = (uint32_t)(c ^ T::turn(16 * half) ^ T::turn(first) ^ T::turn(sub)) << 4;
+                if (most >= 15) {
+                    const uint32_t at = (uint32_t)(first + sub) * bytes;
 #pragma unroll
-                for (int i = 0; i < kMine; ++i) {
-                    const int p = (load0 + i) * 64 + ln, r = (unsigned)p / (unsigned)T::kP, c = p - r * T::kP;
-                    const int piece = c < T::kLatent ? c ^ T::swizzle(16 * half + r) : T::kLatent + ((c - T::kLatent) ^ (r & 7));
-                    load_to_lds(from, min(r, most) * bytes + min(piece, pieces - 1) * 16, to + half * 16 * kRow + (load0 + i) * 1024);
+                    for (int i = 0; i < kMine; ++i)
+                        load_to_lds(from, at + i * T::kPer * bytes + (turned ^ (uint32_t)T::turn(i * T::kPer) << 4), lds_to + i * 1024);
+                } else {
+#pragma unroll 1
+                    for (int i = 0; i < kMine; ++i) {
+                        const int r = first + i * T::kPer + sub;
+                        load_to_lds(from, min(r, most) * bytes + (turned ^ (uint32_t)T::turn(i * T::kPer) << 4), __builtin_amdgcn_readfirstlane(lds_to + i * 1024));
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < kMineKeys; ++i) {
+                    const int r = 8 * (share * kMineKeys + i) + (ln >> 3), piece = (ln & 7) ^ (r >> 1 & 7);
+                    load_to_lds(from, min(r, most) * bytes + T::kRow + min(piece, R / 8 - 1) * 16,
+                                to + T::kKeys + (16 * half + 8 * (share * kMineKeys + i)) * 128);
                 }
                 if (kCodes && rw == (kRW == 1 ? 0 : kRW / 2 * half)) {
                     const char *sc = scalar(reinterpret_cast<const char *>(a.c.k_scale + (((int64_t)((unsigned)pg < (unsigned)n_pages ? pg : 0) << shift) + off)));
@@ -178,29 +207,33 @@ __global__ __launch_bounds__(256, kNT == 1 && kKW == 1 ? 2 : 1) void latent_kern
                 }
             }
         };
-        // Eight elements of a key operand: piece (in eights of elements) c of row r.
-        auto key8 = [&](const char *row, int r, int c) {
-            if (kCodes)
-                return [](u32x2 w) { return widen8<kFmtE4m3>(w.x, w.y); }(*reinterpret_cast<const u32x2 *>(row + ((c >> 1 ^ T::swizzle(r)) << 4) + 8 * (c & 1)));
-            return *reinterpret_cast<const u32x4 *>(row + ((c ^ T::swizzle(r)) << 4));
-        };
         const int key_v = 4 * g + (n >> 2), key_c = n < 8 ? 4 * g + (n >> 1) : 16 + 4 * g + ((n - 8) >> 1);
         auto attend = [&](const int &j0, const int &step, const uint32_t &valid) {
-            const char *in = lds_all + (kw * kBuffers + (kBuffers == 2 ? step & 1 : 0)) * T::kBytes;
+            keep_all();
+            const int in = (kw * kBuffers + (kBuffers == 2 ? step & 1 : 0)) * T::kBytes;
             const float *scales = reinterpret_cast<const float *>(lds_all + kTiles) + (kw * 2 + (step & 1)) * 32;
-            int nn = n, gg = g;
-            asm volatile("" : "+v"(nn), "+v"(gg));   // places are formed anew in every step
+            // Operands' places, formed anew in every step: held through the loop, they would take registers.
+            int kb = in + n * T::kRow + ((T::kCodes ? g >> 1 : g) ^ T::turn(n)) * 16 + (T::kCodes ? 8 * (g & 1) : 0);
+            int rb = in + T::kKeys + n * 128 + ((g ^ (n >> 1 & 7)) << 4);
+            asm volatile("" : "+v"(kb), "+v"(rb));
             f32x4 sc[kNT][2];
             __builtin_amdgcn_s_setprio(1);
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                const int r = 16 * b + nn;
-                const char *row = in + r * kRow;
 #pragma unroll
                 for (int t = 0; t < kNT; ++t) sc[t][b] = f32x4{0, 0, 0, 0};
 #pragma unroll
                 for (int k = 0; k < kSteps; ++k) {
-                    const u32x4 kf = key8(row, r, 4 * k + gg);
+                    constexpr int kUnit = kCodes ? 2 : 4;   // pieces of 32 elements
+                    const int c = kUnit * k;
+                    const char *p = lds_all + (kb ^ (((c & 15) ^ b) & (T::kLatent - 1)) << 4) + (c >> 4) * 256 + b * 16 * T::kRow;
+                    u32x4 kf;
+                    if (kCodes) {
+                        const u32x2 w = *reinterpret_cast<const u32x2 *>(p);
+                        kf = widen8<kFmtE4m3>(w.x, w.y);
+                    } else {
+                        kf = *reinterpret_cast<const u32x4 *>(p);
+                    }
 #pragma unroll
                     for (int t = 0; t < kNT; ++t) {
                         sc[t][b] = mfma16(kf, qf[t][k], sc[t][b]);
@@ -215,7 +248,7 @@ __global__ __launch_bounds__(256, kNT == 1 && kKW == 1 ? 2 : 1) void latent_kern
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     if (32 * k >= R) break;
-                    const u32x4 kf = *reinterpret_cast<const u32x4 *>(row + ((T::kLatent + ((4 * k + gg) ^ (r & 7))) << 4));
+                    const u32x4 kf = *reinterpret_cast<const u32x4 *>(lds_all + (rb ^ k << 6) + b * 16 * 128);
 #pragma unroll
                     for (int t = 0; t < kNT; ++t) sc[t][b] = mfma16(kf, qf[t][kSteps + k], sc[t][b]);
                 }
@@ -247,8 +280,13 @@ __global__ __launch_bounds__(256, kNT == 1 && kKW == 1 ? 2 : 1) void latent_kern
                     m[t] = now;
                     l[t] *= up;
 #pragma unroll
-                    for (int b = 0; b < kBlocks; ++b) o[t][b] *= up;
+                    for (int b = 0; b < kBlocks; ++b) {
+                        o[t][b] *= up;
+                        keep(o[t][b]);
+                        __builtin_amdgcn_sched_barrier(0);   // a few at a time pass through the other registers
+                    }
                 }
+                keep_all();
                 const float ref = m[t] == kNegInf ? 0.0f : m[t];
                 float p[8];
 #pragma unroll
@@ -281,19 +319,20 @@ __global__ __launch_bounds__(256, kNT == 1 && kKW == 1 ? 2 : 1) void latent_kern
                 }
             }
             __builtin_amdgcn_s_setprio(1);
-            int kv = kCodes ? key_c : key_v, nv = n;
-            asm volatile("" : "+v"(kv), "+v"(nv));
-            const char *row = in + kv * kRow;
+            const int kv = kCodes ? key_c : key_v;
+            int vb = in + kv * T::kRow + ((T::kCodes ? 0 : n >> 1 & 1) ^ T::turn(kv)) * 16 + 8 * (n & 1);
+            asm volatile("" : "+v"(vb));
 #pragma unroll
             for (int b = 0; b < kBlocks; ++b) {
+                const int c = kCodes ? b : 2 * b;
+                const char *p = lds_all + (vb ^ (c & 15 & (T::kLatent - 1)) << 4) + (c >> 4) * 256;
                 u32x4 vf;
                 if (kCodes) {
-                    const u32x2 w = read_tr8(row + ((b ^ T::swizzle(kv)) << 4) + 8 * (nv & 1));
+                    const u32x2 w = read_tr8(p);
                     vf = widen8<kFmtE4m3>(w.x, w.y);
                 } else {
-                    // rows kv and 16 + kv, whose swizzles differ in bit 3
-                    const int c = (2 * b + (nv >> 1 & 1)) ^ T::swizzle(kv);
-                    const u32x2 u = read_tr16(row + (c << 4) + 8 * (nv & 1)), w = read_tr16(row + 16 * kRow + ((c ^ 8) << 4) + 8 * (nv & 1));
+                    // rows kv and 16 + kv, whose turns differ in bit 0
+                    const u32x2 u = read_tr16(p), w = read_tr16(lds_all + (vb ^ ((c & 15) ^ 1) << 4) + (c >> 4) * 256 + 16 * T::kRow);
                     vf = u32x4{u.x, u.y, w.x, w.y};
                 }
 #pragma unroll
@@ -323,6 +362,7 @@ __global__ __launch_bounds__(256, kNT == 1 && kKW == 1 ? 2 : 1) void latent_kern
                     fetch(next, step + 1);
                 }
                 if (j0 < k1 && j0 + 31 >= wlo && j0 < whi) attend(j0, step, valid);
+                keep_all();
                 valid = valid_in;
                 wait_loads();
                 __syncthreads();
@@ -334,12 +374,14 @@ __global__ __launch_bounds__(256, kNT == 1 && kKW == 1 ? 2 : 1) void latent_kern
                 fetch(j0, 0);
                 wait_loads();
                 if (j0 + 31 >= wlo && j0 < whi) attend(j0, 0, valid_in);
+                keep_all();
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // read before the next rows come in
             }
             __syncthreads();
         }
     }
 
+    keep_all();
     // Outputs, of a piece of the keys or of all: normalised, in bf16, with the reference and the sum
     // of a piece.
     const CoreArgs y = argument_again<CoreArgs>();
