@@ -76,7 +76,7 @@ struct Plan {
 
 // Which kernel a bf16 or e4m3 call takes, and how its keys are divided, as plan_of in
 // k_attn.hip does it.
-Plan plan_of(const LatentJob &job) {
+Plan plan_of(const LatentJob &job, int fmt) {
     const AttnJob &a = job.a;
     Plan p{};
     const int64_t rows = a.max_q > 0 ? (int64_t)a.max_q * a.group : 1;
@@ -90,7 +90,7 @@ Plan plan_of(const LatentJob &job) {
     if (a.mask == kMaskCausal && a.window && (int64_t)a.window + a.max_q < span) span = (int64_t)a.window + a.max_q;
     span += 31;
     const int64_t tiles = (int64_t)a.c.n_seq * p.sp.tiles;
-    const int64_t places = p.kind.tiles == 1 && p.kind.row_waves == 4 ? kWorkgroups : kWorkgroups / 2;
+    const int64_t places = kWorkgroups / 2 * workgroups_per_cu(fmt, a.c.d, p.kind.tiles, p.kind.row_waves);
     const int64_t want = 2 * tiles > places ? 2 * places : places;
     int64_t chunk = (span * tiles + want - 1) / want;
     p.sp.least = kMinChunk;
@@ -161,9 +161,9 @@ hipError_t launch_f32(LatentJob a, const Places &w, char *ws, hipStream_t s) {
 
 bool latent_can_expand(const LatentJob &, bool) { return false; }
 
-LatentNeeds latent_needs(const LatentJob &a, int, bool f32, int) {
+LatentNeeds latent_needs(const LatentJob &a, int fmt, bool f32, int) {
     const int64_t rows = (int64_t)a.a.T * a.a.n_q;
-    const Plan p = plan_of(a);
+    const Plan p = plan_of(a, fmt);
     LatentNeeds n{places_of(a, p, f32).bytes, p.items};
     if (f32) n.workgroups = ((int64_t)a.a.c.n_seq * a.a.max_q * a.a.group + 3) / 4;
     // the products around it, of tokens and heads
@@ -174,7 +174,7 @@ LatentNeeds latent_needs(const LatentJob &a, int, bool f32, int) {
 
 hipError_t launch_latent(const LatentJob &job, int fmt, bool f32, int, void *ws, hipStream_t s) {
     LatentJob a = job;
-    const Plan p = plan_of(a);
+    const Plan p = plan_of(a, fmt);
     const Places w = places_of(a, p, f32);
     char *at = static_cast<char *>(ws);
     if (f32) return launch_f32(a, w, at, s);

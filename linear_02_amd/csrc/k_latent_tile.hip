@@ -37,16 +37,19 @@ struct Tile {
 // kNT: tiles of 16 rows per wave. kRW x kKW waves: over rows, and over keys. kExact: queries'
 // and weights' remainders are multiplied too.
 template <int F, int L, int kNT, int kRW, int kKW, bool kExact>
-__global__ __launch_bounds__(256, kNT == 1 && kKW == 1 ? 2 : 1) void latent_kernel(CoreArgs x) {
+__global__ __launch_bounds__(256, workgroups_per_cu(F, L, kNT, kRW)) void latent_kernel(CoreArgs x) {
     typedef Tile<F, L> T;
     constexpr bool kCodes = T::kCodes;
     constexpr int kSteps = L / 32, kBlocks = L / 16;
     constexpr int kBuffers = kKW == 4 ? 1 : 2;
+    constexpr int kAhead = 4;                                 // operands read ahead of the products
     constexpr int kScales = kCodes ? kKW * 2 * 32 * 4 : 0;    // [group][step % 2][32]
     constexpr int kTiles = kKW * kBuffers * T::kBytes, kJoin = kKW > 1 ? 4 * kBlocks * 1024 : 0;
-    constexpr int kMain = kTiles + kScales > kJoin ? kTiles + kScales : kJoin;
+    constexpr int kPatch = kTiles + kScales;                  // a patch of every wave, for the rescaling
+    constexpr int kUsed = kPatch + (kNT == 2 ? 16384 : 0), kMain = kUsed > kJoin ? kUsed : kJoin;
     __shared__ __align__(16) char lds_all[kMain + 512];
     int (*range)[4] = reinterpret_cast<int (*)[4]>(lds_all + kMain);                   // [lo, hi][wave]
+    constexpr bool kAccum = workgroups_per_cu(F, L, kNT, kRW) == 1;   // one wave per SIMD
     const AttnJob &a = x.a;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
@@ -64,10 +67,10 @@ __global__ __launch_bounds__(256, kNT == 1 && kKW == 1 ? 2 : 1) void latent_kern
     };
     const int r0 = rows_of(tile, rows).first;
 
-    // With one wave per SIMD, outputs live in accumulation registers. Said where paths meet and where
+    // Outputs live in accumulation registers then. Said where paths meet and where
     // anything but a product writes them: else the compiler moves all of them there and back in every step.
     auto keep = [](f32x4 &v) {
-        if (kNT == 2 || kKW > 1) asm volatile("" : "+a"(v));
+        if (kAccum) asm volatile("" : "+a"(v));
     };
     u32x4 qf[kNT][kSteps + 2], ql[kExact ? kNT : 1][kExact ? kSteps : 1];
     f32x4 o[kNT][kBlocks];
@@ -86,22 +89,21 @@ __global__ __launch_bounds__(256, kNT == 1 && kKW == 1 ? 2 : 1) void latent_kern
         const int r = r0 + 16 * t + n, i = r / a.group;
         const bool on = r < rows;
         const int64_t at = (int64_t)(q.q0 + (on ? i : 0)) * a.ldq + (int64_t)(on ? r - i * a.group : 0) * (L + R) + 8 * g;
+        // Of a row that there is not, and of elements behind the head's: read somewhere, and masked.
+        auto place = [&](int k) { return k < kSteps ? 32 * k : min(32 * k, L + R - 32); };
+        auto kept = [&](int k) { return on && (k <= kSteps || R > 32) ? 0xFFFFFFFFu : 0u; };
         if (!kExact) {
             const uint16_t *qp = static_cast<const uint16_t *>(a.q) + at;
 #pragma unroll
-            for (int k = 0; k < kSteps + 2; ++k) {
-                qf[t][k] = u32x4{0, 0, 0, 0};
-                if (on && 32 * k < L + R) qf[t][k] = ldg(reinterpret_cast<const u32x4 *>(qp + 32 * k)) ^ sign;
-            }
+            for (int k = 0; k < kSteps + 2; ++k) qf[t][k] = (ldg(reinterpret_cast<const u32x4 *>(qp + place(k))) ^ sign) & kept(k);
         } else {
             // fp32 queries: a bf16 head and a bf16 remainder; the rotated part is exact in bf16.
             const float *qp = static_cast<const float *>(a.q) + at;
 #pragma unroll
             for (int k = 0; k < kSteps + 2; ++k) {
-                f32x4 v[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-                if (on && 32 * k < L + R)
+                f32x4 v[2];
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) v[e] = ldg(reinterpret_cast<const f32x4 *>(qp + 32 * k + 4 * e));
+                for (int e = 0; e < 2; ++e) v[e] = ldg(reinterpret_cast<const f32x4 *>(qp + place(k) + 4 * e));
                 uint32_t h[4], w[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -109,8 +111,8 @@ __global__ __launch_bounds__(256, kNT == 1 && kKW == 1 ? 2 : 1) void latent_kern
                     h[e] = pack2(v0, v1);
                     w[e] = pack2(v0 - bf16_f(h[e] & 0xFFFFu), v1 - __uint_as_float(h[e] & 0xFFFF0000u));
                 }
-                qf[t][k] = u32x4{h[0], h[1], h[2], h[3]} ^ sign;
-                if (k < kSteps) ql[t][k] = u32x4{w[0], w[1], w[2], w[3]} ^ sign;
+                qf[t][k] = (u32x4{h[0], h[1], h[2], h[3]} ^ sign) & kept(k);
+                if (k < kSteps) ql[t][k] = (u32x4{w[0], w[1], w[2], w[3]} ^ sign) & kept(k);
             }
         }
         const Sees see = sees(a, q, i);
@@ -216,6 +218,7 @@ __global__ __launch_bounds__(256, kNT == 1 && kKW == 1 ? 2 : 1) void latent_kern
             int kb = in + n * T::kRow + ((T::kCodes ? g >> 1 : g) ^ T::turn(n)) * 16 + (T::kCodes ? 8 * (g & 1) : 0);
             int rb = in + T::kKeys + n * 128 + ((g ^ (n >> 1 & 7)) << 4);
             asm volatile("" : "+v"(kb), "+v"(rb));
+            const uint32_t second = R > 32 ? 0xFFFFFFFFu : 0u;
             f32x4 sc[kNT][2];
             __builtin_amdgcn_s_setprio(1);
 #pragma unroll
@@ -247,12 +250,25 @@ __global__ __launch_bounds__(256, kNT == 1 && kKW == 1 ? 2 : 1) void latent_kern
                 }
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    if (32 * k >= R) break;
-                    const u32x4 kf = *reinterpret_cast<const u32x4 *>(lds_all + (rb ^ k << 6) + b * 16 * 128);
+                    u32x4 kf = *reinterpret_cast<const u32x4 *>(lds_all + (rb ^ k << 6) + b * 16 * 128);
+                    if (k) kf &= second;   // what lies in the place of elements that there are not may be anything
 #pragma unroll
                     for (int t = 0; t < kNT; ++t) sc[t][b] = mfma16(kf, qf[t][kSteps + k], sc[t][b]);
                 }
             }
+            // Operand reads run kAhead ahead of the products: left to itself the compiler reads each
+            // operand right before its use.
+            __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int k = 0; k < kSteps + 2; ++k) {
+                    if (k < kSteps)
+                        __builtin_amdgcn_sched_group_barrier(0x008, kExact ? 2 * kNT : kNT, 0);
+                    else
+                        __builtin_amdgcn_sched_group_barrier(0x008, kNT, 0);
+                    if (b * (kSteps + 2) + k + kAhead < 2 * (kSteps + 2) + (kCodes ? 2 : 0)) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                }
             __builtin_amdgcn_s_setprio(0);
             u32x4 ph[kNT], pl[kNT];
             const bool all = j0 >= flo && j0 + 32 <= min(fhi, k1) && valid == 0xFFFFFFFFu;
@@ -261,7 +277,7 @@ __global__ __launch_bounds__(256, kNT == 1 && kKW == 1 ? 2 : 1) void latent_kern
                 float v[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[e] = sc[t][e >> 2][e & 3];
-                if (!all) {
+                if (__builtin_expect(!all, 0)) {
                     const CoreArgs again = argument_again<CoreArgs>();
                     const Seq qq = seq_of(again.a, work.s);
                     const int r = rows_of(work.tile, 0).first + 16 * t + (threadIdx.x & 15);
@@ -274,16 +290,39 @@ __global__ __launch_bounds__(256, kNT == 1 && kKW == 1 ? 2 : 1) void latent_kern
                 for (int e = 1; e < 8; ++e) top = fmaxf(top, v[e]);
                 top = groups_max(top);
                 top = top == kNegInf ? top : top * scale2;
-                if (__any(top > m[t] + 8.0f)) {
+                if (__builtin_expect(__any(top > m[t] + 8.0f), 0)) {
                     // The reference moves only when a score passes it by 2^8: sums stay in range.
-                    const float now = fmaxf(m[t], top), up = now == m[t] ? 1.0f : __builtin_amdgcn_exp2f(m[t] - now);
+                    const float was = m[t], now = fmaxf(was, top), up = now == was ? 1.0f : __builtin_amdgcn_exp2f(was - now);
                     m[t] = now;
                     l[t] *= up;
+                    if (kNT == 1) {
 #pragma unroll
-                    for (int b = 0; b < kBlocks; ++b) {
-                        o[t][b] *= up;
-                        keep(o[t][b]);
-                        __builtin_amdgcn_sched_barrier(0);   // a few at a time pass through the other registers
+                        for (int b = 0; b < kBlocks; ++b) {
+                            o[t][b] *= up;
+                            keep(o[t][b]);
+                        }
+                    } else if (__any(was != kNegInf)) {   // else they are 0 still
+                        // By way of LDS: told to multiply them, the compiler brings all outputs over into the
+                        // other registers at once, and spills queries for it, which every step then reads back
+                        // behind its loads on their way. The products that wrote them are a step behind.
+                        const uint32_t by = lds_byte(lds_all) + kPatch + wave * 4096 + lane * 16;
+#pragma unroll
+                        for (int b = 0; b < kBlocks; b += 4) {
+                            f32x4 v[4];
+                            asm volatile("s_nop 15\n\ts_nop 3\n\t"
+                                         "ds_write_b128 %8, %4\n\tds_write_b128 %8, %5 offset:1024\n\tds_write_b128 %8, %6 offset:2048\n\tds_write_b128 %8, %7 offset:3072\n\t"
+                                         "ds_read_b128 %0, %8\n\tds_read_b128 %1, %8 offset:1024\n\tds_read_b128 %2, %8 offset:2048\n\tds_read_b128 %3, %8 offset:3072\n\t"
+                                         "s_waitcnt lgkmcnt(0)"
+                                         : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3])
+                                         : "a"(o[t][b]), "a"(o[t][b + 1]), "a"(o[t][b + 2]), "a"(o[t][b + 3]), "v"(by) : "memory");
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) v[i] *= up;
+                            asm volatile("ds_write_b128 %8, %4\n\tds_write_b128 %8, %5 offset:1024\n\tds_write_b128 %8, %6 offset:2048\n\tds_write_b128 %8, %7 offset:3072\n\t"
+                                         "ds_read_b128 %0, %8\n\tds_read_b128 %1, %8 offset:1024\n\tds_read_b128 %2, %8 offset:2048\n\tds_read_b128 %3, %8 offset:3072\n\t"
+                                         "s_waitcnt lgkmcnt(0)"
+                                         : "=&a"(o[t][b]), "=&a"(o[t][b + 1]), "=&a"(o[t][b + 2]), "=&a"(o[t][b + 3])
+                                         : "v"(v[0]), "v"(v[1]), "v"(v[2]), "v"(v[3]), "v"(by) : "memory");
+                        }
                     }
                 }
                 keep_all();
@@ -340,6 +379,13 @@ __global__ __launch_bounds__(256, kNT == 1 && kKW == 1 ? 2 : 1) void latent_kern
                     o[t][b] = mfma16(vf, ph[t], o[t][b]);
                     if (kExact) o[t][b] = mfma16(vf, pl[t], o[t][b]);
                 }
+            }
+            constexpr int kReads = kCodes ? 1 : 2;   // of an operand
+            __builtin_amdgcn_sched_group_barrier(0x100, kReads * kAhead, 1);
+#pragma unroll
+            for (int i = 0; i < kBlocks; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x008, kExact ? 2 * kNT : kNT, 1);
+                if (i + kAhead < kBlocks) __builtin_amdgcn_sched_group_barrier(0x100, kReads, 1);
             }
             __builtin_amdgcn_s_setprio(0);
         };

@@ -23,6 +23,11 @@ struct CoreKind {
     int tiles, row_waves;
     bool exact;
 };
+// Workgroups of it that share a CU. Widened codes of a latent of 512 take more registers than
+// half a SIMD has.
+constexpr int workgroups_per_cu(int fmt, int latent, int tiles, int row_waves) {
+    return tiles == 1 && row_waves == 4 && !(fmt == kFmtE4m3 && latent == 512) ? 2 : 1;
+}
 void launch_latent_tile(const CoreArgs &x, int fmt, const CoreKind &k, unsigned blocks, hipStream_t s);
 
 // Products of every token and head (k_latent_heads.hip): into the latent space (out: bf16, or
