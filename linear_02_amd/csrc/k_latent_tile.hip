@@ -70,7 +70,7 @@ __global__ __launch_bounds__(256, workgroups_per_cu(F, L, kNT, kRW)) void latent
     // Outputs live in accumulation registers then. Said where paths meet and where
     // anything but a product writes them: else the compiler moves all of them there and back in every step.
     auto keep = [](f32x4 &v) {
-        if (kAccum) asm volatile("" : "+a"(v));
+        if (kAccum) asm("" : "+a"(v));
     };
     u32x4 qf[kNT][kSteps + 2], ql[kExact ? kNT : 1][kExact ? kSteps : 1];
     f32x4 o[kNT][kBlocks];
@@ -220,55 +220,48 @@ __global__ __launch_bounds__(256, workgroups_per_cu(F, L, kNT, kRW)) void latent
             asm volatile("" : "+v"(kb), "+v"(rb));
             const uint32_t second = R > 32 ? 0xFFFFFFFFu : 0u;
             f32x4 sc[kNT][2];
-            __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
+            for (int b = 0; b < 2; ++b)
 #pragma unroll
                 for (int t = 0; t < kNT; ++t) sc[t][b] = f32x4{0, 0, 0, 0};
-#pragma unroll
-                for (int k = 0; k < kSteps; ++k) {
-                    constexpr int kUnit = kCodes ? 2 : 4;   // pieces of 32 elements
-                    const int c = kUnit * k;
-                    const char *p = lds_all + (kb ^ (((c & 15) ^ b) & (T::kLatent - 1)) << 4) + (c >> 4) * 256 + b * 16 * T::kRow;
-                    u32x4 kf;
-                    if (kCodes) {
-                        const u32x2 w = *reinterpret_cast<const u32x2 *>(p);
-                        kf = widen8<kFmtE4m3>(w.x, w.y);
-                    } else {
-                        kf = *reinterpret_cast<const u32x4 *>(p);
-                    }
-#pragma unroll
-                    for (int t = 0; t < kNT; ++t) {
-                        sc[t][b] = mfma16(kf, qf[t][k], sc[t][b]);
-                        if (kExact) sc[t][b] = mfma16(kf, ql[t][k], sc[t][b]);
-                    }
+            // Key operand i: rows 16 (i / kEach) .., elements 32 (i % kEach) .. of them, the rotated ones last.
+            constexpr int kEach = kSteps + 2, kAll = 2 * kEach;
+            auto operand = [&](int i) {
+                const int b = i / kEach, k = i % kEach;
+                if (k >= kSteps) {
+                    u32x4 kf = *reinterpret_cast<const u32x4 *>(lds_all + (rb ^ (k - kSteps) << 6) + b * 16 * 128);
+                    return k > kSteps ? kf & second : kf;   // what lies in the place of elements that there are not may be anything
                 }
-                if (kCodes) {
+                const int c = (kCodes ? 2 : 4) * k;
+                const char *p = lds_all + (kb ^ (((c & 15) ^ b) & (T::kLatent - 1)) << 4) + (c >> 4) * 256 + b * 16 * T::kRow;
+                if (!kCodes) return *reinterpret_cast<const u32x4 *>(p);
+                const u32x2 w = *reinterpret_cast<const u32x2 *>(p);
+                return u32x4{w.x, w.y, 0, 0};
+            };
+            // Reads run kAhead ahead of the products, in this order: left to itself the compiler reads each
+            // operand right before its use.
+            u32x4 kf[kAhead];
+            __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) kf[i] = operand(i);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < kAll; ++i) {
+                const int b = i / kEach, k = i % kEach;
+                const u32x4 here = kCodes && k < kSteps ? widen8<kFmtE4m3>(kf[i % kAhead].x, kf[i % kAhead].y) : kf[i % kAhead];
+                if (kCodes && k == kSteps) {
                     const f32x4 ks = *reinterpret_cast<const f32x4 *>(scales + 16 * b + 4 * g);
 #pragma unroll
                     for (int t = 0; t < kNT; ++t) sc[t][b] *= ks;
                 }
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    u32x4 kf = *reinterpret_cast<const u32x4 *>(lds_all + (rb ^ k << 6) + b * 16 * 128);
-                    if (k) kf &= second;   // what lies in the place of elements that there are not may be anything
-#pragma unroll
-                    for (int t = 0; t < kNT; ++t) sc[t][b] = mfma16(kf, qf[t][kSteps + k], sc[t][b]);
+                for (int t = 0; t < kNT; ++t) {
+                    sc[t][b] = mfma16(here, qf[t][k], sc[t][b]);
+                    if (kExact && k < kSteps) sc[t][b] = mfma16(here, ql[t][k < kSteps ? k : 0], sc[t][b]);
                 }
+                if (i + kAhead < kAll) kf[i % kAhead] = operand(i + kAhead);
+                __builtin_amdgcn_sched_barrier(0);
             }
-            // Operand reads run kAhead ahead of the products: left to itself the compiler reads each
-            // operand right before its use.
-            __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int k = 0; k < kSteps + 2; ++k) {
-                    if (k < kSteps)
-                        __builtin_amdgcn_sched_group_barrier(0x008, kExact ? 2 * kNT : kNT, 0);
-                    else
-                        __builtin_amdgcn_sched_group_barrier(0x008, kNT, 0);
-                    if (b * (kSteps + 2) + k + kAhead < 2 * (kSteps + 2) + (kCodes ? 2 : 0)) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-                }
             __builtin_amdgcn_s_setprio(0);
             u32x4 ph[kNT], pl[kNT];
             const bool all = j0 >= flo && j0 + 32 <= min(fhi, k1) && valid == 0xFFFFFFFFu;
