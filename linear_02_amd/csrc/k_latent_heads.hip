@@ -1,5 +1,5 @@
-// Around latent attention in bf16: every head's queries into the latent space, the join of
-// divided keys, and every head's outputs out of it.
+// Around latent attention: every head's queries into the latent space and outputs out of it in
+// bf16, and the join of divided keys.
 //
 // q'[t][h] = W_h^K^T q[t][h] and o[t][h] = W_h^V o'[t][h]: per head a product with T columns
 // and a weight of its own, so both are bound by reading the weights where tokens are few.
@@ -116,6 +116,8 @@ __device__ __forceinline__ int sequence_of(const AttnJob &a, const Pieces &p, in
 }
 
 // The joined output of row t, head h, elements 8 lane .. + 7; false: the row has no result.
+// E: of the pieces' outputs.
+template <class E>
 __device__ __forceinline__ bool joined(const CoreArgs &x, const Pieces &pieces, int t, int h, float (&o)[8]) {
     const AttnJob &a = x.a;
     const Split &sp = x.sp;
@@ -127,7 +129,7 @@ __device__ __forceinline__ bool joined(const CoreArgs &x, const Pieces &pieces, 
     const Seq q = seq_of(a, s);
     if (t < q.q0 || t >= q.q0 + q.rows) return false;
     const bool on = 8 * lane < L;
-    auto add = [&](const uint16_t *p, float w) {
+    auto add = [&](const E *p, float w) {
         float v[8];
         query4(p + 8 * lane, v);
         query4(p + 8 * lane + 4, v + 4);
@@ -135,7 +137,7 @@ __device__ __forceinline__ bool joined(const CoreArgs &x, const Pieces &pieces, 
         for (int e = 0; e < 8; ++e) o[e] += v[e] * w;
     };
     if (sp.n_split == 1) {
-        if (on) add(static_cast<const uint16_t *>(a.o) + (size_t)t * a.ldo + (size_t)h * L, 1.0f);
+        if (on) add(static_cast<const E *>(a.o) + (size_t)t * a.ldo + (size_t)h * L, 1.0f);
         return true;
     }
     const int r = (t - q.q0) * a.group + h, tile = r / sp.tile_rows;
@@ -157,20 +159,21 @@ __device__ __forceinline__ bool joined(const CoreArgs &x, const Pieces &pieces, 
     const float l = wave_sum(up), inv = l == 0.0f ? 0.0f : 1.0f / l;
     for (int p = 0; p < n; ++p) {
         const float w = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(up), p)) * inv;
-        if (w != 0.0f && on) add(reinterpret_cast<const uint16_t *>(sp.part) + (at + p * next) * L, w);
+        if (w != 0.0f && on) add(reinterpret_cast<const E *>(sp.part) + (at + p * next) * L, w);
     }
     return true;
 }
 
-// Without weights: a wave a row.
+// On its own (without weights, and in fp32): a wave a row.
+template <class E>
 __global__ __launch_bounds__(256) void join_kernel(CoreArgs x) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int64_t w = (int64_t)blockIdx.x * 4 + wave;
     const int t = (int)(w / x.a.n_q), h = (int)(w - (int64_t)t * x.a.n_q);
     if (t >= x.a.T) return;
     float o[8];
-    if (!joined(x, pieces_of_call(x.a, x.sp), t, h, o) || 8 * lane >= x.a.c.d) return;
-    uint16_t *to = static_cast<uint16_t *>(x.a.o) + (size_t)t * x.a.ldo + (size_t)h * x.a.c.d + 8 * lane;
+    if (!joined<E>(x, pieces_of_call(x.a, x.sp), t, h, o) || 8 * lane >= x.a.c.d) return;
+    E *to = static_cast<E *>(x.a.o) + (size_t)t * x.a.ldo + (size_t)h * x.a.c.d + 8 * lane;
     put4(to, o);
     put4(to + 4, o + 4);
 }
@@ -196,7 +199,7 @@ __global__ __launch_bounds__(256) void up_kernel(UpArgs u) {
 #pragma unroll 1
     for (int i = wave; i < 16; i += 4) {
         float o[8];
-        const bool on = joined(u.x, pieces, t0 + i, h, o);
+        const bool on = joined<uint16_t>(u.x, pieces, t0 + i, h, o);
         if (lane == 0) live[i] = on;
         if (8 * lane >= L) continue;
         uint32_t hi[4], lo[4];
@@ -252,8 +255,12 @@ void launch_up(const LatentJob &a, const CoreArgs &x, hipStream_t s) {
     hipLaunchKernelGGL(up_kernel, dim3((unsigned)(units * splits)), dim3(256), 0, s, UpArgs{a, x, splits});
 }
 
-void launch_join(const CoreArgs &x, hipStream_t s) {
-    hipLaunchKernelGGL(join_kernel, dim3((unsigned)(((int64_t)x.a.T * x.a.n_q + 3) / 4)), dim3(256), 0, s, x);
+void launch_join(const CoreArgs &x, bool f32, hipStream_t s) {
+    const dim3 g((unsigned)(((int64_t)x.a.T * x.a.n_q + 3) / 4)), b(256);
+    if (f32)
+        hipLaunchKernelGGL((join_kernel<float>), g, b, 0, s, x);
+    else
+        hipLaunchKernelGGL((join_kernel<uint16_t>), g, b, 0, s, x);
 }
 
 }  // namespace wl

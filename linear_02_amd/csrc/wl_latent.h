@@ -34,7 +34,12 @@ void launch_latent_tile(const CoreArgs &x, int fmt, const CoreKind &k, unsigned 
 // fp32), and out of it, with the join of divided keys.
 void launch_absorb(const LatentJob &a, void *out, bool f32_out, hipStream_t s);
 void launch_up(const LatentJob &a, const CoreArgs &x, hipStream_t s);
-void launch_join(const CoreArgs &x, hipStream_t s);
+void launch_join(const CoreArgs &x, bool f32, hipStream_t s);
+
+// The same in fp32 (k_latent_f32.hip); outputs in the latent space are joined before launch_up_f32.
+void launch_latent_f32(const CoreArgs &x, const CoreKind &k, unsigned blocks, hipStream_t s);
+void launch_absorb_f32(const LatentJob &a, float *out, hipStream_t s);
+void launch_up_f32(const LatentJob &a, const float *in, hipStream_t s);
 
 // Bytes of a cache row.
 template <int F>
