@@ -570,7 +570,7 @@ wl_status wl_latent_read(const wl_latent_read_args *a, void *hip_stream);
  *   form  WL_LATENT_ABSORBED  q is taken to the latent space, W_h^K^T q, and attends
  *                             there; W_h^V is applied to the outputs
  *         WL_LATENT_EXPANDED  keys and values are formed once in the workspace.
- *                             With w, bf16 tensors, nope and value both 64 or both
+ *                             With w, a bf16 cache, nope and value both 64 or both
  *                             128 only (else WL_ERR_UNSUPPORTED)
  *         WL_LATENT_AUTO      the one that takes less time: expanded for prompts
  * Numerics in bf16: q in the latent space, outputs there before W_h^V, expanded keys

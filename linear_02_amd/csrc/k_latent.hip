@@ -83,11 +83,50 @@ Places places_of(const LatentJob &a, const Plan &p, bool f32) {
     return w;
 }
 
+// Expanded keys and values of a call at once, at most; heads are taken in groups that fit.
+constexpr size_t kExpandedBytes = (size_t)8 << 30;
+
+struct Expanded {
+    int heads;         // of a group
+    int keys, blocks, tiles;
+    size_t bytes;      // of the keys, and of the values
+};
+Expanded expanded_of(const LatentJob &job) {
+    const AttnJob &a = job.a;
+    Expanded e{};
+    const int64_t room = (int64_t)a.c.max_pages << a.c.page_shift;
+    const int64_t keys = a.max_kv < room ? a.max_kv : room;
+    e.blocks = (int)((keys + 127) / 128);
+    e.keys = 128 * e.blocks;
+    e.tiles = (a.max_q + 127) / 128;
+    const size_t one = (size_t)a.c.n_seq * e.keys * job.nope * 2;
+    const size_t fit = one ? kExpandedBytes / (2 * one) : a.n_q;
+    e.heads = fit < 1 ? 1 : fit > (size_t)a.n_q ? a.n_q : (int)fit;
+    e.bytes = pad(one * e.heads);
+    return e;
+}
+
+// Queries of a sequence from which on the expanded form is taken, and the fewest workgroups
+// for which it is: with fewer, the absorbed form divides the keys.
+constexpr int kExpandedRows = 192, kExpandedWorkgroups = 128;
+
+bool expands(const LatentJob &a, int fmt, int form) {
+    if (form != kFormAuto) return form == kFormExpanded;
+    if (!latent_can_expand(a, fmt) || a.a.max_q < kExpandedRows) return false;
+    const Expanded e = expanded_of(a);
+    return (int64_t)e.heads * e.tiles * a.a.c.n_seq >= kExpandedWorkgroups;
+}
+
 }  // namespace
 
-bool latent_can_expand(const LatentJob &, bool) { return false; }
+bool latent_can_expand(const LatentJob &a, int fmt) { return a.w && fmt == kFmtBf16 && a.nope == a.value && (a.nope == 64 || a.nope == 128); }
 
-LatentNeeds latent_needs(const LatentJob &a, int fmt, bool f32, int) {
+LatentNeeds latent_needs(const LatentJob &a, int fmt, bool f32, int form) {
+    if (expands(a, fmt, form)) {
+        const Expanded e = expanded_of(a);
+        const int64_t wide = e.blocks > e.tiles ? e.blocks : e.tiles;
+        return {2 * e.bytes, (int64_t)a.a.c.n_seq * wide * e.heads};
+    }
     const int64_t rows = (int64_t)a.a.T * a.a.n_q;
     const Plan p = plan_of(a, fmt);
     LatentNeeds n{places_of(a, p, f32).bytes, p.items};
@@ -97,8 +136,20 @@ LatentNeeds latent_needs(const LatentJob &a, int fmt, bool f32, int) {
     return n;
 }
 
-hipError_t launch_latent(const LatentJob &job, int fmt, bool f32, int, void *ws, hipStream_t s) {
+hipError_t launch_latent(const LatentJob &job, int fmt, bool f32, int form, void *ws, hipStream_t s) {
     LatentJob a = job;
+    if (expands(a, fmt, form)) {
+        const Expanded e = expanded_of(a);
+        ExpandArgs x{a.a, a.w, static_cast<uint16_t *>(ws), reinterpret_cast<uint16_t *>(static_cast<char *>(ws) + e.bytes), a.rot, 0, 0, e.keys, e.blocks, e.tiles};
+        x.a.group = 1;
+        for (x.first = 0; x.first < a.a.n_q; x.first += e.heads) {
+            x.heads = a.a.n_q - x.first < e.heads ? a.a.n_q - x.first : e.heads;
+            launch_expanded(x, a.nope, s);
+            const hipError_t err = hipGetLastError();
+            if (err != hipSuccess) return err;
+        }
+        return hipSuccess;
+    }
     const Plan p = plan_of(a, fmt);
     const Places w = places_of(a, p, f32);
     char *at = static_cast<char *>(ws);

@@ -41,6 +41,18 @@ void launch_latent_f32(const CoreArgs &x, const CoreKind &k, unsigned blocks, hi
 void launch_absorb_f32(const LatentJob &a, float *out, hipStream_t s);
 void launch_up_f32(const LatentJob &a, const float *in, hipStream_t s);
 
+// The expanded form, of heads first .. first + heads - 1 (k_latent_expand.hip). a: the call's
+// own q and o, [T][n_q][nope + rot] and [T][n_q][value].
+struct ExpandArgs {
+    AttnJob a;
+    const void *w;
+    uint16_t *k, *v;       // [n_seq][heads][keys][nope], [value]
+    int rot, first, heads;
+    int keys;              // room of a sequence, a multiple of 128
+    int blocks, tiles;     // of 128 keys, of 128 queries of a sequence, at most
+};
+void launch_expanded(const ExpandArgs &x, int d, hipStream_t s);
+
 // Bytes of a cache row.
 template <int F>
 __device__ __forceinline__ int latent_row_bytes(int latent, int rot) {

@@ -82,7 +82,7 @@ struct LatentNeeds {
     size_t scratch;       // bytes
     int64_t workgroups;   // of the largest launch
 };
-bool latent_can_expand(const LatentJob &a, bool f32);
+bool latent_can_expand(const LatentJob &a, int fmt);
 LatentNeeds latent_needs(const LatentJob &a, int fmt, bool f32, int form);
 hipError_t launch_latent(const LatentJob &a, int fmt, bool f32, int form, void *ws, hipStream_t stream);
 

@@ -166,8 +166,8 @@ wl_status check_latent_attention(const wl_latent_attention_args *a, wl::LatentJo
     j.rot = c->rot, j.nope = a->nope, j.value = a->value, j.ldq = a->ldq, j.ldo = a->ldo;
     j.scale = a->scale;
     const bool f32 = a->dtype == WL_DTYPE_F32;
-    if (a->form == WL_LATENT_EXPANDED && !wl::latent_can_expand(j, f32))
-        return fail(WL_ERR_UNSUPPORTED, "WL_LATENT_EXPANDED needs w, bf16 tensors, and nope=%d and value=%d both 64 or both 128", a->nope, a->value);
+    if (a->form == WL_LATENT_EXPANDED && !wl::latent_can_expand(j, c->format))
+        return fail(WL_ERR_UNSUPPORTED, "WL_LATENT_EXPANDED needs w, a bf16 cache, and nope=%d and value=%d both 64 or both 128", a->nope, a->value);
     *form = a->form;
     if (a->T == 0) return WL_OK;
     const int64_t wq = (int64_t)a->n_q * (a->nope + c->rot), wo = (int64_t)a->n_q * a->value;
