@@ -598,7 +598,7 @@ wl_status wl_latent_attention(const wl_latent_attention_args *a, void *ws, size_
  *   target, draft  [T] rows of `vocab`, ld apart (any ld >= vocab), 16-byte aligned;
  *                  WL_VERIFY_LOGITS: p = softmax(x / temperature);
  *                  WL_VERIFY_PROBABILITIES: p = x, negative and NaN as 0
- *                  (a NaN logit counts as -inf)
+ *                  (a NaN logit counts as -inf, +inf as the largest number)
  *   token    int32 [T]; q_start as in wl_attention, rows outside every sequence are
  *            left as they were; at most max_q rows of a sequence, 1 <= max_q <= 1024
  *   parent   int32 [T] or NULL: the row, within its sequence, that a drafted row follows
