@@ -10,7 +10,10 @@
 //   64 rows    four waves of 16 rows, two workgroups per CU
 //   32 rows    two pairs of waves, each pair with keys of its own
 //   16 rows    every wave with keys of its own, which it fetches for itself and waits
-//              for alone; joined in LDS at the end
+//              for alone; joined in LDS at the end. Where two buffers of latents fit, the
+//              rotated keys, which only the scores need, are read first, and the next rows
+//              come in behind that (e4m3, 64 streams of 16 heads over up to 16384 keys:
+//              150 us with one buffer, 132 us so)
 // Rows of e4m3 stay codes in LDS and are widened as operands: half the LDS traffic, and
 // the vector units have the time beside the products.
 #include "wl_latent.h"
@@ -28,7 +31,7 @@ template <int F, int L>
 struct Tile {
     static constexpr bool kCodes = F == kFmtE4m3;
     static constexpr int kLatent = kCodes ? L / 16 : L / 8;
-    static constexpr int kRow = 16 * kLatent, kKeys = 32 * kRow, kBytes = kKeys + 32 * 128;
+    static constexpr int kRow = 16 * kLatent, kKeys = 32 * kRow;
     static constexpr int kLoads = 16 * kLatent / 64;          // of the latents of 16 rows
     static constexpr int kPer = 64 / kLatent;                 // rows of a load
     static __device__ __forceinline__ int turn(int r) { return ((r & 7) << 1 | ((r >> 3 ^ r >> 4) & 1)) & (kLatent - 1); }
@@ -41,10 +44,13 @@ __global__ __launch_bounds__(256, workgroups_per_cu(F, L, kNT, kRW)) void latent
     typedef Tile<F, L> T;
     constexpr bool kCodes = T::kCodes;
     constexpr int kSteps = L / 32, kBlocks = L / 16;
-    constexpr int kBuffers = kKW == 4 ? 1 : 2;
+    // Waves with keys of their own: two buffers of latents and one of keys, where LDS has room.
+    constexpr bool kKeysFirst = kKW == 4 && T::kKeys <= 16384;
+    constexpr int kBuffers = kKW < 4 || kKeysFirst ? 2 : 1, kKeyBuffers = kKW < 4 ? 2 : 1;
+    constexpr int kGroup = kBuffers * T::kKeys + kKeyBuffers * 32 * 128;
     constexpr int kAhead = 4;                                 // operands read ahead of the products
     constexpr int kScales = kCodes ? kKW * 2 * 32 * 4 : 0;    // [group][step % 2][32]
-    constexpr int kTiles = kKW * kBuffers * T::kBytes, kJoin = kKW > 1 ? 4 * kBlocks * 1024 : 0;
+    constexpr int kTiles = kKW * kGroup, kJoin = kKW > 1 ? 4 * kBlocks * 1024 : 0;
     constexpr int kPatch = kTiles + kScales;                  // a patch of every wave, for the rescaling
     constexpr int kUsed = kPatch + (kNT == 2 ? 16384 : 0), kMain = kUsed > kJoin ? kUsed : kJoin;
     __shared__ __align__(16) char lds_all[kMain + 512];
@@ -173,7 +179,8 @@ __global__ __launch_bounds__(256, workgroups_per_cu(F, L, kNT, kRW)) void latent
         uint32_t valid_in = 0;
         auto fetch = [&](int j0, int step) {
             valid_in = (has_page(0) ? 0xFFFFu : 0u) | (has_page(1) ? 0xFFFF0000u : 0u);
-            const uint32_t to = lds_byte(lds_all) + (kw * kBuffers + (kBuffers == 2 ? step & 1 : 0)) * T::kBytes;
+            const uint32_t to = lds_byte(lds_all) + kw * kGroup + (kBuffers == 2 ? step & 1 : 0) * T::kKeys;
+            const uint32_t key_to = lds_byte(lds_all) + kw * kGroup + kBuffers * T::kKeys + (kKeyBuffers == 2 ? step & 1 : 0) * 32 * 128;
             int ln = lane;
             asm volatile("" : "+v"(ln));   // what follows from it is not kept through the loop
 #pragma unroll
@@ -201,7 +208,7 @@ __global__ __launch_bounds__(256, workgroups_per_cu(F, L, kNT, kRW)) void latent
                 for (int i = 0; i < kMineKeys; ++i) {
                     const int r = 8 * (share * kMineKeys + i) + (ln >> 3), piece = (ln & 7) ^ (r >> 1 & 7);
                     load_to_lds(from, min(r, most) * bytes + T::kRow + min(piece, R / 8 - 1) * 16,
-                                to + T::kKeys + (16 * half + 8 * (share * kMineKeys + i)) * 128);
+                                key_to + (16 * half + 8 * (share * kMineKeys + i)) * 128);
                 }
                 if (kCodes && rw == (kRW == 1 ? 0 : kRW / 2 * half)) {
                     const char *sc = scalar(reinterpret_cast<const char *>(a.c.k_scale + (((int64_t)((unsigned)pg < (unsigned)n_pages ? pg : 0) << shift) + off)));
@@ -210,13 +217,14 @@ __global__ __launch_bounds__(256, workgroups_per_cu(F, L, kNT, kRW)) void latent
             }
         };
         const int key_v = 4 * g + (n >> 2), key_c = n < 8 ? 4 * g + (n >> 1) : 16 + 4 * g + ((n - 8) >> 1);
-        auto attend = [&](const int &j0, const int &step, const uint32_t &valid) {
+        auto attend = [&](const int &j0, const int &step, const uint32_t &valid, auto &&fetch_next) {
             keep_all();
-            const int in = (kw * kBuffers + (kBuffers == 2 ? step & 1 : 0)) * T::kBytes;
+            const int in = kw * kGroup + (kBuffers == 2 ? step & 1 : 0) * T::kKeys;
+            const int keys_in = kw * kGroup + kBuffers * T::kKeys + (kKeyBuffers == 2 ? step & 1 : 0) * 32 * 128;
             const float *scales = reinterpret_cast<const float *>(lds_all + kTiles) + (kw * 2 + (step & 1)) * 32;
             // Operands' places, formed anew in every step: held through the loop, they would take registers.
             int kb = in + n * T::kRow + ((T::kCodes ? g >> 1 : g) ^ T::turn(n)) * 16 + (T::kCodes ? 8 * (g & 1) : 0);
-            int rb = in + T::kKeys + n * 128 + ((g ^ (n >> 1 & 7)) << 4);
+            int rb = keys_in + n * 128 + ((g ^ (n >> 1 & 7)) << 4);
             asm volatile("" : "+v"(kb), "+v"(rb));
             const uint32_t second = R > 32 ? 0xFFFFFFFFu : 0u;
             f32x4 sc[kNT][2];
@@ -224,13 +232,14 @@ __global__ __launch_bounds__(256, workgroups_per_cu(F, L, kNT, kRW)) void latent
             for (int b = 0; b < 2; ++b)
 #pragma unroll
                 for (int t = 0; t < kNT; ++t) sc[t][b] = f32x4{0, 0, 0, 0};
-            // Key operand i: rows 16 (i / kEach) .., elements 32 (i % kEach) .. of them, the rotated ones last.
-            constexpr int kEach = kSteps + 2, kAll = 2 * kEach;
+            // Key operand i: rows 16 (i % 2) .., elements 32 (i / 2) .. of them, the rotated ones last. Both halves in
+            // turn, so that a product does not wait for the one before it.
+            constexpr int kEach = kKeysFirst ? kSteps : kSteps + 2, kAll = 2 * kEach;
             auto operand = [&](int i) {
-                const int b = i / kEach, k = i % kEach;
+                const int b = i & 1, k = i >> 1;
                 if (k >= kSteps) {
                     u32x4 kf = *reinterpret_cast<const u32x4 *>(lds_all + (rb ^ (k - kSteps) << 6) + b * 16 * 128);
-                    return k > kSteps ? kf & second : kf;   // what lies in the place of elements that there are not may be anything
+                    return kf;
                 }
                 const int c = (kCodes ? 2 : 4) * k;
                 const char *p = lds_all + (kb ^ (((c & 15) ^ b) & (T::kLatent - 1)) << 4) + (c >> 4) * 256 + b * 16 * T::kRow;
@@ -241,14 +250,29 @@ __global__ __launch_bounds__(256, workgroups_per_cu(F, L, kNT, kRW)) void latent
             // Reads run kAhead ahead of the products, in this order: left to itself the compiler reads each
             // operand right before its use.
             u32x4 kf[kAhead];
+            f32x4 rotated[2];
+            if (kKeysFirst) {
+                // The rotated part first: with it read, the wave's next rows may come in.
+#pragma unroll
+                for (int i = 0; i < 4; ++i) kf[i] = operand(2 * kSteps + i);
+                asm volatile("s_waitcnt lgkmcnt(0)" : "+v"(kf[0]), "+v"(kf[1]), "+v"(kf[2]), "+v"(kf[3])::"memory");
+                fetch_next();
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    rotated[b] = mfma16(kf[b], qf[0][kSteps], f32x4{0, 0, 0, 0});
+                    rotated[b] = mfma16(kf[2 + b] & second, qf[0][kSteps + 1], rotated[b]);
+                    if (!kCodes) sc[0][b] = rotated[b];
+                }
+            }
             __builtin_amdgcn_s_setprio(1);
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) kf[i] = operand(i);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int i = 0; i < kAll; ++i) {
-                const int b = i / kEach, k = i % kEach;
-                const u32x4 here = kCodes && k < kSteps ? widen8<kFmtE4m3>(kf[i % kAhead].x, kf[i % kAhead].y) : kf[i % kAhead];
+                const int b = i & 1, k = i >> 1;
+                u32x4 here = kCodes && k < kSteps ? widen8<kFmtE4m3>(kf[i % kAhead].x, kf[i % kAhead].y) : kf[i % kAhead];
+                if (k > kSteps) here &= second;   // what lies in the place of elements that there are not may be anything
                 if (kCodes && k == kSteps) {
                     const f32x4 ks = *reinterpret_cast<const f32x4 *>(scales + 16 * b + 4 * g);
 #pragma unroll
@@ -263,6 +287,14 @@ __global__ __launch_bounds__(256, workgroups_per_cu(F, L, kNT, kRW)) void latent
                 __builtin_amdgcn_sched_barrier(0);
             }
             __builtin_amdgcn_s_setprio(0);
+            if (kKeysFirst && kCodes) {
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const f32x4 ks = *reinterpret_cast<const f32x4 *>(scales + 16 * b + 4 * g);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[0][b][e] = __builtin_fmaf(sc[0][b][e], ks[e], rotated[b][e]);
+                }
+            }
             u32x4 ph[kNT], pl[kNT];
             const bool all = j0 >= flo && j0 + 32 <= min(fhi, k1) && valid == 0xFFFFFFFFu;
 #pragma unroll
@@ -400,7 +432,7 @@ __global__ __launch_bounds__(256, workgroups_per_cu(F, L, kNT, kRW)) void latent
                     look(next);
                     fetch(next, step + 1);
                 }
-                if (j0 < k1 && j0 + 31 >= wlo && j0 < whi) attend(j0, step, valid);
+                if (j0 < k1 && j0 + 31 >= wlo && j0 < whi) attend(j0, step, valid, [] {});
                 keep_all();
                 valid = valid_in;
                 wait_loads();
@@ -408,13 +440,21 @@ __global__ __launch_bounds__(256, workgroups_per_cu(F, L, kNT, kRW)) void latent
             }
         } else {
             // The wave's own keys, 32 of every 128: nothing to meet for.
-            for (int j0 = k0 + 32 * kw; j0 < k1; j0 += 128) {
-                look(j0);
-                fetch(j0, 0);
+            int j0 = k0 + 32 * kw;
+            auto come = [&](int j, int step) {
+                if (j < k1) {
+                    look(j);
+                    fetch(j, step);
+                }
+            };
+            if (kKeysFirst) come(j0, 0);
+            for (int step = 0; j0 < k1; j0 += 128, ++step) {
+                if (!kKeysFirst) come(j0, step);
                 wait_loads();
-                if (j0 + 31 >= wlo && j0 < whi) attend(j0, 0, valid_in);
+                const uint32_t valid = valid_in;
+                attend(j0, step, valid, [&] { come(j0 + 128, step + 1); });
                 keep_all();
-                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // read before the next rows come in
+                if (!kKeysFirst) asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // read before the next rows come in
             }
             __syncthreads();
         }
