@@ -46,23 +46,32 @@ __global__ __launch_bounds__(256) void absorb_kernel(LatentJob a, E *out) {
             }
         }
     }
+    auto row = [&](int t) { return static_cast<const uint16_t *>(a.q) + (size_t)min(t + n, t1 - 1) * a.ldq + (size_t)h * width + 8 * g; };
+    u32x4 qf[8];   // the widest head has 256 elements
+    auto read = [&](int t) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k < N / 32) qf[k] = ldg(reinterpret_cast<const u32x4 *>(row(t) + 32 * k));
+    };
+    read(t0);
     wait_loads();
     __syncthreads();
     for (int t = t0; t < t1; t += 16) {
         const bool on = t + n < t1;
-        const uint16_t *q = static_cast<const uint16_t *>(a.q) + (size_t)(on ? t + n : t) * a.ldq + (size_t)h * width + 8 * g;
         f32x4 o[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-        for (int k = 0; k < N / 32; ++k) {
-            const u32x4 qf = ldg(reinterpret_cast<const u32x4 *>(q + 32 * k));
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            if (k >= N / 32) break;
             // Slot (g, e) of the product over 32 rows stands for row 8 g + e in both operands.
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 const int c = 2 * (2 * wave + b) + (n >> 1 & 1), r = 32 * k + 8 * g + (n >> 2);
                 auto at = [&](int r) { return lds + r * kColumns * 2 + ((c ^ (r & 7) << 1) << 4) + 8 * (n & 1); };
                 const u32x2 x = read_tr16(at(r)), y = read_tr16(at(r + 4));
-                o[b] = mfma16(u32x4{x.x, x.y, y.x, y.y}, qf, o[b]);
+                o[b] = mfma16(u32x4{x.x, x.y, y.x, y.y}, qf[k], o[b]);
             }
         }
+        if (t + 16 < t1) read(t + 16);
         if (!on) continue;
         E *to = out + ((size_t)(t + n) * H + h) * (L + R) + l0 + 32 * wave + 4 * g;
 #pragma unroll
@@ -95,90 +104,134 @@ __device__ __forceinline__ Pieces pieces_of_call(const AttnJob &a, const Split &
     return p;
 }
 
-// Row t's sequence, -1: it has no result. The same in all lanes.
+// Row t's sequence; t and it are the same in the 16 lanes of a group.
 __device__ __forceinline__ int sequence_of(const AttnJob &a, const Pieces &p, int t) {
-    int s;
+    const int lane = threadIdx.x & 63;
     if (a.c.n_seq <= 64) {
-        const uint64_t before = __ballot((int)(threadIdx.x & 63) < a.c.n_seq && p.q_start <= t);
-        s = before ? 63 - __clzll((long long)before) : 0;
-    } else {
-        int lo = 0, hi = a.c.n_seq;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (a.q_start[mid] <= t)
-                lo = mid;
-            else
-                hi = mid;
+        int s = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int tj = __builtin_amdgcn_readlane(t, 16 * j);
+            const uint64_t before = __ballot(lane < a.c.n_seq && p.q_start <= tj);
+            s = lane >> 4 == j && before ? 63 - __clzll((long long)before) : s;
         }
-        s = lo;
+        return s;
     }
-    return __builtin_amdgcn_readfirstlane(s);
+    int lo = 0, hi = a.c.n_seq;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a.q_start[mid] <= t)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
 }
 
-// The joined output of row t, head h, elements 8 lane .. + 7; false: the row has no result.
+__device__ __forceinline__ float element_of(const u32x4 *v, int e, uint16_t) {
+    const uint32_t w = v[0][e >> 1];
+    return e & 1 ? __uint_as_float(w & 0xFFFF0000u) : bf16_f(w & 0xFFFFu);
+}
+__device__ __forceinline__ float element_of(const u32x4 *v, int e, float) { return __uint_as_float(v[e >> 2][e & 3]); }
+
+// The joined output of row t, head h, the same in the 16 lanes of a group: lane n of it gets
+// elements 128 c + 8 n .. + 7. false: the row has no result. A wave joins four rows at once with
+// several pieces of each on their way: a row after the other, a piece after the other, it waited
+// for each (31 us instead of 10 for 32 tokens of 128 heads with about 8 pieces each).
 // E: of the pieces' outputs.
-template <class E>
-__device__ __forceinline__ bool joined(const CoreArgs &x, const Pieces &pieces, int t, int h, float (&o)[8]) {
+template <class E, int L>
+__device__ __forceinline__ bool joined(const CoreArgs &x, const Pieces &pieces, int t, int h, float (&o)[L / 128][8]) {
+    constexpr int kParts = L / 128, kWords = sizeof(E) / 2, kAtOnce = 4 / kWords;
     const AttnJob &a = x.a;
     const Split &sp = x.sp;
-    const int lane = threadIdx.x & 63, L = a.c.d;
+    const int lane = threadIdx.x & 63, n = lane & 15;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] = 0.0f;
-    if (t >= a.T) return false;
+    for (int c = 0; c < kParts; ++c)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[c][e] = 0.0f;
     const int s = sequence_of(a, pieces, t);
     const Seq q = seq_of(a, s);
-    if (t < q.q0 || t >= q.q0 + q.rows) return false;
-    const bool on = 8 * lane < L;
-    auto add = [&](const E *p, float w) {
-        float v[8];
-        query4(p + 8 * lane, v);
-        query4(p + 8 * lane + 4, v + 4);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] += v[e] * w;
-    };
+    const bool on = t < a.T && t >= q.q0 && t < q.q0 + q.rows;
     if (sp.n_split == 1) {
-        if (on) add(static_cast<const E *>(a.o) + (size_t)t * a.ldo + (size_t)h * L, 1.0f);
-        return true;
-    }
-    const int r = (t - q.q0) * a.group + h, tile = r / sp.tile_rows;
-    int first, n;
-    if (sp.planned) {
-        n = __builtin_amdgcn_readlane(pieces.n, s);
-        first = __builtin_amdgcn_readlane(pieces.first, s) + tile * n;
-    } else {
-        first = (s * sp.tiles + tile) * sp.n_split, n = sp.n_split;
-    }
-    const int64_t at = part_row(a, sp, first, 0, tile, r), next = sp.rows;
-    float2 v = make_float2(kNegInf, 0.0f);
-    if (lane < n) v = sp.ml[at + lane * next];
-    float m = v.x;
+        const E *p = static_cast<const E *>(a.o) + (on ? (size_t)t * a.ldo + (size_t)h * L : 0) + 8 * n;
 #pragma unroll
-    for (int y = 1; y < 64; y <<= 1) m = fmaxf(m, __shfl_xor(m, y));
-    // A piece without visible keys weighs nothing; one whose sum is NaN makes the row NaN.
-    const float up = v.x == kNegInf && v.y == 0.0f ? 0.0f : v.y != v.y ? v.y : __builtin_amdgcn_exp2f(v.x - m) * v.y;
-    const float l = wave_sum(up), inv = l == 0.0f ? 0.0f : 1.0f / l;
-    for (int p = 0; p < n; ++p) {
-        const float w = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(up), p)) * inv;
-        if (w != 0.0f && on) add(reinterpret_cast<const E *>(sp.part) + (at + p * next) * L, w);
+        for (int c = 0; c < kParts; ++c) {
+            u32x4 v[kWords];
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) v[i] = ldg(reinterpret_cast<const u32x4 *>(p + 128 * c) + i);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[c][e] = element_of(v, e, E());
+        }
+        return on;
     }
-    return true;
+    const int r = on ? (t - q.q0) * a.group + h : 0, tile = r / sp.tile_rows;
+    const int per = __shfl(pieces.n, s), before = __shfl(pieces.first, s);
+    const int first = !on ? 0 : sp.planned ? before + tile * per : (s * sp.tiles + tile) * sp.n_split;
+    const int have = !on ? 0 : sp.planned ? per : sp.n_split;
+    const int64_t at = part_row(a, sp, first, 0, tile, r), next = sp.rows;
+    static_assert(kMaxSplit <= 64, "four pieces a lane");
+    float2 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = n + 16 * i < have ? sp.ml[at + (n + 16 * i) * next] : make_float2(kNegInf, 0.0f);
+    float m = fmaxf(fmaxf(v[0].x, v[1].x), fmaxf(v[2].x, v[3].x));
+#pragma unroll
+    for (int y = 1; y < 16; y <<= 1) m = fmaxf(m, __shfl_xor(m, y));
+    // A piece without visible keys weighs nothing; one whose sum is NaN makes the row NaN.
+    float up[4], l = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        up[i] = v[i].x == kNegInf && v[i].y == 0.0f ? 0.0f : v[i].y != v[i].y ? v[i].y : __builtin_amdgcn_exp2f(v[i].x - m) * v[i].y;
+        l += up[i];
+    }
+    int most = have;
+#pragma unroll
+    for (int y = 1; y < 16; y <<= 1) l += __shfl_xor(l, y);
+#pragma unroll
+    for (int y = 16; y < 64; y <<= 1) most = max(most, __shfl_xor(most, y));
+    most = __builtin_amdgcn_readfirstlane(most);
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const E *part = reinterpret_cast<const E *>(sp.part) + at * L + 8 * n;
+    for (int p0 = 0; p0 < most; p0 += kAtOnce) {
+        u32x4 raw[kAtOnce][kParts][kWords];
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j)
+#pragma unroll
+            for (int c = 0; c < kParts; ++c)
+#pragma unroll
+                for (int i = 0; i < kWords; ++i)   // behind a row's pieces: its first one again, which weighs nothing then
+                    raw[j][c][i] = ldg(reinterpret_cast<const u32x4 *>(part + (p0 + j < have ? p0 + j : 0) * next * L + 128 * c) + i);
+        const int turn = p0 >> 4;
+        const float mine = turn == 0 ? up[0] : turn == 1 ? up[1] : turn == 2 ? up[2] : up[3];
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+            const float got = __shfl(mine, (lane & 48) | ((p0 + j) & 15)) * inv, w = p0 + j < have ? got : 0.0f;
+#pragma unroll
+            for (int c = 0; c < kParts; ++c)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float y = element_of(raw[j][c], e, E());
+                    o[c][e] = w == 0.0f ? o[c][e] : __builtin_fmaf(y, w, o[c][e]);
+                }
+        }
+    }
+    return on;
 }
 
-// On its own (without weights, and in fp32): a wave a row.
-template <class E>
+// On its own (without weights, and in fp32): 16 lanes a row.
+template <class E, int L>
 __global__ __launch_bounds__(256) void join_kernel(CoreArgs x) {
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const int64_t w = (int64_t)blockIdx.x * 4 + wave;
+    const int n = threadIdx.x & 15;
+    const int64_t w = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
     const int t = (int)(w / x.a.n_q), h = (int)(w - (int64_t)t * x.a.n_q);
-    if (t >= x.a.T) return;
-    float o[8];
-    if (!joined<E>(x, pieces_of_call(x.a, x.sp), t, h, o) || 8 * lane >= x.a.c.d) return;
-    E *to = static_cast<E *>(x.a.o) + (size_t)t * x.a.ldo + (size_t)h * x.a.c.d + 8 * lane;
-    put4(to, o);
-    put4(to + 4, o + 4);
+    float o[L / 128][8];
+    if (!joined<E, L>(x, pieces_of_call(x.a, x.sp), t, h, o)) return;
+    E *to = static_cast<E *>(x.a.o) + (size_t)t * x.a.ldo + (size_t)h * L + 8 * n;
+#pragma unroll
+    for (int c = 0; c < L / 128; ++c) {
+        put4(to + 128 * c, o[c]);
+        put4(to + 128 * c + 4, o[c] + 4);
+    }
 }
-
-constexpr int kPitch = kMaxLatent + 8;   // elements of an LDS row of outputs
 
 struct UpArgs {
     LatentJob a;
@@ -186,55 +239,76 @@ struct UpArgs {
     int splits;   // of `value`, a workgroup each
 };
 
+template <int L>
 __global__ __launch_bounds__(256) void up_kernel(UpArgs u) {
+    constexpr int kPitch = L + 8;   // elements of an LDS row of outputs
+    constexpr int kOwn = L / 4;     // a wave's part of the latent axis
     __shared__ __align__(16) uint16_t head[16][kPitch], rest[16][kPitch];
-    __shared__ f32x4 part[4][2][64];
+    __shared__ f32x4 part[2][4][2][64];
     __shared__ int live[16];
     const LatentJob &a = u.a;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15, g = lane >> 4;
-    const int L = a.a.c.d, N = a.nope, V = a.value, H = a.a.n_q;
+    const int N = a.nope, V = a.value, H = a.a.n_q;
     const int unit = blockIdx.x / u.splits, split = blockIdx.x - unit * u.splits, block = unit / H, h = unit - block * H;
     const int t0 = 16 * block;
-    const Pieces pieces = pieces_of_call(u.x.a, u.x.sp);
-#pragma unroll 1
-    for (int i = wave; i < 16; i += 4) {
-        float o[8];
-        const bool on = joined<uint16_t>(u.x, pieces, t0 + i, h, o);
-        if (lane == 0) live[i] = on;
-        if (8 * lane >= L) continue;
-        uint32_t hi[4], lo[4];
+    const int per = V / u.splits, v_from = split * per, v_to = v_from + per;
+    const uint16_t *w = static_cast<const uint16_t *>(a.w) + ((size_t)h * (N + V) + N + n) * L + wave * kOwn + 8 * g;
+    u32x4 ahead[2][kOwn / 32];
+    auto read = [&](int v0) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            hi[e] = pack2(o[2 * e], o[2 * e + 1]);
-            lo[e] = pack2(o[2 * e] - bf16_f(hi[e] & 0xFFFFu), o[2 * e + 1] - __uint_as_float(hi[e] & 0xFFFF0000u));
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int k = 0; k < kOwn / 32; ++k) ahead[b][k] = ldg(reinterpret_cast<const u32x4 *>(w + (size_t)(v0 + 16 * b) * L + 32 * k));
+    };
+    read(v_from);   // come in while the pieces are joined
+    {
+        const int i = 4 * wave + g;
+        float o[L / 128][8];
+        const bool on = joined<uint16_t, L>(u.x, pieces_of_call(u.x.a, u.x.sp), t0 + i, h, o);
+        if (n == 0) live[i] = on;
+#pragma unroll
+        for (int c = 0; c < L / 128; ++c) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                hi[e] = pack2(o[c][2 * e], o[c][2 * e + 1]);
+                lo[e] = pack2(o[c][2 * e] - bf16_f(hi[e] & 0xFFFFu), o[c][2 * e + 1] - __uint_as_float(hi[e] & 0xFFFF0000u));
+            }
+            *reinterpret_cast<u32x4 *>(&head[i][128 * c + 8 * n]) = u32x4{hi[0], hi[1], hi[2], hi[3]};
+            *reinterpret_cast<u32x4 *>(&rest[i][128 * c + 8 * n]) = u32x4{lo[0], lo[1], lo[2], lo[3]};
         }
-        *reinterpret_cast<u32x4 *>(&head[i][8 * lane]) = u32x4{hi[0], hi[1], hi[2], hi[3]};
-        *reinterpret_cast<u32x4 *>(&rest[i][8 * lane]) = u32x4{lo[0], lo[1], lo[2], lo[3]};
     }
     __syncthreads();
-    const int per = V / u.splits, mine = L / 4;   // a wave's part of the latent axis
-    for (int v0 = split * per; v0 < (split + 1) * per; v0 += 32) {
-        const uint16_t *w = static_cast<const uint16_t *>(a.w) + ((size_t)h * (N + V) + N + v0 + n) * L + wave * mine + 8 * g;
-        f32x4 o[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-#pragma unroll 4
-        for (int k = 0; k < mine / 32; ++k) {
-            const u32x4 w0 = ldg(reinterpret_cast<const u32x4 *>(w + 32 * k)), w1 = ldg(reinterpret_cast<const u32x4 *>(w + 16 * L + 32 * k));
-            const int at = wave * mine + 32 * k + 8 * g;
-            const u32x4 x = *reinterpret_cast<const u32x4 *>(&head[n][at]), y = *reinterpret_cast<const u32x4 *>(&rest[n][at]);
-            o[0] = mfma16(w0, x, o[0]);
-            o[1] = mfma16(w1, x, o[1]);
-            o[0] = mfma16(w0, y, o[0]);
-            o[1] = mfma16(w1, y, o[1]);
+    u32x4 x[kOwn / 32], y[kOwn / 32];
+#pragma unroll
+    for (int k = 0; k < kOwn / 32; ++k) {
+        x[k] = *reinterpret_cast<const u32x4 *>(&head[n][wave * kOwn + 32 * k + 8 * g]);
+        y[k] = *reinterpret_cast<const u32x4 *>(&rest[n][wave * kOwn + 32 * k + 8 * g]);
+    }
+    int turn = 0;
+    for (int v0 = v_from; v0 < v_to; v0 += 32, turn ^= 1) {
+        u32x4 now[2][kOwn / 32];
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int k = 0; k < kOwn / 32; ++k) now[b][k] = ahead[b][k];
+        if (v0 + 32 < v_to) read(v0 + 32);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            f32x4 o{0, 0, 0, 0};
+#pragma unroll
+            for (int k = 0; k < kOwn / 32; ++k) {
+                o = mfma16(now[b][k], x[k], o);
+                o = mfma16(now[b][k], y[k], o);
+            }
+            part[turn][wave][b][lane] = o;
         }
-        part[wave][0][lane] = o[0];
-        part[wave][1][lane] = o[1];
         __syncthreads();
         if (wave < 2 && live[n]) {   // wave b: rows v0 + 16 b + 4 g .. + 3 of token n
-            const f32x4 s = part[0][wave][lane] + part[1][wave][lane] + part[2][wave][lane] + part[3][wave][lane];
+            const f32x4 s = part[turn][0][wave][lane] + part[turn][1][wave][lane] + part[turn][2][wave][lane] + part[turn][3][wave][lane];
             const float v[4] = {s.x, s.y, s.z, s.w};
             put4(static_cast<uint16_t *>(a.o) + (size_t)(t0 + n) * a.ldo + (size_t)h * V + v0 + 16 * wave + 4 * g, v);
         }
-        __syncthreads();
     }
 }
 
@@ -252,15 +326,30 @@ void launch_absorb(const LatentJob &a, void *out, bool f32_out, hipStream_t s) {
 void launch_up(const LatentJob &a, const CoreArgs &x, hipStream_t s) {
     const int64_t units = (int64_t)(a.a.T + 15) / 16 * a.a.n_q;
     const int splits = units >= 256 ? 1 : a.value / 32;
-    hipLaunchKernelGGL(up_kernel, dim3((unsigned)(units * splits)), dim3(256), 0, s, UpArgs{a, x, splits});
+    const dim3 g((unsigned)(units * splits)), b(256);
+    const UpArgs u{a, x, splits};
+    switch (a.a.c.d) {
+        case 128: hipLaunchKernelGGL((up_kernel<128>), g, b, 0, s, u); break;
+        case 256: hipLaunchKernelGGL((up_kernel<256>), g, b, 0, s, u); break;
+        default: hipLaunchKernelGGL((up_kernel<512>), g, b, 0, s, u);
+    }
+}
+
+template <class E>
+static void join(const CoreArgs &x, hipStream_t s) {
+    const dim3 g((unsigned)(((int64_t)x.a.T * x.a.n_q + 15) / 16)), b(256);
+    switch (x.a.c.d) {
+        case 128: hipLaunchKernelGGL((join_kernel<E, 128>), g, b, 0, s, x); break;
+        case 256: hipLaunchKernelGGL((join_kernel<E, 256>), g, b, 0, s, x); break;
+        default: hipLaunchKernelGGL((join_kernel<E, 512>), g, b, 0, s, x);
+    }
 }
 
 void launch_join(const CoreArgs &x, bool f32, hipStream_t s) {
-    const dim3 g((unsigned)(((int64_t)x.a.T * x.a.n_q + 3) / 4)), b(256);
     if (f32)
-        hipLaunchKernelGGL((join_kernel<float>), g, b, 0, s, x);
+        join<float>(x, s);
     else
-        hipLaunchKernelGGL((join_kernel<uint16_t>), g, b, 0, s, x);
+        join<uint16_t>(x, s);
 }
 
 }  // namespace wl
