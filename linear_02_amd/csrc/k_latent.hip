@@ -75,7 +75,7 @@ Places places_of(const LatentJob &a, const Plan &p, bool f32) {
     };
     if (a.w) {
         w.q = take(rows * (L + a.rot) * (f32 || p.kind.exact ? 4 : 2));
-        if (!split || f32) w.o = take(rows * L * (f32 ? 4 : 2));
+        if (!split) w.o = take(rows * L * (f32 ? 4 : 2));
     }
     if (split) {
         w.part = take((size_t)p.items * p.sp.rows * L * (f32 ? 4 : 2));
@@ -133,7 +133,7 @@ LatentNeeds latent_needs(const LatentJob &a, int fmt, bool f32, int form) {
     const Plan p = plan_of(a, fmt);
     LatentNeeds n{places_of(a, p, f32).bytes, p.items};
     // the products around it, of tokens and heads
-    const int64_t around = (rows + 15) / 16 * 8 + 8 * a.a.n_q;
+    const int64_t around = (f32 ? rows : (rows + 15) / 16 * 8) + 8 * a.a.n_q;
     if (around > n.workgroups) n.workgroups = around;
     return n;
 }
@@ -175,15 +175,10 @@ hipError_t launch_latent(const LatentJob &job, int fmt, bool f32, int form, void
     else
         launch_latent_tile(x, fmt, p.kind, (unsigned)p.sp.items, s);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    if ((f32 || !a.w) && p.sp.n_split > 1) {
+    if (a.w)
+        launch_up(a, x, f32, s);
+    else if (p.sp.n_split > 1)
         launch_join(x, f32, s);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-    }
-    if (!a.w) return hipSuccess;
-    if (f32)
-        launch_up_f32(a, static_cast<const float *>(x.a.o), s);
-    else
-        launch_up(a, x, s);
     return hipGetLastError();
 }
 

@@ -1,5 +1,4 @@
-// Latent attention in fp32: the core over fp32 rows on the fp32 matrix instructions, and
-// every head's products into the latent space and out of it.
+// Latent attention in fp32: the core over fp32 rows on the fp32 matrix instructions.
 //
 // v_mfma_f32_16x16x4_f32, D = A B + C: lane l holds A[m = l & 15][k = l >> 4], B[k][n = l & 15]
 // and C[m = 4 (l >> 4) + i][n] (i = 0..3). As in bf16 (k_latent_tile.hip), scores are formed
@@ -258,76 +257,6 @@ __global__ __launch_bounds__(256, 1) void latent_f32_kernel(CoreArgs x) {
         }
 }
 
-constexpr int kTokens = 8;   // of a workgroup of the products around it: each weight is read once for them
-
-// q' = W^K^T q of every token and head, its rotated part beside it. A thread a column.
-__global__ __launch_bounds__(256) void absorb_kernel(LatentJob a, float *out) {
-    __shared__ float qs[256][kTokens];
-    const int H = a.a.n_q, L = a.a.c.d, N = a.nope, R = a.rot;
-    const int block = blockIdx.x / H, h = blockIdx.x - block * H, t0 = block * kTokens, n_t = min(kTokens, a.a.T - t0);
-    for (int i = threadIdx.x; i < kTokens * (N + R); i += 256) {
-        const int t = i / (N + R), e = i - t * (N + R);
-        const float v = t < n_t ? static_cast<const float *>(a.q)[(size_t)(t0 + t) * a.ldq + (size_t)h * (N + R) + e] : 0.0f;
-        if (e < N)
-            qs[e][t] = v;
-        else if (t < n_t)
-            out[((size_t)(t0 + t) * H + h) * (L + R) + L + e - N] = v;
-    }
-    __syncthreads();
-    const float *w = static_cast<const float *>(a.w) + (size_t)h * (N + a.value) * L;
-    for (int l = threadIdx.x; l < L; l += 256) {
-        float s[kTokens] = {};
-#pragma unroll 4
-        for (int n = 0; n < N; ++n) {
-            const float x = ldg(w + (size_t)n * L + l);
-#pragma unroll
-            for (int t = 0; t < kTokens; ++t) s[t] += qs[n][t] * x;
-        }
-        for (int t = 0; t < n_t; ++t) out[((size_t)(t0 + t) * H + h) * (L + R) + l] = s[t];
-    }
-}
-
-// o = W^V o' of every token and head that has a result. Thread (v, p): row v's part p of the latent.
-__global__ __launch_bounds__(256) void up_kernel(LatentJob a, const float *in) {
-    __shared__ __align__(16) float xs[kTokens][kMaxLatent];
-    __shared__ float part[256][kTokens + 1];
-    __shared__ int live[kTokens];
-    const int H = a.a.n_q, L = a.a.c.d, N = a.nope, V = a.value;
-    const int block = blockIdx.x / H, h = blockIdx.x - block * H, t0 = block * kTokens, n_t = min(kTokens, a.a.T - t0);
-    if ((int)threadIdx.x < kTokens) live[threadIdx.x] = (int)threadIdx.x < n_t && has_result(a.a, t0 + threadIdx.x);
-    __syncthreads();
-    for (int i = threadIdx.x; i < kTokens * L; i += 256) {
-        const int t = i / L, e = i - t * L;
-        xs[t][e] = live[t] ? in[((size_t)(t0 + t) * H + h) * L + e] : 0.0f;
-    }
-    __syncthreads();
-    const int parts = V <= 64 ? 4 : V <= 128 ? 2 : 1, per = 256 / parts, span = L / parts;
-    const int v = threadIdx.x % per, p = threadIdx.x / per;
-    float s[kTokens] = {};
-    if (v < V) {
-        const float *w = static_cast<const float *>(a.w) + ((size_t)h * (N + V) + N + v) * L + p * span;
-#pragma unroll 2
-        for (int l = 0; l < span; l += 4) {
-            const f32x4 x = ldg(reinterpret_cast<const f32x4 *>(w + l));
-#pragma unroll
-            for (int t = 0; t < kTokens; ++t) {
-                const f32x4 y = *reinterpret_cast<const f32x4 *>(&xs[t][p * span + l]);
-                s[t] += x.x * y.x + x.y * y.y + x.z * y.z + x.w * y.w;
-            }
-        }
-    }
-#pragma unroll
-    for (int t = 0; t < kTokens; ++t) part[threadIdx.x][t] = s[t];
-    __syncthreads();
-    if (p || v >= V) return;
-    for (int t = 0; t < n_t; ++t) {
-        if (!live[t]) continue;
-        float sum = 0.0f;
-        for (int k = 0; k < parts; ++k) sum += part[k * per + v][t];
-        static_cast<float *>(a.o)[(size_t)(t0 + t) * a.ldo + (size_t)h * V + v] = sum;
-    }
-}
-
 template <int L>
 void run(const CoreArgs &x, const CoreKind &k, unsigned blocks, hipStream_t s) {
     if (k.row_waves == 4)
@@ -344,14 +273,6 @@ void launch_latent_f32(const CoreArgs &x, const CoreKind &k, unsigned blocks, hi
         case 256: run<256>(x, k, blocks, s); break;
         default: run<512>(x, k, blocks, s);
     }
-}
-
-void launch_absorb_f32(const LatentJob &a, float *out, hipStream_t s) {
-    hipLaunchKernelGGL(absorb_kernel, dim3((unsigned)((int64_t)(a.a.T + kTokens - 1) / kTokens * a.a.n_q)), dim3(256), 0, s, a, out);
-}
-
-void launch_up_f32(const LatentJob &a, const float *in, hipStream_t s) {
-    hipLaunchKernelGGL(up_kernel, dim3((unsigned)((int64_t)(a.a.T + kTokens - 1) / kTokens * a.a.n_q)), dim3(256), 0, s, a, in);
 }
 
 }  // namespace wl

@@ -1,9 +1,9 @@
-// Around latent attention: every head's queries into the latent space and outputs out of it in
-// bf16, and the join of divided keys.
+// Around latent attention: every head's queries into the latent space and outputs out of it, and
+// the join of divided keys.
 //
 // q'[t][h] = W_h^K^T q[t][h] and o[t][h] = W_h^V o'[t][h]: per head a product with T columns
 // and a weight of its own, so both are bound by reading the weights where tokens are few.
-// Both are formed transposed on the matrix cores (rows of the weight times tokens): 16
+// In bf16 both are formed transposed on the matrix cores (rows of the weight times tokens): 16
 // tokens are the columns of a product, and a lane gets four neighbouring outputs of one token.
 //   into   a workgroup takes 128 columns of one head's W^K, which LDS's transposing reads turn
 //   out    a workgroup takes 16 tokens of one head: it joins their pieces' outputs into LDS, as
@@ -217,7 +217,7 @@ __device__ __forceinline__ bool joined(const CoreArgs &x, const Pieces &pieces, 
     return on;
 }
 
-// On its own (without weights, and in fp32): 16 lanes a row.
+// On its own (without weights): 16 lanes a row.
 template <class E, int L>
 __global__ __launch_bounds__(256) void join_kernel(CoreArgs x) {
     const int n = threadIdx.x & 15;
@@ -312,6 +312,90 @@ __global__ __launch_bounds__(256) void up_kernel(UpArgs u) {
     }
 }
 
+constexpr int kTokensF32 = 8;   // of a workgroup of the product into the latent space in fp32
+
+// q' = W^K^T q in fp32: 64 columns of one head's latent axis, each wave a quarter of the sum's rows.
+__global__ __launch_bounds__(256) void absorb_f32_kernel(LatentJob a, float *out) {
+    __shared__ float qs[256][kTokensF32], part[4][kTokensF32][64];
+    const int H = a.a.n_q, L = a.a.c.d, N = a.nope, R = a.rot;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int parts = L / 64, unit = blockIdx.x / parts, l0 = (blockIdx.x - unit * parts) * 64;
+    const int block = unit / H, h = unit - block * H, t0 = block * kTokensF32, n_t = min(kTokensF32, a.a.T - t0);
+    const float *q = static_cast<const float *>(a.q) + (size_t)t0 * a.ldq + (size_t)h * (N + R);
+    for (int i = threadIdx.x; i < kTokensF32 * (N + R); i += 256) {
+        const int t = i / (N + R), e = i - t * (N + R);
+        const float v = t < n_t ? q[(size_t)t * a.ldq + e] : 0.0f;
+        if (e < N)
+            qs[e][t] = v;
+        else if (l0 == 0 && t < n_t)
+            out[((size_t)(t0 + t) * H + h) * (L + R) + L + e - N] = v;
+    }
+    __syncthreads();
+    const int own = N / 4;
+    const float *w = static_cast<const float *>(a.w) + ((size_t)h * (N + a.value) + wave * own) * L + l0 + lane;
+    float s[kTokensF32] = {};
+#pragma unroll 8
+    for (int n = 0; n < own; ++n) {
+        const float x = ldg(w + (size_t)n * L);
+#pragma unroll
+        for (int t = 0; t < kTokensF32; ++t) s[t] += qs[wave * own + n][t] * x;
+    }
+#pragma unroll
+    for (int t = 0; t < kTokensF32; ++t) part[wave][t][lane] = s[t];
+    __syncthreads();
+    for (int t = wave; t < n_t; t += 4)
+        out[((size_t)(t0 + t) * H + h) * (L + R) + l0 + lane] = part[0][t][lane] + part[1][t][lane] + part[2][t][lane] + part[3][t][lane];
+}
+
+// o = W^V o' in fp32: 16 tokens of one head, 16 rows of the weight at a time with 16 lanes each.
+template <int L>
+__global__ __launch_bounds__(256) void up_f32_kernel(UpArgs u) {
+    __shared__ __align__(16) float xs[16][L];
+    __shared__ int live[16];
+    const LatentJob &a = u.a;
+    const int n = threadIdx.x & 15, i = threadIdx.x >> 4;
+    const int N = a.nope, V = a.value, H = a.a.n_q;
+    const int unit = blockIdx.x / u.splits, split = blockIdx.x - unit * u.splits, block = unit / H, h = unit - block * H;
+    const int t0 = 16 * block, per = V / u.splits, v_from = split * per, v_to = v_from + per;
+    {
+        float o[L / 128][8];
+        const bool on = joined<float, L>(u.x, pieces_of_call(u.x.a, u.x.sp), t0 + i, h, o);
+        if (n == 0) live[i] = on;
+#pragma unroll
+        for (int c = 0; c < L / 128; ++c) {
+            *reinterpret_cast<f32x4 *>(&xs[i][128 * c + 8 * n]) = f32x4{o[c][0], o[c][1], o[c][2], o[c][3]};
+            *reinterpret_cast<f32x4 *>(&xs[i][128 * c + 8 * n + 4]) = f32x4{o[c][4], o[c][5], o[c][6], o[c][7]};
+        }
+    }
+    __syncthreads();
+    for (int v0 = v_from; v0 < v_to; v0 += 16) {
+        asm volatile("" ::: "memory");   // outputs are read from LDS again: they would not fit the registers
+        const float *w = static_cast<const float *>(a.w) + ((size_t)h * (N + V) + N + v0 + i) * L + 4 * n;
+        f32x4 x[L / 64];
+#pragma unroll
+        for (int k = 0; k < L / 64; ++k) x[k] = ldg(reinterpret_cast<const f32x4 *>(w + 64 * k));
+        float s[16];
+#pragma unroll
+        for (int t = 0; t < 16; ++t) {
+            s[t] = 0.0f;
+#pragma unroll
+            for (int k = 0; k < L / 64; ++k) {
+                const f32x4 y = *reinterpret_cast<const f32x4 *>(&xs[t][64 * k + 4 * n]);
+                s[t] += x[k].x * y.x + x[k].y * y.y + x[k].z * y.z + x[k].w * y.w;
+            }
+        }
+        // Summed over the 16 lanes, token n's in lane n.
+#pragma unroll
+        for (int y = 8; y; y >>= 1)
+#pragma unroll
+            for (int t = 0; t < y; ++t) {
+                const float keep = n & y ? s[t + y] : s[t], give = n & y ? s[t] : s[t + y];
+                s[t] = keep + __shfl_xor(give, y);
+            }
+        if (live[n]) static_cast<float *>(a.o)[(size_t)(t0 + n) * a.ldo + (size_t)h * V + v0 + i] = s[0];
+    }
+}
+
 }  // namespace
 
 void launch_absorb(const LatentJob &a, void *out, bool f32_out, hipStream_t s) {
@@ -323,16 +407,34 @@ void launch_absorb(const LatentJob &a, void *out, bool f32_out, hipStream_t s) {
         hipLaunchKernelGGL((absorb_kernel<uint16_t>), g, b, lds, s, a, static_cast<uint16_t *>(out));
 }
 
-void launch_up(const LatentJob &a, const CoreArgs &x, hipStream_t s) {
+// Fewer units of 16 tokens and a head than this are divided over `value`, and every part joins
+// their pieces again: 16 units divided and not, the whole call, 24.9 and 27.6 us (one token of 16
+// heads), 37.0 and 48.7 us in fp32; 224 units of about 10 pieces, this kernel, 28 and 15 us.
+constexpr int64_t kUnits = 128;
+
+void launch_up(const LatentJob &a, const CoreArgs &x, bool f32, hipStream_t s) {
     const int64_t units = (int64_t)(a.a.T + 15) / 16 * a.a.n_q;
-    const int splits = units >= 256 ? 1 : a.value / 32;
+    const int splits = units >= kUnits ? 1 : a.value / (f32 ? 16 : 32);
     const dim3 g((unsigned)(units * splits)), b(256);
     const UpArgs u{a, x, splits};
+    if (f32) {
+        switch (a.a.c.d) {
+            case 128: hipLaunchKernelGGL((up_f32_kernel<128>), g, b, 0, s, u); break;
+            case 256: hipLaunchKernelGGL((up_f32_kernel<256>), g, b, 0, s, u); break;
+            default: hipLaunchKernelGGL((up_f32_kernel<512>), g, b, 0, s, u);
+        }
+        return;
+    }
     switch (a.a.c.d) {
         case 128: hipLaunchKernelGGL((up_kernel<128>), g, b, 0, s, u); break;
         case 256: hipLaunchKernelGGL((up_kernel<256>), g, b, 0, s, u); break;
         default: hipLaunchKernelGGL((up_kernel<512>), g, b, 0, s, u);
     }
+}
+
+void launch_absorb_f32(const LatentJob &a, float *out, hipStream_t s) {
+    const dim3 g((unsigned)((int64_t)(a.a.T + kTokensF32 - 1) / kTokensF32 * a.a.n_q * (a.a.c.d / 64)));
+    hipLaunchKernelGGL(absorb_f32_kernel, g, dim3(256), 0, s, a, out);
 }
 
 template <class E>

@@ -33,13 +33,12 @@ void launch_latent_tile(const CoreArgs &x, int fmt, const CoreKind &k, unsigned 
 // Products of every token and head (k_latent_heads.hip): into the latent space (out: bf16, or
 // fp32), and out of it, with the join of divided keys.
 void launch_absorb(const LatentJob &a, void *out, bool f32_out, hipStream_t s);
-void launch_up(const LatentJob &a, const CoreArgs &x, hipStream_t s);
+void launch_absorb_f32(const LatentJob &a, float *out, hipStream_t s);
+void launch_up(const LatentJob &a, const CoreArgs &x, bool f32, hipStream_t s);
 void launch_join(const CoreArgs &x, bool f32, hipStream_t s);
 
-// The same in fp32 (k_latent_f32.hip); outputs in the latent space are joined before launch_up_f32.
+// The core in fp32 (k_latent_f32.hip).
 void launch_latent_f32(const CoreArgs &x, const CoreKind &k, unsigned blocks, hipStream_t s);
-void launch_absorb_f32(const LatentJob &a, float *out, hipStream_t s);
-void launch_up_f32(const LatentJob &a, const float *in, hipStream_t s);
 
 // The expanded form, of heads first .. first + heads - 1 (k_latent_expand.hip). a: the call's
 // own q and o, [T][n_q][nope + rot] and [T][n_q][value].
@@ -61,20 +60,6 @@ __device__ __forceinline__ int latent_row_bytes(int latent, int rot) {
 
 __device__ __forceinline__ float element(const uint16_t *p) { return bf16_f(ldg(p)); }
 __device__ __forceinline__ float element(const float *p) { return ldg(p); }
-
-// Whether row t belongs to a sequence's first max_q rows.
-__device__ __forceinline__ bool has_result(const AttnJob &a, int t) {
-    int lo = 0, hi = a.c.n_seq;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a.q_start[mid] <= t)
-            lo = mid;
-        else
-            hi = mid;
-    }
-    const Seq q = seq_of(a, lo);
-    return t >= q.q0 && t < q.q0 + q.rows;
-}
 
 // One wave, one query row (token i, head h), keys [j0, j1): the definition, key by key,
 // with the running maximum m (in powers of two) and sum l of a softmax. A key that the
