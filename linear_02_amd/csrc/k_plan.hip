@@ -173,8 +173,11 @@ __global__ __launch_bounds__(256) void fill_kernel(PlanJob a, const int32_t *scr
          (int)(blockIdx.x * 256 + threadIdx.x), (int)(gridDim.x * 256));
 }
 
-// Rows of a batch that the planning workgroup fills by itself.
-constexpr int kOneLaunchRows = 8192;
+// Rows of a batch that the planning workgroup fills by itself. 256 sequences, in one launch and in
+// two, replayed from a graph: 1024 rows 5.9 and 8.1 us, 4096 rows 8.1 and 8.3 us, 8192 rows 10.9 and
+// 8.4 us. (Pages given back may be more, and are not known here: 9000 of 1000 sequences in a call of
+// one row take 17 us.)
+constexpr int kOneLaunchRows = 4096;
 
 bool one_launch(const PlanJob &a) { return a.n_seq <= kThreads && a.T <= kOneLaunchRows; }
 
@@ -191,7 +194,8 @@ hipError_t launch_plan(const PlanJob &a, void *ws, hipStream_t s) {
     hipLaunchKernelGGL((plan_kernel<false>), dim3(1), dim3(kThreads), 0, s, a, scratch);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const int blocks = a.T / 1024 < 64 ? 64 : a.T / 1024 > 2048 ? 2048 : a.T / 1024;
+    // A row a thread: 1000 sequences and 130000 rows 12.7 us with four, 7 us with one.
+    const int blocks = a.T / 256 < 64 ? 64 : a.T / 256 > 2048 ? 2048 : a.T / 256;
     hipLaunchKernelGGL(fill_kernel, dim3(blocks), dim3(256), 0, s, a, scratch);
     return hipGetLastError();
 }
