@@ -108,15 +108,28 @@ Expanded expanded_of(const LatentJob &job) {
     return e;
 }
 
-// Queries of a sequence from which on the expanded form is taken, and the fewest workgroups
-// for which it is: with fewer, the absorbed form divides the keys.
-constexpr int kExpandedRows = 192, kExpandedWorkgroups = 128;
-
-bool expands(const LatentJob &a, int fmt, int form) {
+// Which form AUTO takes. The expanded one forms all keys and values once, and multiplies less per
+// query and key then; 128 queries of a head are one workgroup that walks all of their keys, so it wants
+// many of those, or few keys. Both times are estimated in us from constants fitted to measurements at a
+// latent of 512 and heads of 128 + 64 (absorbed, expanded; n_seq x queries over keys, heads):
+//   1 x 128 over 4096, 32    78, 186     1 x 512 over 4096, 32   199, 186     1 x 512 over 8192, 16   183, 311
+//   1 x 192 over 192, 128    82, 30      1 x 512 over 512, 32     83, 40      1 x 2048 over 2048, 8   128, 86
+//   1 x 256 over 4096, 128  362, 384     8 x 192 over 4096, 32   646, 657     8 x 256 over 2048, 32   420, 344
+// Calls of fewer queries than a tile has stay absorbed: the first constant is of many rows.
+bool expands(const LatentJob &job, int fmt, int form) {
+    const AttnJob &a = job.a;
     if (form != kFormAuto) return form == kFormExpanded;
-    if (!latent_can_expand(a, fmt) || a.a.max_q < kExpandedRows) return false;
-    const Expanded e = expanded_of(a);
-    return (int64_t)e.heads * e.tiles * a.a.c.n_seq >= kExpandedWorkgroups;
+    if (!latent_can_expand(job, fmt) || a.max_q < 128) return false;
+    const Expanded e = expanded_of(job);
+    // Never where the other form's workspace or launch would be beyond what calls may have.
+    if (2 * e.bytes > kExpandedBytes + 512 || (int64_t)a.c.n_seq * (e.blocks > e.tiles ? e.blocks : e.tiles) * e.heads >= 1 << 23) return false;
+    const double keys = e.keys, L = a.c.d, H = a.n_q;
+    const double seen = a.mask == kMaskCausal && a.window && (double)a.window + a.max_q < keys ? (double)a.window + a.max_q : keys;
+    const double tiles = (double)a.c.n_seq * e.tiles * H;
+    const double absorbed = 50 + 1.05e-9 * 2 * a.T * H * seen * (2 * L + job.rot);
+    const double expanded = 10 + 1.88e-9 * 2 * a.c.n_seq * keys * H * (job.nope + job.value) * L +
+                            0.0286 * seen * (tiles < 394 ? 1.0 : tiles * (0.65 / 256));
+    return expanded < absorbed;
 }
 
 }  // namespace
