@@ -249,6 +249,38 @@ def test_more_sequences_than_lanes(wl, fmt):
 
 
 @pytest.mark.parametrize("fmt", [BF, E4M3, F32])
+@pytest.mark.parametrize("n_seq,H,V", [(70, 32, 64), (130, 16, 32), (40, 48, 96)])
+def test_joins_of_many_units(wl, fmt, n_seq, H, V):
+    """Divided keys of more than 128 units of 16 tokens and a head, below and above a lane a sequence."""
+    rng = random.Random(n_seq)
+    seqs = [(rng.choice((0, 20, 300, 1500)), rng.choice((0, 1, 1, 2))) for _ in range(n_seq)]
+    Batch(wl, seqs, H, 128, 64, 64, V, fmt, page=32, seed=n_seq, gap=1, tail=20).check(wl, "many units", max_kv=4000, form="absorbed")
+
+
+@pytest.mark.parametrize("fmt", [BF, E4M3, F32])
+def test_captured_and_replayed_over_changing_lengths(wl, fmt):
+    """Lengths and rows that change between replays, the same call made eagerly beside them."""
+    b = Batch(wl, [(900, 2), (37, 1), (400, 3)], 12, fmt=fmt, page=32, seed=16, tail=3)
+    starts, lens = i32(b.starts), i32(b.lens)
+    call = wl.latent_attention_call(b.q, b.cache, b.w, starts, lens, 3, 1000, b.scale)
+    g, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s), torch.cuda.graph(g, stream=s):
+        call.launch()
+    torch.cuda.current_stream().wait_stream(s)
+    for k, (first, rows) in enumerate([([902, 38, 403], b.starts), ([0, 38, 1], b.starts), ([500, 1, 403], [0, 3, 3, 4]), ([902, 0, 20], [2, 2, 3, 6])]):
+        starts.copy_(i32(rows))
+        lens.copy_(i32(first))
+        b.q.copy_(torch.randn(b.q.shape, generator=torch.Generator().manual_seed(k)))
+        call.out.fill_(5.0)
+        g.replay()
+        o = torch.full_like(call.out, 5.0)
+        wl.wl_latent_attention(b.q, b.cache, b.w, starts, lens, 3, 1000, b.scale, o=o)
+        assert torch.equal(call.out, o)
+        assert (o[rows[-1]:] == 5.0).all() and (o[:rows[0]] == 5.0).all()
+
+
+@pytest.mark.parametrize("fmt", [BF, E4M3, F32])
 def test_limits_of_rows_and_keys(wl, fmt):
     """Rows beyond max_q have no result, keys beyond max_kv or the table are not seen, a sequence shorter than its
     new tokens has rows that see nothing."""
