@@ -572,7 +572,7 @@ wl_status wl_latent_read(const wl_latent_read_args *a, void *hip_stream);
  *         WL_LATENT_EXPANDED  keys and values are formed once in the workspace.
  *                             With w, a bf16 cache, nope and value both 64 or both
  *                             128 only (else WL_ERR_UNSUPPORTED)
- *         WL_LATENT_AUTO      the one that takes less time: expanded for prompts
+ *         WL_LATENT_AUTO      the one estimated to take less time: expanded for prompts
  * Numerics in bf16: q in the latent space, outputs there before W_h^V, expanded keys
  * and values and the weights of the second product are each rounded to bf16 once;
  * sums are fp32. dtype f32 is fp32 throughout.

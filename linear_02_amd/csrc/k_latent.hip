@@ -9,7 +9,9 @@ size_t pad(size_t b) { return (b + 255) & ~(size_t)255; }
 
 // Fewest keys of a piece. Waves with keys of their own (calls of at most 16 rows a sequence) read a
 // piece in 128-key steps and join it themselves: one token of 16 heads over 4000 keys, whole call,
-// 27.2 us with 256 and 26.0 us with 128.
+// 27.2 us with 256 and 26.0 us with 128. In fp32, 4 streams of 3 tokens and 16 heads over 1024 keys take
+// 63 us with 64 and 83 with 128. Elsewhere 256: 2 streams of 128 heads over 2000 keys 49 us, 64 with 512,
+// 44 with 128, which costs where pieces are many (32 heads of 8 streams over 4096 keys 34 and 35).
 constexpr int kMinChunk = 256, kMinChunkOwn = 128, kMinChunkF32 = 64;
 
 struct Plan {
@@ -25,15 +27,21 @@ Plan plan_of(const LatentJob &job, int fmt) {
     const AttnJob &a = job.a;
     Plan p{};
     const int64_t rows = a.max_q > 0 ? (int64_t)a.max_q * a.group : 1;
-    p.kind.tiles = rows > 64 && !f32 ? 2 : 1;
+    int64_t span = a.max_kv;
+    if (a.mask == kMaskCausal && a.window && (int64_t)a.window + a.max_q < span) span = (int64_t)a.window + a.max_q;
+    span += 31;
+    // 32 rows a wave, which halves the reads of LDS, once their tiles in pieces of 256 keys of max_kv fill the
+    // CUs; else 16, two workgroups a CU (128 heads of one token, 32 and 16 rows a wave: 8 streams of 4096
+    // keys 55 and 46 us, 64 of them 131 and 138; 1 x 128 over 16384 570 and 609). Waves over keys instead of
+    // rows where rows are few: 64 streams of 32 heads over 4096 e4m3 keys 74 us with two pairs, 100 with four
+    // waves of rows; 16 heads take 3 us more by four waves with keys of their own than by pairs over 4096
+    // bf16 keys of 8 streams, for remainders that pairs do not have the registers for.
+    p.kind.tiles = rows > 64 && !f32 && (double)((rows + 127) / 128) * a.c.n_seq * ((span + kMinChunk - 1) / kMinChunk) >= kWorkgroups / 2 ? 2 : 1;
     p.kind.row_waves = rows > (f32 ? 16 : 32) ? 4 : rows > 16 ? 2 : 1;
     p.kind.exact = p.kind.row_waves == 1 && job.w && !f32;
     p.sp.tile_rows = 16 * p.kind.tiles * p.kind.row_waves;
     p.sp.rows = (int)(rows < p.sp.tile_rows ? rows : p.sp.tile_rows);
     p.sp.tiles = (int)((rows + p.sp.tile_rows - 1) / p.sp.tile_rows);
-    int64_t span = a.max_kv;
-    if (a.mask == kMaskCausal && a.window && (int64_t)a.window + a.max_q < span) span = (int64_t)a.window + a.max_q;
-    span += 31;
     const int64_t tiles = (int64_t)a.c.n_seq * p.sp.tiles;
     const int64_t places = kWorkgroups / 2 * (f32 ? 1 : workgroups_per_cu(fmt, a.c.d, p.kind.tiles, p.kind.row_waves));
     const int64_t want = 2 * tiles > places ? 2 * places : places;

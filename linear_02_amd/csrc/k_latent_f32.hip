@@ -10,7 +10,8 @@
 //   over 16 rows   four waves of 16 rows share 16 keys at a time, in two buffers
 //   16 rows        every wave with keys of its own, joined in LDS at the end
 // Bound by the fp32 matrix instructions (2 x 16 x 16 x 4 operations in 32 cycles of a SIMD)
-// where rows are many, by latency where they are few.
+// where rows are many, by latency where they are few (4 streams of 3 tokens, 16 heads and a latent of 256 over
+// up to 1024 keys 19 us).
 #include "wl_latent.h"
 
 namespace wl {

@@ -16,6 +16,13 @@
 //              150 us with one buffer, 132 us so)
 // Rows of e4m3 stay codes in LDS and are widened as operands: half the LDS traffic, and
 // the vector units have the time beside the products.
+// Few rows are bound by memory (64 streams of 16 heads over up to 16384 e4m3 keys 105 us, 4.3 TB/s), many
+// by what one wave per SIMD waits for between its products (32 streams of 128 heads over up to 8192 bf16
+// keys 76 us, 620 TFLOP/s).
+// With more than 16 rows, queries in the latent space and weights are bf16, each off by at most 2^-9 and
+// summed as rounded: the error of the output is 0.0027 of its norm, where its own rounding is 0.0017;
+// remainders, as 16 rows have them, would double the products. Outputs of pieces are bf16, so that they
+// are half the bytes written and read again.
 #include "wl_latent.h"
 
 namespace wl {
