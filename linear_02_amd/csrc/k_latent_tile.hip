@@ -342,15 +342,15 @@ __global__ __launch_bounds__(256, workgroups_per_cu(F, L, kNT, kRW)) void latent
                         for (int b = 0; b < kBlocks; b += 4) {
                             f32x4 v[4];
                             asm volatile("s_nop 15\n\ts_nop 3\n\t"
-                                         "ds_write_b128 %8, %4\n\tds_write_b128 %8, %5 offset:1024\n\tds_write_b128 %8, %6 offset:2048\n\tds_write_b128 %8, %7 offset:3072\n\t"
-                                         "ds_read_b128 %0, %8\n\tds_read_b128 %1, %8 offset:1024\n\tds_read_b128 %2, %8 offset:2048\n\tds_read_b128 %3, %8 offset:3072\n\t"
+                                         "ds_write_b128 %8, %4\n\tds_write_b128 %8, %5 offset:1024\n\tds_write_b128 %8, %6 offset:2048\n\tds_write_b128 %8, %7 offset:3*1024\n\t"
+                                         "ds_read_b128 %0, %8\n\tds_read_b128 %1, %8 offset:1024\n\tds_read_b128 %2, %8 offset:2048\n\tds_read_b128 %3, %8 offset:3*1024\n\t"
                                          "s_waitcnt lgkmcnt(0)"
                                          : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3])
                                          : "a"(o[t][b]), "a"(o[t][b + 1]), "a"(o[t][b + 2]), "a"(o[t][b + 3]), "v"(by) : "memory");
 #pragma unroll
                             for (int i = 0; i < 4; ++i) v[i] *= up;
-                            asm volatile("ds_write_b128 %8, %4\n\tds_write_b128 %8, %5 offset:1024\n\tds_write_b128 %8, %6 offset:2048\n\tds_write_b128 %8, %7 offset:3072\n\t"
-                                         "ds_read_b128 %0, %8\n\tds_read_b128 %1, %8 offset:1024\n\tds_read_b128 %2, %8 offset:2048\n\tds_read_b128 %3, %8 offset:3072\n\t"
+                            asm volatile("ds_write_b128 %8, %4\n\tds_write_b128 %8, %5 offset:1024\n\tds_write_b128 %8, %6 offset:2048\n\tds_write_b128 %8, %7 offset:3*1024\n\t"
+                                         "ds_read_b128 %0, %8\n\tds_read_b128 %1, %8 offset:1024\n\tds_read_b128 %2, %8 offset:2048\n\tds_read_b128 %3, %8 offset:3*1024\n\t"
                                          "s_waitcnt lgkmcnt(0)"
                                          : "=&a"(o[t][b]), "=&a"(o[t][b + 1]), "=&a"(o[t][b + 2]), "=&a"(o[t][b + 3])
                                          : "v"(v[0]), "v"(v[1]), "v"(v[2]), "v"(v[3]), "v"(by) : "memory");
