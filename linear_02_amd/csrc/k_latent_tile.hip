@@ -61,7 +61,10 @@ __global__ __launch_bounds__(256, workgroups_per_cu(F, L, kNT, kRW)) void latent
     constexpr int kPatch = kTiles + kScales;                  // a patch of every wave, for the rescaling
     constexpr int kUsed = kPatch + (kNT == 2 ? 16384 : 0), kMain = kUsed > kJoin ? kUsed : kJoin;
     __shared__ __align__(16) char lds_all[kMain + 512];
+    // Behind the tiles, the waves' key ranges and what their join exchanges. These lie apart: a workgroup without keys
+    // meets no barrier between the reads of the one and the first write of the other.
     int (*range)[4] = reinterpret_cast<int (*)[4]>(lds_all + kMain);                   // [lo, hi][wave]
+    float *shared = reinterpret_cast<float *>(lds_all + kMain + 256);                  // [wave][row]
     constexpr bool kAccum = workgroups_per_cu(F, L, kNT, kRW) == 1;   // one wave per SIMD
     const AttnJob &a = x.a;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -534,29 +537,29 @@ __global__ __launch_bounds__(256, workgroups_per_cu(F, L, kNT, kRW)) void latent
         f32x4 *mine = reinterpret_cast<f32x4 *>(lds_all);
 #pragma unroll
         for (int c = 0; c < kBlocks; ++c) mine[(wave * kBlocks + c) * 64 + lane] = o[0][c];
-        if (g == 0) reinterpret_cast<float *>(range)[wave * 16 + n] = m[0];
+        if (g == 0) shared[wave * 16 + n] = m[0];
         __syncthreads();
         float ms[kKW], top = kNegInf;
 #pragma unroll
         for (int w = 0; w < kKW; ++w) {
-            ms[w] = reinterpret_cast<const float *>(range)[(w * kRW + rw) * 16 + n];
+            ms[w] = shared[(w * kRW + rw) * 16 + n];
             top = fmaxf(top, ms[w]);
         }
         __syncthreads();
-        if (g == 0) reinterpret_cast<float *>(range)[wave * 16 + n] = l[0];
+        if (g == 0) shared[wave * 16 + n] = l[0];
         __syncthreads();
         float sum = 0.0f, up[kKW];
 #pragma unroll
         for (int w = 0; w < kKW; ++w) {
             up[w] = ms[w] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(ms[w] - top);
-            sum += up[w] * reinterpret_cast<const float *>(range)[(w * kRW + rw) * 16 + n];
+            sum += up[w] * shared[(w * kRW + rw) * 16 + n];
         }
         __syncthreads();
-        if (lane == 0) reinterpret_cast<uint32_t *>(range)[wave] = again;
+        if (lane == 0) reinterpret_cast<uint32_t *>(shared)[wave] = again;
         __syncthreads();
         again = 0;
 #pragma unroll
-        for (int w = 0; w < kKW; ++w) again |= reinterpret_cast<const uint32_t *>(range)[w * kRW + rw];
+        for (int w = 0; w < kKW; ++w) again |= reinterpret_cast<const uint32_t *>(shared)[w * kRW + rw];
         again = __builtin_amdgcn_readfirstlane(again);
         const int r = r0 + n;
         if (r < rows && !(again >> n & 1u)) {
