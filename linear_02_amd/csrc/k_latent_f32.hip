@@ -33,7 +33,10 @@ __global__ __launch_bounds__(256, 1) void latent_f32_kernel(CoreArgs x) {
     constexpr int kTiles = kKW * kBuffers * T::kBytes, kJoin = kKW > 1 ? 4 * kGroups * 4096 : 0;
     constexpr int kMain = kTiles > kJoin ? kTiles : kJoin;
     __shared__ __align__(16) char lds_all[kMain + 512];
+    // The waves' key ranges and what their join exchanges lie apart: a workgroup without keys meets no barrier between
+    // the reads of the one and the first write of the other.
     int (*range)[4] = reinterpret_cast<int (*)[4]>(lds_all + kMain);   // [lo, hi][wave]
+    float *shared = reinterpret_cast<float *>(lds_all + kMain + 256);  // [wave][row]
     const AttnJob &a = x.a;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4, rw = wave % kRW, kw = wave / kRW;
@@ -193,7 +196,6 @@ __global__ __launch_bounds__(256, 1) void latent_f32_kernel(CoreArgs x) {
     odd |= odd >> 32;
     odd |= odd >> 16;
     uint32_t again = (uint32_t)odd & 0xFFFFu;
-    float *shared = reinterpret_cast<float *>(range);
     float up[kKW] = {1.0f}, sum = l, top = m;
     if (kKW > 1) {
         f32x4 *mine = reinterpret_cast<f32x4 *>(lds_all);
@@ -215,11 +217,11 @@ __global__ __launch_bounds__(256, 1) void latent_f32_kernel(CoreArgs x) {
             sum += up[w] * shared[w * 16 + n];
         }
         __syncthreads();
-        if (lane == 0) reinterpret_cast<uint32_t *>(range)[wave] = again;
+        if (lane == 0) reinterpret_cast<uint32_t *>(shared)[wave] = again;
         __syncthreads();
         again = 0;
 #pragma unroll
-        for (int w = 0; w < kKW; ++w) again |= reinterpret_cast<const uint32_t *>(range)[w];
+        for (int w = 0; w < kKW; ++w) again |= reinterpret_cast<const uint32_t *>(shared)[w];
         again = __builtin_amdgcn_readfirstlane(again);
     }
     if (on && !(again >> n & 1u)) {

@@ -8,10 +8,10 @@ import random
 import pytest
 import torch
 
-from tests.test_gpu_latent import BF, E4M3, Batch, wl  # noqa: F401
+from tests.test_gpu_latent import BF, E4M3, F32, Batch, wl  # noqa: F401
 
 pytestmark = pytest.mark.gpu
-FORMATS = [BF, E4M3]
+FORMATS = [BF, E4M3, F32]
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
