@@ -619,7 +619,8 @@ wl_status wl_latent_attention(const wl_latent_attention_args *a, void *ws, size_
  *          gives -1 as the new one
  *   path   or NULL: the rows, within the sequence, whose keys stay: 0, then those of
  *          the tokens that stay, then -1
- *   n_out  [n_seq] tokens in out (those that stay + 1; 0 without rows)
+ *   n_out  [n_seq] tokens in out (those that stay + 1; 0 without rows). With T == 0 it is
+ *          all that is written, and may be NULL like the other pointers
  *   len    or NULL: [n_seq], n_out is added (the keys that stay, as `past` of wl_batch_plan)
  * Sums are fp64. dtype: of target and draft. vocab >= 1.
  *   ws   ws_bytes >= wl_verify_drafts_workspace_bytes(a), its first WL_SYNC_BYTES not

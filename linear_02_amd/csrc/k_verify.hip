@@ -546,6 +546,11 @@ __global__ __launch_bounds__(64) void follow_kernel(VerifyJob a, const int32_t *
     }
 }
 
+__global__ __launch_bounds__(kThreads) void no_rows_kernel(VerifyJob a) {
+    const int64_t s = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (s < a.n_seq) a.n_out[s] = 0;
+}
+
 // A row's chunks: a wave each, as many as kWavesWanted of all rows give, with 64 groups of 16 bytes or
 // more each (32 chains of 5 rows of 131072 logits, with the draft's, replayed from a graph: 66 us so, 88
 // with 4096 waves).
@@ -589,6 +594,11 @@ hipError_t run(const VerifyJob &a, void *ws, hipStream_t s) {
 }
 
 }  // namespace
+
+hipError_t launch_verify_no_rows(const VerifyJob &a, hipStream_t s) {
+    hipLaunchKernelGGL(no_rows_kernel, dim3((unsigned)(((int64_t)a.n_seq + kThreads - 1) / kThreads)), dim3(kThreads), 0, s, a);
+    return hipGetLastError();
+}
 
 int64_t verify_workgroups(const VerifyJob &a, bool f32) {
     const VerifyJob j = divided(a, f32);

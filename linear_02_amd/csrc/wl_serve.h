@@ -33,6 +33,8 @@ struct VerifyJob {
 int64_t verify_workgroups(const VerifyJob &a, bool f32);
 size_t verify_scratch(const VerifyJob &a, bool f32);
 hipError_t launch_verify(VerifyJob a, bool f32, void *ws, hipStream_t stream);
+// Of a batch without rows: n_out of its sequences.
+hipError_t launch_verify_no_rows(const VerifyJob &a, hipStream_t stream);
 
 // ---- the latent cache (k_latent_rows.hip) ----------------------------------------
 constexpr int kMaxLatent = 512, kMaxRot = 64;

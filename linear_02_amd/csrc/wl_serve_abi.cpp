@@ -212,7 +212,16 @@ wl_status check_verify(const wl_verify_args *a, wl::VerifyJob *job) {
     if (a->kind != WL_VERIFY_LOGITS && a->kind != WL_VERIFY_PROBABILITIES)
         return fail(WL_ERR_INVALID_ARG, "kind=%d is neither WL_VERIFY_LOGITS nor WL_VERIFY_PROBABILITIES", a->kind);
     if (a->draft && a->parent) return fail(WL_ERR_INVALID_ARG, "parent (trees) does not go with a draft's distribution");
-    if (a->T == 0) return WL_OK;
+    if (a->T == 0) {   // n_out is all there is to write
+        if (!a->n_out) return WL_OK;
+        if ((st = need(a->n_out, 4, "n_out")) != WL_OK) return st;
+        const size_t n = a->n_seq;
+        if ((st = check_out(array(a->n_out, n, "n_out"), {array(a->q_start, n + 1, "q_start"), array(a->temperature, n, "temperature"),
+                                                         array(a->len, n, "len")})) != WL_OK)
+            return st;
+        job->n_out = a->n_out, job->n_seq = a->n_seq;
+        return WL_OK;
+    }
     if (a->T > kMaxTokens) return fail(WL_ERR_UNSUPPORTED, "T=%d exceeds %d", a->T, kMaxTokens);
     if ((st = need(a->target, 16, "target")) != WL_OK || (st = need(a->token, 4, "token")) != WL_OK ||
         (st = need(a->q_start, 4, "q_start")) != WL_OK || (st = need(a->u, 8, "u")) != WL_OK ||
@@ -374,7 +383,7 @@ wl_status wl_verify_drafts(const wl_verify_args *a, void *ws, size_t ws_bytes, v
     wl::VerifyJob j{};
     wl_status st = check_verify(a, &j);
     if (st != WL_OK) return st;
-    if (a->T == 0) return ok();
+    if (a->T == 0) return a->n_out ? launched(wl::launch_verify_no_rows(j, static_cast<hipStream_t>(hip_stream)), "verification") : ok();
     const bool f32 = a->dtype == WL_DTYPE_F32;
     const size_t scratch = wl::verify_scratch(j, f32), T = a->T, n = a->n_seq;
     void *at;

@@ -193,3 +193,11 @@ def test_steps_take_them(wl):
     for op in (8, 15, 21):
         ops[0].op = op
         assert wl.lib.wl_step_ops_workspace_bytes(ops, 1) == 0
+
+
+@pytest.mark.parametrize("bad", [dict(n_out=P[6] + 2), dict(n_out=P[3] + 4), dict(n_out=P[5]), dict(n_out=P[9] - 4)])
+def test_verify_of_no_rows_refuses(wl, bad):
+    """With T == 0 the counts are still written."""
+    a = struct(wl.VerifyArgs, **(VERIFY | dict(T=0) | bad))
+    assert wl.lib.wl_verify_drafts(ctypes.byref(a), None, 0, None) == 1 and b"n_out" in wl.lib.wl_last_error()
+    assert wl.lib.wl_verify_drafts_workspace_bytes(ctypes.byref(a)) == 0
