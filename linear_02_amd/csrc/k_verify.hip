@@ -386,10 +386,13 @@ __device__ __forceinline__ double wave_scan(double v) {
 
 // The first token at which the running sum of weights passes u times the whole, -1 if
 // there is none: `mine` is the lane's chunk's part. By a whole workgroup.
+// A scan over lanes adds up every lane's sum in another order, so that a running sum may fall, or pass the
+// border at a lane without weight, by a rounding. Only lanes with weight are asked, and the first that passes
+// is taken, whatever the ones behind it say.
 template <class E, bool kLogits>
 __device__ __forceinline__ int draw(const VerifyJob &a, const Weights<E, kLogits> &w, double mine, float u) {
     __shared__ double part[kWaves];
-    __shared__ int found, lasts[kWaves];
+    __shared__ int found[kWaves], lasts[kWaves];
     constexpr int G = Row<E, kLogits>::G;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const double run = wave_scan(mine), whole = __shfl(run, 63), aim = (double)u * whole;
@@ -398,7 +401,6 @@ __device__ __forceinline__ int draw(const VerifyJob &a, const Weights<E, kLogits
     const int chunk = past ? __ffsll((unsigned long long)past) - 1 : 63 - __clzll((long long)some);
     double base = __shfl(run, chunk > 0 ? chunk - 1 : 0);
     if (chunk == 0) base = 0.0;
-    if (threadIdx.x == 0) found = -1;
     const int shift = w.p.shift, first = chunk * a.groups, last = min(first + a.groups, (a.vocab + shift + G - 1) / G);
     int late = -1;   // the last token with any weight
     for (int g0 = first; g0 < last; g0 += kThreads) {
@@ -424,22 +426,21 @@ __device__ __forceinline__ int draw(const VerifyJob &a, const Weights<E, kLogits
             if (i == wave) before = all;
             all += part[i];
         }
-        // The first thread whose sum passes: those behind it see that the one before them has.
-        const double up = before + in_wave, ahead = before + (in_wave - sum);
-        const uint64_t hits = __ballot(up > aim);
-        const bool mine_first = hits && (__ffsll((unsigned long long)hits) - 1) == lane && !(before > aim);
-        if (mine_first) {
-            double r = ahead;
-            int x = -1;
+        const uint64_t hits = __ballot(sum > 0.0 && before + in_wave > aim);
+        int x = -1;
+        if (hits && lane == __ffsll((unsigned long long)hits) - 1) {
+            double r = before + (in_wave - sum);
 #pragma unroll
             for (int k = 0; k < G; ++k) {
                 r += v[k];
-                if (x < 0 && r > aim) x = g * G - shift + k;
+                if (x < 0 && v[k] > 0.0 && r > aim) x = g * G - shift + k;
             }
-            found = x >= 0 ? x : late;   // `late` is in this group: its sum is not 0
+            if (x < 0) x = late;   // in this group, which has weight
         }
+        if (lane == (hits ? __ffsll((unsigned long long)hits) - 1 : 0)) found[wave] = x;
         __syncthreads();
-        if (found >= 0) return found;
+        for (int i = 0; i < kWaves; ++i)
+            if (found[i] >= 0) return found[i];
         base = all;
     }
     // The chunk's sum passed, in another order of adding, but not the running one.
