@@ -28,7 +28,7 @@ struct Span {
     int lo, hi;
 };
 __device__ __forceinline__ Span span_of(const AttnJob &a, const Seq &q) {
-    const int lo = a.mask == kMaskCausal && a.window ? min(max(q.ctx - a.window + 1, 0), q.kv) : 0;
+    const int lo = a.mask == kMaskCausal && a.window && q.ctx >= a.window ? min(q.ctx - a.window + 1, q.kv) : 0;
     return {lo, a.mask == kMaskCausal ? max(min(q.ctx + q.rows, q.kv), 0) : q.kv};
 }
 

@@ -44,7 +44,7 @@ __device__ __forceinline__ Sees sees(const AttnJob &a, const Seq &q, int i) {
         v.hi = q.kv;
     } else if (a.mask == kMaskCausal) {
         v.hi = max(min(at + 1, q.kv), 0);
-        if (a.window) v.lo = max(at - a.window + 1, 0);
+        if (a.window) v.lo = at >= a.window ? at - a.window + 1 : 0;   // no difference that passes 32 bits
     } else {
         const int t = q.q0 + i;
         v.hi = max(min(q.ctx, q.kv), 0);
