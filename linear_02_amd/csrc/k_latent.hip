@@ -83,10 +83,10 @@ Places places_of(const LatentJob &a, const Plan &p, bool f32) {
     };
     if (a.w) {
         w.q = take(rows * (L + a.rot) * (f32 || p.kind.exact ? 4 : 2));
-        if (!split) w.o = take(rows * L * (f32 ? 4 : 2));
+        if (!split) w.o = take(rows * L * 4);
     }
     if (split) {
-        w.part = take((size_t)p.items * p.sp.rows * L * (f32 ? 4 : 2));
+        w.part = take((size_t)p.items * p.sp.rows * L * 4);
         w.ml = take((size_t)p.items * p.sp.rows * 8);
     }
     w.bytes = at;
@@ -176,7 +176,7 @@ hipError_t launch_latent(const LatentJob &job, int fmt, bool f32, int form, void
     const Plan p = plan_of(a, fmt);
     const Places w = places_of(a, p, f32);
     char *at = static_cast<char *>(ws);
-    CoreArgs x{a.a, p.sp, a.rot};
+    CoreArgs x{a.a, p.sp, a.rot, a.w || f32};
     hipError_t e;
     if (a.w) {
         if (f32)

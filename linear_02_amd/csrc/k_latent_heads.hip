@@ -129,20 +129,13 @@ __device__ __forceinline__ int sequence_of(const AttnJob &a, const Pieces &p, in
     return lo;
 }
 
-__device__ __forceinline__ float element_of(const u32x4 *v, int e, uint16_t) {
-    const uint32_t w = v[0][e >> 1];
-    return e & 1 ? __uint_as_float(w & 0xFFFF0000u) : bf16_f(w & 0xFFFFu);
-}
-__device__ __forceinline__ float element_of(const u32x4 *v, int e, float) { return __uint_as_float(v[e >> 2][e & 3]); }
-
 // The joined output of row t, head h, the same in the 16 lanes of a group: lane n of it gets
 // elements 128 c + 8 n .. + 7. false: the row has no result. A wave joins four rows at once with
 // several pieces of each on their way: a row after the other, a piece after the other, it waited
 // for each (31 us instead of 18 for 32 tokens of 128 heads with about 8 pieces each).
-// E: of the pieces' outputs.
-template <class E, int L>
+template <int L>
 __device__ __forceinline__ bool joined(const CoreArgs &x, const Pieces &pieces, int t, int h, float (&o)[L / 128][8]) {
-    constexpr int kParts = L / 128, kWords = sizeof(E) / 2, kAtOnce = 4 / kWords;
+    constexpr int kParts = L / 128, kAtOnce = 2;
     const AttnJob &a = x.a;
     const Split &sp = x.sp;
     const int lane = threadIdx.x & 63, n = lane & 15;
@@ -154,14 +147,11 @@ __device__ __forceinline__ bool joined(const CoreArgs &x, const Pieces &pieces, 
     const Seq q = seq_of(a, s);
     const bool on = t < a.T && t >= q.q0 && t < q.q0 + q.rows;
     if (sp.n_split == 1) {
-        const E *p = static_cast<const E *>(a.o) + (on ? (size_t)t * a.ldo + (size_t)h * L : 0) + 8 * n;
+        const float *p = static_cast<const float *>(a.o) + (on ? (size_t)t * a.ldo + (size_t)h * L : 0) + 8 * n;
 #pragma unroll
         for (int c = 0; c < kParts; ++c) {
-            u32x4 v[kWords];
-#pragma unroll
-            for (int i = 0; i < kWords; ++i) v[i] = ldg(reinterpret_cast<const u32x4 *>(p + 128 * c) + i);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) o[c][e] = element_of(v, e, E());
+            query4(p + 128 * c, o[c]);
+            query4(p + 128 * c + 4, o[c] + 4);
         }
         return on;
     }
@@ -191,16 +181,16 @@ __device__ __forceinline__ bool joined(const CoreArgs &x, const Pieces &pieces, 
     for (int y = 16; y < 64; y <<= 1) most = max(most, __shfl_xor(most, y));
     most = __builtin_amdgcn_readfirstlane(most);
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    const E *part = reinterpret_cast<const E *>(sp.part) + at * L + 8 * n;
+    const float *part = sp.part + at * L + 8 * n;
     for (int p0 = 0; p0 < most; p0 += kAtOnce) {
-        u32x4 raw[kAtOnce][kParts][kWords];
+        f32x4 raw[kAtOnce][kParts][2];
 #pragma unroll
         for (int j = 0; j < kAtOnce; ++j)
 #pragma unroll
             for (int c = 0; c < kParts; ++c)
 #pragma unroll
-                for (int i = 0; i < kWords; ++i)   // behind a row's pieces: its first one again, which weighs nothing then
-                    raw[j][c][i] = ldg(reinterpret_cast<const u32x4 *>(part + (p0 + j < have ? p0 + j : 0) * next * L + 128 * c) + i);
+                for (int i = 0; i < 2; ++i)   // behind a row's pieces: its first one again, which weighs nothing then
+                    raw[j][c][i] = ldg(reinterpret_cast<const f32x4 *>(part + (p0 + j < have ? p0 + j : 0) * next * L + 128 * c) + i);
         const int turn = p0 >> 4;
         const float mine = turn == 0 ? up[0] : turn == 1 ? up[1] : turn == 2 ? up[2] : up[3];
 #pragma unroll
@@ -209,10 +199,7 @@ __device__ __forceinline__ bool joined(const CoreArgs &x, const Pieces &pieces, 
 #pragma unroll
             for (int c = 0; c < kParts; ++c)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float y = element_of(raw[j][c], e, E());
-                    o[c][e] = w == 0.0f ? o[c][e] : __builtin_fmaf(y, w, o[c][e]);
-                }
+                for (int e = 0; e < 8; ++e) o[c][e] = w == 0.0f ? o[c][e] : __builtin_fmaf(raw[j][c][e >> 2][e & 3], w, o[c][e]);
         }
     }
     return on;
@@ -225,7 +212,7 @@ __global__ __launch_bounds__(256) void join_kernel(CoreArgs x) {
     const int64_t w = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
     const int t = (int)(w / x.a.n_q), h = (int)(w - (int64_t)t * x.a.n_q);
     float o[L / 128][8];
-    if (!joined<E, L>(x, pieces_of_call(x.a, x.sp), t, h, o)) return;
+    if (!joined<L>(x, pieces_of_call(x.a, x.sp), t, h, o)) return;
     E *to = static_cast<E *>(x.a.o) + (size_t)t * x.a.ldo + (size_t)h * L + 8 * n;
 #pragma unroll
     for (int c = 0; c < L / 128; ++c) {
@@ -265,7 +252,7 @@ __global__ __launch_bounds__(256) void up_kernel(UpArgs u) {
     {
         const int i = 4 * wave + g;
         float o[L / 128][8];
-        const bool on = joined<uint16_t, L>(u.x, pieces_of_call(u.x.a, u.x.sp), t0 + i, h, o);
+        const bool on = joined<L>(u.x, pieces_of_call(u.x.a, u.x.sp), t0 + i, h, o);
         if (n == 0) live[i] = on;
 #pragma unroll
         for (int c = 0; c < L / 128; ++c) {
@@ -360,7 +347,7 @@ __global__ __launch_bounds__(256) void up_f32_kernel(UpArgs u) {
     const int t0 = 16 * block, per = V / u.splits, v_from = split * per, v_to = v_from + per;
     {
         float o[L / 128][8];
-        const bool on = joined<float, L>(u.x, pieces_of_call(u.x.a, u.x.sp), t0 + i, h, o);
+        const bool on = joined<L>(u.x, pieces_of_call(u.x.a, u.x.sp), t0 + i, h, o);
         if (n == 0) live[i] = on;
 #pragma unroll
         for (int c = 0; c < L / 128; ++c) {

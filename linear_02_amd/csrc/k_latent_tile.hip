@@ -21,8 +21,7 @@
 // keys 76 us, 620 TFLOP/s).
 // With more than 16 rows, queries in the latent space and weights are bf16, each off by at most 2^-9 and
 // summed as rounded: the error of the output is 0.0027 of its norm, where its own rounding is 0.0017;
-// remainders, as 16 rows have them, would double the products. Outputs of pieces are bf16, so that they
-// are half the bytes written and read again.
+// remainders, as 16 rows have them, would double the products.
 #include "wl_latent.h"
 
 namespace wl {
@@ -471,16 +470,19 @@ __global__ __launch_bounds__(256, workgroups_per_cu(F, L, kNT, kRW)) void latent
     }
 
     keep_all();
-    // Outputs, of a piece of the keys or of all: normalised, in bf16, with the reference and the sum
-    // of a piece.
+    // Outputs, of a piece of the keys or of all: normalised, with the reference and the sum of a piece.
     const CoreArgs y = argument_again<CoreArgs>();
     const AttnJob &b = y.a;
     const Split &sp = y.sp;
     const Seq qq = seq_of(b, s);
-    auto place = [&](int r) {
+    const bool wide = sp.n_split > 1 || y.wide;
+    auto put = [&](int r, int at, const float *v) {
         const int i = r / b.group;
-        return sp.n_split > 1 ? reinterpret_cast<uint16_t *>(sp.part) + part_row(b, sp, work.part, 0, tile, r) * L
-                              : static_cast<uint16_t *>(b.o) + (size_t)(qq.q0 + i) * b.ldo + (size_t)(r - i * b.group) * L;
+        const size_t in_o = (size_t)(qq.q0 + i) * b.ldo + (size_t)(r - i * b.group) * L;
+        if (wide)
+            put4((sp.n_split > 1 ? sp.part + part_row(b, sp, work.part, 0, tile, r) * L : static_cast<float *>(b.o) + in_o) + at, v);
+        else
+            put4(static_cast<uint16_t *>(b.o) + in_o + at, v);
     };
     auto put_stat = [&](int r, float mm, float ll) {
         if (sp.n_split > 1) sp.ml[part_row(b, sp, work.part, 0, tile, r)] = make_float2(mm, ll);
@@ -495,8 +497,8 @@ __global__ __launch_bounds__(256, workgroups_per_cu(F, L, kNT, kRW)) void latent
             if (8 * lane < L) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) acc[e] = ll == 0.0f ? 0.0f : acc[e] / ll;
-                put4(place(rr) + 8 * lane, acc);
-                put4(place(rr) + 8 * lane + 4, acc + 4);
+                put(rr, 8 * lane, acc);
+                put(rr, 8 * lane + 4, acc + 4);
             }
             if (lane == 0) put_stat(rr, mm, ll);
         }
@@ -518,11 +520,10 @@ __global__ __launch_bounds__(256, workgroups_per_cu(F, L, kNT, kRW)) void latent
             const uint32_t again = odd_rows(t);
             if (r < rows && !(again >> n & 1u)) {
                 const float inv = l[t] == 0.0f ? 0.0f : 1.0f / l[t];
-                uint16_t *to = place(r) + 4 * g;
 #pragma unroll
                 for (int c = 0; c < kBlocks; ++c) {
                     const float v[4] = {o[t][c].x * inv, o[t][c].y * inv, o[t][c].z * inv, o[t][c].w * inv};
-                    put4(to + 16 * c, v);
+                    put(r, 16 * c + 4 * g, v);
                 }
                 if (g == 0) put_stat(r, m[t], l[t]);
             }
@@ -564,7 +565,6 @@ __global__ __launch_bounds__(256, workgroups_per_cu(F, L, kNT, kRW)) void latent
         const int r = r0 + n;
         if (r < rows && !(again >> n & 1u)) {
             const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-            uint16_t *to = place(r) + 4 * g;
 #pragma unroll
             for (int c = 0; c < kOwn; ++c) {
                 const int at = kw * kOwn + c;
@@ -572,7 +572,7 @@ __global__ __launch_bounds__(256, workgroups_per_cu(F, L, kNT, kRW)) void latent
 #pragma unroll
                 for (int w = 0; w < kKW; ++w) v += mine[((w * kRW + rw) * kBlocks + at) * 64 + lane] * up[w];
                 const float e[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
-                put4(to + 16 * at, e);
+                put(r, 16 * at + 4 * g, e);
             }
             if (kw == 0 && g == 0) put_stat(r, top, sum);
         }

@@ -10,11 +10,14 @@
 namespace wl {
 
 // a: latent queries [T][heads][latent + rot] over one key/value head whose rows are
-// the values too, first `latent` elements of them; a.o: [T][heads][latent].
+// the values too, first `latent` elements of them; a.o: [T][heads][latent], and the outputs of
+// pieces of divided keys. What something is formed from yet (pieces to be joined, outputs that W^V
+// is applied to) is fp32.
 struct CoreArgs {
     AttnJob a;
     Split sp;
     int rot;
+    int wide;   // a.o is fp32
 };
 
 // Which kernel: tiles of 16 rows per wave, waves over rows (the others over keys), whether

@@ -19,7 +19,7 @@ FAR = 1 << 17   # keys, far above all lengths here
 
 
 def tile_rows(wl, b, max_q, max_kv, window=0, mask="causal"):  # noqa: F811
-    """Rows of a tile of the call's partial outputs, from its workspace: per piece and row one output and two fp32."""
+    """Rows of a tile of the call's partial outputs, from its workspace: per piece and row one output and two numbers, all fp32."""
     kw = dict(window=window)
     if mask == "tree":
         kw["tree"] = torch.zeros(b.T, 1, dtype=torch.int32, device=b.q.device)
@@ -34,7 +34,7 @@ def tile_rows(wl, b, max_q, max_kv, window=0, mask="causal"):  # noqa: F811
         span = max_kv if mask == "tree" or not window else min(window + min(max_q, b.T), max_kv)
         pieces = min(-(-(span + 31) // 256), 64)
         for items in [min(tiles * pieces, want + tiles) for want in (256, 512, 1024)] if n_seq <= 64 else range(tiles, tiles * 64 + 1, tiles):
-            if need == pad(items * kept * L * 2) + pad(items * kept * 8):
+            if need == pad(items * kept * L * 4) + pad(items * kept * 8):
                 return t
     return 0
 
