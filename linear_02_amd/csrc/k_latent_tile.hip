@@ -5,9 +5,8 @@
 // its first `latent` elements serve both products. Queries, scores, weights and outputs
 // stay in registers from the first key to the last; at a latent of 512 that is 128 of
 // outputs and 72 of queries for every 16 rows a wave has.
-//   many rows  four waves of 32 rows share a tile of keys (one wave per SIMD, which
-//              then has 512 registers): an operand read from LDS serves two products
-//   64 rows    four waves of 16 rows, two workgroups per CU
+//   many rows  four waves of 16 rows share a tile of keys, two workgroups per CU where
+//              registers allow, so that one's softmax falls into the other's products
 //   32 rows    two pairs of waves, each pair with keys of its own
 //   16 rows    every wave with keys of its own, which it fetches for itself and waits
 //              for alone; joined in LDS at the end. Where two buffers of latents fit, the
@@ -19,9 +18,8 @@
 // Few rows are bound by memory (64 streams of 16 heads over up to 16384 e4m3 keys 105 us, 4.3 TB/s), many
 // by what one wave per SIMD waits for between its products (32 streams of 128 heads over up to 8192 bf16
 // keys 76 us, 620 TFLOP/s).
-// With more than 16 rows, queries in the latent space and weights are bf16, each off by at most 2^-9 and
-// summed as rounded: the error of the output is 0.0027 of its norm, where its own rounding is 0.0017;
-// remainders, as 16 rows have them, would double the products.
+// Weights are multiplied as a bf16 head and its remainder (2^-16 off): rounded to bf16, with queries rounded
+// too, outputs were off by up to 1.6 times what their own rounding costs.
 #include "wl_latent.h"
 
 namespace wl {
@@ -43,10 +41,10 @@ struct Tile {
     static __device__ __forceinline__ int turn(int r) { return ((r & 7) << 1 | ((r >> 3 ^ r >> 4) & 1)) & (kLatent - 1); }
 };
 
-// kNT: tiles of 16 rows per wave. kRW x kKW waves: over rows, and over keys. kExact: queries'
-// and weights' remainders are multiplied too.
-template <int F, int L, int kNT, int kRW, int kKW, bool kExact>
-__global__ __launch_bounds__(256, workgroups_per_cu(F, L, kNT, kRW)) void latent_kernel(CoreArgs x) {
+// kRW x kKW waves: over tiles of 16 rows, and over keys. kExact: queries are fp32, and their remainders are
+// multiplied too. Those of weights always are.
+template <int F, int L, int kRW, int kKW, bool kExact>
+__global__ __launch_bounds__(256, workgroups_per_cu(F, L, kRW)) void latent_kernel(CoreArgs x) {
     typedef Tile<F, L> T;
     constexpr bool kCodes = T::kCodes;
     constexpr int kSteps = L / 32, kBlocks = L / 16;
@@ -57,14 +55,13 @@ __global__ __launch_bounds__(256, workgroups_per_cu(F, L, kNT, kRW)) void latent
     constexpr int kAhead = 4;                                 // operands read ahead of the products
     constexpr int kScales = kCodes ? kKW * 2 * 32 * 4 : 0;    // [group][step % 2][32]
     constexpr int kTiles = kKW * kGroup, kJoin = kKW > 1 ? 4 * kBlocks * 1024 : 0;
-    constexpr int kPatch = kTiles + kScales;                  // a patch of every wave, for the rescaling
-    constexpr int kUsed = kPatch + (kNT == 2 ? 16384 : 0), kMain = kUsed > kJoin ? kUsed : kJoin;
+    constexpr int kMain = kTiles + kScales > kJoin ? kTiles + kScales : kJoin;
     __shared__ __align__(16) char lds_all[kMain + 512];
     // Behind the tiles, the waves' key ranges and what their join exchanges. These lie apart: a workgroup without keys
     // meets no barrier between the reads of the one and the first write of the other.
     int (*range)[4] = reinterpret_cast<int (*)[4]>(lds_all + kMain);                   // [lo, hi][wave]
     float *shared = reinterpret_cast<float *>(lds_all + kMain + 256);                  // [wave][row]
-    constexpr bool kAccum = workgroups_per_cu(F, L, kNT, kRW) == 1;   // one wave per SIMD
+    constexpr bool kAccum = workgroups_per_cu(F, L, kRW) == 1;   // one wave per SIMD
     const AttnJob &a = x.a;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
@@ -74,34 +71,27 @@ __global__ __launch_bounds__(256, workgroups_per_cu(F, L, kNT, kRW)) void latent
     const int tile = work.tile, s = work.s;
     if (s < 0) return;
     const int rows = q.rows * a.group, R = x.rot;
-    constexpr int kRows = 16 * kNT * kRW;
-    if (tile * kRows >= rows) return;
-    auto rows_of = [](int tile, int) {
-        const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % kRW;
-        return WaveRows{tile * kRows + 16 * kNT * w, kNT};
-    };
-    const int r0 = rows_of(tile, rows).first;
+    if (tile * 16 * kRW >= rows) return;
+    auto first_row = [](int tile) { return 16 * (tile * kRW + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % kRW); };
+    const int r0 = first_row(tile);
 
     // Outputs live in accumulation registers then. Said where paths meet and where
     // anything but a product writes them: else the compiler moves all of them there and back in every step.
     auto keep = [](f32x4 &v) {
         if (kAccum) asm("" : "+a"(v));
     };
-    u32x4 qf[kNT][kSteps + 2], ql[kExact ? kNT : 1][kExact ? kSteps : 1];
-    f32x4 o[kNT][kBlocks];
-    float m[kNT], l[kNT];
+    u32x4 qf[kSteps + 2], ql[kExact ? kSteps : 1];
+    f32x4 o[kBlocks];
+    float m = kNegInf, l = 0.0f;
     auto keep_all = [&]() {
 #pragma unroll
-        for (int t = 0; t < kNT; ++t)
-#pragma unroll
-            for (int b = 0; b < kBlocks; ++b) keep(o[t][b]);
+        for (int b = 0; b < kBlocks; ++b) keep(o[b]);
     };
     int lo = 0x7FFFFFFF, hi = 0, flo = 0, fhi = 0x7FFFFFFF;   // some row sees [lo, hi), every row [flo, fhi)
     const uint32_t sign = a.scale2 < 0.0f ? 0x80008000u : 0u;   // a negative scale goes into the queries
     const float scale2 = fmaxf(fabsf(a.scale2), 0x1p-126f);   // not 0: -inf marks an unseen key
-#pragma unroll
-    for (int t = 0; t < kNT; ++t) {
-        const int r = r0 + 16 * t + n, i = r / a.group;
+    {
+        const int r = r0 + n, i = r / a.group;
         const bool on = r < rows;
         const int64_t at = (int64_t)(q.q0 + (on ? i : 0)) * a.ldq + (int64_t)(on ? r - i * a.group : 0) * (L + R) + 8 * g;
         // Of a row that there is not, and of elements behind the head's: read somewhere, and masked.
@@ -110,7 +100,7 @@ __global__ __launch_bounds__(256, workgroups_per_cu(F, L, kNT, kRW)) void latent
         if (!kExact) {
             const uint16_t *qp = static_cast<const uint16_t *>(a.q) + at;
 #pragma unroll
-            for (int k = 0; k < kSteps + 2; ++k) qf[t][k] = (ldg(reinterpret_cast<const u32x4 *>(qp + place(k))) ^ sign) & kept(k);
+            for (int k = 0; k < kSteps + 2; ++k) qf[k] = (ldg(reinterpret_cast<const u32x4 *>(qp + place(k))) ^ sign) & kept(k);
         } else {
             // fp32 queries: a bf16 head and a bf16 remainder; the rotated part is exact in bf16.
             const float *qp = static_cast<const float *>(a.q) + at;
@@ -126,23 +116,22 @@ __global__ __launch_bounds__(256, workgroups_per_cu(F, L, kNT, kRW)) void latent
                     h[e] = pack2(v0, v1);
                     w[e] = pack2(v0 - bf16_f(h[e] & 0xFFFFu), v1 - __uint_as_float(h[e] & 0xFFFF0000u));
                 }
-                qf[t][k] = (u32x4{h[0], h[1], h[2], h[3]} ^ sign) & kept(k);
-                if (k < kSteps) ql[t][k] = (u32x4{w[0], w[1], w[2], w[3]} ^ sign) & kept(k);
+                qf[k] = (u32x4{h[0], h[1], h[2], h[3]} ^ sign) & kept(k);
+                if (k < kSteps) ql[k] = (u32x4{w[0], w[1], w[2], w[3]} ^ sign) & kept(k);
             }
         }
         const Sees see = sees(a, q, i);
         if (on) {   // an unused column is never the reason to mask
-            lo = min(lo, see.tree ? min(see.lo, max(q.ctx, 0)) : see.lo);
-            hi = max(hi, see.tree ? q.kv : see.hi);
-            flo = max(flo, see.lo);
-            fhi = min(fhi, see.hi);
+            lo = see.tree ? min(see.lo, max(q.ctx, 0)) : see.lo;
+            hi = see.tree ? q.kv : see.hi;
+            flo = see.lo;
+            fhi = see.hi;
         }
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b) {
-            o[t][b] = f32x4{0, 0, 0, 0};
-            keep(o[t][b]);
+            o[b] = f32x4{0, 0, 0, 0};
+            keep(o[b]);
         }
-        m[t] = kNegInf, l[t] = 0.0f;
     }
 #pragma unroll
     for (int y = 1; y < 16; y <<= 1) {
@@ -236,11 +225,7 @@ __global__ __launch_bounds__(256, workgroups_per_cu(F, L, kNT, kRW)) void latent
             int rb = keys_in + n * 128 + ((g ^ (n >> 1 & 7)) << 4);
             asm volatile("" : "+v"(kb), "+v"(rb));
             const uint32_t second = R > 32 ? 0xFFFFFFFFu : 0u;
-            f32x4 sc[kNT][2];
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int t = 0; t < kNT; ++t) sc[t][b] = f32x4{0, 0, 0, 0};
+            f32x4 sc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
             // Key operand i: rows 16 (i % 2) .., elements 32 (i / 2) .. of them, the rotated ones last. Both halves in
             // turn, so that a product does not wait for the one before it.
             constexpr int kEach = kKeysFirst ? kSteps : kSteps + 2, kAll = 2 * kEach;
@@ -268,9 +253,9 @@ __global__ __launch_bounds__(256, workgroups_per_cu(F, L, kNT, kRW)) void latent
                 fetch_next();
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
-                    rotated[b] = mfma16(kf[b], qf[0][kSteps], f32x4{0, 0, 0, 0});
-                    rotated[b] = mfma16(kf[2 + b] & second, qf[0][kSteps + 1], rotated[b]);
-                    if (!kCodes) sc[0][b] = rotated[b];
+                    rotated[b] = mfma16(kf[b], qf[kSteps], f32x4{0, 0, 0, 0});
+                    rotated[b] = mfma16(kf[2 + b] & second, qf[kSteps + 1], rotated[b]);
+                    if (!kCodes) sc[b] = rotated[b];
                 }
             }
             __builtin_amdgcn_s_setprio(1);
@@ -282,16 +267,9 @@ __global__ __launch_bounds__(256, workgroups_per_cu(F, L, kNT, kRW)) void latent
                 const int b = i & 1, k = i >> 1;
                 u32x4 here = kCodes && k < kSteps ? widen8<kFmtE4m3>(kf[i % kAhead].x, kf[i % kAhead].y) : kf[i % kAhead];
                 if (k > kSteps) here &= second;   // what lies in the place of elements that there are not may be anything
-                if (kCodes && k == kSteps) {
-                    const f32x4 ks = *reinterpret_cast<const f32x4 *>(scales + 16 * b + 4 * g);
-#pragma unroll
-                    for (int t = 0; t < kNT; ++t) sc[t][b] *= ks;
-                }
-#pragma unroll
-                for (int t = 0; t < kNT; ++t) {
-                    sc[t][b] = mfma16(here, qf[t][k], sc[t][b]);
-                    if (kExact && k < kSteps) sc[t][b] = mfma16(here, ql[t][k < kSteps ? k : 0], sc[t][b]);
-                }
+                if (kCodes && k == kSteps) sc[b] *= *reinterpret_cast<const f32x4 *>(scales + 16 * b + 4 * g);
+                sc[b] = mfma16(here, qf[k], sc[b]);
+                if (kExact && k < kSteps) sc[b] = mfma16(here, ql[k < kSteps ? k : 0], sc[b]);
                 if (i + kAhead < kAll) kf[i % kAhead] = operand(i + kAhead);
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -301,96 +279,54 @@ __global__ __launch_bounds__(256, workgroups_per_cu(F, L, kNT, kRW)) void latent
                 for (int b = 0; b < 2; ++b) {
                     const f32x4 ks = *reinterpret_cast<const f32x4 *>(scales + 16 * b + 4 * g);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) sc[0][b][e] = __builtin_fmaf(sc[0][b][e], ks[e], rotated[b][e]);
+                    for (int e = 0; e < 4; ++e) sc[b][e] = __builtin_fmaf(sc[b][e], ks[e], rotated[b][e]);
                 }
             }
-            u32x4 ph[kNT], pl[kNT];
             const bool all = j0 >= flo && j0 + 32 <= min(fhi, k1) && valid == 0xFFFFFFFFu;
+            float v[8];
 #pragma unroll
-            for (int t = 0; t < kNT; ++t) {
-                float v[8];
+            for (int e = 0; e < 8; ++e) v[e] = sc[e >> 2][e & 3];
+            if (__builtin_expect(!all, 0)) {
+                const CoreArgs again = argument_again<CoreArgs>();
+                const Seq qq = seq_of(again.a, work.s);
+                const int r = first_row(work.tile) + (threadIdx.x & 15);
+                const uint32_t mine = (visible32(again.a, qq, sees(again.a, qq, r / again.a.group), j0) & valid & bits(0, k1 - j0)) >> (4 * g);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = sc[t][e >> 2][e & 3];
-                if (__builtin_expect(!all, 0)) {
-                    const CoreArgs again = argument_again<CoreArgs>();
-                    const Seq qq = seq_of(again.a, work.s);
-                    const int r = rows_of(work.tile, 0).first + 16 * t + (threadIdx.x & 15);
-                    const uint32_t mine = (visible32(again.a, qq, sees(again.a, qq, r / again.a.group), j0) & valid & bits(0, k1 - j0)) >> (4 * g);
+                for (int e = 0; e < 8; ++e) v[e] = mine & (1u << (16 * (e >> 2) + (e & 3))) ? v[e] : kNegInf;
+            }
+            float top = v[0];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] = mine & (1u << (16 * (e >> 2) + (e & 3))) ? v[e] : kNegInf;
-                }
-                float top = v[0];
+            for (int e = 1; e < 8; ++e) top = fmaxf(top, v[e]);
+            top = groups_max(top);
+            top = top == kNegInf ? top : top * scale2;
+            if (__builtin_expect(__any(top > m + 8.0f), 0)) {
+                // The reference moves only when a score passes it by 2^8: sums stay in range.
+                const float now = fmaxf(m, top), up = now == m ? 1.0f : __builtin_amdgcn_exp2f(m - now);
+                m = now;
+                l *= up;
 #pragma unroll
-                for (int e = 1; e < 8; ++e) top = fmaxf(top, v[e]);
-                top = groups_max(top);
-                top = top == kNegInf ? top : top * scale2;
-                if (__builtin_expect(__any(top > m[t] + 8.0f), 0)) {
-                    // The reference moves only when a score passes it by 2^8: sums stay in range.
-                    const float was = m[t], now = fmaxf(was, top), up = now == was ? 1.0f : __builtin_amdgcn_exp2f(was - now);
-                    m[t] = now;
-                    l[t] *= up;
-                    if (kNT == 1) {
-#pragma unroll
-                        for (int b = 0; b < kBlocks; ++b) {
-                            o[t][b] *= up;
-                            keep(o[t][b]);
-                        }
-                    } else if (__any(was != kNegInf)) {   // else they are 0 still
-                        // By way of LDS: told to multiply them, the compiler brings all outputs over into the
-                        // other registers at once, and spills queries for it, which every step then reads back
-                        // behind its loads on their way. The products that wrote them are a step behind.
-                        const uint32_t by = lds_byte(lds_all) + kPatch + wave * 4096 + lane * 16;
-#pragma unroll
-                        for (int b = 0; b < kBlocks; b += 4) {
-                            f32x4 v[4];
-                            asm volatile("s_nop 15\n\ts_nop 3\n\t"
-                                         "ds_write_b128 %8, %4\n\tds_write_b128 %8, %5 offset:1024\n\tds_write_b128 %8, %6 offset:2048\n\tds_write_b128 %8, %7 offset:3*1024\n\t"
-                                         "ds_read_b128 %0, %8\n\tds_read_b128 %1, %8 offset:1024\n\tds_read_b128 %2, %8 offset:2048\n\tds_read_b128 %3, %8 offset:3*1024\n\t"
-                                         "s_waitcnt lgkmcnt(0)"
-                                         : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3])
-                                         : "a"(o[t][b]), "a"(o[t][b + 1]), "a"(o[t][b + 2]), "a"(o[t][b + 3]), "v"(by) : "memory");
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) v[i] *= up;
-                            asm volatile("ds_write_b128 %8, %4\n\tds_write_b128 %8, %5 offset:1024\n\tds_write_b128 %8, %6 offset:2048\n\tds_write_b128 %8, %7 offset:3*1024\n\t"
-                                         "ds_read_b128 %0, %8\n\tds_read_b128 %1, %8 offset:1024\n\tds_read_b128 %2, %8 offset:2048\n\tds_read_b128 %3, %8 offset:3*1024\n\t"
-                                         "s_waitcnt lgkmcnt(0)"
-                                         : "=&a"(o[t][b]), "=&a"(o[t][b + 1]), "=&a"(o[t][b + 2]), "=&a"(o[t][b + 3])
-                                         : "v"(v[0]), "v"(v[1]), "v"(v[2]), "v"(v[3]), "v"(by) : "memory");
-                        }
-                    }
-                }
-                keep_all();
-                const float ref = m[t] == kNegInf ? 0.0f : m[t];
-                float p[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(v[e], scale2, -ref));
-                    if (kCodes || kExact) l[t] += p[e];
-                }
-                if (kCodes) {
-#pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        const f32x4 vs = *reinterpret_cast<const f32x4 *>(scales + 16 * b + 4 * g);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) p[4 * b + e] = p[4 * b + e] == 0.0f ? 0.0f : p[4 * b + e] * vs[e];
-                    }
-                }
-                ph[t] = u32x4{pack2(p[0], p[1]), pack2(p[2], p[3]), pack2(p[4], p[5]), pack2(p[6], p[7])};
-                if (kExact) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        w[e] = pack2(p[2 * e] - bf16_f(ph[t][e] & 0xFFFFu), p[2 * e + 1] - __uint_as_float(ph[t][e] & 0xFFFF0000u));
-                    pl[t] = u32x4{w[0], w[1], w[2], w[3]};
-                } else if (!kCodes) {
-                    // the sum of the weights as the product will use them
-                    constexpr uint32_t kOnes = 0x3F803F80u;
-                    l[t] = dot2(ph[t].x, kOnes, l[t]);
-                    l[t] = dot2(ph[t].y, kOnes, l[t]);
-                    l[t] = dot2(ph[t].z, kOnes, l[t]);
-                    l[t] = dot2(ph[t].w, kOnes, l[t]);
+                for (int b = 0; b < kBlocks; ++b) {
+                    o[b] *= up;
+                    keep(o[b]);
                 }
             }
+            keep_all();
+            const float ref = m == kNegInf ? 0.0f : m;
+            float p[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) l += p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(v[e], scale2, -ref));
+            if (kCodes) {
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const f32x4 vs = *reinterpret_cast<const f32x4 *>(scales + 16 * b + 4 * g);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) p[4 * b + e] = p[4 * b + e] == 0.0f ? 0.0f : p[4 * b + e] * vs[e];
+                }
+            }
+            const u32x4 ph = {pack2(p[0], p[1]), pack2(p[2], p[3]), pack2(p[4], p[5]), pack2(p[6], p[7])};
+            u32x4 pl;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) pl[e] = pack2(p[2 * e] - bf16_f(ph[e] & 0xFFFFu), p[2 * e + 1] - __uint_as_float(ph[e] & 0xFFFF0000u));
             __builtin_amdgcn_s_setprio(1);
             const int kv = kCodes ? key_c : key_v;
             int vb = in + kv * T::kRow + ((T::kCodes ? 0 : n >> 1 & 1) ^ T::turn(kv)) * 16 + 8 * (n & 1);
@@ -408,17 +344,14 @@ __global__ __launch_bounds__(256, workgroups_per_cu(F, L, kNT, kRW)) void latent
                     const u32x2 u = read_tr16(p), w = read_tr16(lds_all + (vb ^ ((c & 15) ^ 1) << 4) + (c >> 4) * 256 + 16 * T::kRow);
                     vf = u32x4{u.x, u.y, w.x, w.y};
                 }
-#pragma unroll
-                for (int t = 0; t < kNT; ++t) {
-                    o[t][b] = mfma16(vf, ph[t], o[t][b]);
-                    if (kExact) o[t][b] = mfma16(vf, pl[t], o[t][b]);
-                }
+                o[b] = mfma16(vf, ph, o[b]);
+                o[b] = mfma16(vf, pl, o[b]);
             }
             constexpr int kReads = kCodes ? 1 : 2;   // of an operand
             __builtin_amdgcn_sched_group_barrier(0x100, kReads * kAhead, 1);
 #pragma unroll
             for (int i = 0; i < kBlocks; ++i) {
-                __builtin_amdgcn_sched_group_barrier(0x008, kExact ? 2 * kNT : kNT, 1);
+                __builtin_amdgcn_sched_group_barrier(0x008, 2, 1);
                 if (i + kAhead < kBlocks) __builtin_amdgcn_sched_group_barrier(0x100, kReads, 1);
             }
             __builtin_amdgcn_s_setprio(0);
@@ -503,42 +436,33 @@ __global__ __launch_bounds__(256, workgroups_per_cu(F, L, kNT, kRW)) void latent
             if (lane == 0) put_stat(rr, mm, ll);
         }
     };
-    auto odd_rows = [&](int t) {
-        float check = l[t] * 0.0f;
+    l = groups_sum(l);
+    float check = l * 0.0f;
 #pragma unroll
-        for (int c = 0; c < kBlocks; ++c) check += o[t][c].x * 0.0f + o[t][c].y * 0.0f + o[t][c].z * 0.0f + o[t][c].w * 0.0f;
-        uint64_t odd = __ballot(r0 + 16 * t + n < rows && check != 0.0f);
-        odd |= odd >> 32;
-        odd |= odd >> 16;
-        return (uint32_t)odd & 0xFFFFu;
-    };
+    for (int c = 0; c < kBlocks; ++c) check += o[c].x * 0.0f + o[c].y * 0.0f + o[c].z * 0.0f + o[c].w * 0.0f;
+    const int r = r0 + n;
+    uint64_t odd = __ballot(r < rows && check != 0.0f);
+    odd |= odd >> 32;
+    odd |= odd >> 16;
+    uint32_t again = (uint32_t)odd & 0xFFFFu;
     if constexpr (kKW == 1) {
+        if (r < rows && !(again >> n & 1u)) {
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
-        for (int t = 0; t < kNT; ++t) {
-            const int r = r0 + 16 * t + n;
-            l[t] = groups_sum(l[t]);
-            const uint32_t again = odd_rows(t);
-            if (r < rows && !(again >> n & 1u)) {
-                const float inv = l[t] == 0.0f ? 0.0f : 1.0f / l[t];
-#pragma unroll
-                for (int c = 0; c < kBlocks; ++c) {
-                    const float v[4] = {o[t][c].x * inv, o[t][c].y * inv, o[t][c].z * inv, o[t][c].w * inv};
-                    put(r, 16 * c + 4 * g, v);
-                }
-                if (g == 0) put_stat(r, m[t], l[t]);
+            for (int c = 0; c < kBlocks; ++c) {
+                const float v[4] = {o[c].x * inv, o[c].y * inv, o[c].z * inv, o[c].w * inv};
+                put(r, 16 * c + 4 * g, v);
             }
-            redo(again, r0 + 16 * t);
+            if (g == 0) put_stat(r, m, l);
         }
+        redo(again, r0);
     } else {
         // The groups' outputs meet in LDS, each wave joins a part of the columns.
         constexpr int kOwn = kBlocks / kKW;
-        static_assert(kNT == 1, "waves over keys have one tile of rows");
-        l[0] = groups_sum(l[0]);
-        uint32_t again = odd_rows(0);
         f32x4 *mine = reinterpret_cast<f32x4 *>(lds_all);
 #pragma unroll
-        for (int c = 0; c < kBlocks; ++c) mine[(wave * kBlocks + c) * 64 + lane] = o[0][c];
-        if (g == 0) shared[wave * 16 + n] = m[0];
+        for (int c = 0; c < kBlocks; ++c) mine[(wave * kBlocks + c) * 64 + lane] = o[c];
+        if (g == 0) shared[wave * 16 + n] = m;
         __syncthreads();
         float ms[kKW], top = kNegInf;
 #pragma unroll
@@ -547,7 +471,7 @@ __global__ __launch_bounds__(256, workgroups_per_cu(F, L, kNT, kRW)) void latent
             top = fmaxf(top, ms[w]);
         }
         __syncthreads();
-        if (g == 0) shared[wave * 16 + n] = l[0];
+        if (g == 0) shared[wave * 16 + n] = l;
         __syncthreads();
         float sum = 0.0f, up[kKW];
 #pragma unroll
@@ -562,7 +486,6 @@ __global__ __launch_bounds__(256, workgroups_per_cu(F, L, kNT, kRW)) void latent
 #pragma unroll
         for (int w = 0; w < kKW; ++w) again |= reinterpret_cast<const uint32_t *>(shared)[w * kRW + rw];
         again = __builtin_amdgcn_readfirstlane(again);
-        const int r = r0 + n;
         if (r < rows && !(again >> n & 1u)) {
             const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
@@ -583,16 +506,14 @@ __global__ __launch_bounds__(256, workgroups_per_cu(F, L, kNT, kRW)) void latent
 template <int F, int L>
 void run(const CoreArgs &x, const CoreKind &k, unsigned blocks, hipStream_t s) {
     const dim3 g(blocks), b(256);
-    if (k.tiles == 2)
-        hipLaunchKernelGGL((latent_kernel<F, L, 2, 4, 1, false>), g, b, 0, s, x);
-    else if (k.row_waves == 4)
-        hipLaunchKernelGGL((latent_kernel<F, L, 1, 4, 1, false>), g, b, 0, s, x);
+    if (k.row_waves == 4)
+        hipLaunchKernelGGL((latent_kernel<F, L, 4, 1, false>), g, b, 0, s, x);
     else if (k.row_waves == 2)
-        hipLaunchKernelGGL((latent_kernel<F, L, 1, 2, 2, false>), g, b, 0, s, x);
+        hipLaunchKernelGGL((latent_kernel<F, L, 2, 2, false>), g, b, 0, s, x);
     else if (k.exact)
-        hipLaunchKernelGGL((latent_kernel<F, L, 1, 1, 4, true>), g, b, 0, s, x);
+        hipLaunchKernelGGL((latent_kernel<F, L, 1, 4, true>), g, b, 0, s, x);
     else
-        hipLaunchKernelGGL((latent_kernel<F, L, 1, 1, 4, false>), g, b, 0, s, x);
+        hipLaunchKernelGGL((latent_kernel<F, L, 1, 4, false>), g, b, 0, s, x);
 }
 
 template <int F>

@@ -20,16 +20,16 @@ struct CoreArgs {
     int wide;   // a.o is fp32
 };
 
-// Which kernel: tiles of 16 rows per wave, waves over rows (the others over keys), whether
-// queries are fp32 and multiplied with their remainders.
+// Which kernel: waves over tiles of 16 rows (the others over keys), whether queries are fp32
+// and multiplied with their remainders.
 struct CoreKind {
-    int tiles, row_waves;
+    int row_waves;
     bool exact;
 };
 // Workgroups of it that share a CU. Widened codes of a latent of 512 take more registers than
 // half a SIMD has.
-constexpr int workgroups_per_cu(int fmt, int latent, int tiles, int row_waves) {
-    return tiles == 1 && row_waves == 4 && !(fmt == kFmtE4m3 && latent == 512) ? 2 : 1;
+constexpr int workgroups_per_cu(int fmt, int latent, int row_waves) {
+    return row_waves == 4 && !(fmt == kFmtE4m3 && latent == 512) ? 2 : 1;
 }
 void launch_latent_tile(const CoreArgs &x, int fmt, const CoreKind &k, unsigned blocks, hipStream_t s);
 

@@ -1,9 +1,5 @@
-"""Latent attention by the kernel of 32 rows a wave, which calls of many (token, head) rows take, and by
-every kernel over keys whose scores rise along the sequence, against the definition in 64 bits.
-
-The kernel is chosen by T, max_q, n_seq and max_kv; a max_kv far above the lengths, as a recorded step has
-it, chooses it for few keys. Which one a call takes shows in its workspace, whose partial outputs are of
-whole tiles of rows."""
+"""Latent attention of many (token, head) rows, and by every kernel over keys whose scores rise along the
+sequence, against the definition in 64 bits. max_kv is far above the lengths, as a recorded step has it."""
 from __future__ import annotations
 
 import random
@@ -18,27 +14,6 @@ pytestmark = pytest.mark.gpu
 FAR = 1 << 17   # keys, far above all lengths here
 
 
-def tile_rows(wl, b, max_q, max_kv, window=0, mask="causal"):  # noqa: F811
-    """Rows of a tile of the call's partial outputs, from its workspace: per piece and row one output and two numbers, all fp32."""
-    kw = dict(window=window)
-    if mask == "tree":
-        kw["tree"] = torch.zeros(b.T, 1, dtype=torch.int32, device=b.q.device)
-    call = wl.latent_attention_call(b.q, b.cache, b.w, i32(b.starts), i32(b.lens), max_q, max_kv, b.scale, form="absorbed", **kw)
-    L, R, n_seq = b.cache.latent, b.cache.rot, len(b.lens)
-    pad = lambda n: -(-n // 256) * 256  # noqa: E731
-    queries = 0 if b.w is None else pad(b.T * b.H * (L + R) * 2)
-    need = wl.lib.wl_latent_attention_workspace_bytes(call.args) - wl.SYNC_BYTES - queries
-    rows = min(max_q, b.T) * b.H
-    for t in (64, 128):
-        tiles, kept = n_seq * -(-rows // t), min(rows, t)
-        span = max_kv if mask == "tree" or not window else min(window + min(max_q, b.T), max_kv)
-        pieces = min(-(-(span + 31) // 256), 64)
-        for items in [min(tiles * pieces, want + tiles) for want in (256, 512, 1024)] if n_seq <= 64 else range(tiles, tiles * 64 + 1, tiles):
-            if need == pad(items * kept * L * 4) + pad(items * kept * 8):
-                return t
-    return 0
-
-
 SHAPES = [(512, 64, 128, 128), (512, 32, 64, 96), (256, 64, 64, 64), (256, 32, 96, 32), (128, 64, 64, 64)]
 
 
@@ -48,8 +23,7 @@ def test_causal(wl, fmt, L, R, N, V):  # noqa: F811
     """Tiles that are full, that end inside a wave and that have one row; sequences of no rows and of few keys."""
     for k, (H, seqs) in enumerate(((120, [(70, 1), (0, 1), (300, 1)]), (43, [(500, 3), (0, 0), (31, 1), (5, 6)]), (12, [(0, 43), (90, 11)]))):
         b = Batch(wl, seqs, H, L, R, N, V, fmt, page=(16, 32, 64)[k], seed=L + k, gap=1, tail=2)
-        assert tile_rows(wl, b, max(b.rows), FAR) == 128
-        b.check(wl, f"{H} heads", max_kv=FAR, form="absorbed")
+            b.check(wl, f"{H} heads", max_kv=FAR, form="absorbed")
 
 
 @pytest.mark.parametrize("fmt", [BF, E4M3])
@@ -58,7 +32,6 @@ def test_causal(wl, fmt, L, R, N, V):  # noqa: F811
 def test_trees_windows_and_full(wl, fmt, L, window):  # noqa: F811
     b = Batch(wl, [(80, 9), (0, 40), (300, 1), (33, 24)], 11, L, 64, 64, 64, fmt, page=32, seed=3)
     tree, pos = b.trees()
-    assert tile_rows(wl, b, 40, FAR, window, "tree") == 128
     kw = dict(max_kv=FAR, form="absorbed")
     b.check(wl, "tree", tree=tree, q_pos=pos, window=window, **kw)
     b.check(wl, "tree without positions", tree=tree, window=window, **kw)
@@ -68,8 +41,7 @@ def test_trees_windows_and_full(wl, fmt, L, window):  # noqa: F811
 
 @pytest.mark.parametrize("fmt", [BF, E4M3])
 def test_causal_windows(wl, fmt):  # noqa: F811
-    """A window bounds the keys, so that it takes many sequences to come to this kernel: 64, and 70, where lanes
-    do not plan."""
+    """Of 64 sequences, and of 70, whose pieces lanes do not plan."""
     rng = random.Random(5)
     for n_seq, window in ((64, 40), (70, 17)):
         b = Batch(wl, [(rng.choice((0, 20, 150)), rng.choice((0, 1, 3, 7))) for _ in range(n_seq)], 64, 512, 64, 64, 64, fmt, page=32, seed=n_seq, tail=500)
@@ -80,7 +52,6 @@ def test_causal_windows(wl, fmt):  # noqa: F811
 @pytest.mark.parametrize("L", [256, 512])
 def test_without_weights(wl, fmt, L):  # noqa: F811
     b = Batch(wl, [(90, 3), (500, 1), (0, 5)], 30, L, 64, fmt=fmt, weights=False, seed=4, gap=1)
-    assert tile_rows(wl, b, 5, FAR) == 128
     b.check(wl, "latent", max_kv=FAR)
 
 
@@ -88,7 +59,6 @@ def test_without_weights(wl, fmt, L):  # noqa: F811
 def test_more_sequences_than_lanes(wl, fmt):  # noqa: F811
     rng = random.Random(8)
     b = Batch(wl, [(rng.randrange(0, 500), rng.choice((0, 1, 2))) for _ in range(66)], 40, 512, 64, 64, 64, fmt, seed=8, page=32)
-    assert tile_rows(wl, b, 2, 5000) == 128
     b.check(wl, "66 sequences", max_kv=5000, form="absorbed")
 
 
@@ -111,7 +81,6 @@ def test_missing_pages(wl, fmt, L):  # noqa: F811
     wide = torch.full((2, FAR // 16), -1, dtype=torch.int32, device=t.device)
     wide[:, :t.shape[1]] = t
     b.cache = wl.LatentCache(b.cache.rows, wide, L, 64, b.cache.scale)
-    assert tile_rows(wl, b, 2, FAR) == 128
     o = b.check(wl, "missing pages, far max_kv", max_kv=FAR, form="absorbed")
     assert (o[2] == 0).all()
 
@@ -124,7 +93,6 @@ def test_unseen_keys_have_no_influence(wl, fmt, L):  # noqa: F811
     b = Batch(wl, [(70, 4), (33, 1)], 40, L, 64, 64, 64, fmt, seed=11)
     tree = i32([[1], [3], [5], [9], [1]])     # tokens 1, 2 and 3 follow token 0
     kw = dict(tree=tree, window=20, max_kv=FAR, form="absorbed")
-    assert tile_rows(wl, b, 4, FAR, 20, "tree") == 128
     clean = b.check(wl, "clean", **kw)
     ref, slack = serve_ref.latent_attention(b.q, b.cache, b.w, i32(b.starts), i32(b.lens), b.scale, tree=tree, window=20)
     rows = b.cache.rows
@@ -147,7 +115,6 @@ def test_unseen_keys_have_no_influence(wl, fmt, L):  # noqa: F811
 def test_captured_and_replayed_over_changing_lengths(wl, fmt):  # noqa: F811
     b = Batch(wl, [(900, 2), (37, 1), (400, 3)], 48, fmt=fmt, page=32, seed=16, tail=3)
     starts, lens = i32(b.starts), i32(b.lens)
-    assert tile_rows(wl, b, 3, FAR) == 128
     call = wl.latent_attention_call(b.q, b.cache, b.w, starts, lens, 3, FAR, b.scale)
     g, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())

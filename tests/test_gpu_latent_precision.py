@@ -41,3 +41,21 @@ SHORT, LONG = [(30, 2), (9, 1)], [(3000, 2), (700, 1)]
 def test_few_rows(wl, fmt, L, R, N, V, seqs):  # noqa: F811
     """Up to 16 rows: queries, weights and outputs in the latent space keep fp32's precision, divided keys or not."""
     assert off(wl, batch(wl, 8, seqs, L, R, N, V, fmt, True)) <= ONE
+
+
+@pytest.mark.parametrize("fmt", [BF, E4M3])
+@pytest.mark.parametrize("L,R,N,V", SHAPES)
+@pytest.mark.parametrize("H", [14, 30, 64])
+@pytest.mark.parametrize("seqs", [[(30, 2), (9, 1)], [(300, 2), (200, 1)], [(3000, 2), (700, 1)]])
+def test_more_rows(wl, fmt, L, R, N, V, H, seqs):  # noqa: F811
+    """28, 60 and 128 rows: at most the queries are rounded beside the output."""
+    assert off(wl, batch(wl, H, seqs, L, R, N, V, fmt, True)) <= TWO
+
+
+@pytest.mark.parametrize("fmt", [BF, E4M3])
+@pytest.mark.parametrize("L", [128, 256, 512])
+@pytest.mark.parametrize("H", [8, 14, 64])
+def test_without_weights(wl, fmt, L, H):  # noqa: F811
+    """Queries are as given then, and outputs are rounded once."""
+    for seqs in (SHORT, LONG):
+        assert off(wl, batch(wl, H, seqs, L, 64, 64, 64, fmt, False), form="auto") <= ONE
