@@ -23,7 +23,7 @@ def test_causal(wl, fmt, L, R, N, V):  # noqa: F811
     """Tiles that are full, that end inside a wave and that have one row; sequences of no rows and of few keys."""
     for k, (H, seqs) in enumerate(((120, [(70, 1), (0, 1), (300, 1)]), (43, [(500, 3), (0, 0), (31, 1), (5, 6)]), (12, [(0, 43), (90, 11)]))):
         b = Batch(wl, seqs, H, L, R, N, V, fmt, page=(16, 32, 64)[k], seed=L + k, gap=1, tail=2)
-            b.check(wl, f"{H} heads", max_kv=FAR, form="absorbed")
+        b.check(wl, f"{H} heads", max_kv=FAR, form="absorbed")
 
 
 @pytest.mark.parametrize("fmt", [BF, E4M3])
