@@ -573,10 +573,10 @@ wl_status wl_latent_read(const wl_latent_read_args *a, void *hip_stream);
  *                             With w, a bf16 cache, nope and value both 64 or both
  *                             128 only (else WL_ERR_UNSUPPORTED)
  *         WL_LATENT_AUTO      the one estimated to take less time: expanded for prompts
- * Numerics in bf16: absorbed, q in the latent space is rounded to bf16 above 16 rows
- * (min(max_q, T) n_q) of a sequence; expanded, keys, values and the weights of the second
- * product are rounded to bf16. Sums and outputs in the latent space are fp32, weights of the
- * absorbed form too. dtype f32 is fp32 throughout.
+ * Numerics in bf16: sums are fp32. Absorbed, q and the outputs in the latent space are fp32
+ * too, multiplied, as the weights, in two parts of bf16 (over e4m3 rows q as fp16 times a power
+ * of two of the row's). Expanded, keys, values and weights are rounded to bf16. dtype f32 is
+ * fp32 throughout.
  *   ws   ws_bytes >= wl_latent_attention_workspace_bytes(a), as in wl_attention */
 enum { WL_LATENT_AUTO = 0, WL_LATENT_ABSORBED = 1, WL_LATENT_EXPANDED = 2 };
 typedef struct {

@@ -31,15 +31,14 @@ Plan plan_of(const LatentJob &job, int fmt) {
     if (a.mask == kMaskCausal && a.window && (int64_t)a.window + a.max_q < span) span = (int64_t)a.window + a.max_q;
     span += 31;
     // Waves over keys instead of rows where rows are few: 64 streams of 32 heads over 4096 e4m3 keys 74 us with
-    // two pairs, 100 with four waves of rows; 16 heads take 3 us more by four waves with keys of their own than
-    // by pairs over 4096 bf16 keys of 8 streams, for remainders that pairs do not have the registers for.
+    // two pairs, 100 with four waves of rows.
     p.kind.row_waves = rows > (f32 ? 16 : 32) ? 4 : rows > 16 ? 2 : 1;
-    p.kind.exact = p.kind.row_waves == 1 && job.w && !f32;
+    p.kind.exact = job.w && !f32;
     p.sp.tile_rows = 16 * p.kind.row_waves;
     p.sp.rows = (int)(rows < p.sp.tile_rows ? rows : p.sp.tile_rows);
     p.sp.tiles = (int)((rows + p.sp.tile_rows - 1) / p.sp.tile_rows);
     const int64_t tiles = (int64_t)a.c.n_seq * p.sp.tiles;
-    const int64_t places = kWorkgroups / 2 * (f32 ? 1 : workgroups_per_cu(fmt, a.c.d, p.kind.row_waves));
+    const int64_t places = kWorkgroups / 2 * (f32 ? 1 : workgroups_per_cu(fmt, a.c.d, p.kind.row_waves, p.kind.exact));
     const int64_t want = 2 * tiles > places ? 2 * places : places;
     int64_t chunk = (span * tiles + want - 1) / want;
     p.sp.least = f32 ? kMinChunkF32 : p.kind.row_waves == 1 ? kMinChunkOwn : kMinChunk;

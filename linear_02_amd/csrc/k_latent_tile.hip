@@ -18,8 +18,9 @@
 // Few rows are bound by memory (64 streams of 16 heads over up to 16384 e4m3 keys 105 us, 4.3 TB/s), many
 // by what one wave per SIMD waits for between its products (32 streams of 128 heads over up to 8192 bf16
 // keys 76 us, 620 TFLOP/s).
-// Weights are multiplied as a bf16 head and its remainder (2^-16 off): rounded to bf16, with queries rounded
-// too, outputs were off by up to 1.6 times what their own rounding costs.
+// Nothing is rounded to bf16 but the output: weights, and queries that the product into the latent space left in
+// fp32, are multiplied as a bf16 head and its remainder (2^-16 off), queries of codes as fp16 (2^-11). With
+// both rounded to bf16 outputs were off by 1.6 times what their own rounding costs, with queries alone 1.41.
 #include "wl_latent.h"
 
 namespace wl {
@@ -41,12 +42,13 @@ struct Tile {
     static __device__ __forceinline__ int turn(int r) { return ((r & 7) << 1 | ((r >> 3 ^ r >> 4) & 1)) & (kLatent - 1); }
 };
 
-// kRW x kKW waves: over tiles of 16 rows, and over keys. kExact: queries are fp32, and their remainders are
-// multiplied too. Those of weights always are.
+// kRW x kKW waves: over tiles of 16 rows, and over keys. kExact: queries are fp32. Over bf16 rows they
+// are multiplied as a bf16 head and its remainder; over codes, which fp16 holds too, as fp16 times a power of
+// two of the row's own, in one product. Weights are multiplied with their remainders.
 template <int F, int L, int kRW, int kKW, bool kExact>
-__global__ __launch_bounds__(256, workgroups_per_cu(F, L, kRW)) void latent_kernel(CoreArgs x) {
+__global__ __launch_bounds__(256, workgroups_per_cu(F, L, kRW, kExact)) void latent_kernel(CoreArgs x) {
     typedef Tile<F, L> T;
-    constexpr bool kCodes = T::kCodes;
+    constexpr bool kCodes = T::kCodes, kHalf = kExact && kCodes, kSplit = kExact && !kCodes;
     constexpr int kSteps = L / 32, kBlocks = L / 16;
     // Waves with keys of their own: two buffers of latents and one of keys, where LDS has room.
     constexpr bool kKeysFirst = kKW == 4 && T::kKeys <= 16384;
@@ -61,7 +63,7 @@ __global__ __launch_bounds__(256, workgroups_per_cu(F, L, kRW)) void latent_kern
     // meets no barrier between the reads of the one and the first write of the other.
     int (*range)[4] = reinterpret_cast<int (*)[4]>(lds_all + kMain);                   // [lo, hi][wave]
     float *shared = reinterpret_cast<float *>(lds_all + kMain + 256);                  // [wave][row]
-    constexpr bool kAccum = workgroups_per_cu(F, L, kRW) == 1;   // one wave per SIMD
+    constexpr bool kAccum = workgroups_per_cu(F, L, kRW, kExact) == 1;   // one wave per SIMD
     const AttnJob &a = x.a;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
@@ -80,7 +82,8 @@ __global__ __launch_bounds__(256, workgroups_per_cu(F, L, kRW)) void latent_kern
     auto keep = [](f32x4 &v) {
         if (kAccum) asm("" : "+a"(v));
     };
-    u32x4 qf[kSteps + 2], ql[kExact ? kSteps : 1];
+    u32x4 qf[kSteps + 2], ql[kSplit ? kSteps : 1];
+    float unscale = 1.0f;   // of fp16 queries
     f32x4 o[kBlocks];
     float m = kNegInf, l = 0.0f;
     auto keep_all = [&]() {
@@ -102,22 +105,36 @@ __global__ __launch_bounds__(256, workgroups_per_cu(F, L, kRW)) void latent_kern
 #pragma unroll
             for (int k = 0; k < kSteps + 2; ++k) qf[k] = (ldg(reinterpret_cast<const u32x4 *>(qp + place(k))) ^ sign) & kept(k);
         } else {
-            // fp32 queries: a bf16 head and a bf16 remainder; the rotated part is exact in bf16.
+            // fp32 queries; the rotated part is exact in bf16.
             const float *qp = static_cast<const float *>(a.q) + at;
+            f32x4 v[kSteps + 2][2];
+#pragma unroll
+            for (int k = 0; k < kSteps + 2; ++k)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) v[k][e] = ldg(reinterpret_cast<const f32x4 *>(qp + place(k) + 4 * e));
+            float scale = 1.0f;
+            if (kHalf) {
+                // The largest becomes 2^14 to 2^15: what lies 2^28 below it has fp16's full precision yet. An infinity stays
+                // one, and the row is done again.
+                float most = 0.0f;
+#pragma unroll
+                for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(v[k][e >> 2][e & 3]));
+                const int up = 14 - min(max((int)(__float_as_uint(groups_max(most)) >> 23) - 127, -86), 114);
+                scale = __uint_as_float((uint32_t)(127 + up) << 23), unscale = __uint_as_float((uint32_t)(127 - up) << 23);
+            }
 #pragma unroll
             for (int k = 0; k < kSteps + 2; ++k) {
-                f32x4 v[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) v[e] = ldg(reinterpret_cast<const f32x4 *>(qp + place(k) + 4 * e));
                 uint32_t h[4], w[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float v0 = v[e >> 1][2 * (e & 1)], v1 = v[e >> 1][2 * (e & 1) + 1];
-                    h[e] = pack2(v0, v1);
+                    const float v0 = v[k][e >> 1][2 * (e & 1)], v1 = v[k][e >> 1][2 * (e & 1) + 1];
+                    h[e] = kHalf && k < kSteps ? pack_half2(v0 * scale, v1 * scale) : pack2(v0, v1);
                     w[e] = pack2(v0 - bf16_f(h[e] & 0xFFFFu), v1 - __uint_as_float(h[e] & 0xFFFF0000u));
                 }
                 qf[k] = (u32x4{h[0], h[1], h[2], h[3]} ^ sign) & kept(k);
-                if (k < kSteps) ql[k] = (u32x4{w[0], w[1], w[2], w[3]} ^ sign) & kept(k);
+                if (kSplit && k < kSteps) ql[k] = (u32x4{w[0], w[1], w[2], w[3]} ^ sign) & kept(k);
             }
         }
         const Sees see = sees(a, q, i);
@@ -265,11 +282,12 @@ __global__ __launch_bounds__(256, workgroups_per_cu(F, L, kRW)) void latent_kern
 #pragma unroll
             for (int i = 0; i < kAll; ++i) {
                 const int b = i & 1, k = i >> 1;
-                u32x4 here = kCodes && k < kSteps ? widen8<kFmtE4m3>(kf[i % kAhead].x, kf[i % kAhead].y) : kf[i % kAhead];
+                u32x4 here = kf[i % kAhead];
+                if (kCodes && k < kSteps) here = kHalf ? widen_half8(here.x, here.y) : widen8<kFmtE4m3>(here.x, here.y);
                 if (k > kSteps) here &= second;   // what lies in the place of elements that there are not may be anything
-                if (kCodes && k == kSteps) sc[b] *= *reinterpret_cast<const f32x4 *>(scales + 16 * b + 4 * g);
-                sc[b] = mfma16(here, qf[k], sc[b]);
-                if (kExact && k < kSteps) sc[b] = mfma16(here, ql[k < kSteps ? k : 0], sc[b]);
+                if (kCodes && k == kSteps) sc[b] = sc[b] * unscale * *reinterpret_cast<const f32x4 *>(scales + 16 * b + 4 * g);
+                sc[b] = kHalf && k < kSteps ? mfma16_half(here, qf[k], sc[b]) : mfma16(here, qf[k], sc[b]);
+                if (kSplit && k < kSteps) sc[b] = mfma16(here, ql[k < kSteps ? k : 0], sc[b]);
                 if (i + kAhead < kAll) kf[i % kAhead] = operand(i + kAhead);
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -279,7 +297,7 @@ __global__ __launch_bounds__(256, workgroups_per_cu(F, L, kRW)) void latent_kern
                 for (int b = 0; b < 2; ++b) {
                     const f32x4 ks = *reinterpret_cast<const f32x4 *>(scales + 16 * b + 4 * g);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) sc[b][e] = __builtin_fmaf(sc[b][e], ks[e], rotated[b][e]);
+                    for (int e = 0; e < 4; ++e) sc[b][e] = __builtin_fmaf(sc[b][e] * unscale, ks[e], rotated[b][e]);
                 }
             }
             const bool all = j0 >= flo && j0 + 32 <= min(fhi, k1) && valid == 0xFFFFFFFFu;
@@ -503,17 +521,23 @@ __global__ __launch_bounds__(256, workgroups_per_cu(F, L, kRW)) void latent_kern
     }
 }
 
+template <int F, int L, int kRW, int kKW>
+void launch(const CoreArgs &x, const CoreKind &k, unsigned blocks, hipStream_t s) {
+    const dim3 g(blocks), b(256);
+    if (k.exact)
+        hipLaunchKernelGGL((latent_kernel<F, L, kRW, kKW, true>), g, b, 0, s, x);
+    else
+        hipLaunchKernelGGL((latent_kernel<F, L, kRW, kKW, false>), g, b, 0, s, x);
+}
+
 template <int F, int L>
 void run(const CoreArgs &x, const CoreKind &k, unsigned blocks, hipStream_t s) {
-    const dim3 g(blocks), b(256);
     if (k.row_waves == 4)
-        hipLaunchKernelGGL((latent_kernel<F, L, 4, 1, false>), g, b, 0, s, x);
+        launch<F, L, 4, 1>(x, k, blocks, s);
     else if (k.row_waves == 2)
-        hipLaunchKernelGGL((latent_kernel<F, L, 2, 2, false>), g, b, 0, s, x);
-    else if (k.exact)
-        hipLaunchKernelGGL((latent_kernel<F, L, 1, 4, true>), g, b, 0, s, x);
+        launch<F, L, 2, 2>(x, k, blocks, s);
     else
-        hipLaunchKernelGGL((latent_kernel<F, L, 1, 4, false>), g, b, 0, s, x);
+        launch<F, L, 1, 4>(x, k, blocks, s);
 }
 
 template <int F>

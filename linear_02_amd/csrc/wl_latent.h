@@ -20,16 +20,16 @@ struct CoreArgs {
     int wide;   // a.o is fp32
 };
 
-// Which kernel: waves over tiles of 16 rows (the others over keys), whether queries are fp32
-// and multiplied with their remainders.
+// Which kernel: waves over tiles of 16 rows (the others over keys), whether queries are fp32, as
+// the product into the latent space leaves them (else bf16, as given).
 struct CoreKind {
     int row_waves;
     bool exact;
 };
-// Workgroups of it that share a CU. Widened codes of a latent of 512 take more registers than
-// half a SIMD has.
-constexpr int workgroups_per_cu(int fmt, int latent, int row_waves) {
-    return row_waves == 4 && !(fmt == kFmtE4m3 && latent == 512) ? 2 : 1;
+// Workgroups of it that share a CU. At a latent of 512 widened codes, and remainders of queries, take more
+// registers than half a SIMD has.
+constexpr int workgroups_per_cu(int fmt, int latent, int row_waves, bool exact) {
+    return row_waves == 4 && (latent < 512 || (fmt == kFmtBf16 && !exact)) ? 2 : 1;
 }
 void launch_latent_tile(const CoreArgs &x, int fmt, const CoreKind &k, unsigned blocks, hipStream_t s);
 

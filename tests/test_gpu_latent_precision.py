@@ -48,8 +48,21 @@ def test_few_rows(wl, fmt, L, R, N, V, seqs):  # noqa: F811
 @pytest.mark.parametrize("H", [14, 30, 64])
 @pytest.mark.parametrize("seqs", [[(30, 2), (9, 1)], [(300, 2), (200, 1)], [(3000, 2), (700, 1)]])
 def test_more_rows(wl, fmt, L, R, N, V, H, seqs):  # noqa: F811
-    """28, 60 and 128 rows: at most the queries are rounded beside the output."""
-    assert off(wl, batch(wl, H, seqs, L, R, N, V, fmt, True)) <= TWO
+    """28, 60 and 128 rows: the output's is the only rounding to bf16."""
+    assert off(wl, batch(wl, H, seqs, L, R, N, V, fmt, True)) <= ONE
+
+
+@pytest.mark.parametrize("fmt", [BF, E4M3])
+@pytest.mark.parametrize("L,H", [(512, 8), (512, 64), (256, 14), (128, 64)])
+@pytest.mark.parametrize("small", [2.0 ** -30, 1.0])
+def test_queries_of_any_size(wl, fmt, L, H, small):  # noqa: F811
+    """Queries of rows far apart in size, and some elements of each far below its largest."""
+    b = batch(wl, H, [(200, 2), (50, 1)], L, 64, 64, 64, fmt, True)
+    q = b.q.view(b.T, H, -1)
+    q[:, ::2, :64] *= small
+    q[:, :, 5] *= 2.0 ** -12
+    q[0, 1, :64] = 0
+    assert off(wl, b) <= ONE
 
 
 @pytest.mark.parametrize("fmt", [BF, E4M3])
