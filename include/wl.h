@@ -575,7 +575,8 @@ wl_status wl_latent_read(const wl_latent_read_args *a, void *hip_stream);
  *         WL_LATENT_AUTO      the one estimated to take less time: expanded for prompts
  * Numerics in bf16: sums are fp32. Absorbed, q and the outputs in the latent space are fp32
  * too, multiplied, as the weights, in two parts of bf16 (over e4m3 rows q as fp16 times a power
- * of two of the row's). Expanded, keys, values and weights are rounded to bf16. dtype f32 is
+ * of two of the row's). Expanded, q, keys and values are fp16 times a power of two of every row's
+ * own, weights fp16. So outputs are off by little more than their rounding to bf16. dtype f32 is
  * fp32 throughout.
  *   ws   ws_bytes >= wl_latent_attention_workspace_bytes(a), as in wl_attention */
 enum { WL_LATENT_AUTO = 0, WL_LATENT_ABSORBED = 1, WL_LATENT_EXPANDED = 2 };

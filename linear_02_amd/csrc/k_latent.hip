@@ -95,6 +95,7 @@ struct Expanded {
     int heads;         // of a group
     int keys, blocks, tiles;
     size_t bytes;      // of the keys, and of the values
+    size_t all;        // with their scales
 };
 Expanded expanded_of(const LatentJob &job) {
     const AttnJob &a = job.a;
@@ -104,10 +105,11 @@ Expanded expanded_of(const LatentJob &job) {
     e.blocks = (int)((keys + 127) / 128);
     e.keys = 128 * e.blocks;
     e.tiles = (a.max_q + 127) / 128;
-    const size_t one = (size_t)a.c.n_seq * e.keys * job.nope * 2;
-    const size_t fit = one ? kExpandedBytes / (2 * one) : a.n_q;
+    const size_t rows = (size_t)a.c.n_seq * e.keys, one = rows * job.nope * 2;   // of a head
+    const size_t fit = one ? kExpandedBytes / (2 * one + 8 * rows) : a.n_q;
     e.heads = fit < 1 ? 1 : fit > (size_t)a.n_q ? a.n_q : (int)fit;
     e.bytes = pad(one * e.heads);
+    e.all = 2 * e.bytes + pad(8 * rows * e.heads);
     return e;
 }
 
@@ -125,7 +127,7 @@ bool expands(const LatentJob &job, int fmt, int form) {
     if (!latent_can_expand(job, fmt) || a.max_q < 128) return false;
     const Expanded e = expanded_of(job);
     // Never where the other form's workspace or launch would be beyond what calls may have.
-    if (2 * e.bytes > kExpandedBytes + 512 || (int64_t)a.c.n_seq * (e.blocks > e.tiles ? e.blocks : e.tiles) * e.heads >= 1 << 23) return false;
+    if (e.all > kExpandedBytes + 1024 || (int64_t)a.c.n_seq * (e.blocks > e.tiles ? e.blocks : e.tiles) * e.heads >= 1 << 23) return false;
     const double keys = e.keys, L = a.c.d, H = a.n_q;
     const double seen = a.mask == kMaskCausal && a.window && (double)a.window + a.max_q < keys ? (double)a.window + a.max_q : keys;
     const double tiles = (double)a.c.n_seq * e.tiles * H;
@@ -143,7 +145,7 @@ LatentNeeds latent_needs(const LatentJob &a, int fmt, bool f32, int form) {
     if (expands(a, fmt, form)) {
         const Expanded e = expanded_of(a);
         const int64_t wide = e.blocks > e.tiles ? e.blocks : e.tiles;
-        return {2 * e.bytes, (int64_t)a.a.c.n_seq * wide * e.heads};
+        return {e.all, (int64_t)a.a.c.n_seq * wide * e.heads};
     }
     const int64_t rows = (int64_t)a.a.T * a.a.n_q;
     const Plan p = plan_of(a, fmt);
@@ -158,7 +160,9 @@ hipError_t launch_latent(const LatentJob &job, int fmt, bool f32, int form, void
     LatentJob a = job;
     if (expands(a, fmt, form)) {
         const Expanded e = expanded_of(a);
-        ExpandArgs x{a.a, a.w, static_cast<uint16_t *>(ws), reinterpret_cast<uint16_t *>(static_cast<char *>(ws) + e.bytes), a.rot, 0, 0, e.keys, e.blocks, e.tiles};
+        char *at = static_cast<char *>(ws);
+        ExpandArgs x{a.a, a.w, reinterpret_cast<uint16_t *>(at), reinterpret_cast<uint16_t *>(at + e.bytes), reinterpret_cast<float *>(at + 2 * e.bytes),
+                     a.rot, 0, 0, e.keys, e.blocks, e.tiles};
         x.a.group = 1;
         for (x.first = 0; x.first < a.a.n_q; x.first += e.heads) {
             x.heads = a.a.n_q - x.first < e.heads ? a.a.n_q - x.first : e.heads;

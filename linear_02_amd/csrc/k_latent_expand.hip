@@ -13,6 +13,9 @@
 //           workspace and `rot` from the cache (they are the same for all heads), 32 at a time
 //           through two LDS buffers; two workgroups share a CU, so that one's softmax falls into
 //           the other's products.
+// Expanded rows are fp16 times a power of two of each row's own, weights fp16 too: an eighth of the error of bf16,
+// which put outputs at 1.5 to 1.8 times what their own rounding costs (1.02 now), in as many products. A scale of
+// more than one row would let a row that a query does not see take precision from those that it sees.
 // 2048 tokens over 4000 keys, 32 heads of 128 + 64, latent 512: 57 us for the first (590 TFLOP/s), 167 for
 // the second (750), the matrix products and the softmax between them.
 #include "wl_latent.h"
@@ -105,20 +108,42 @@ __global__ __launch_bounds__(256) void expand_kernel(ExpandArgs x) {
         wait_loads();
         __syncthreads();
     }
-    uint16_t *base = (wave < 2 ? x.k : x.v) + ((size_t)s * x.heads + head) * x.keys * kD + (wave & 1) * (kD / 2) + 8 * g;
+    // Two waves share a key's row: its largest finite element decides over the scale.
+    float *largest = reinterpret_cast<float *>(lds);   // [wave][key]
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const int j = j0 + 16 * i + n;
+        float top = 0.0f;
+#pragma unroll
+        for (int b = 0; b < 2 * kPairs; ++b)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float a = fabsf(o[b][i][e]);
+                top = fmaxf(top, a < __builtin_inff() ? a : 0.0f);
+            }
+        top = groups_max(top);
+        if (g == 0) largest[wave * kBlock + 16 * i + n] = top;
+    }
+    __syncthreads();
+    const size_t unit_rows = ((size_t)s * x.heads + head) * x.keys;
+    uint16_t *base = (wave < 2 ? x.k : x.v) + unit_rows * kD + (wave & 1) * (kD / 2) + 8 * g;
+    float *scales = x.scales + 2 * (unit_rows + j0) + 32 * (wave >> 1);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int at = 16 * i + n, j = j0 + at;
+        const HalfScale to = half_scale(fmaxf(largest[wave * kBlock + at], largest[(wave ^ 1) * kBlock + at]));
+        if (g == 0 && (wave & 1) == 0) scales[(at >> 5) * 64 + (at & 31)] = to.down;   // of every key of the block: all are read
         if (j >= see.hi) continue;
         const bool there = has >> i & 1u;
 #pragma unroll
         for (int p = 0; p < kPairs; ++p) {
-            const f32x4 u = o[2 * p][i], v = o[2 * p + 1][i];
-            const u32x4 e = {pack2(u.x, u.y), pack2(u.z, u.w), pack2(v.x, v.y), pack2(v.z, v.w)};
+            const f32x4 u = o[2 * p][i] * to.up, v = o[2 * p + 1][i] * to.up;
+            const u32x4 e = {pack_half2(u.x, u.y), pack_half2(u.z, u.w), pack_half2(v.x, v.y), pack_half2(v.z, v.w)};
             *reinterpret_cast<u32x4 *>(base + (size_t)j * kD + 32 * p) = there ? e : u32x4{0, 0, 0, 0};
         }
     }
 }
+
+__device__ __forceinline__ float half_element(const uint16_t *p) { return (float)__builtin_bit_cast(_Float16, ldg(p)); }
 
 // One wave, one query row: the definition, key by key, over the expanded keys and values.
 // Lane holds output elements 2 lane, 2 lane + 1 (unnormalised).
@@ -133,6 +158,7 @@ __device__ void expanded_row(const ExpandArgs &x, const Seq &q, int i, int head,
     float m = kNegInf;
     l = 0.0f, acc[0] = acc[1] = 0.0f;
     const Span span = span_of(a, q);
+    const float *scales = x.scales + 2 * ((size_t)q.s * x.heads + head) * x.keys;
     const int j0 = v.tree ? min(v.lo, max(q.ctx, 0)) : v.lo, j1 = v.tree ? q.kv : v.hi;
     for (int j = max(j0, span.lo); j < min(j1, span.hi); ++j) {
         if (!visible(a, q, v, j)) continue;
@@ -140,8 +166,10 @@ __device__ void expanded_row(const ExpandArgs &x, const Seq &q, int i, int head,
         if ((unsigned)page >= (unsigned)a.c.n_pages) continue;
         const int64_t row = ((int64_t)page << a.c.page_shift) + (j & ((1 << a.c.page_shift) - 1));
         const uint16_t *rp = static_cast<const uint16_t *>(a.c.k) + row * (a.c.d + x.rot) + a.c.d;
+        const float *scale = scales + (size_t)(j >> 5) * 64 + (j & 31);
+        const float ks = scale[0], vs = scale[32];
         float s = key ? qr * element(rp + lane) : 0.0f;
-        if (on) s += q0 * element(kp + (size_t)j * kD + 2 * lane) + q1 * element(kp + (size_t)j * kD + 2 * lane + 1);
+        if (on) s += q0 * (ks * half_element(kp + (size_t)j * kD + 2 * lane)) + q1 * (ks * half_element(kp + (size_t)j * kD + 2 * lane + 1));
         s = wave_sum(s) * a.scale2;
         if (s == kNegInf) continue;
         const float top = s > m ? s : m;   // a NaN score leaves m and makes p NaN
@@ -152,7 +180,7 @@ __device__ void expanded_row(const ExpandArgs &x, const Seq &q, int i, int head,
         if (l != l) break;   // the row is NaN, whatever follows
         if (on)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) acc[e] = acc[e] * up + (p != 0.0f ? p * element(vp + (size_t)j * kD + 2 * lane + e) : 0.0f);
+            for (int e = 0; e < 2; ++e) acc[e] = acc[e] * up + (p != 0.0f ? p * (vs * half_element(vp + (size_t)j * kD + 2 * lane + e)) : 0.0f);
     }
 }
 
@@ -161,8 +189,9 @@ __global__ __launch_bounds__(256, 2) void attend_kernel(ExpandArgs x) {
     constexpr int kSteps = kD / 32, kBlocks = kD / 16, kRow = 2 * kD, kPieces = kD / 8, kPer = 64 / kPieces;   // rows of a load
     constexpr int kK = 32 * kRow, kBuffer = 2 * kK + 32 * 128;   // keys, values, rotated keys
     constexpr int kAhead = 4;
-    __shared__ __align__(16) char lds[2 * kBuffer + 64];
-    int (*range)[4] = reinterpret_cast<int (*)[4]>(lds + 2 * kBuffer);
+    constexpr int kScales = 2 * kBuffer, kRange = kScales + 2 * 256;   // [step % 2][of keys, of values][32]
+    __shared__ __align__(16) char lds[kRange + 64];
+    int (*range)[4] = reinterpret_cast<int (*)[4]>(lds + kRange);
     const AttnJob &a = x.a;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15, g = lane >> 4;
     const int head = (int)(blockIdx.x % x.heads), unit = (int)(blockIdx.x / x.heads);
@@ -174,20 +203,37 @@ __global__ __launch_bounds__(256, 2) void attend_kernel(ExpandArgs x) {
     const uint16_t *kp = x.k + ((size_t)s * x.heads + head) * x.keys * kD, *vp = x.v + ((size_t)s * x.heads + head) * x.keys * kD;
     u32x4 qf[2][kSteps + 2];
     f32x4 o[2][kBlocks];
-    float m[2], l[2];
+    // References, sums; of a row's scores; outputs and sums are held times 2^in_o, which brings weights times their
+    // values' scales into fp16's range.
+    float m[2], l[2], scale2[2];
+    int in_o[2];
     int lo = 0x7FFFFFFF, hi = 0, flo = 0, fhi = 0x7FFFFFFF;   // some row sees [lo, hi), every row [flo, fhi)
     const uint32_t sign = a.scale2 < 0.0f ? 0x80008000u : 0u;
-    const float scale2 = fmaxf(fabsf(a.scale2), 0x1p-126f);
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
         const int i = r0 + 16 * t + n;
         const bool on = i < q.rows;
         const uint16_t *qp = static_cast<const uint16_t *>(a.q) + (size_t)(q.q0 + (on ? i : 0)) * a.ldq + (size_t)(x.first + head) * (kD + R) + 8 * g;
+        float most = 0.0f;
 #pragma unroll
         for (int k = 0; k < kSteps + 2; ++k) {
             const uint32_t kept = on && 32 * k < kD + R ? 0xFFFFFFFFu : 0u;
             qf[t][k] = (ldg(reinterpret_cast<const u32x4 *>(qp + min(32 * k, kD + R - 32))) ^ sign) & kept;
+            if (k < kSteps)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) most = fmaxf(most, fmaxf(fabsf(bf16_f(qf[t][k][e] & 0xFFFFu)), fabsf(__uint_as_float(qf[t][k][e] & 0xFFFF0000u))));
         }
+        // Queries are multiplied by a power of two of the row's, the rotated ones, which stay bf16, by the same. (Where all are
+        // below 2^-46 it is no larger: scale2 stays a number then.)
+        const HalfScale to = half_scale(fmaxf(groups_max(most), 0x1p-46f));
+        scale2[t] = fmaxf(fabsf(a.scale2) * to.down, 0x1p-126f), in_o[t] = -90;
+#pragma unroll
+        for (int k = 0; k < kSteps + 2; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float q0 = bf16_f(qf[t][k][e] & 0xFFFFu) * to.up, q1 = __uint_as_float(qf[t][k][e] & 0xFFFF0000u) * to.up;
+                qf[t][k][e] = k < kSteps ? pack_half2(q0, q1) : pack2(q0, q1);
+            }
         const Sees see = sees(a, q, i);
         if (on) {
             lo = min(lo, see.tree ? min(see.lo, max(q.ctx, 0)) : see.lo);
@@ -233,6 +279,7 @@ __global__ __launch_bounds__(256, 2) void attend_kernel(ExpandArgs x) {
         auto turn_k = [](int r) { return kD == 128 ? r & 15 : r >> 1 & 7; };
         auto turn_v = [](int r) { return kD == 128 ? (r & 7) << 1 : (r >> 1 & 3) << 1; };
         const char *kpool = scalar(reinterpret_cast<const char *>(kp)), *vpool = scalar(reinterpret_cast<const char *>(vp));
+        const char *spool = scalar(reinterpret_cast<const char *>(x.scales + 2 * ((size_t)s * x.heads + head) * x.keys));
         uint32_t valid_in = 0;
         auto fetch = [&](int j0, int step) {
             valid_in = ((unsigned)page[0] < (unsigned)n_pages ? 0xFFFFu : 0u) | ((unsigned)page[1] < (unsigned)n_pages ? 0xFFFF0000u : 0u);
@@ -251,6 +298,7 @@ __global__ __launch_bounds__(256, 2) void attend_kernel(ExpandArgs x) {
             const char *rf = scalar(static_cast<const char *>(a.c.k) + ((((int64_t)((unsigned)pg < (unsigned)n_pages ? pg : 0)) << shift) + off) * bytes + 2 * a.c.d);
             const int r = 8 * (wave & 1) + (ln >> 3), piece = (ln & 7) ^ (r >> 1 & 7);
             load_to_lds(rf, min(r, last - min(jh, last & ~15)) * bytes + min(piece, R / 8 - 1) * 16, to + 2 * kK + 8 * wave * 128);
+            if (wave == 0) load_to_lds4(scalar(spool + (int64_t)j0 * 8), ln * 4, lds_byte(lds) + kScales + (step & 1) * 256);
         };
         const int key_v = 4 * g + (n >> 2);
         const uint32_t second = R > 32 ? 0xFFFFFFFFu : 0u;
@@ -258,9 +306,9 @@ __global__ __launch_bounds__(256, 2) void attend_kernel(ExpandArgs x) {
             const int in = (step & 1) * kBuffer;
             int kb = in + n * kRow + ((g ^ turn_k(n)) << 4), rb = in + 2 * kK + n * 128 + ((g ^ (n >> 1 & 7)) << 4);
             asm volatile("" : "+v"(kb), "+v"(rb));
-            f32x4 sc[2][2];
+            f32x4 sc[2][2], rotated[2][2];
 #pragma unroll
-            for (int t = 0; t < 2; ++t) sc[t][0] = sc[t][1] = f32x4{0, 0, 0, 0};
+            for (int t = 0; t < 2; ++t) sc[t][0] = sc[t][1] = rotated[t][0] = rotated[t][1] = f32x4{0, 0, 0, 0};
             constexpr int kEach = kSteps + 2, kAll = 2 * kEach;
             // Rows n and 16 + n are turned alike: bit 4 is in neither turn.
             auto operand = [&](int i) {
@@ -278,18 +326,30 @@ __global__ __launch_bounds__(256, 2) void attend_kernel(ExpandArgs x) {
                 const int b = i / kEach, k = i % kEach;
                 const u32x4 here = k > kSteps ? kf[i % kAhead] & second : kf[i % kAhead];
 #pragma unroll
-                for (int t = 0; t < 2; ++t) sc[t][b] = mfma16(here, qf[t][k], sc[t][b]);
+                for (int t = 0; t < 2; ++t) {
+                    if (k < kSteps)
+                        sc[t][b] = mfma16_half(here, qf[t][k], sc[t][b]);
+                    else
+                        rotated[t][b] = mfma16(here, qf[t][k], rotated[t][b]);
+                }
                 if (i + kAhead < kAll) kf[i % kAhead] = operand(i + kAhead);
                 __builtin_amdgcn_sched_barrier(0);
             }
             __builtin_amdgcn_s_setprio(0);
             u32x4 ph[2];
+            const char *scales = lds + kScales + (step & 1) * 256 + 16 * g;
+            f32x4 ks[2], vs[2];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) ks[b] = *reinterpret_cast<const f32x4 *>(scales + 64 * b), vs[b] = *reinterpret_cast<const f32x4 *>(scales + 128 + 64 * b);
+            float most = vs[0].x;
+#pragma unroll
+            for (int e = 1; e < 8; ++e) most = fmaxf(most, vs[e >> 2][e & 3]);
             const bool all = j0 >= flo && j0 + 32 <= min(fhi, k1) && valid == 0xFFFFFFFFu;
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 float v[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = sc[t][e >> 2][e & 3];
+                for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(sc[t][e >> 2][e & 3], ks[e >> 2][e & 3], rotated[t][e >> 2][e & 3]);
                 if (__builtin_expect(!all, 0)) {
                     const ExpandArgs again = argument_again<ExpandArgs>();
                     const Seq qq = seq_of(again.a, s);
@@ -301,26 +361,31 @@ __global__ __launch_bounds__(256, 2) void attend_kernel(ExpandArgs x) {
 #pragma unroll
                 for (int e = 1; e < 8; ++e) top = fmaxf(top, v[e]);
                 top = groups_max(top);
-                top = top == kNegInf ? top : top * scale2;
-                if (__builtin_expect(__any(top > m[t] + 8.0f), 0)) {
-                    // The reference moves only when a score passes it by 2^8: sums stay in range.
+                top = top == kNegInf ? top : top * scale2[t];
+                if (__builtin_expect(__any(top > m[t] + 8.0f || ldexpf(most, in_o[t]) > 128.0f), 0)) {
+                    // The reference moves only when a score passes it by 2^8: sums stay in range. in_o moves with it, or
+                    // when a weight times its value's scale might pass fp16's range: the largest of them so far becomes 2^3 to 2^4.
                     const float now = fmaxf(m[t], top), up = now == m[t] ? 1.0f : __builtin_amdgcn_exp2f(m[t] - now);
-                    m[t] = now;
-                    l[t] *= up;
+                    const float ref = now == kNegInf ? 0.0f : now;
+                    float large = 0.0f;
 #pragma unroll
-                    for (int b = 0; b < kBlocks; ++b) o[t][b] *= up;
+                    for (int e = 0; e < 8; ++e) large = fmaxf(large, __builtin_amdgcn_exp2f(__builtin_fmaf(v[e], scale2[t], -ref)) * vs[e >> 2][e & 3]);
+                    large = fmaxf(groups_max(large), ldexpf(8.0f * up, -in_o[t]));
+                    const int is = min(max(130 - (int)(__float_as_uint(large) >> 23), -90), 90);
+                    const float by = ldexpf(up, is - in_o[t]);
+                    m[t] = now, in_o[t] = is;
+                    l[t] *= by;
+#pragma unroll
+                    for (int b = 0; b < kBlocks; ++b) o[t][b] *= by;
                 }
-                const float ref = m[t] == kNegInf ? 0.0f : m[t];
+                const float ref = (float)in_o[t] - (m[t] == kNegInf ? 0.0f : m[t]);
                 float p[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(v[e], scale2, -ref));
-                ph[t] = u32x4{pack2(p[0], p[1]), pack2(p[2], p[3]), pack2(p[4], p[5]), pack2(p[6], p[7])};
-                // the sum of the weights as the product will use them
-                constexpr uint32_t kOnes = 0x3F803F80u;
-                l[t] = dot2(ph[t].x, kOnes, l[t]);
-                l[t] = dot2(ph[t].y, kOnes, l[t]);
-                l[t] = dot2(ph[t].z, kOnes, l[t]);
-                l[t] = dot2(ph[t].w, kOnes, l[t]);
+                for (int e = 0; e < 8; ++e) {
+                    l[t] += p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(v[e], scale2[t], ref));
+                    p[e] *= vs[e >> 2][e & 3];
+                }
+                ph[t] = u32x4{pack_half2(p[0], p[1]), pack_half2(p[2], p[3]), pack_half2(p[4], p[5]), pack_half2(p[6], p[7])};
             }
             int vb = in + kK + key_v * kRow + ((turn_v(key_v) | (n >> 1 & 1)) << 4) + 8 * (n & 1);
             asm volatile("" : "+v"(vb));
@@ -330,7 +395,7 @@ __global__ __launch_bounds__(256, 2) void attend_kernel(ExpandArgs x) {
                 const char *p = lds + (vb ^ b << 5);
                 const u32x2 u = read_tr16(p), w = read_tr16(p + 16 * kRow);
 #pragma unroll
-                for (int t = 0; t < 2; ++t) o[t][b] = mfma16(u32x4{u.x, u.y, w.x, w.y}, ph[t], o[t][b]);
+                for (int t = 0; t < 2; ++t) o[t][b] = mfma16_half(u32x4{u.x, u.y, w.x, w.y}, ph[t], o[t][b]);
             }
             __builtin_amdgcn_sched_group_barrier(0x100, 2 * kAhead, 1);
 #pragma unroll

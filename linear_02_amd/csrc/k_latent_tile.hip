@@ -113,16 +113,14 @@ __global__ __launch_bounds__(256, workgroups_per_cu(F, L, kRW, kExact)) void lat
 #pragma unroll
                 for (int e = 0; e < 2; ++e) v[k][e] = ldg(reinterpret_cast<const f32x4 *>(qp + place(k) + 4 * e));
             float scale = 1.0f;
-            if (kHalf) {
-                // The largest becomes 2^14 to 2^15: what lies 2^28 below it has fp16's full precision yet. An infinity stays
-                // one, and the row is done again.
+            if (kHalf) {   // with an infinity the row is done again
                 float most = 0.0f;
 #pragma unroll
                 for (int k = 0; k < kSteps; ++k)
 #pragma unroll
                     for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(v[k][e >> 2][e & 3]));
-                const int up = 14 - min(max((int)(__float_as_uint(groups_max(most)) >> 23) - 127, -86), 114);
-                scale = __uint_as_float((uint32_t)(127 + up) << 23), unscale = __uint_as_float((uint32_t)(127 - up) << 23);
+                const HalfScale to = half_scale(groups_max(most));
+                scale = to.up, unscale = to.down;
             }
 #pragma unroll
             for (int k = 0; k < kSteps + 2; ++k) {

@@ -48,12 +48,23 @@ void launch_latent_f32(const CoreArgs &x, const CoreKind &k, unsigned blocks, hi
 struct ExpandArgs {
     AttnJob a;
     const void *w;
-    uint16_t *k, *v;       // [n_seq][heads][keys][nope], [value]
+    uint16_t *k, *v;       // [n_seq][heads][keys][nope], [value], fp16
+    float *scales;         // [n_seq][heads][keys / 32][2][32]: what a row of k, and of v, is to be multiplied with
     int rot, first, heads;
     int keys;              // room of a sequence, a multiple of 128
     int blocks, tiles;     // of 128 keys, of 128 queries of a sequence, at most
 };
 void launch_expanded(const ExpandArgs &x, int d, hipStream_t s);
+
+// The power of two that brings a row's largest element to 2^14 .. 2^15 in fp16, and its inverse. What lies up
+// to 2^28 below the largest has fp16's full precision then, 2^-11; an infinity stays one.
+struct HalfScale {
+    float up, down;
+};
+__device__ __forceinline__ HalfScale half_scale(float most) {
+    const int k = 14 - min(max((int)(__float_as_uint(most) >> 23) - 127, -112), 127);
+    return {__uint_as_float((uint32_t)(127 + k) << 23), __uint_as_float((uint32_t)(127 - k) << 23)};
+}
 
 // Bytes of a cache row.
 template <int F>

@@ -9,6 +9,7 @@ of the output's own, which is what is measured here. A sum of 512 random squares
 from __future__ import annotations
 
 import pytest
+import torch
 
 from tests import serve_ref
 from tests.layer_ref import f64
@@ -72,3 +73,40 @@ def test_without_weights(wl, fmt, L, H):  # noqa: F811
     """Queries are as given then, and outputs are rounded once."""
     for seqs in (SHORT, LONG):
         assert off(wl, batch(wl, H, seqs, L, 64, 64, 64, fmt, False), form="auto") <= ONE
+
+
+@pytest.mark.parametrize("L,R,D", [(512, 64, 128), (256, 32, 64), (128, 64, 128), (512, 32, 64)])
+@pytest.mark.parametrize("seqs", [[(20, 33), (0, 9)], [(300, 140)], [(1500, 20), (40, 130)]])
+def test_expanded(wl, L, R, D, seqs):  # noqa: F811
+    """Expanded keys and values and the weights are fp16: 2^-11 each, an eighth of the output's rounding."""
+    assert off(wl, batch(wl, 3, seqs, L, R, D, D, BF, True), form="expanded") <= ONE
+
+
+@pytest.mark.parametrize("mask", ["causal", "full"])
+def test_expanded_rows_of_any_size(wl, mask):  # noqa: F811
+    """Latents of rows far apart in size: each expanded row has a scale of its own, and weights times these stay
+    within fp16, whether the large rows come first or last, with high scores or low ones."""
+    for seed, sizes in enumerate(([0, 6, 3], [0, -20, -40], [20, 0, -20], [0, 15, 30], [40, 0, -40], [-30, 0, 30])):
+        b = batch(wl, 4, [(180, 70), (100, 30)], 256, 64, 64, 64, BF, True)
+        rows = b.cache.rows
+        g = torch.Generator().manual_seed(seed)
+        which = torch.randint(3, rows.shape[:2], generator=g)
+        rows[..., :256] *= (2.0 ** torch.tensor(sizes, dtype=torch.float64))[which].to(rows.device)[..., None].to(BF)
+        # the latents' part of a score is kept near 1 for the largest
+        q = b.q.view(b.T, 4, -1)
+        q[:, :, :64] *= 2.0 ** -max(sizes)
+        q[:, :, 64:] *= 4.0
+        assert off(wl, b, form="expanded", mask=mask) <= ONE, sizes
+
+
+@pytest.mark.parametrize("form", ["expanded", "absorbed"])
+@pytest.mark.parametrize("size", [100, 40, -100])
+def test_rows_that_some_queries_do_not_see(wl, form, size):  # noqa: F811
+    """A latent 2^100 times the others', seen by its own query alone in a tree, takes nothing from the others'."""
+    b = batch(wl, 3, [(70, 4), (33, 1)], 256, 64, 128, 128, BF, True)
+    b.cache.rows[b.cache.table[0, 72 // 64].item(), 72 % 64, :256] *= 2.0 ** size
+    tree = i32([[1], [3], [5], [9], [1]])     # tokens 1, 2 and 3 follow token 0
+    o = f64(b.run(wl, form=form, tree=tree, max_kv=128))
+    ref, _ = serve_ref.latent_attention(b.q, b.cache, b.w, i32(b.starts), i32(b.lens), b.scale, tree=tree)
+    rows = torch.tensor([0, 1, 3, 4])
+    assert float((o[rows] - ref[rows]).norm() / (ref[rows].to(BF).double() - ref[rows]).norm()) <= ONE
