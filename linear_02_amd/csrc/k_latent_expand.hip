@@ -432,7 +432,7 @@ __global__ __launch_bounds__(256, 2) void attend_kernel(ExpandArgs x) {
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b) check += o[t][b].x * 0.0f + o[t][b].y * 0.0f + o[t][b].z * 0.0f + o[t][b].w * 0.0f;
         // A row with an infinity or a NaN is done again key by key: one that it does not see may have got in as 0 * NaN.
-        uint64_t odd = __ballot(i < q.rows && check != 0.0f);
+        uint64_t odd = __ballot(i < q.rows && (check != 0.0f || beyond(m[t])));
         odd |= odd >> 32;
         odd |= odd >> 16;
         const uint32_t again = (uint32_t)odd & 0xFFFFu;

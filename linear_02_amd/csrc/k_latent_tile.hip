@@ -457,7 +457,7 @@ __global__ __launch_bounds__(256, workgroups_per_cu(F, L, kRW, kExact)) void lat
 #pragma unroll
     for (int c = 0; c < kBlocks; ++c) check += o[c].x * 0.0f + o[c].y * 0.0f + o[c].z * 0.0f + o[c].w * 0.0f;
     const int r = r0 + n;
-    uint64_t odd = __ballot(r < rows && check != 0.0f);
+    uint64_t odd = __ballot(r < rows && (check != 0.0f || beyond(m)));
     odd |= odd >> 32;
     odd |= odd >> 16;
     uint32_t again = (uint32_t)odd & 0xFFFFu;

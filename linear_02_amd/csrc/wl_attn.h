@@ -61,6 +61,11 @@ __device__ __forceinline__ bool visible(const AttnJob &a, const Seq &q, const Se
     return b < 32ll * a.tree_words && (v.tree[b >> 5] >> (b & 31) & 1u);
 }
 
+// A weight is 2^(score scale - m) in one fused operation, where m is that of the largest score, rounded: off by
+// the same factor in all of a row, which leaves fp32's range where scores are beyond 2^30. Rows beyond 2^24 are
+// done again key by key, which rounds both alike.
+__device__ __forceinline__ bool beyond(float m) { return m != kNegInf && fabsf(m) > 0x1p24f; }
+
 // Four elements of a cache row as fp32, at element `at` of the pool.
 template <int F>
 __device__ __forceinline__ void cache4(const void *pool, int64_t at, float *v) {

@@ -338,7 +338,7 @@ __device__ __forceinline__ void finish(const TileArgs &x, const Work &work, R ro
             if (16 * b < d) check += o[t][b].x * 0.0f + o[t][b].y * 0.0f + o[t][b].z * 0.0f + o[t][b].w * 0.0f;
         // A row with an infinity or a NaN is done again key by key: one that it does
         // not see may have got in as 0 * NaN.
-        uint64_t odd = __ballot(r < rows && check != 0.0f);
+        uint64_t odd = __ballot(r < rows && (check != 0.0f || beyond(m[t])));
         odd |= odd >> 32;
         odd |= odd >> 16;
         const uint32_t again = (uint32_t)odd & 0xFFFFu;
