@@ -115,11 +115,15 @@ Expanded expanded_of(const LatentJob &job) {
 
 // Which form AUTO takes. The expanded one forms all keys and values once, and multiplies less per
 // query and key then; 128 queries of a head are one workgroup that walks all of their keys, so it wants
-// many of those, or few keys. Both times are estimated in us from constants fitted to measurements at a
-// latent of 512 and heads of 128 + 64 (absorbed, expanded; n_seq x queries over keys, heads):
-//   1 x 128 over 4096, 32    78, 186     1 x 512 over 4096, 32   199, 186     1 x 512 over 8192, 16   183, 311
-//   1 x 192 over 192, 128    82, 30      1 x 512 over 512, 32     83, 40      1 x 2048 over 2048, 8   128, 86
-//   1 x 256 over 4096, 128  362, 384     8 x 192 over 4096, 32   646, 657     8 x 256 over 2048, 32   420, 344
+// many of those, or few keys. Both times are estimated in us from constants fitted to measurements
+// (absorbed, expanded; n_seq x queries over up to so many keys, heads; latent 512, heads of 128 + 64):
+//   1 x 128 over 4096, 32   109, 216     1 x 512 over 4096, 32   289, 214     1 x 512 over 8192, 16   275, 357
+//   1 x 192 over 192, 128    95, 36      1 x 512 over 512, 32     92, 47      1 x 2048 over 2048, 8   176, 101
+//   1 x 256 over 4096, 128  549, 422     8 x 192 over 4096, 32   578, 495     8 x 256 over 2048, 32   499, 305
+// and, of 1 x 512 over 4096 and 8 x 256 over 2048, 32 heads, at a latent of 256 with heads of 128: 150, 199 and 243, 246;
+// 256 with 64: 139, 153 and 229, 142; 128 with 64: 102, 148 and 143, 128. The one taken is the faster or within 3 %,
+// but for 8 x 192 over 4096 and the last, absorbed at 1.16 and 1.12 times the other: of 8 sequences of uneven lengths
+// the host knows the longest.
 // Calls of fewer queries than a tile has stay absorbed: the first constant is of many rows.
 bool expands(const LatentJob &job, int fmt, int form) {
     const AttnJob &a = job.a;
@@ -131,9 +135,9 @@ bool expands(const LatentJob &job, int fmt, int form) {
     const double keys = e.keys, L = a.c.d, H = a.n_q;
     const double seen = a.mask == kMaskCausal && a.window && (double)a.window + a.max_q < keys ? (double)a.window + a.max_q : keys;
     const double tiles = (double)a.c.n_seq * e.tiles * H;
-    const double absorbed = 50 + 1.05e-9 * 2 * a.T * H * seen * (2 * L + job.rot);
-    const double expanded = 10 + 1.88e-9 * 2 * a.c.n_seq * keys * H * (job.nope + job.value) * L +
-                            0.0286 * seen * (tiles < 394 ? 1.0 : tiles * (0.65 / 256));
+    const double absorbed = 50 + (L == 512 ? 1.6e-9 : 1.15e-9) * 2 * a.T * H * seen * (2 * L + job.rot);   // two workgroups a CU below 512
+    const double expanded = 10 + 2e-9 * 2 * a.c.n_seq * keys * H * (job.nope + job.value) * L +
+                            0.0327 * seen * (tiles < 394 ? 1.0 : tiles * (0.65 / 256));
     return expanded < absorbed;
 }
 
