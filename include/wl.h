@@ -573,6 +573,9 @@ wl_status wl_latent_read(const wl_latent_read_args *a, void *hip_stream);
  *                             With w, a bf16 cache, nope and value both 64 or both
  *                             128 only (else WL_ERR_UNSUPPORTED)
  *         WL_LATENT_AUTO      the one estimated to take less time: expanded for prompts
+ *         The expanded form's workspace holds n_seq min(max_kv, max_pages page) keys and
+ *         values of as many heads at once as fit 8 GiB, of one at least. AUTO stays absorbed
+ *         where that one is more.
  * Numerics in bf16: sums are fp32. Absorbed, q and the outputs in the latent space are fp32
  * too, multiplied, as the weights, in two parts of bf16 (over e4m3 rows q as fp16 times a power
  * of two of the row's). Expanded, q, keys and values are fp16 times a power of two of every row's

@@ -7,11 +7,12 @@ namespace {
 
 size_t pad(size_t b) { return (b + 255) & ~(size_t)255; }
 
-// Fewest keys of a piece. Waves with keys of their own (calls of at most 16 rows a sequence) read a
-// piece in 128-key steps and join it themselves: one token of 16 heads over 4000 keys, whole call,
-// 27.2 us with 256 and 26.0 us with 128. In fp32, 4 streams of 3 tokens and 16 heads over 1024 keys take
-// 63 us with 64 and 83 with 128. Elsewhere 256: 2 streams of 128 heads over 2000 keys 49 us, 64 with 512,
-// 44 with 128, which costs where pieces are many (32 heads of 8 streams over 4096 keys 34 and 35).
+// Fewest keys of a piece (whole calls, replayed from a graph). Waves with keys of their own (calls of at most 16
+// rows a sequence) read a piece in 128-key steps: one token of 16 heads over 1000 keys takes 26.8 us with 128 and
+// 28.2 with 256, over 4000 33.9 and 31.3, 8 streams over up to 4096 41.8 and 37.2. In fp32, 4 streams of 3
+// tokens and 16 heads over 1024 keys take 63 us with 64 and 83 with 128. Elsewhere 256: 2 streams of 128 heads
+// over up to 2000 keys 46.5 us, 58.8 with 512, 42.5 with 128, which costs where pieces are many (32 heads of
+// 8 streams over up to 4096 keys 42.1 and 46.0).
 constexpr int kMinChunk = 256, kMinChunkOwn = 128, kMinChunkF32 = 64;
 
 struct Plan {
@@ -30,8 +31,9 @@ Plan plan_of(const LatentJob &job, int fmt) {
     int64_t span = a.max_kv;
     if (a.mask == kMaskCausal && a.window && (int64_t)a.window + a.max_q < span) span = (int64_t)a.window + a.max_q;
     span += 31;
-    // Waves over keys instead of rows where rows are few: 64 streams of 32 heads over 4096 e4m3 keys 74 us with
-    // two pairs, 100 with four waves of rows.
+    // Waves over keys instead of rows where rows are few: 64 streams of 32 heads over up to 4096 e4m3 keys 74 us with
+    // two pairs, 94 with four waves of rows; of 16 heads 61 us with four waves that have keys of their own, 69 with
+    // pairs (one token over 1000 bf16 keys 26.8 and 30.3).
     p.kind.row_waves = rows > (f32 ? 16 : 32) ? 4 : rows > 16 ? 2 : 1;
     p.kind.exact = job.w && !f32;
     p.sp.tile_rows = 16 * p.kind.row_waves;
@@ -66,7 +68,7 @@ Plan plan_of(const LatentJob &job, int fmt) {
 struct Places {
     size_t q, o, part, ml, bytes;
 };
-Places places_of(const LatentJob &a, const Plan &p, bool f32) {
+Places places_of(const LatentJob &a, const Plan &p) {
     const size_t rows = (size_t)a.a.T * a.a.n_q, L = a.a.c.d;
     const bool split = p.sp.n_split > 1;
     Places w{};
@@ -77,7 +79,7 @@ Places places_of(const LatentJob &a, const Plan &p, bool f32) {
         return here;
     };
     if (a.w) {
-        w.q = take(rows * (L + a.rot) * (f32 || p.kind.exact ? 4 : 2));
+        w.q = take(rows * (L + a.rot) * 4);
         if (!split) w.o = take(rows * L * 4);
     }
     if (split) {
@@ -153,7 +155,7 @@ LatentNeeds latent_needs(const LatentJob &a, int fmt, bool f32, int form) {
     }
     const int64_t rows = (int64_t)a.a.T * a.a.n_q;
     const Plan p = plan_of(a, fmt);
-    LatentNeeds n{places_of(a, p, f32).bytes, p.items};
+    LatentNeeds n{places_of(a, p).bytes, p.items};
     // the products around it, of tokens and heads
     const int64_t around = (f32 ? rows : (rows + 15) / 16 * 8) + 8 * a.a.n_q;
     if (around > n.workgroups) n.workgroups = around;
@@ -177,7 +179,7 @@ hipError_t launch_latent(const LatentJob &job, int fmt, bool f32, int form, void
         return hipSuccess;
     }
     const Plan p = plan_of(a, fmt);
-    const Places w = places_of(a, p, f32);
+    const Places w = places_of(a, p);
     char *at = static_cast<char *>(ws);
     CoreArgs x{a.a, p.sp, a.rot, a.w || f32};
     hipError_t e;
@@ -185,7 +187,7 @@ hipError_t launch_latent(const LatentJob &job, int fmt, bool f32, int form, void
         if (f32)
             launch_absorb_f32(a, reinterpret_cast<float *>(at + w.q), s);
         else
-            launch_absorb(a, at + w.q, p.kind.exact, s);
+            launch_absorb(a, reinterpret_cast<float *>(at + w.q), s);
         if ((e = hipGetLastError()) != hipSuccess) return e;
         x.a.q = at + w.q, x.a.ldq = x.a.n_q * (x.a.c.d + a.rot);
         x.a.o = at + w.o, x.a.ldo = x.a.n_q * x.a.c.d;

@@ -1,10 +1,10 @@
 // Latent attention in the expanded form, for prompts over bf16 rows: every head's keys and
 // values formed once per call, then attention over them head by head.
 //
-// Expanded, a pair of a query and a key takes nope + rot + value products instead of the 2
-// latent + rot of the latent space, for latent (nope + value) more per key: less from some
-// 170 queries of a sequence on (latent 512, heads of 128 and 64), where the products are
-// equally fast.
+// Expanded, a pair of a query and a key takes nope + rot + value products instead of the 4
+// latent + rot of the latent space with its remainders, for latent (nope + value) more per key:
+// less from some 75 queries of a sequence on (latent 512, heads of 128 and 64), where the
+// products are equally fast.
 //   expand  [W^K; W^V] of a head times 128 keys' latents, a matrix product with both sides
 //           through LDS 64 elements at a time, in two buffers. A wave has 64 rows of the
 //           weight and all keys; rows are dealt to the matrix instruction so that a lane gets
@@ -16,8 +16,8 @@
 // Expanded rows are fp16 times a power of two of each row's own, weights fp16 too: an eighth of the error of bf16,
 // which put outputs at 1.5 to 1.8 times what their own rounding costs (1.02 now), in as many products. A scale of
 // more than one row would let a row that a query does not see take precision from those that it sees.
-// 2048 tokens over 4000 keys, 32 heads of 128 + 64, latent 512: 57 us for the first (590 TFLOP/s), 167 for
-// the second (750), the matrix products and the softmax between them.
+// 2048 tokens over 4000 keys, 32 heads of 128 + 64, latent 512, traced: 62 to 66 us for the first, 194 to 203 for
+// the second, the matrix products and the softmax between them, 229 us for the untraced call.
 #include "wl_latent.h"
 
 namespace wl {

@@ -6,10 +6,10 @@
 // In bf16 both are formed transposed on the matrix cores (rows of the weight times tokens): 16
 // tokens are the columns of a product, and a lane gets four neighbouring outputs of one token.
 //   into   a workgroup takes 128 columns of one head's W^K, which LDS's transposing reads turn
-//   out    a workgroup takes 16 tokens of one head: it joins their pieces' outputs into LDS, as
-//          a bf16 head and a bf16 remainder (so o' is not rounded), and its four waves share
-//          the latent axis of the product, whose partial sums meet in LDS
-// 32 tokens of 128 heads: 8.5 us into (16.8 MB of weights), 18 out of it, with 33 MB of partial outputs.
+//   out    a workgroup takes 16 tokens of one head: it joins their pieces' outputs, which are fp32, into
+//          LDS, as a bf16 head and a bf16 remainder (so o' is not rounded), and its four waves
+//          share the latent axis of the product, whose partial sums meet in LDS
+// 32 tokens of 128 heads: 10 us into (16.8 MB of weights), 19 out of it, with up to 42 MB of partial outputs.
 #include "wl_latent.h"
 
 namespace wl {
@@ -19,8 +19,7 @@ namespace {
 constexpr int kColumns = 128;        // of the latent axis, a workgroup of the product into it
 constexpr int kTokens = 64;          // tokens of a workgroup there
 
-template <class E>
-__global__ __launch_bounds__(256) void absorb_kernel(LatentJob a, E *out) {
+__global__ __launch_bounds__(256) void absorb_kernel(LatentJob a, float *out) {
     extern __shared__ __align__(16) char lds[];   // [nope][kColumns] bf16: piece c of row r at c ^ 2 (r & 7)
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15, g = lane >> 4;
     const int L = a.a.c.d, N = a.nope, R = a.rot, H = a.a.n_q;
@@ -38,13 +37,9 @@ __global__ __launch_bounds__(256) void absorb_kernel(LatentJob a, E *out) {
         for (int i = threadIdx.x; i < (t1 - t0) * pieces; i += 256) {
             const int t = t0 + i / pieces, c = i % pieces;
             const u32x4 v = ldg(reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(a.q) + (size_t)t * a.ldq + (size_t)h * width + N + 8 * c));
-            E *to = out + ((size_t)t * H + h) * (L + R) + L + 8 * c;
-            if (sizeof(E) == 2) {
-                *reinterpret_cast<u32x4 *>(to) = v;
-            } else {
-                *reinterpret_cast<f32x4 *>(to) = f32x4{bf16_f(v.x & 0xFFFFu), __uint_as_float(v.x & 0xFFFF0000u), bf16_f(v.y & 0xFFFFu), __uint_as_float(v.y & 0xFFFF0000u)};
-                *reinterpret_cast<f32x4 *>(to + 4) = f32x4{bf16_f(v.z & 0xFFFFu), __uint_as_float(v.z & 0xFFFF0000u), bf16_f(v.w & 0xFFFFu), __uint_as_float(v.w & 0xFFFF0000u)};
-            }
+            float *to = out + ((size_t)t * H + h) * (L + R) + L + 8 * c;
+            *reinterpret_cast<f32x4 *>(to) = f32x4{bf16_f(v.x & 0xFFFFu), __uint_as_float(v.x & 0xFFFF0000u), bf16_f(v.y & 0xFFFFu), __uint_as_float(v.y & 0xFFFF0000u)};
+            *reinterpret_cast<f32x4 *>(to + 4) = f32x4{bf16_f(v.z & 0xFFFFu), __uint_as_float(v.z & 0xFFFF0000u), bf16_f(v.w & 0xFFFFu), __uint_as_float(v.w & 0xFFFF0000u)};
         }
     }
     auto row = [&](int t) { return static_cast<const uint16_t *>(a.q) + (size_t)min(t + n, t1 - 1) * a.ldq + (size_t)h * width + 8 * g; };
@@ -74,7 +69,7 @@ __global__ __launch_bounds__(256) void absorb_kernel(LatentJob a, E *out) {
         }
         if (t + 16 < t1) read(t + 16);
         if (!on) continue;
-        E *to = out + ((size_t)(t + n) * H + h) * (L + R) + l0 + 32 * wave + 4 * g;
+        float *to = out + ((size_t)(t + n) * H + h) * (L + R) + l0 + 32 * wave + 4 * g;
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
             const float v[4] = {o[b].x, o[b].y, o[b].z, o[b].w};
@@ -386,13 +381,10 @@ __global__ __launch_bounds__(256) void up_f32_kernel(UpArgs u) {
 
 }  // namespace
 
-void launch_absorb(const LatentJob &a, void *out, bool f32_out, hipStream_t s) {
+void launch_absorb(const LatentJob &a, float *out, hipStream_t s) {
     const dim3 g((unsigned)((int64_t)(a.a.T + kTokens - 1) / kTokens * a.a.n_q * (a.a.c.d / kColumns))), b(256);
     const size_t lds = (size_t)a.nope * kColumns * 2;
-    if (f32_out)
-        hipLaunchKernelGGL((absorb_kernel<float>), g, b, lds, s, a, static_cast<float *>(out));
-    else
-        hipLaunchKernelGGL((absorb_kernel<uint16_t>), g, b, lds, s, a, static_cast<uint16_t *>(out));
+    hipLaunchKernelGGL(absorb_kernel, g, b, lds, s, a, out);
 }
 
 // Fewer units of 16 tokens and a head than this are divided over `value`, and every part joins

@@ -4,20 +4,23 @@
 // of (token, head) rows and brings every cache row once into LDS, 32 at a time, where
 // its first `latent` elements serve both products. Queries, scores, weights and outputs
 // stay in registers from the first key to the last; at a latent of 512 that is 128 of
-// outputs and 72 of queries for every 16 rows a wave has.
+// outputs, 72 of queries and 64 of their remainders for the 16 rows that a wave has.
 //   many rows  four waves of 16 rows share a tile of keys, two workgroups per CU where
 //              registers allow, so that one's softmax falls into the other's products
 //   32 rows    two pairs of waves, each pair with keys of its own
 //   16 rows    every wave with keys of its own, which it fetches for itself and waits
 //              for alone; joined in LDS at the end. Where two buffers of latents fit, the
 //              rotated keys, which only the scores need, are read first, and the next rows
-//              come in behind that (e4m3, 64 streams of 16 heads over up to 16384 keys:
-//              150 us with one buffer, 132 us so)
+//              come in behind that (e4m3, 64 streams of 16 heads over up to 16384 keys,
+//              whole call, with queries in two products: 150 us with one buffer, 132 us so)
 // Rows of e4m3 stay codes in LDS and are widened as operands: half the LDS traffic, and
 // the vector units have the time beside the products.
-// Few rows are bound by memory (64 streams of 16 heads over up to 16384 e4m3 keys 105 us, 4.3 TB/s), many
-// by what one wave per SIMD waits for between its products (32 streams of 128 heads over up to 8192 bf16
-// keys 76 us, 620 TFLOP/s).
+// Few rows are bound by memory (64 streams of 16 heads over up to 16384 e4m3 keys 106 us, 4.3 TB/s), many at a
+// latent of 512 by what one wave per SIMD waits for between its products, which remainders double (32 streams of
+// 128 heads over up to 8192 bf16 keys 114 to 129 us, some 750 TFLOP/s of them). Two workgroups a CU, which
+// queries rounded to bf16 would leave room for, took 119 us for that call instead of 127, 98 instead of 110 for 4
+// trees of 32 tokens and 32 heads, 653 instead of 862 for 2048 tokens over 4000 keys; 32 rows a wave, with weights'
+// remainders alone, 124, 108 and 755.
 // Nothing is rounded to bf16 but the output: weights, and queries that the product into the latent space left in
 // fp32, are multiplied as a bf16 head and its remainder (2^-16 off), queries of codes as fp16 (2^-11). With
 // both rounded to bf16 outputs were off by 1.6 times what their own rounding costs, with queries alone 1.41.

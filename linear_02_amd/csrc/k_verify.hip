@@ -10,8 +10,8 @@
 // fp64 throughout (off by about 1e-15 of the whole, where neighbouring borders lie 1e-5
 // apart), and the test u draft < p has no division in it.
 //
-// Bound by the vector units, which take 35 us for the powers of 288 rows of 131072 bf16 logits, 2.2 TB/s: every row is read once, in up to 64 chunks of a
-// wave each, for a chunk's largest entry and the sum of its powers relative to that; a chunk
+// Bound by the vector units, which take 35 us for the powers of 288 rows of 131072 bf16 logits, 2.2 TB/s:
+// every row is read once, in up to 64 chunks of a wave each, for a chunk's largest entry and the sum of its powers relative to that; a chunk
 // of a row (of two, with a draft) is then read again to find the token in it. All later steps
 // join a row's chunks in one wave, a lane each. Rows start anywhere (an odd vocabulary):
 // they are read in aligned groups of 16 bytes, the first and last element by element.

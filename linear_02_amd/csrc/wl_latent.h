@@ -33,9 +33,9 @@ constexpr int workgroups_per_cu(int fmt, int latent, int row_waves, bool exact) 
 }
 void launch_latent_tile(const CoreArgs &x, int fmt, const CoreKind &k, unsigned blocks, hipStream_t s);
 
-// Products of every token and head (k_latent_heads.hip): into the latent space (out: bf16, or
-// fp32), and out of it, with the join of divided keys.
-void launch_absorb(const LatentJob &a, void *out, bool f32_out, hipStream_t s);
+// Products of every token and head (k_latent_heads.hip): into the latent space, where queries are
+// fp32, and out of it, with the join of divided keys.
+void launch_absorb(const LatentJob &a, float *out, hipStream_t s);
 void launch_absorb_f32(const LatentJob &a, float *out, hipStream_t s);
 void launch_up(const LatentJob &a, const CoreArgs &x, bool f32, hipStream_t s);
 void launch_join(const CoreArgs &x, bool f32, hipStream_t s);
